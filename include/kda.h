@@ -73,7 +73,7 @@ extern "C" {
 
 typedef enum {
     KDA_OK = 0,
-    KDA_ERR_INVALID_ARG = 1, /* null pointer, negative size, bad cu_seqlens on host */
+    KDA_ERR_INVALID_ARG = 1, /* null pointer, negative size, bad cu_seqlens or page */
     KDA_ERR_UNSUPPORTED = 2, /* head dim or dtype the library does not implement */
     KDA_ERR_ALIGNMENT = 3,   /* a pointer is not 16-byte aligned                  */
     KDA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed                 */
@@ -83,7 +83,9 @@ typedef enum {
     KDA_ERR_RANGE = 8        /* a state-pass operand left the fp16 range          */
 } kda_status_t;
 
-typedef enum { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype_t;
+/* KDA_F16 and KDA_E4M3 (8 bits: 4 of exponent, 3 of fraction, no infinities)
+ * are types of the paged cache and the draft calls only. */
+typedef enum { KDA_BF16 = 0, KDA_F32 = 1, KDA_F16 = 2, KDA_E4M3 = 3 } kda_dtype_t;
 
 /*
  * kda_chunk_fwd -- chunked prefill of B fixed-length sequences.
@@ -384,14 +386,159 @@ KDA_API kda_status_t kda_decode_commit(const void* q, const void* k, const void*
                                        const int* accepted, int N, int K, int H, int d_k,
                                        int d_v, cudaStream_t stream);
 
+/*
+ * The attention layers of a hybrid stack (one to every three recurrent ones:
+ * orkas.ai, "Kimi K3 architecture", section "Sequenz: Drei Viertel der
+ * Schichten lesen nicht mehr alles") keep every token's key and value.  The
+ * cache of a request is then per-token pages plus the fixed states above
+ * (same page, section "Die Rechnung landet in der
+ * Bereitstellungsinfrastruktur").  kda_paged_cache_t describes the pages of
+ * one attention layer; the caller owns every buffer it points to.
+ *   k, v        : pages; channel c of head h of row t of page p is element
+ *                 p * page_stride + t * token_stride + h * head_stride + c
+ *                 (strides in elements, the same for k and v; each a multiple
+ *                 of 16 bytes; the layout of rows and heads is the caller's)
+ *   block_table : DEVICE int32 [n_seq, table_width], rows table_stride apart;
+ *                 position p of sequence n is row p % page_size of page
+ *                 block_table[n][p / page_size].  Entries of positions that a
+ *                 call does not touch may hold anything.
+ *   lens        : DEVICE int32 [n_seq], tokens of each sequence in the cache
+ *                 before the call's new ones.  The calls only read it; the
+ *                 caller advances it when tokens are kept.
+ *   dtype       : KDA_BF16, KDA_F16 or KDA_E4M3; a stored value stands for
+ *                 stored * k_scale (keys) or stored * v_scale (values)
+ *   d           : 64 or 128
+ * Both calls below take K new tokens for each sequence, of which the first
+ * counts[n] are real (counts: DEVICE int32 [n_seq], clamped to [0, K]; NULL:
+ * all of them).  Token i of sequence n has position lens[n] + i.  A page
+ * outside [0, num_pages) or a position outside the table is never touched:
+ * the token is left out and KDA_ERR_INVALID_ARG is set in the device status
+ * word.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    const int* block_table;
+    const int* lens;
+    long long page_stride, token_stride, head_stride;
+    long long table_stride;
+    float k_scale, v_scale;
+    kda_dtype_t dtype;
+    int n_seq, num_pages, page_size, table_width, H_kv, d;
+} kda_paged_cache_t;
+
+/*
+ * kda_cache_append -- writes the keys and values of new tokens into their
+ * pages, rotated by their position on the way, and rotates the queries.
+ *   k, v        : [n_seq, K, H_kv, d] in dtype (KDA_BF16 or KDA_F16), or, with
+ *                 cu_seqlens, packed [T, H_kv, d]; token rows k_stride and
+ *                 v_stride elements apart, heads of a token d apart (slices
+ *                 of one projection's output are taken as they are)
+ *   q, q_out    : [same tokens, H_q, d] in dtype, token rows q_stride and
+ *                 q_out_stride apart, or both NULL; q_out may be q.  Every
+ *                 token's query is written, also beyond counts[n].
+ *   inv_freq    : DEVICE fp64 [rot_dim / 2], radians per position: pair j of a
+ *                 head is turned by position * inv_freq[j]; NULL with
+ *                 rot_dim 0 (no rotation)
+ *   rot_dim     : the first rot_dim channels are rotated (even, at most d);
+ *                 pair j is channels (j, j + rot_dim / 2), or (2 j, 2 j + 1)
+ *                 with interleaved != 0
+ *   cu_seqlens  : DEVICE int32 [n_seq + 1] (as in kda_varlen_fwd), or NULL;
+ *                 with it K is ignored and counts must be NULL
+ *   T           : token rows in total (n_seq * K without cu_seqlens)
+ * The angle is formed in 64-bit fixed point, so it is as exact at position
+ * 10^6 as at 1.  Products are fp32; each stored value is rounded once.  An
+ * 8-bit cache saturates at +-448.  cu_seqlens that are not offsets of T rows
+ * set KDA_ERR_INVALID_ARG in the device status word; rows without a sequence
+ * are then not written.  Rows of an input that the call does not store are
+ * still read.  The pages must not alias k or v.
+ */
+KDA_API kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void* k, const void* v,
+                                      const void* q, void* q_out, kda_dtype_t dtype,
+                                      long long k_stride, long long v_stride, long long q_stride,
+                                      long long q_out_stride, const double* inv_freq, int rot_dim,
+                                      int interleaved, const int* cu_seqlens, const int* counts,
+                                      int K, int T, int H_q, cudaStream_t stream);
+
+/*
+ * kda_cache_attend -- attention of the K newest tokens of each sequence over
+ * its pages (which hold those tokens already: kda_cache_append first).
+ *   q       : [n_seq, K, H_q, d] in dtype (KDA_BF16 or KDA_F16); token rows
+ *             q_stride elements apart, heads d apart.  H_q is a multiple of
+ *             H_kv; query head h reads key head h / (H_q / H_kv).  A 16-bit
+ *             cache has the type of q.
+ *   out     : [n_seq, K, H_q, d] in dtype, contiguous
+ *   lse     : [n_seq, K, H_q] fp32, or NULL: ln sum exp of the scores
+ *   scale   : multiplies q . k
+ *   window  : 0, or the number of newest positions, its own among them, that a
+ *             token sees
+ *   max_len : an upper bound on lens[n] + K, or 0 for what the table holds; it
+ *             sizes the launch (a sequence beyond it is read to its end)
+ * Token i of sequence n sees positions max(0, p - window + 1) .. p with
+ * p = lens[n] + i (lens[n] may be negative).  Where nothing is seen (a token
+ * beyond counts[n], an empty sequence), out is 0 and lse is -infinity;
+ * nothing stored at a position that a token does not see reaches its output,
+ * whatever it holds.  The scores, the softmax and its sums are fp32; the
+ * weights are rounded to the 16-bit type for the product with the values.
+ * Results do not depend on anything but the arguments (no atomics).
+ *   workspace : kda_cache_attend_workspace_size() bytes, 16-byte aligned, for
+ *             the parts of a sequence's softmax that different blocks compute
+ */
+KDA_API kda_status_t kda_cache_attend(const kda_paged_cache_t* cache, const void* q,
+                                      kda_dtype_t dtype, long long q_stride, void* out, float* lse,
+                                      const int* counts, int K, int H_q, float scale, int window,
+                                      int max_len, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream);
+KDA_API size_t kda_cache_attend_workspace_size(int n_seq, int K, int H_q, int H_kv, int d,
+                                               int max_len);
+
+/*
+ * kda_draft_accept -- decides how many drafted tokens of each sequence are
+ * kept, and draws the token after them, so that the tokens are distributed
+ * as the target's.  All randomness is an argument.
+ *   draft_tokens : int32 [N, K]
+ *   draft_probs  : [N, K, V] in dtype (KDA_F32, KDA_BF16 or KDA_F16), the draft
+ *                  model's probabilities that each draft was drawn from, or
+ *                  NULL (drafts that are no random draw: probability 1)
+ *   target_probs : [N, K + 1, V] in dtype, the target's probabilities after
+ *                  0 .. K drafts
+ *                  (both: vocabulary contiguous; rows *_stride_k and sequences
+ *                  *_stride_n elements apart)
+ *   uniform      : fp32 [N, K + 1] in [0, 1): entry i decides on draft i, entry
+ *                  K draws the token
+ *   draft_lens   : int32 [N], drafts of each sequence (clamped to K; negative:
+ *                  an idle sequence), or NULL (K each)
+ *   counts       : int32 [N] out, tokens gained: drafts kept plus the one
+ *                  drawn (0 for an idle sequence).  kda_decode_commit takes it
+ *                  when its inputs are the last token and the drafts, and the
+ *                  cache's lens advance by it.
+ *   tokens       : int32 [N, K + 1] out: the drafts kept, the token drawn, -1
+ * Draft i is kept while uniform[i] * q_i < p_i, with p_i and q_i the two
+ * probabilities of draft i.  At the first draft a that is not kept the weights
+ * are max(target[a] - draft[a], 0) (without draft_probs: target[a] without the
+ * draft's entry), after the last one target[a], also where no weight is
+ * positive.  The token drawn is the first whose running sum of weights is
+ * more than uniform[K] times their total.  Sums are in 64 bits.  Weights that
+ * are not positive and finite count as zero; where all are, the token is -1.
+ * A draft outside [0, V) is not kept and sets KDA_ERR_INVALID_ARG in the
+ * device status word.
+ */
+KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft_probs,
+                                      const void* target_probs, kda_dtype_t dtype,
+                                      long long draft_stride_n, long long draft_stride_k,
+                                      long long target_stride_n, long long target_stride_k,
+                                      const float* uniform, const int* draft_lens, int* counts,
+                                      int* tokens, int N, int K, int V, cudaStream_t stream);
+
 /* Static description of a status code (never NULL). */
 KDA_API const char* kda_status_string(kda_status_t status);
 
 /*
  * Reads and clears the device status word that kernels set on a decay-bound
  * violation (when checking is on), on a wait that hit its iteration limit,
- * on a packed-sequence plan that had to clamp cu_seqlens, or on a state or
- * corrected value outside the fp16 operand range (KDA_ERR_RANGE).
+ * on a packed-sequence plan that had to clamp cu_seqlens, on a page, position
+ * or draft outside its range, or on a state or corrected value outside the
+ * fp16 operand range (KDA_ERR_RANGE).
  * Synchronises `stream`.  Returns KDA_OK when nothing was flagged.
  */
 KDA_API kda_status_t kda_last_device_status(cudaStream_t stream);

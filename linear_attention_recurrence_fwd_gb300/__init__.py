@@ -6,9 +6,10 @@ exported here are thin ctypes bindings with the same names as the C entry
 points in ``include/kda.h``.  There is no CPU fallback: a missing library
 raises on first use.
 """
-from .binding import (KDAError, kda_chunk_fwd, kda_chunk_fwd_noalloc, kda_decode_step,
+from .binding import (KDAError, PagedCache, kda_cache_append, kda_cache_attend, kda_chunk_fwd,
+                      kda_chunk_fwd_noalloc, kda_decode_step, kda_draft_accept,
                       kda_last_device_status, kda_status_string, kda_varlen_fwd, kda_version)
 
-__all__ = ["KDAError", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_varlen_fwd",
-           "kda_decode_step",
+__all__ = ["KDAError", "PagedCache", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_varlen_fwd",
+           "kda_decode_step", "kda_cache_append", "kda_cache_attend", "kda_draft_accept",
            "kda_last_device_status", "kda_status_string", "kda_version"]

@@ -7,6 +7,7 @@ The Python names match the C entry points (include/kda.h).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -16,7 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libkda.so")
 PROBE_LIB_PATH = os.path.join(PKG, "libkda_probe.so")
 
-KDA_BF16, KDA_F32 = 0, 1
+KDA_BF16, KDA_F32, KDA_F16, KDA_E4M3 = 0, 1, 2, 3
 STATUS = {
     0: "ok", 1: "invalid argument", 2: "unsupported shape or dtype",
     3: "pointer not 16-byte aligned", 4: "CUDA error", 5: "log_alpha outside [-5, 0]",
@@ -31,7 +32,9 @@ EXPORTS = ["kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_chunk_fwd_noall
            "kda_chunk_fwd_host", "kda_chunk_fwd_host_workspace_size",
            "kda_decode_commit",
            "kda_varlen_fwd",
-           "kda_varlen_fwd_workspace_size", "kda_decode_step", "kda_status_string",
+           "kda_varlen_fwd_workspace_size", "kda_decode_step", "kda_cache_append",
+           "kda_cache_attend", "kda_cache_attend_workspace_size", "kda_draft_accept",
+           "kda_status_string",
            "kda_last_device_status", "kda_version"]
 
 
@@ -45,6 +48,7 @@ _lib = None
 _probe = None
 
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 
 def load(path: str = LIB_PATH):
@@ -91,6 +95,14 @@ def load(path: str = LIB_PATH):
         lib.kda_varlen_fwd_workspace_size.restype = _sz
         lib.kda_chunk_fwd_launches.argtypes = [_i, _i, _i]
         lib.kda_chunk_fwd_launches.restype = _i
+        lib.kda_cache_append.argtypes = [_vp] * 5 + [_i] + [_ll] * 4 + [_vp, _i, _i, _vp, _vp, _i, _i, _i, _vp]
+        lib.kda_cache_append.restype = _i
+        lib.kda_cache_attend.argtypes = [_vp, _vp, _i, _ll, _vp, _vp, _vp, _i, _i, _f, _i, _i, _vp, _sz, _vp]
+        lib.kda_cache_attend.restype = _i
+        lib.kda_cache_attend_workspace_size.argtypes = [_i] * 6
+        lib.kda_cache_attend_workspace_size.restype = _sz
+        lib.kda_draft_accept.argtypes = [_vp, _vp, _vp, _i] + [_ll] * 4 + [_vp] * 4 + [_i] * 3 + [_vp]
+        lib.kda_draft_accept.restype = _i
         lib.kda_status_string.argtypes = [_i]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_last_device_status.argtypes = [_vp]
@@ -126,6 +138,12 @@ def _p(t):
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(stream):
+    """Allocate for `stream`: what the caching allocator hands out must belong
+    to the stream that the call runs on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _check(code, where):
@@ -393,6 +411,209 @@ def kda_decode_commit(q, k, v, log_alpha, beta, state, accepted, stream=None):
                                  _p(accepted), N, K, H, dk, dv, _stream(stream)),
            "kda_decode_commit")
     return state
+
+
+class _CacheStruct(ctypes.Structure):
+    """kda_paged_cache_t (include/kda.h)."""
+    _fields_ = ([(n, _vp) for n in ("k", "v", "block_table", "lens")] +
+                [(n, _ll) for n in ("page_stride", "token_stride", "head_stride", "table_stride")] +
+                [("k_scale", _f), ("v_scale", _f)] +
+                [(n, _i) for n in ("dtype", "n_seq", "num_pages", "page_size", "table_width", "H_kv", "d")])
+
+
+_CODES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32, torch.float16: KDA_F16,
+          torch.float8_e4m3fn: KDA_E4M3}
+
+
+class PagedCache:
+    """The pages of one attention layer and which sequence holds them.
+
+    k_pages, v_pages: [num_pages, page_size, H_kv, d] bf16, fp16 or
+    float8_e4m3fn, of equal strides, channels contiguous (for pages laid out
+    head by head, pass a transposed view); block_table: int32 [N, width];
+    lens: int32 [N], the tokens held before a call's new ones.  The tensors
+    stay the caller's: pages, table and lens are read by every call as they
+    are then, and lens is advanced by the caller (`cache.lens.add_(counts)`).
+    k_scale, v_scale: what a stored 1.0 stands for.
+    """
+
+    def __init__(self, k_pages, v_pages, block_table, lens, k_scale=1.0, v_scale=1.0):
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            if not t.is_cuda or t.dim() != 4 or t.dtype not in _CODES or t.dtype == torch.float32:
+                raise ValueError(f"{name} must be a CUDA tensor [num_pages, page_size, H_kv, d] of "
+                                 "bfloat16, float16 or float8_e4m3fn")
+        if (k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or
+                k_pages.dtype != v_pages.dtype):
+            raise ValueError("k_pages and v_pages must agree in shape, strides and dtype")
+        if k_pages.stride(3) != 1:
+            raise ValueError("the channels of a page must be contiguous")
+        if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or (
+                block_table.shape[1] > 1 and block_table.stride(1) != 1):
+            raise ValueError("block_table must be a CUDA int32 tensor [N, width] with contiguous rows")
+        _need(lens, torch.int32, "lens")
+        if lens.shape != (block_table.shape[0],):
+            raise ValueError("lens must have one entry for each row of block_table")
+        self.k_pages, self.v_pages, self.block_table, self.lens = k_pages, v_pages, block_table, lens
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        pages, page_size, heads, d = k_pages.shape
+        self.n_seq, self.heads, self.d, self.page_size = lens.numel(), heads, d, page_size
+        self.capacity = block_table.shape[1] * page_size  # tokens a row of the table holds
+        self.device = k_pages.device
+        self._struct = _CacheStruct(
+            k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
+            k_pages.stride(0), k_pages.stride(1), k_pages.stride(2), block_table.stride(0),
+            self.k_scale, self.v_scale, _CODES[k_pages.dtype], self.n_seq, pages, page_size,
+            block_table.shape[1], heads, d)
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _token_stride(x, d, name):
+    """The elements between the tokens of x ([T, H, d] or [N, K, H, d], heads
+    packed, sequences of equal length one after the other)."""
+    s = x.stride()
+    if not x.is_cuda or x.shape[-1] != d or (s[-1] != 1 and d > 1) or (s[-2] != d and x.shape[-2] > 1):
+        raise ValueError(f"{name} must be a CUDA tensor of heads of {d} channels, packed within a token")
+    if x.dim() == 3:
+        return s[0]
+    if x.shape[1] == 1:
+        return s[0]
+    if x.shape[0] > 1 and s[0] != x.shape[1] * s[1]:
+        raise ValueError(f"the tokens of {name} must be evenly spaced")
+    return s[1]
+
+
+def _counts_ptr(counts, n_seq):
+    if counts is None:
+        return None
+    _need(counts, torch.int32, "counts")
+    if counts.shape != (n_seq,):
+        raise ValueError(f"counts must have {n_seq} entries")
+    return counts.data_ptr()
+
+
+def kda_cache_append(k, v, cache, q=None, inv_freq=None, interleaved=False, cu_seqlens=None,
+                     counts=None, q_out=None, stream=None):
+    """New tokens' keys and values into their pages, keys (and queries, if
+    given) rotated by position * inv_freq on the way.  k, v [N,K,H_kv,d], or
+    packed [T,H_kv,d] with cu_seqlens int32 [N+1]; q the same with H_q heads;
+    inv_freq fp64 [rot_dim/2] or None (no rotation); counts int32 [N]: how many
+    of the K tokens are real.  Returns the rotated queries (q_out), or None."""
+    lib = load()
+    if k.dim() != (4 if cu_seqlens is None else 3) or k.shape != v.shape:
+        raise ValueError("k and v must be [N, K, H_kv, d], or [T, H_kv, d] with cu_seqlens")
+    if k.dtype != v.dtype or k.dtype not in _CODES or (q is not None and q.dtype != k.dtype):
+        raise ValueError("k, v and q must have one dtype, bfloat16 or float16")
+    H, d = cache.heads, cache.d
+    if k.shape[-2] != H:
+        raise ValueError(f"k has {k.shape[-2]} heads, the cache {H}")
+    if cu_seqlens is None:
+        K, T, cu = k.shape[1], k.shape[0] * k.shape[1], None
+        if k.shape[0] != cache.n_seq:
+            raise ValueError(f"k has {k.shape[0]} sequences, the cache {cache.n_seq}")
+    else:
+        _need(cu_seqlens, torch.int32, "cu_seqlens")
+        if cu_seqlens.shape != (cache.n_seq + 1,):
+            raise ValueError(f"cu_seqlens must have {cache.n_seq + 1} entries")
+        K, T, cu = 0, k.shape[0], cu_seqlens.data_ptr()
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, torch.float64, "inv_freq")
+        rot = 2 * inv_freq.numel()
+    qp = qo = None
+    qs = qos = Hq = 0
+    if q is not None:
+        if q.shape[:-2] != k.shape[:-2]:
+            raise ValueError("q and k must have the same tokens")
+        qs, Hq = _token_stride(q, d, "q"), q.shape[-2]
+        if q_out is None:
+            with _on(stream):
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError("q_out must have q's shape and dtype")
+        qos = _token_stride(q_out, d, "q_out")
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(lib.kda_cache_append(
+        cache._ref, k.data_ptr(), v.data_ptr(), qp, qo, _CODES[k.dtype], _token_stride(k, d, "k"),
+        _token_stride(v, d, "v"), qs, qos, inv_freq.data_ptr() if rot else None, rot,
+        int(interleaved), cu, _counts_ptr(counts, cache.n_seq), K, T, Hq, _stream(stream)),
+        "kda_cache_append")
+    return q_out
+
+
+def kda_cache_attend(q, cache, scale=None, window=0, counts=None, max_len=0, out=None,
+                     return_lse=False, stream=None):
+    """Attention of each sequence's K newest tokens, already appended, over its
+    pages: token i at position lens[n] + i sees every position up to its own,
+    or the `window` newest of them.  q [N,K,H_q,d] bf16 or fp16; scale defaults
+    to 1/sqrt(d); max_len: an upper bound on lens + K (0: what the table
+    holds).  Returns out [N,K,H_q,d], and with return_lse also the fp32 log of
+    the sum of exponentials [N,K,H_q]."""
+    lib = load()
+    if q.dim() != 4 or q.shape[0] != cache.n_seq or q.dtype not in _CODES:
+        raise ValueError(f"q must be [{cache.n_seq}, K, H_q, {cache.d}] in bfloat16 or float16")
+    N, K, Hq, d = q.shape
+    qs = _token_stride(q, cache.d, "q")
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, with q's shape and dtype")
+    need = lib.kda_cache_attend_workspace_size(N, K, Hq, cache.heads, d, max_len or cache.capacity)
+    with _on(stream):
+        if out is None:
+            out = torch.empty((N, K, Hq, d), dtype=q.dtype, device=q.device)
+        lse = torch.empty((N, K, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _check(lib.kda_cache_attend(
+        cache._ref, q.data_ptr(), _CODES[q.dtype], qs, out.data_ptr(),
+        lse.data_ptr() if return_lse else None, _counts_ptr(counts, N), K, Hq,
+        d ** -0.5 if scale is None else float(scale), int(window), int(max_len),
+        ws.data_ptr() if need else None, need, _stream(stream)), "kda_cache_attend")
+    return (out, lse) if return_lse else out
+
+
+def kda_draft_accept(draft_tokens, draft_probs, target_probs, uniform, draft_lens=None, counts=None,
+                     tokens=None, stream=None):
+    """How many of each sequence's K drafted tokens are kept, and the token
+    drawn after them.  draft_tokens int32 [N,K]; draft_probs [N,K,V] (or None:
+    drafts that are no random draw) and target_probs [N,K+1,V] in one dtype
+    (fp32, bf16 or fp16); uniform fp32 [N,K+1] in [0, 1); draft_lens int32 [N]
+    (negative: an idle sequence).  Returns (counts int32 [N], the tokens gained
+    by each sequence, and tokens int32 [N,K+1], -1 beyond them)."""
+    lib = load()
+    N, K1, V = target_probs.shape
+    K = K1 - 1
+    _need(draft_tokens, torch.int32, "draft_tokens")
+    _need(uniform, torch.float32, "uniform")
+    if K < 0 or draft_tokens.shape != (N, K) or uniform.shape != (N, K1):
+        raise ValueError("draft_tokens must be [N, K] and uniform [N, K + 1] for target_probs [N, K + 1, V]")
+    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+        if t is not None and (not t.is_cuda or t.dtype not in _CODES or t.dtype != target_probs.dtype or
+                              (t.stride(2) != 1 and V > 1)):
+            raise ValueError(f"{name} must be a CUDA tensor of float32, bfloat16 or float16 with "
+                             "contiguous rows, of target_probs' dtype")
+    if draft_probs is not None and draft_probs.shape != (N, K, V):
+        raise ValueError(f"draft_probs must be {(N, K, V)}")
+    if draft_lens is not None:
+        _need(draft_lens, torch.int32, "draft_lens")
+        if draft_lens.shape != (N,):
+            raise ValueError(f"draft_lens must have {N} entries")
+    for t, shape, name in ((counts, (N,), "counts"), (tokens, (N, K1), "tokens")):
+        if t is not None:
+            _need(t, torch.int32, name)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {shape}")
+    with _on(stream):
+        if counts is None:
+            counts = torch.empty((N,), dtype=torch.int32, device=target_probs.device)
+        if tokens is None:
+            tokens = torch.empty((N, K1), dtype=torch.int32, device=target_probs.device)
+    dsn, dsk = (0, 0) if draft_probs is None else draft_probs.stride()[:2]
+    _check(lib.kda_draft_accept(
+        draft_tokens.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
+        target_probs.data_ptr(), _CODES[target_probs.dtype], dsn, dsk, target_probs.stride(0),
+        target_probs.stride(1), uniform.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(),
+        counts.data_ptr(), tokens.data_ptr(), N, K, V, _stream(stream)), "kda_draft_accept")
+    return counts, tokens
 
 
 def kda_chunk_fwd_launches(B, T, H):

@@ -337,6 +337,130 @@ kda_status_t kda_decode_commit(const void* q, const void* k, const void* v, cons
                                              true, accepted, N, K, H, 1.f, stream));
 }
 
+namespace {
+
+int element_bytes(kda_dtype_t t) {
+  switch (t) {
+    case KDA_F32: return 4;
+    case KDA_BF16: case KDA_F16: return 2;
+    case KDA_E4M3: return 1;
+  }
+  return 0;
+}
+
+// rows `stride` elements apart start on 16-byte boundaries
+bool aligned_rows(const void* p, long long stride, kda_dtype_t t) {
+  return aligned16(p) && (stride * element_bytes(t)) % 16 == 0;
+}
+
+// What both cache calls ask of the cache and of the new tokens' type.
+kda_status_t validate_cache(const kda_paged_cache_t* c, kda_dtype_t dtype) {
+  if (!c) return KDA_ERR_INVALID_ARG;
+  if (c->n_seq < 0 || c->num_pages < 0 || c->page_size <= 0 || c->table_width < 0 || c->H_kv <= 0 ||
+      c->d <= 0 || c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0 ||
+      c->table_stride < 0)
+    return KDA_ERR_INVALID_ARG;
+  if (!(c->k_scale > 0.f) || !(c->v_scale > 0.f)) return KDA_ERR_INVALID_ARG;
+  if (dtype != KDA_BF16 && dtype != KDA_F16) return KDA_ERR_UNSUPPORTED;
+  if (c->dtype != KDA_E4M3 && c->dtype != dtype) return KDA_ERR_UNSUPPORTED;
+  if (c->d != 64 && c->d != 128) return KDA_ERR_UNSUPPORTED;
+  if ((long long)c->table_width * c->page_size > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+  if (c->n_seq > 0 && (!c->lens || (c->table_width > 0 && !c->block_table)))
+    return KDA_ERR_INVALID_ARG;
+  if (c->num_pages > 0 && (!c->k || !c->v)) return KDA_ERR_INVALID_ARG;
+  if (!aligned_rows(c->k, c->page_stride, c->dtype) || !aligned_rows(c->v, c->token_stride, c->dtype) ||
+      !aligned_rows(nullptr, c->head_stride, c->dtype))
+    return KDA_ERR_ALIGNMENT;
+  return KDA_OK;
+}
+
+}  // namespace
+
+kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void* k, const void* v,
+                              const void* q, void* q_out, kda_dtype_t dtype, long long k_stride,
+                              long long v_stride, long long q_stride, long long q_out_stride,
+                              const double* inv_freq, int rot_dim, int interleaved,
+                              const int* cu_seqlens, const int* counts, int K, int T, int H_q,
+                              cudaStream_t stream) {
+  kda_status_t st = validate_cache(cache, dtype);
+  if (st != KDA_OK) return st;
+  if (T < 0 || K < 0 || (!cu_seqlens && (long long)cache->n_seq * K != T)) return KDA_ERR_INVALID_ARG;
+  if (cu_seqlens && counts) return KDA_ERR_INVALID_ARG;
+  if (T > 0 && (!k || !v)) return KDA_ERR_INVALID_ARG;
+  if (!q != !q_out || (q && H_q <= 0)) return KDA_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim % 2 || rot_dim > cache->d || (rot_dim > 0 && !inv_freq))
+    return KDA_ERR_INVALID_ARG;
+  if (k_stride < 0 || v_stride < 0 || q_stride < 0 || q_out_stride < 0) return KDA_ERR_INVALID_ARG;
+  if (!aligned_rows(k, k_stride, dtype) || !aligned_rows(v, v_stride, dtype) ||
+      !aligned_rows(q, q ? q_stride : 0, dtype) || !aligned_rows(q_out, q ? q_out_stride : 0, dtype) ||
+      (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+    return KDA_ERR_ALIGNMENT;
+  if (q && H_q > (1 << 16)) return KDA_ERR_UNSUPPORTED;
+  if (cache->H_kv > (1 << 16)) return KDA_ERR_UNSUPPORTED;
+  if (T == 0) return KDA_OK;
+  kda::AppendProblem p{*cache, k, v, q, q_out, dtype, k_stride, v_stride, q_stride, q_out_stride,
+                       inv_freq, rot_dim, interleaved, cu_seqlens, counts, K, T, q ? H_q : 0, nullptr};
+  cudaError_t e = kda::chunk_status_address(&p.status);
+  return from_cuda(e == cudaSuccess ? kda::launch_cache_append(p, stream) : e);
+}
+
+size_t kda_cache_attend_workspace_size(int n_seq, int K, int H_q, int H_kv, int d, int max_len) {
+  if (n_seq <= 0 || K <= 0 || H_kv <= 0 || H_q <= 0 || H_q % H_kv || !(d == 64 || d == 128) ||
+      max_len < 0)
+    return 0;
+  return kda::attend_workspace_bytes(n_seq, K, H_q, H_kv, d, max_len);
+}
+
+kda_status_t kda_cache_attend(const kda_paged_cache_t* cache, const void* q, kda_dtype_t dtype,
+                              long long q_stride, void* out, float* lse, const int* counts, int K,
+                              int H_q, float scale, int window, int max_len, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+  kda_status_t st = validate_cache(cache, dtype);
+  if (st != KDA_OK) return st;
+  if (K < 0 || H_q <= 0 || H_q % cache->H_kv || window < 0 || max_len < 0 || q_stride < 0)
+    return KDA_ERR_INVALID_ARG;
+  const long long rows = (long long)cache->n_seq * K * H_q;
+  if (rows > 0 && (!q || !out)) return KDA_ERR_INVALID_ARG;
+  if (!aligned_rows(q, q_stride, dtype) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return KDA_ERR_ALIGNMENT;
+  if (rows > 0x3fffffffLL) return KDA_ERR_UNSUPPORTED;
+  if (rows == 0) return KDA_OK;
+  if (max_len == 0) max_len = cache->table_width * cache->page_size;
+  const size_t need = kda_cache_attend_workspace_size(cache->n_seq, K, H_q, cache->H_kv, cache->d, max_len);
+  if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return KDA_ERR_ALIGNMENT;
+  kda::AttendProblem p{*cache, q, dtype, q_stride, out, lse, counts, K, H_q, scale, window, max_len, nullptr};
+  cudaError_t e = kda::chunk_status_address(&p.status);
+  return from_cuda(e == cudaSuccess ? kda::launch_cache_attend(p, workspace, stream) : e);
+}
+
+kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft_probs,
+                              const void* target_probs, kda_dtype_t dtype, long long draft_stride_n,
+                              long long draft_stride_k, long long target_stride_n,
+                              long long target_stride_k, const float* uniform,
+                              const int* draft_lens, int* counts, int* tokens, int N, int K, int V,
+                              cudaStream_t stream) {
+  if (N < 0 || K < 0 || V <= 0) return KDA_ERR_INVALID_ARG;
+  if (draft_stride_n < 0 || draft_stride_k < 0 || target_stride_n < 0 || target_stride_k < 0)
+    return KDA_ERR_INVALID_ARG;
+  if (N > 0 && (!target_probs || !uniform || !counts || !tokens || (K > 0 && !draft_tokens)))
+    return KDA_ERR_INVALID_ARG;
+  if (dtype != KDA_F32 && dtype != KDA_BF16 && dtype != KDA_F16) return KDA_ERR_UNSUPPORTED;
+  const uintptr_t odd = element_bytes(dtype) - 1;
+  if ((reinterpret_cast<uintptr_t>(target_probs) & odd) || (reinterpret_cast<uintptr_t>(draft_probs) & odd) ||
+      (reinterpret_cast<uintptr_t>(uniform) & 3u) || (reinterpret_cast<uintptr_t>(counts) & 3u) ||
+      (reinterpret_cast<uintptr_t>(tokens) & 3u) || (reinterpret_cast<uintptr_t>(draft_tokens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(draft_lens) & 3u))
+    return KDA_ERR_ALIGNMENT;
+  if ((long long)N * (K + 1LL) > 0x7fffffffLL || V > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+  if (N == 0) return KDA_OK;
+  kda::AcceptProblem p{draft_tokens, draft_probs, target_probs, dtype, draft_stride_n, draft_stride_k,
+                       target_stride_n, target_stride_k, uniform, draft_lens, counts, tokens, N, K, V,
+                       nullptr};
+  cudaError_t e = kda::chunk_status_address(&p.status);
+  return from_cuda(e == cudaSuccess ? kda::launch_draft_accept(p, stream) : e);
+}
+
 kda_status_t kda_last_device_status(cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   const int s = kda::read_and_clear_chunk_status(stream, &e);

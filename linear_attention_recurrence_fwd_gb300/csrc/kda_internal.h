@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime_api.h>
 
+#include "../../include/kda.h"
+
 namespace kda {
 
 __device__ __forceinline__ void store_out(float* p, float x) { *p = x; }
@@ -100,7 +102,53 @@ int chunk_fwd_launches(bool packed, int n_seq, int max_len, int H);
 size_t noalloc_max_records();
 cudaError_t launch_chunk_fwd_noalloc(const ChunkProblem& p, cudaStream_t stream);
 
-// Device status word of the chunk kernels (0 = ok, else a kda_status_t).
+// Device status word (0 = ok, else a kda_status_t), and its address on the
+// current device for kernels of other translation units.
 int read_and_clear_chunk_status(cudaStream_t stream, cudaError_t* err);
+cudaError_t chunk_status_address(int** status);
+
+// The calls around a paged cache (see include/kda.h for the arguments).
+struct AppendProblem {
+  kda_paged_cache_t cache;
+  const void *k, *v, *q;
+  void* q_out;
+  kda_dtype_t dtype;
+  long long k_stride, v_stride, q_stride, q_out_stride;
+  const double* inv_freq;
+  int rot_dim, interleaved;
+  const int *cu_seqlens, *counts;
+  int K, T, H_q;  // H_q = 0 without queries
+  int* status;
+};
+cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t stream);
+
+struct AttendProblem {
+  kda_paged_cache_t cache;
+  const void* q;
+  kda_dtype_t dtype;
+  long long q_stride;
+  void* out;
+  float* lse;
+  const int* counts;
+  int K, H_q;
+  float scale;
+  int window, max_len;
+  int* status;
+};
+size_t attend_workspace_bytes(int n_seq, int K, int H_q, int H_kv, int d, int max_len);
+cudaError_t launch_cache_attend(const AttendProblem& p, void* workspace, cudaStream_t stream);
+
+struct AcceptProblem {
+  const int* draft_tokens;
+  const void *draft, *target;
+  kda_dtype_t dtype;
+  long long draft_stride_n, draft_stride_k, target_stride_n, target_stride_k;
+  const float* uniform;
+  const int* draft_lens;
+  int *counts, *tokens;
+  int N, K, V;
+  int* status;
+};
+cudaError_t launch_draft_accept(const AcceptProblem& p, cudaStream_t stream);
 
 }  // namespace kda

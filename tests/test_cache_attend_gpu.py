@@ -1,0 +1,219 @@
+"""Attention of the newest tokens over a paged cache, against fp64.
+
+Every position that a token must not see holds NaN (unowned rows and pages),
+so a masked value that reached an output would show."""
+import math
+
+import pytest
+import torch
+
+from linear_attention_recurrence_fwd_gb300 import binding, build
+from cache_cases import NAN, assert_within, attend_reference, make_cache
+
+pytestmark = pytest.mark.gpu
+BF, FP, E4 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(cuda_device):
+    build.build()
+
+
+def check(lens, K=1, Hq=4, Hkv=2, d=128, page=16, act=BF, dtype=None, window=0, counts=None,
+          layout="token", scale=None, k_scale=1.0, v_scale=1.0, seed=0, mult=1.5, **kw):
+    dtype = act if dtype is None else dtype
+    cache, keys, values = make_cache(lens, K, Hkv, d, page, dtype, seed, layout, k_scale=k_scale,
+                                     v_scale=v_scale)
+    g = torch.Generator().manual_seed(seed + 1)
+    q = (mult * torch.randn((len(lens), K, Hq, d), generator=g)).to(act)
+    cnt = None if counts is None else torch.tensor(counts, dtype=torch.int32).cuda()
+    out, lse = binding.kda_cache_attend(q.cuda(), cache, scale=scale, window=window, counts=cnt,
+                                        return_lse=True, **kw)
+    torch.cuda.synchronize()
+    assert binding.kda_last_device_status() == 0
+    ref, rlse, tol, ltol = attend_reference(q, keys, values, lens, counts,
+                                            d ** -0.5 if scale is None else scale, window)
+    assert_within(lse, rlse, ltol, "lse")
+    assert_within(out, ref, tol, "out")
+    return cache, q, out, lse
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("act,dtype", [(BF, BF), (FP, FP), (BF, E4), (FP, E4)])
+def test_types_and_head_dims(act, dtype, d):
+    check([0, 1, 2, 15, 16, 63, 64, 65, 200], act=act, dtype=dtype, d=d,
+          k_scale=0.5 if dtype == E4 else 1.0, v_scale=0.25 if dtype == E4 else 1.0)
+
+
+@pytest.mark.parametrize("Hq,Hkv,K", [(1, 1, 1), (5, 5, 1), (7, 1, 1), (8, 2, 1), (16, 1, 1), (17, 1, 1),
+                                      (32, 2, 1), (12, 3, 3), (8, 1, 5), (32, 2, 4), (33, 1, 2),
+                                      (16, 2, 9), (14, 2, 5), (64, 1, 3)])
+def test_head_layouts_and_rows(Hq, Hkv, K):
+    check([0, 3, 70, 129, 300], K=K, Hq=Hq, Hkv=Hkv, seed=Hq + K)
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 16, 48, 64, 100, 128, 1000])
+@pytest.mark.parametrize("layout", ["token", "head"])
+def test_page_sizes_and_layouts(page, layout):
+    check([0, 62, 63, 64, 99, 100, 511], K=2, page=page, layout=layout, d=64, seed=page)
+
+
+@pytest.mark.parametrize("window", [1, 2, 17, 64, 100, 5000])
+@pytest.mark.parametrize("K", [1, 4])
+def test_windows(window, K):
+    check([0, 1, 16, 63, 64, 130, 700], K=K, window=window, seed=window)
+
+
+@pytest.mark.parametrize("K,counts", [(1, [0, 1, 0, 1]), (5, [0, 5, 2, 1]), (3, [3, 0, 0, 0])])
+def test_rows_that_see_nothing(K, counts):
+    cache, q, out, lse = check([0, 100, 64, 300], K=K, counts=counts)
+    for n, c in enumerate(counts):
+        assert (out[n, c:] == 0).all() and (lse[n, c:] == -math.inf).all()
+
+
+def test_negative_lengths_see_nothing_or_little():
+    # position lens + i: -1, 0, 1 for the first sequence, none for the others
+    check([-1, -3, -100], K=3)
+
+
+def test_one_long_sequence():
+    check([70001], Hq=8, Hkv=1, page=64)
+
+
+def test_long_and_short_sequences_together():
+    check([20000, 0, 5, 9000, 1, 1, 33, 12345], K=2, Hq=8, Hkv=2, page=32, seed=5)
+
+
+def test_many_sequences():
+    lens = [(37 * n) % 1500 for n in range(300)]
+    check(lens, Hq=2, Hkv=1, d=64, page=16)
+
+
+def test_max_len_is_a_bound_and_may_be_short():
+    _, _, out, _ = check([100, 2000, 7], Hq=4, Hkv=1, max_len=2001)
+    _, _, other, _ = check([100, 2000, 7], Hq=4, Hkv=1, max_len=10)
+    assert torch.allclose(out.float(), other.float(), atol=2 ** -6)
+
+
+def test_large_scores_and_equal_scores():
+    check([500], Hq=4, Hkv=1, mult=30.0, scale=1.0)   # one position takes nearly all
+    check([500], Hq=4, Hkv=1, mult=0.0)               # every position the same
+
+
+def test_projection_slice_as_queries():
+    lens, K, Hq, d = [5, 80], 3, 4, 128
+    cache, keys, values = make_cache(lens, K, 2, d, 16, BF)
+    fused = torch.randn((2 * K, (Hq + 4) * d), generator=torch.Generator().manual_seed(3)).to(BF).cuda()
+    q = fused[:, :Hq * d].unflatten(1, (Hq, d)).unflatten(0, (2, K))
+    assert not q.is_contiguous()
+    out = binding.kda_cache_attend(q, cache)
+    ref, _, tol, _ = attend_reference(q, keys, values, lens, None, d ** -0.5, 0)
+    assert_within(out, ref, tol, "out")
+
+
+def test_infinite_and_nan_in_a_later_draft_do_not_reach_earlier_tokens():
+    """Token 1 of 3 holds infinities and NaN: token 0 must not notice, tokens 1 and 2 must."""
+    lens, K, d = [70], 3, 128
+    cache, keys, values = make_cache(lens, K, 1, d, 16, BF)
+    pos = lens[0] + 1
+    page = int(cache.block_table[0, pos // 16])
+    q = torch.randn((1, K, 2, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    for bad in (NAN, math.inf):
+        cache.v_pages[page, pos % 16] = bad
+        cache.k_pages[page, pos % 16] = 0
+        out = binding.kda_cache_attend(q.cuda(), cache)
+        ref, _, tol, _ = attend_reference(q[:, :1], [keys[0][:lens[0] + 1]], [values[0][:lens[0] + 1]],
+                                          lens, None, d ** -0.5, 0)
+        assert_within(out[:, :1], ref, tol, "token 0")
+        assert not torch.isfinite(out[:, 1:].float()).any()
+
+
+def test_nan_before_the_window_stays_out():
+    lens, d = [300], 64
+    cache, keys, values = make_cache(lens, 1, 1, d, 16, BF)
+    for x in (cache.k_pages, cache.v_pages):
+        for p in range(0, 251):  # positions 251.. are seen (window 50)
+            x[int(cache.block_table[0, p // 16]), p % 16] = NAN
+    q = torch.randn((1, 1, 2, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), cache, window=50)
+    ref, _, tol, _ = attend_reference(q, keys, values, lens, None, d ** -0.5, 50)
+    assert_within(out, ref, tol, "out")
+
+
+def test_offsets_beyond_32_bits():
+    """Three pages 2^31 - 128 elements apart (an 8-bit cache of 6 GB)."""
+    Hkv, d, page, step = 1, 128, 16, (1 << 31) - 128
+    bufs = [torch.empty(2 * step + page * Hkv * d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    pools = [b.view(E4).as_strided((3, page, Hkv, d), (step, Hkv * d, d, 1)) for b in bufs]
+    g = torch.Generator().manual_seed(6)
+    toks = [torch.randn((48, Hkv, d), generator=g).to(E4) for _ in range(2)]
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32)
+    for pool, tok in zip(pools, toks):
+        for j, p in enumerate(table[0].tolist()):
+            pool[p].copy_(tok[16 * j:16 * j + 16].cuda())
+    cache = binding.PagedCache(*pools, table.cuda(), torch.tensor([46], dtype=torch.int32).cuda())
+    q = torch.randn((1, 1, 4, d), generator=g).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), cache)
+    ref, _, tol, _ = attend_reference(q, [toks[0].double()], [toks[1].double()], [46], None, d ** -0.5, 0)
+    assert_within(out, ref, tol, "out")
+
+
+def test_pages_outside_the_pool_are_left_out_and_flagged():
+    lens, d = [100, 40], 128
+    cache, keys, values = make_cache(lens, 1, 1, d, 16, BF)
+    binding.kda_last_device_status()
+    cache.block_table[0, 2] = 10 ** 6
+    cache.block_table[0, 4] = -7
+    q = torch.randn((2, 1, 2, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), cache)
+    torch.cuda.synchronize()
+    assert binding.kda_last_device_status() == 1
+    kept = [j for j in range(101) if j // 16 not in (2, 4)]
+    ref, _, tol, _ = attend_reference(q, [keys[0][kept], keys[1]], [values[0][kept], values[1]],
+                                      [len(kept) - 1, 40], None, d ** -0.5, 0)
+    assert_within(out, ref, tol, "out")
+
+
+def test_lengths_beyond_the_table_are_clamped_and_flagged():
+    lens, d = [31, 5], 64
+    cache, keys, values = make_cache(lens, 1, 1, d, 16, BF)
+    cache.lens[0] = 1000  # the table holds 32 positions
+    q = torch.randn((2, 1, 2, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), cache)
+    torch.cuda.synchronize()
+    assert binding.kda_last_device_status() == 1
+    ref, _, tol, _ = attend_reference(q, keys, values, lens, None, d ** -0.5, 0)
+    assert_within(out, ref, tol, "out")
+
+
+def test_other_stream_repeats_and_graph():
+    """The same bits on another stream, on a second call, and from a graph
+    whose lens change between replays."""
+    lens, K = [3000, 17, 600], 2
+    cache, keys, values = make_cache(lens, K, 2, 128, 16, BF)
+    q = torch.randn((3, K, 8, 128), generator=torch.Generator().manual_seed(8)).to(BF).cuda()
+    first = binding.kda_cache_attend(q, cache)
+    assert torch.equal(first, binding.kda_cache_attend(q, cache))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = binding.kda_cache_attend(q, cache, stream=side)
+    side.synchronize()
+    assert torch.equal(first, other)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = binding.kda_cache_attend(q, cache)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(first, out)
+    cache.lens.copy_(torch.tensor([1999, 16, 0], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    ref, _, tol, _ = attend_reference(q.cpu(), keys, values, [1999, 16, 0], None, 128 ** -0.5, 0)
+    assert_within(out, ref, tol, "replayed")
+
+
+def test_no_sequences_and_no_tokens():
+    cache, _, _ = make_cache([], 1, 2, 64, 16, BF)
+    assert binding.kda_cache_attend(torch.empty((0, 1, 2, 64), dtype=BF, device="cuda"), cache).shape == (0, 1, 2, 64)
+    cache, _, _ = make_cache([5], 0, 2, 64, 16, BF)
+    assert binding.kda_cache_attend(torch.empty((1, 0, 2, 64), dtype=BF, device="cuda"), cache).shape == (1, 0, 2, 64)

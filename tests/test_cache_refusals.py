@@ -1,0 +1,145 @@
+"""What the calls around a paged cache refuse, before any CUDA call: no GPU
+is needed, and the fake pointers are never dereferenced."""
+import ctypes
+
+import pytest
+import torch
+
+from linear_attention_recurrence_fwd_gb300 import binding, build
+
+F = 4096           # aligned fake pointer
+BF16, F32, F16, E4M3 = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load()
+
+
+def cache(**kw):
+    f = dict(k=F, v=F, block_table=F, lens=F, page_stride=16 * 2 * 128, token_stride=256, head_stride=128,
+             table_stride=4, k_scale=1.0, v_scale=1.0, dtype=BF16, n_seq=3, num_pages=8, page_size=16,
+             table_width=4, H_kv=2, d=128)
+    f.update(kw)
+    return binding._CacheStruct(**f)
+
+
+BAD_CACHES = [(dict(n_seq=-1), 1), (dict(num_pages=-1), 1), (dict(page_size=0), 1), (dict(table_width=-1), 1),
+              (dict(H_kv=0), 1), (dict(d=0), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(lens=None), 1),
+              (dict(block_table=None), 1), (dict(k_scale=0.0), 1), (dict(v_scale=float("nan")), 1),
+              (dict(page_stride=-8), 1), (dict(table_stride=-1), 1), (dict(dtype=F32), 2), (dict(dtype=F16), 2),
+              (dict(dtype=9), 2), (dict(d=96), 2), (dict(d=256), 2), (dict(table_width=1 << 28), 2),
+              (dict(k=F + 8), 3), (dict(v=F + 2), 3), (dict(page_stride=4), 3), (dict(token_stride=132), 3),
+              (dict(head_stride=4), 3), (dict(dtype=E4M3, token_stride=264), 3)]
+
+
+def append(lib, c=None, k=F, v=F, q=F, q_out=F, dtype=BF16, ks=512, vs=512, qs=512, qos=512, inv=F, rot=128,
+           cu=None, counts=None, K=2, T=6, Hq=4):
+    ref = None if c is False else ctypes.addressof(c or cache())
+    return lib.kda_cache_append(ref, k, v, q, q_out, dtype, ks, vs, qs, qos, inv, rot, 0, cu, counts, K, T, Hq, None)
+
+
+def attend(lib, c=None, q=F, dtype=BF16, qs=512, out=F, lse=F, counts=None, K=2, Hq=4, window=0, max_len=0,
+           ws=None, wsb=0):
+    ref = None if c is False else ctypes.addressof(c or cache())
+    return lib.kda_cache_attend(ref, q, dtype, qs, out, lse, counts, K, Hq, 1.0, window, max_len, ws, wsb, None)
+
+
+@pytest.mark.parametrize("fields,code", BAD_CACHES, ids=[str(sorted(f)[0]) + str(i) for i, (f, _) in enumerate(BAD_CACHES)])
+def test_bad_caches(lib, fields, code):
+    bad = cache(**fields)
+    assert append(lib, bad) == code
+    assert attend(lib, bad) == code
+
+
+def test_append_arguments(lib):
+    assert append(lib, False) == 1
+    assert append(lib, k=None) == 1 and append(lib, v=None) == 1
+    assert append(lib, q=None) == 1 and append(lib, q_out=None) == 1 and append(lib, Hq=0) == 1
+    assert append(lib, T=5) == 1 and append(lib, T=-1) == 1 and append(lib, K=-2) == 1
+    assert append(lib, cu=F, counts=F) == 1
+    assert append(lib, rot=3) == 1 and append(lib, rot=130) == 1 and append(lib, inv=None) == 1
+    assert append(lib, ks=-512) == 1
+    assert append(lib, dtype=F32) == 2 and append(lib, dtype=E4M3) == 2
+    assert append(lib, k=F + 8) == 3 and append(lib, q_out=F + 4) == 3 and append(lib, vs=516) == 3
+    assert append(lib, inv=F + 4) == 3
+    assert append(lib, K=0, T=0) == 0  # nothing to do
+
+
+def test_attend_arguments(lib):
+    assert attend(lib, False) == 1
+    assert attend(lib, q=None) == 1 and attend(lib, out=None) == 1
+    assert attend(lib, Hq=3) == 1 and attend(lib, Hq=0) == 1
+    assert attend(lib, K=-1) == 1 and attend(lib, window=-1) == 1 and attend(lib, max_len=-1) == 1
+    assert attend(lib, dtype=F32) == 2
+    assert attend(lib, q=F + 8) == 3 and attend(lib, out=F + 8) == 3 and attend(lib, lse=F + 2) == 3
+    assert attend(lib, qs=516) == 3
+    assert attend(lib, K=0) == 0 and attend(lib, cache(n_seq=0)) == 0
+
+
+def test_attend_workspace_size_of_nonsense_is_zero(lib):
+    size = lib.kda_cache_attend_workspace_size
+    assert size(0, 1, 4, 2, 128, 100) == 0 and size(1, 1, 3, 2, 128, 100) == 0
+    assert size(1, 1, 4, 2, 96, 100) == 0 and size(1, 1, 4, 2, 128, -1) == 0
+
+
+def test_accept_arguments(lib):
+    def call(toks=F, draft=F, target=F, dtype=F32, strides=(400, 100, 500, 100), u=F, lens=None, counts=F,
+             out=F, N=2, K=4, V=100):
+        return lib.kda_draft_accept(toks, draft, target, dtype, *strides, u, lens, counts, out, N, K, V, None)
+    assert call(toks=None) == 1 and call(target=None) == 1 and call(u=None) == 1
+    assert call(counts=None) == 1 and call(out=None) == 1
+    assert call(N=-1) == 1 and call(K=-1) == 1 and call(V=0) == 1
+    assert call(strides=(-1, 0, 0, 0)) == 1
+    assert call(dtype=E4M3) == 2 and call(dtype=7) == 2
+    assert call(target=F + 2) == 3 and call(draft=F + 1, dtype=BF16) == 3 and call(u=F + 1) == 3
+    assert call(N=0) == 0
+
+
+def test_host_tensors_are_refused():
+    pages = torch.zeros((2, 16, 1, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        binding.PagedCache(pages, pages, torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        binding.kda_draft_accept(torch.zeros((1, 1), dtype=torch.int32), None, torch.zeros((1, 2, 4)), torch.zeros((1, 2)))
+
+
+@pytest.mark.gpu
+def test_tensors_that_do_not_fit_are_refused(cuda_device):
+    build.build()
+    bf, i32, dev = torch.bfloat16, torch.int32, "cuda"
+    pages = torch.zeros((2, 16, 2, 64), dtype=bf, device=dev)
+    table, lens = torch.zeros((3, 1), dtype=i32, device=dev), torch.zeros(3, dtype=i32, device=dev)
+    for k, v, t, n in ((pages.float(), pages.float(), table, lens), (pages, pages[:1], table, lens),
+                       (pages, pages.half(), table, lens), (pages[..., ::2], pages[..., ::2], table, lens),
+                       (pages, pages, table.long(), lens), (pages, pages, table, lens[:2]),
+                       (pages, pages.transpose(0, 1), table, lens), (pages[0], pages[0], table, lens)):
+        with pytest.raises(ValueError):
+            binding.PagedCache(k, v, t, n)
+    c = binding.PagedCache(pages, pages.clone(), table, lens)
+    q = torch.zeros((3, 2, 4, 64), dtype=bf, device=dev)
+    k = torch.zeros((3, 2, 2, 64), dtype=bf, device=dev)
+    for bad in (q[:2], q[..., :32], q.float().double(), q.transpose(1, 2), q[0], q.cpu(), q[:, ::2].repeat(1, 2, 1, 1)[:, ::2].expand(3, 2, 4, 64)[:, :, ::2]):
+        with pytest.raises((ValueError, binding.KDAError)):
+            binding.kda_cache_attend(bad, c)
+    with pytest.raises(ValueError):
+        binding.kda_cache_attend(q, c, counts=torch.zeros(2, dtype=i32, device=dev))
+    with pytest.raises(ValueError):
+        binding.kda_cache_attend(q, c, out=torch.empty((3, 2, 4, 32), dtype=bf, device=dev))
+    with pytest.raises(binding.KDAError):
+        binding.kda_cache_attend(q.half(), c)  # a 16-bit cache has the type of the queries
+    for args, kw in (((k[:2], k[:2], c), {}), ((k, k[:, :1], c), {}), ((k[:, :, :1], k[:, :, :1], c), {}),
+                     ((k, k, c), dict(q=q[:, :1])), ((k, k, c), dict(q_out=q)), ((k, k, c), dict(q=q.half())),
+                     ((k, k, c), dict(inv_freq=torch.zeros(32, device=dev))),
+                     ((k, k, c), dict(cu_seqlens=torch.zeros(4, dtype=i32, device=dev))),
+                     ((k.flatten(0, 1), k.flatten(0, 1), c), dict(cu_seqlens=torch.zeros(3, dtype=i32, device=dev))),
+                     ((k, k.cpu(), c), {})):
+        with pytest.raises((ValueError, binding.KDAError)):
+            binding.kda_cache_append(*args, **kw)
+    p = torch.zeros((2, 3, 10), device=dev)
+    toks, u = torch.zeros((2, 2), dtype=i32, device=dev), torch.zeros((2, 3), device=dev)
+    for args in ((toks[:1], None, p, u), (toks, p, p, u), (toks, None, p, u[:, :2]), (toks.long(), None, p, u),
+                 (toks, p[:, :2].half(), p, u), (toks, None, p.transpose(1, 2)[:, :3], u), (toks, None, p.double(), u)):
+        with pytest.raises((ValueError, binding.KDAError)):
+            binding.kda_draft_accept(*args)
