@@ -408,6 +408,7 @@ KDA_API kda_status_t kda_decode_commit(const void* q, const void* k, const void*
  *   dtype       : KDA_BF16, KDA_F16 or KDA_E4M3; a stored value stands for
  *                 stored * k_scale (keys) or stored * v_scale (values)
  *   d           : 64 or 128
+ * table_width * page_size is at most 2^30.
  * Both calls below take K new tokens for each sequence, of which the first
  * counts[n] are real (counts: DEVICE int32 [n_seq], clamped to [0, K]; NULL:
  * all of them).  Token i of sequence n has position lens[n] + i.  A page

@@ -364,7 +364,7 @@ kda_status_t validate_cache(const kda_paged_cache_t* c, kda_dtype_t dtype) {
   if (dtype != KDA_BF16 && dtype != KDA_F16) return KDA_ERR_UNSUPPORTED;
   if (c->dtype != KDA_E4M3 && c->dtype != dtype) return KDA_ERR_UNSUPPORTED;
   if (c->d != 64 && c->d != 128) return KDA_ERR_UNSUPPORTED;
-  if ((long long)c->table_width * c->page_size > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
+  if ((long long)c->table_width * c->page_size > (1LL << 30)) return KDA_ERR_UNSUPPORTED;
   if (c->n_seq > 0 && (!c->lens || (c->table_width > 0 && !c->block_table)))
     return KDA_ERR_INVALID_ARG;
   if (c->num_pages > 0 && (!c->k || !c->v)) return KDA_ERR_INVALID_ARG;
@@ -425,7 +425,9 @@ kda_status_t kda_cache_attend(const kda_paged_cache_t* cache, const void* q, kda
     return KDA_ERR_ALIGNMENT;
   if (rows > 0x3fffffffLL) return KDA_ERR_UNSUPPORTED;
   if (rows == 0) return KDA_OK;
-  if (max_len == 0) max_len = cache->table_width * cache->page_size;
+  const int capacity = cache->table_width * cache->page_size;
+  if (!kda::attend_tiles_fit(cache->n_seq, K, H_q, cache->H_kv, capacity)) return KDA_ERR_UNSUPPORTED;
+  if (max_len == 0) max_len = capacity;
   const size_t need = kda_cache_attend_workspace_size(cache->n_seq, K, H_q, cache->H_kv, cache->d, max_len);
   if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   if (need && !aligned16(workspace)) return KDA_ERR_ALIGNMENT;

@@ -135,6 +135,8 @@ struct AttendProblem {
   int window, max_len;
   int* status;
 };
+// Whether the call's tiles of 64 positions can be counted in 32 bits.
+bool attend_tiles_fit(int n_seq, int K, int H_q, int H_kv, int capacity);
 size_t attend_workspace_bytes(int n_seq, int K, int H_q, int H_kv, int d, int max_len);
 cudaError_t launch_cache_attend(const AttendProblem& p, void* workspace, cudaStream_t stream);
 
