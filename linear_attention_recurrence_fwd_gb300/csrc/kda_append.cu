@@ -6,11 +6,19 @@
 // fixed-point fraction of a turn, so the product with the integer p wraps
 // exactly and a position of 2^20 loses nothing (an fp32 angle would be off by
 // 2^20 * 2^-24 radians).
+//
+// The call moves bytes: it is bound by HBM for prompts and by latency for
+// single tokens.  A CTA has 256 threads and 1 or 4 tokens.  A token's sines
+// and cosines are formed once, for all its heads, and kept in shared memory;
+// the heads' first bytes are on their way meanwhile.  A thread takes 8
+// channels and the 8 that they are turned with, 16 bytes each.
 #include "kda_internal.h"
 #include "kda_types.cuh"
 
 namespace kda {
 namespace {
+
+constexpr int THREADS = 256;
 
 // f in radians per position as a fraction of a turn, in units of 2^-64.
 __device__ __forceinline__ long long turn_step(double f) {
@@ -19,56 +27,212 @@ __device__ __forceinline__ long long turn_step(double f) {
   return __double2ll_rn(frac * 9223372036854775808.0) << 1;  // 2^63, then times 2
 }
 
-__device__ __forceinline__ void turn(long long step, int pos, float* c, float* s) {
+__device__ __forceinline__ float2 turn(long long step, int pos) {
   const long long phase = (long long)((unsigned long long)step * (unsigned long long)(long long)pos);
   const float half_turns = (float)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
-  sincospif(half_turns, s, c);
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  return make_float2(c, s);
 }
 
-template <typename T, typename C>
-__global__ void __launch_bounds__(128) append_kernel(AppendProblem p) {
-  const int t = blockIdx.x;
-  // the token's sequence n and its number i in it
+// The sequence of packed row t, found by a whole warp: the first n with
+// cu[n + 1] > t, in steps of 32 probes; -1 where no sequence has the row.
+__device__ __forceinline__ int owner_of(const int* cu, int N, int t, int lane) {
+  int lo = 0, hi = N;  // n is in [lo, hi), or there is none
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int last = min(lo + (lane + 1) * step, hi) - 1;
+    const unsigned past = __ballot_sync(0xffffffffu, cu[last + 1] > t);
+    if (!past) return -1;
+    const int k = __ffs(past) - 1;
+    hi = min(lo + (k + 1) * step, hi);
+    lo = min(lo + k * step, hi - 1);
+    if (step == 1) break;
+  }
+  return lo < hi && t >= cu[lo] ? lo : -1;
+}
+
+struct Place {
+  int pos;
+  bool owned;     // the row has a sequence
+  long long row;  // element of the token's row in the pages, or -1: not stored
+};
+
+// A token's position and its row in the pages; the page is looked up where `store`.
+__device__ __forceinline__ Place place_of(const AppendProblem& p, int t, int lane, bool store) {
+  Place a{0, true, -1};
   int n, i;
-  bool owned = true;
   if (p.cu_seqlens) {
-    if (t == 0) {  // the offsets as a whole: from 0 to T, none decreasing
-      bool bad = p.cu_seqlens[0] != 0 || p.cu_seqlens[p.cache.n_seq] != p.T;
-      for (int m = threadIdx.x; m < p.cache.n_seq; m += blockDim.x)
-        bad |= p.cu_seqlens[m] > p.cu_seqlens[m + 1];
-      if (bad) *p.status = 1;
-    }
-    int lo = 0, hi = p.cache.n_seq;  // the first n with cu[n + 1] > t
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p.cu_seqlens[mid + 1] > t) hi = mid; else lo = mid + 1;
-    }
-    n = lo;
-    owned = n < p.cache.n_seq && t >= p.cu_seqlens[n];
-    i = owned ? t - p.cu_seqlens[n] : 0;
-    if (!owned) {
-      if (threadIdx.x == 0) *p.status = 1;
-      return;
-    }
+    n = owner_of(p.cu_seqlens, p.cache.n_seq, t, lane);
+    if (n < 0) return Place{0, false, -1};
+    i = t - p.cu_seqlens[n];
   } else {
     n = t / p.K;
     i = t - n * p.K;
   }
-  const int pos = p.cache.lens[n] + i;
-  const bool real = !p.counts || i < p.counts[n];
-  long long row = -1;
-  if (real) {
-    if (pos >= 0 && pos / p.cache.page_size < p.cache.table_width) {
-      const int page = p.cache.block_table[n * p.cache.table_stride + pos / p.cache.page_size];
+  a.pos = p.cache.lens[n] + i;
+  if (store && (!p.counts || i < p.counts[n]) && a.pos >= 0) {
+    const int entry = a.pos / p.cache.page_size;
+    if (entry < p.cache.table_width) {
+      const int page = p.cache.block_table[n * p.cache.table_stride + entry];
       if (page >= 0 && page < p.cache.num_pages)
-        row = page * p.cache.page_stride + (pos % p.cache.page_size) * p.cache.token_stride;
+        a.row = page * p.cache.page_stride + (a.pos - entry * p.cache.page_size) * p.cache.token_stride;
     }
-    if (row < 0 && threadIdx.x == 0) *p.status = 1;
   }
-  const int d = p.cache.d, Hkv = p.cache.H_kv;
-  const int half = p.rot_dim / 2, rest = d - p.rot_dim;
-  // pairs first, then the channels that are not turned
-  const int per_head = half + rest;
+  if (store && a.row < 0 && (!p.counts || i < p.counts[n])) *p.status = 1;
+  return a;
+}
+
+// The offsets as a whole: from 0 to T, none decreasing.
+__device__ __forceinline__ void check_offsets(const AppendProblem& p) {
+  bool bad = p.cu_seqlens[0] != 0 || p.cu_seqlens[p.cache.n_seq] != p.T;
+  for (int m = threadIdx.x; m < p.cache.n_seq; m += blockDim.x) bad |= p.cu_seqlens[m] > p.cu_seqlens[m + 1];
+  if (bad) *p.status = 1;
+}
+
+// Eight channels to a row of the cache or of the queries: one rounding each.
+template <typename C> __device__ __forceinline__ void store8(C* dst, const float (&x)[8], float scale) {
+  C y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = from_f32<C>(scale == 1.f ? x[e] : x[e] / scale);
+  if (sizeof(C) == 1) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
+  else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(y);
+}
+
+// jobs: of a head, the pieces that a thread takes: 8 pairs of channels (c and
+// c + rot_dim / 2), then 8 channels that are not turned; or, with neighbouring
+// pairs, 8 channels each.
+template <typename T, typename C, int TOKENS>
+__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendProblem p, int jobs) {
+  constexpr int AHEAD = 3;  // pieces of a thread whose loads are in flight together
+  __shared__ __align__(16) float2 s_turn[TOKENS][64];
+  __shared__ long long s_row[TOKENS];
+  __shared__ int s_owned[TOKENS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t0 = blockIdx.x * TOKENS, tokens = min(TOKENS, p.T - t0);
+  const int d = p.cache.d, half = p.rot_dim / 2, heads = p.H_q + 2 * p.cache.H_kv;
+
+  const int slots = THREADS / jobs, j = tid % jobs, slot = tid / jobs;
+  const bool pairs_apart = !p.interleaved && half > 0;
+  const bool two = pairs_apart && j < half / 8;
+  const int at = two || !pairs_apart ? 8 * j : p.rot_dim + 8 * (j - half / 8);
+  const int work = slot < slots ? tokens * heads : 0;
+
+  uint4 a[AHEAD], b[AHEAD];
+  auto source = [&](int tt, int h) -> const T* {
+    const long long t = t0 + tt;
+    if (h < p.H_q) return static_cast<const T*>(p.q) + t * p.q_stride + h * d + at;
+    h -= p.H_q;
+    if (h < p.cache.H_kv) return static_cast<const T*>(p.k) + t * p.k_stride + h * d + at;
+    return static_cast<const T*>(p.v) + t * p.v_stride + (h - p.cache.H_kv) * d + at;
+  };
+  auto load = [&](int w0) {
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      const int w = w0 + x * slots;
+      if (w < work) {
+        const T* src = source(w / heads, w % heads);
+        a[x] = *reinterpret_cast<const uint4*>(src);
+        if (two) b[x] = *reinterpret_cast<const uint4*>(src + half);
+      }
+    }
+  };
+  load(slot);
+
+  // ---- places and turns: the CTA's warps share its tokens
+  constexpr int WARPS = THREADS / 32, PER = WARPS / TOKENS;  // warps of a token
+  {
+    const int tt = warp / PER, part = warp % PER;
+    if (tt < tokens) {
+      const Place pl = place_of(p, t0 + tt, lane, part == 0);
+      if (part == 0 && lane == 0) {
+        s_row[tt] = pl.row;
+        s_owned[tt] = pl.owned;
+        if (!pl.owned) *p.status = 1;
+      }
+      for (int x = part * 32 + lane; x < half; x += PER * 32) s_turn[tt][x] = turn(turn_step(p.inv_freq[x]), pl.pos);
+    }
+  }
+  if (p.cu_seqlens && blockIdx.x == 0) check_offsets(p);
+  __syncthreads();
+
+  for (int w0 = slot; w0 < work; w0 += AHEAD * slots) {
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      const int w = w0 + x * slots;
+      if (w >= work) break;
+      const int tt = w / heads, h = w % heads;
+      if (!s_owned[tt]) continue;
+      const bool is_q = h < p.H_q, is_k = !is_q && h < p.H_q + p.cache.H_kv;
+      const T* u = reinterpret_cast<const T*>(&a[x]);
+      const T* v = reinterpret_cast<const T*>(&b[x]);
+      float lo[8], hi[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = to_f32(u[e]);
+        hi[e] = two ? to_f32(v[e]) : 0.f;
+      }
+      if (is_q || is_k) {
+        if (two) {
+          const float4* cs = reinterpret_cast<const float4*>(&s_turn[tt][8 * j]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 z = cs[e];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float c = y ? z.z : z.x, s = y ? z.w : z.y;
+              const float r = lo[2 * e + y] * c - hi[2 * e + y] * s;
+              hi[2 * e + y] = lo[2 * e + y] * s + hi[2 * e + y] * c;
+              lo[2 * e + y] = r;
+            }
+          }
+        } else if (p.interleaved) {
+          const float4* cs = reinterpret_cast<const float4*>(&s_turn[tt][at / 2]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 z = cs[e];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              if (at / 2 + 2 * e + y >= half) continue;  // not turned
+              const float c = y ? z.z : z.x, s = y ? z.w : z.y;
+              float &f = lo[4 * e + 2 * y], &g = lo[4 * e + 2 * y + 1];
+              const float r = f * c - g * s;
+              g = f * s + g * c;
+              f = r;
+            }
+          }
+        }
+      }
+      if (is_q) {
+        T* dst = static_cast<T*>(p.q_out) + (long long)(t0 + tt) * p.q_out_stride + h * d + at;
+        store8<T>(dst, lo, 1.f);
+        if (two) store8<T>(dst + half, hi, 1.f);
+      } else if (s_row[tt] >= 0) {
+        const int hk = h - p.H_q - (is_k ? 0 : p.cache.H_kv);
+        C* dst = static_cast<C*>(is_k ? p.cache.k : p.cache.v) + s_row[tt] + hk * p.cache.head_stride + at;
+        const float scale = is_k ? p.cache.k_scale : p.cache.v_scale;
+        store8<C>(dst, lo, scale);
+        if (two) store8<C>(dst + half, hi, scale);
+      }
+    }
+    load(w0 + AHEAD * slots);
+  }
+}
+
+// Any number of turned channels, one pair at a time (pairs rot_dim / 2 apart
+// where that is no multiple of 8: their two halves cannot be read 16 bytes at
+// a time).
+template <typename T, typename C>
+__global__ void __launch_bounds__(128) append_pairs_kernel(const __grid_constant__ AppendProblem p) {
+  const int t = blockIdx.x;
+  const Place pl = place_of(p, t, threadIdx.x & 31, true);
+  if (p.cu_seqlens && t == 0) check_offsets(p);
+  if (!pl.owned) {
+    if (threadIdx.x == 0) *p.status = 1;
+    return;
+  }
+  const int d = p.cache.d, Hkv = p.cache.H_kv, half = p.rot_dim / 2;
+  const int per_head = half + (d - p.rot_dim);  // pairs first, then the channels that are not turned
   for (int w = threadIdx.x; w < (p.H_q + 2 * Hkv) * per_head; w += blockDim.x) {
     const int head = w / per_head, j = w - head * per_head;
     const bool is_q = head < p.H_q, is_k = !is_q && head < p.H_q + Hkv;
@@ -77,22 +241,20 @@ __global__ void __launch_bounds__(128) append_kernel(AppendProblem p) {
                    : is_k ? static_cast<const T*>(p.k) + t * p.k_stride
                           : static_cast<const T*>(p.v) + t * p.v_stride;
     src += h * d;
-    const int a = j < half ? (p.interleaved ? 2 * j : j) : j + half;
-    const int b = j < half ? (p.interleaved ? 2 * j + 1 : j + half) : a;
+    const int a = j < half ? j : j + half, b = j < half ? j + half : a;
     float x = to_f32(src[a]), y = to_f32(src[b]);
     if (j < half && (is_q || is_k)) {
-      float c, s;
-      turn(turn_step(p.inv_freq[j]), pos, &c, &s);
-      const float u = x * c - y * s;
-      y = x * s + y * c;
+      const float2 cs = turn(turn_step(p.inv_freq[j]), pl.pos);
+      const float u = x * cs.x - y * cs.y;
+      y = x * cs.y + y * cs.x;
       x = u;
     }
     if (is_q) {
       T* dst = static_cast<T*>(p.q_out) + t * p.q_out_stride + h * d;
       dst[a] = from_f32<T>(x);
       if (j < half) dst[b] = from_f32<T>(y);
-    } else if (row >= 0) {
-      C* dst = static_cast<C*>(is_k ? p.cache.k : p.cache.v) + row + h * p.cache.head_stride;
+    } else if (pl.row >= 0) {
+      C* dst = static_cast<C*>(is_k ? p.cache.k : p.cache.v) + pl.row + h * p.cache.head_stride;
       const float scale = is_k ? p.cache.k_scale : p.cache.v_scale;
       dst[a] = from_f32<C>(x / scale);
       if (j < half) dst[b] = from_f32<C>(y / scale);
@@ -100,21 +262,30 @@ __global__ void __launch_bounds__(128) append_kernel(AppendProblem p) {
   }
 }
 
-template <typename T>
-cudaError_t launch_typed(const AppendProblem& p, cudaStream_t stream) {
-  if (p.cache.dtype == KDA_E4M3)
-    append_kernel<T, __nv_fp8_e4m3><<<p.T, 128, 0, stream>>>(p);
+template <typename T, typename C> cudaError_t launch_stored(const AppendProblem& p, cudaStream_t stream) {
+  const int half = p.rot_dim / 2;
+  if (!p.interleaved && half % 8) {
+    append_pairs_kernel<T, C><<<p.T, 128, 0, stream>>>(p);
+    return cudaGetLastError();
+  }
+  const int jobs = p.interleaved ? p.cache.d / 8 : half / 8 + (p.cache.d - p.rot_dim) / 8;
+  // A CTA to a token while that leaves no SM idle; four share the cost of a CTA's start.
+  if (p.T <= 1024)
+    append_kernel<T, C, 1><<<p.T, THREADS, 0, stream>>>(p, jobs);
   else
-    append_kernel<T, T><<<p.T, 128, 0, stream>>>(p);
+    append_kernel<T, C, 4><<<(p.T + 3) / 4, THREADS, 0, stream>>>(p, jobs);
   return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch_typed(const AppendProblem& p, cudaStream_t stream) {
+  return p.cache.dtype == KDA_E4M3 ? launch_stored<T, __nv_fp8_e4m3>(p, stream) : launch_stored<T, T>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t stream) {
   if (p.T == 0) return cudaSuccess;
-  return p.dtype == KDA_BF16 ? launch_typed<__nv_bfloat16>(p, stream)
-                             : launch_typed<__half>(p, stream);
+  return p.dtype == KDA_BF16 ? launch_typed<__nv_bfloat16>(p, stream) : launch_typed<__half>(p, stream);
 }
 
 }  // namespace kda
