@@ -3,119 +3,311 @@
 // Draft i is kept while u_i q_i(t_i) < p_i(t_i); the token after the kept ones
 // is the first index whose running sum of weights passes u_K times their
 // total, the weights being max(p_a - q_a, 0) at a draft that is not kept and
-// p_a after the last.  One CTA per sequence: the total, then the 1024-wide
-// stretch in which the running sum passes, then the index in it.  Sums are
-// fp64: an fp32 running sum over 10^5 weights is off by about 10^-7 of the
-// total, enough to change a token in every few hundred draws.
+// p_a after the last.
+//
+// The call reads one row of p and, for a rejected draft, one of q: it is bound
+// by HBM for many sequences and by latency for few.  A cluster of 1 to 8 CTAs
+// takes a sequence and each of its warps a contiguous slice of the vocabulary.
+// The slices' sums meet in every CTA's shared memory; the CTA whose slice
+// holds the border sums that slice again in 256 contiguous pieces, and one
+// warp looks through the piece that holds it, out of L2.
+//
+// Sums: an fp32 running sum over 10^5 weights is off by about 10^-7 of the
+// total, enough to change a token in every few hundred draws, and fp64 runs at
+// a 64th of fp32's rate here.  Threads therefore sum pairs of fp32 numbers
+// (hi + lo, with the exact error of every difference and sum; Knuth's two-sum),
+// which holds 48 bits; sums of threads are fp64.
 #include "kda_internal.h"
 #include "kda_types.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int THREADS = 1024;
+constexpr int THREADS = 256, WARPS = THREADS / 32, MOST = 8;  // CTAs of a cluster
 
-// Sum over the block; every thread gets it.  `scan` gets the inclusive sum up
-// to the caller's thread.
-__device__ double block_scan(double x, double* scratch, double* scan) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double s = x;
+struct Sum {
+  float hi = 0.f, lo = 0.f;
+  // adds x + e, |e| far below |x|
+  __device__ __forceinline__ void add(float x, float e) {
+    const float t = hi + x, z = t - hi;
+    lo += ((hi - (t - z)) + (x - z)) + e;
+    hi = t;
+  }
+  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+};
+
+// The weight max(p - q, 0) as x + e, exactly; 0 where it is not finite.
+__device__ __forceinline__ void difference(float p, float q, float& x, float& e) {
+  x = p - q;
+  const float z = x - p;
+  e = (p - (x - z)) - (q + z);
+  if (!(x > 0.f && x < INFINITY)) x = e = 0.f;
+}
+
+struct Row {
+  const void* top;  // the target's probabilities
+  const void* low;  // the draft model's, or null
+  int skip;         // an entry without weight, or -1
+};
+
+// a weight in fp64
+template <typename T> __device__ __forceinline__ double weight(const Row& r, int j) {
+  double w = (double)to_f32(static_cast<const T*>(r.top)[j]);
+  if (r.low) w -= (double)to_f32(static_cast<const T*>(r.low)[j]);
+  return w > 0. && w < (double)INFINITY && j != r.skip ? w : 0.;
+}
+
+template <typename T> __device__ __forceinline__ void add_one(Sum& s, const Row& r, int j, float p, float q) {
+  float x, e;
+  difference(p, q, x, e);
+  if (j == r.skip) x = e = 0.f;
+  s.add(x, e);
+}
+
+// This lane's share of the weights of [j0, j1), 16 bytes at a time
+template <typename T> __device__ __forceinline__ Sum sum_vectors(const Row& r, int j0, int j1, int lane) {
+  constexpr int VE = 16 / sizeof(T), AHEAD = 4;
+  Sum s;
+  for (int j = j0 + lane * VE; j < j1; j += 32 * VE * AHEAD) {
+    uint4 a[AHEAD], b[AHEAD];
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      const int at = j + x * 32 * VE;
+      a[x] = b[x] = make_uint4(0, 0, 0, 0);
+      if (at < j1) {
+        a[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(r.top) + at);
+        if (r.low) b[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(r.low) + at);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x)
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        add_one<T>(s, r, j + x * 32 * VE + e, to_f32(reinterpret_cast<const T*>(&a[x])[e]),
+                   to_f32(reinterpret_cast<const T*>(&b[x])[e]));
+  }
+  return s;
+}
+
+// The same, one entry at a time (rows that do not start on 16 bytes), `step` apart from j0 on
+template <typename T> __device__ __forceinline__ Sum sum_entries(const Row& r, int j0, int j1, int step) {
+  constexpr int AHEAD = 8;
+  Sum s;
+  for (int j = j0; j < j1; j += step * AHEAD) {
+    float a[AHEAD], b[AHEAD];
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      const int at = j + x * step;
+      a[x] = b[x] = 0.f;
+      if (at < j1) {
+        a[x] = to_f32(static_cast<const T*>(r.top)[at]);
+        if (r.low) b[x] = to_f32(static_cast<const T*>(r.low)[at]);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) add_one<T>(s, r, j + x * step, a[x], b[x]);
+  }
+  return s;
+}
+
+__device__ __forceinline__ double warp_scan(double s, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const double y = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += y;
   }
-  __syncthreads();
-  if (lane == 31) scratch[warp] = s;
-  __syncthreads();
-  double before = 0., total = 0.;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w == warp) before = total;
-    total += scratch[w];
-  }
-  *scan = before + s;
-  return total;
+  return s;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// stores x at the place of `local` in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ void store_remote(const double* local, uint32_t rank, double x) {
+  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
+  asm volatile("{.reg .u32 r; mapa.shared::cluster.u32 r, %0, %1; st.shared::cluster.f64 [r], %2;}" ::"r"(at), "r"(rank),
+               "d"(x) : "memory");
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) accept_kernel(AcceptProblem p) {
-  __shared__ double scratch[THREADS / 32];
-  __shared__ int s_next, s_last;
-  const int n = blockIdx.x, tid = threadIdx.x, K = p.K, V = p.V;
+__global__ void __launch_bounds__(THREADS) accept_kernel(const __grid_constant__ AcceptProblem p, int cluster) {
+  __shared__ double s_slice[2][MOST * WARPS];  // the slices' sums, for each of two attempts
+  __shared__ double s_warp[WARPS];
+  __shared__ int s_next;
+  const int rank = cluster == 1 ? 0 : (int)cluster_rank();
+  const int n = blockIdx.x / cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int K = p.K, V = p.V;
   int* tokens = p.tokens + (long long)n * (K + 1);
-  const int len = p.draft_lens ? min(p.draft_lens[n], K) : K;
-  if (len < 0) {
-    if (tid <= K) tokens[tid] = -1;
-    for (int i = THREADS + tid; i <= K; i += THREADS) tokens[i] = -1;
-    if (tid == 0) p.counts[n] = 0;
-    return;
-  }
+  const int* toks = p.draft_tokens + (long long)n * K;
+  const float* u = p.uniform + (long long)n * (K + 1);
   const T* target = static_cast<const T*>(p.target) + n * p.target_stride_n;
   const T* draft = p.draft ? static_cast<const T*>(p.draft) + n * p.draft_stride_n : nullptr;
-  const float* u = p.uniform + (long long)n * (K + 1);
-  const int* toks = p.draft_tokens + (long long)n * K;
+  const int len = p.draft_lens ? min(p.draft_lens[n], K) : K;
+  const float u_last = u[K];
+
+  // ---- the first draft that is not kept: every warp looks at 32 drafts at a time
   int a = 0;
   bool bad = false;
-  for (; a < len; ++a) {
-    const int t = toks[a];
-    bad = t < 0 || t >= V;
-    if (bad) break;
-    const double qt = draft ? (double)to_f32(draft[a * p.draft_stride_k + t]) : 1.;
-    if (!((double)u[a] * qt < (double)to_f32(target[a * p.target_stride_k + t]))) break;
-  }
-  if (bad && tid == 0) *p.status = 1;
-  const T* top = target + a * p.target_stride_k;
-  const T* low = draft && a < len ? draft + a * p.draft_stride_k : nullptr;
-  int skip = !draft && a < len ? toks[a] : -1;
-  auto weight = [&](int j) -> double {
-    if (j >= V || j == skip) return 0.;
-    double w = (double)to_f32(top[j]);
-    if (low) w -= (double)to_f32(low[j]);
-    return w > 0. && w < (double)INFINITY ? w : 0.;
-  };
-  double total, scan;
-  for (int pass = 0;; ++pass) {
-    double s = 0.;
-    for (int j = tid; j < V; j += THREADS) s += weight(j);
-    total = block_scan(s, scratch, &scan);
-    if (total > 0. || pass == 1) break;
-    low = nullptr;  // no weight is positive: the target's own probabilities
-    skip = -1;
-  }
-  if (tid == 0) s_next = V, s_last = -1;
-  __syncthreads();
-  const double goal = (double)u[K] * total;
-  double base = 0.;
-  for (int j0 = 0; j0 < V; j0 += THREADS) {
-    const double w = weight(j0 + tid);
-    const double sum = block_scan(w, scratch, &scan);
-    if (w > 0.) {
-      atomicMax(&s_last, j0 + tid);
-      if (base + scan > goal) atomicMin(&s_next, j0 + tid);
+  for (int i0 = 0; i0 < K; i0 += 32) {
+    const int i = i0 + lane;
+    bool ok = false, outside = false;
+    if (i < K) {
+      const int t = toks[i];
+      outside = t < 0 || t >= V;
+      if (!outside) {
+        const double qt = draft ? (double)to_f32(draft[i * p.draft_stride_k + t]) : 1.;
+        ok = (double)u[i] * qt < (double)to_f32(target[i * p.target_stride_k + t]);
+      }
     }
-    __syncthreads();
-    if (s_next < V) break;
-    base += sum;
+    const unsigned stop = __ballot_sync(0xffffffffu, !ok || i >= len);
+    a = i0 + (stop ? __ffs(stop) - 1 : 32);
+    bad = stop && __shfl_sync(0xffffffffu, outside, stop ? __ffs(stop) - 1 : 0) && a < len;
+    if (stop) break;
   }
-  if (tid == 0) {
-    tokens[a] = s_next < V ? s_next : s_last;
+  if (len < 0) {  // an idle sequence: the same for the whole cluster
+    if (rank == 0) {
+      for (int i = tid; i <= K; i += THREADS) tokens[i] = -1;
+      if (tid == 0) p.counts[n] = 0;
+    }
+    return;
+  }
+  a = min(a, len);
+  if (bad && tid == 0) *p.status = 1;
+  Row row;
+  row.top = target + a * p.target_stride_k;
+  row.low = draft && a < len ? draft + a * p.draft_stride_k : nullptr;
+  row.skip = !draft && a < len ? toks[a] : -1;
+
+  // ---- slices of 256 E entries, one for each warp of the cluster
+  const int slices = cluster * WARPS, mine = rank * WARPS + warp;
+  const int E = (V + slices * THREADS - 1) / (slices * THREADS);
+  const int L = E * THREADS;
+  const auto odd = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) != 0; };
+  const bool vectors = !odd(row.top) && !(row.low && odd(row.low)) && V % (16 / sizeof(T)) == 0;
+  double goal = 0., before = 0.;
+  int slice = -1;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    const int j0 = (int)min((long long)mine * L, (long long)V), j1 = (int)min((long long)j0 + L, (long long)V);
+    const Sum s = vectors ? sum_vectors<T>(row, j0, j1, lane) : sum_entries<T>(row, j0 + lane, j1, 32);
+    double total = s.value();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (cluster == 1) {
+      if (lane == 0) s_slice[attempt][mine] = total;
+      __syncthreads();
+    } else {
+      if (lane < cluster) store_remote(&s_slice[attempt][mine], lane, total);
+      cluster_sync();
+    }
+    // every warp finds the slice that holds the border: the first whose running sum passes the goal
+    double x = lane * 2 < slices ? s_slice[attempt][lane * 2] : 0., y = lane * 2 + 1 < slices ? s_slice[attempt][lane * 2 + 1] : 0.;
+    const double end = warp_scan(x + y, lane);       // after slice 2 lane + 1
+    const double start = __shfl_up_sync(0xffffffffu, end, 1);
+    const double first = lane ? start : 0.;          // before slice 2 lane
+    const double middle = first + x;
+    const double all = __shfl_sync(0xffffffffu, end, 31);
+    if (!(all > 0.)) {
+      if (!row.low && row.skip < 0) break;
+      row.low = nullptr;  // no weight is positive: the target's own probabilities
+      row.skip = -1;
+      continue;
+    }
+    goal = (double)u_last * all;
+    const unsigned in_x = __ballot_sync(0xffffffffu, x > 0. && middle > goal);
+    const unsigned in_y = __ballot_sync(0xffffffffu, y > 0. && end > goal);
+    const int kx = in_x ? __ffs(in_x) - 1 : 32, ky = in_y ? __ffs(in_y) - 1 : 32;
+    if (kx == 32 && ky == 32) {  // rounding (or u = 1): the last slice that has weight
+      const unsigned has_x = __ballot_sync(0xffffffffu, x > 0.), has_y = __ballot_sync(0xffffffffu, y > 0.);
+      const int lx = has_x ? 31 - __clz(has_x) : -1, ly = has_y ? 31 - __clz(has_y) : -1;
+      slice = ly >= lx ? 2 * ly + 1 : 2 * lx;
+    } else {
+      slice = kx <= ky ? 2 * kx : 2 * ky + 1;
+    }
+    before = __shfl_sync(0xffffffffu, slice & 1 ? middle : first, slice >> 1);
+    break;
+  }
+  // all of the cluster's shared memory has been written: its CTAs go on alone
+  if (slice >= 0 ? slice / WARPS != rank : rank != 0) return;
+
+  // ---- the slice in 256 contiguous pieces, then the piece
+  int next = -1;
+  if (slice >= 0) {
+    const long long s0 = (long long)slice * L;
+    const int j0 = (int)min(s0 + tid * E, (long long)V), j1 = (int)min((long long)j0 + E, (long long)V);
+    const double mine_sum = sum_entries<T>(row, j0, j1, 1).value();
+    double scan = warp_scan(mine_sum, lane);
+    if (tid == 0) s_next = -1;
+    if (lane == 31) s_warp[warp] = scan;
+    __syncthreads();
+    double base = before;
+    for (int w = 0; w < warp; ++w) base += s_warp[w];
+    // the first piece that passes the goal, or else (rounding) the last that has weight: candidates
+    // are numbered so that one maximum decides
+    const bool passes = mine_sum > 0. && base + scan > goal;
+    if (mine_sum > 0.) atomicMax(&s_next, passes ? 2 * THREADS - tid : tid);
+    __syncthreads();
+    const int piece = s_next >= THREADS ? 2 * THREADS - s_next : s_next;
+    if (piece >= 0 && piece / 32 == warp) {
+      const double at = __shfl_sync(0xffffffffu, base + scan - mine_sum, piece & 31);
+      const int p0 = (int)min(s0 + (long long)piece * E, (long long)V), p1 = (int)min((long long)p0 + E, (long long)V);
+      double run = at;
+      int last = -1;
+      for (int q0 = p0; q0 < p1 && next < 0; q0 += 32) {
+        const double w = q0 + lane < p1 ? weight<T>(row, q0 + lane) : 0.;
+        const double sum = run + warp_scan(w, lane);
+        const unsigned pass = __ballot_sync(0xffffffffu, w > 0. && sum > goal), has = __ballot_sync(0xffffffffu, w > 0.);
+        if (pass) next = q0 + __ffs(pass) - 1;
+        if (has) last = q0 + 31 - __clz(has);
+        run = __shfl_sync(0xffffffffu, sum, 31);
+      }
+      if (next < 0) next = last;
+      if (lane == 0) {
+        tokens[a] = next;
+        p.counts[n] = a + 1;
+      }
+    }
+  } else if (tid == 0) {
+    tokens[a] = -1;
     p.counts[n] = a + 1;
   }
   for (int i = tid; i <= K; i += THREADS)
     if (i != a) tokens[i] = i < a ? toks[i] : -1;
 }
 
+template <typename T> cudaError_t launch_typed(const AcceptProblem& p, cudaStream_t stream) {
+  // As many CTAs to a sequence as are resident together for all of them (8 of 256 threads on an SM),
+  // while each has at least 1024 entries.
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  int cluster = MOST;
+  while (cluster > 1 && ((long long)p.N * cluster > 8LL * sms || p.V < 1024 * cluster)) cluster /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.N * cluster);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)cluster, 1u, 1u};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, accept_kernel<T>, p, cluster);
+}
+
 }  // namespace
 
 cudaError_t launch_draft_accept(const AcceptProblem& p, cudaStream_t stream) {
   if (p.N == 0) return cudaSuccess;
-  if (p.dtype == KDA_F32)
-    accept_kernel<float><<<p.N, THREADS, 0, stream>>>(p);
-  else if (p.dtype == KDA_BF16)
-    accept_kernel<__nv_bfloat16><<<p.N, THREADS, 0, stream>>>(p);
-  else
-    accept_kernel<__half><<<p.N, THREADS, 0, stream>>>(p);
-  return cudaGetLastError();
+  switch (p.dtype) {
+    case KDA_F32: return launch_typed<float>(p, stream);
+    case KDA_BF16: return launch_typed<__nv_bfloat16>(p, stream);
+    default: return launch_typed<__half>(p, stream);
+  }
 }
 
 }  // namespace kda

@@ -929,14 +929,6 @@ __global__ void __launch_bounds__(THREADS) join_kernel(const __grid_constant__ P
 
 // ---------------------------------------------------------------- host
 
-int device_sms() {
-  static int sms[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (!sms[dev]) cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
-  return sms[dev];
-}
-
 struct Plan {
   int rows, per, groups, grid, team;  // query rows of a key head, in groups of at most per
   bool whole, by_unit;
@@ -954,7 +946,9 @@ Plan plan_for(int n_seq, int K, int H_q, int H_kv, int d, int max_len) {
   a.per = ((a.rows + a.groups - 1) / a.groups + 15) / 16 * 16;
   a.units = (long long)n_seq * H_kv * a.groups;
   const long long tiles = a.units * ((max_len + TILE - 1) / TILE > 1 ? (max_len + TILE - 1) / TILE : 1);
-  const int resident = (a.per == 16 ? 2 : 1) * device_sms();
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) return a;
+  const int resident = (a.per == 16 ? 2 : 1) * sms;
   // up to 4 tiles (256 positions) a unit is read faster than its parts are joined
   a.whole = max_len <= 4 * TILE;
   const long long want = a.whole ? a.units : tiles;

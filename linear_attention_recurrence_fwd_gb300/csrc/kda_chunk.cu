@@ -2471,6 +2471,8 @@ cudaError_t launch_chunk_fwd_noalloc(const ChunkProblem& pr, cudaStream_t stream
   return launch_impl(pr, nullptr, nullptr, nullptr, static_cast<uint8_t*>(scratch), false, stream);
 }
 
+cudaError_t sm_count(int* sms) { return device_sms(sms); }
+
 cudaError_t chunk_status_address(int** status) {
   return cudaGetSymbolAddress(reinterpret_cast<void**>(status), g_chunk_status);
 }

@@ -106,6 +106,8 @@ cudaError_t launch_chunk_fwd_noalloc(const ChunkProblem& p, cudaStream_t stream)
 // current device for kernels of other translation units.
 int read_and_clear_chunk_status(cudaStream_t stream, cudaError_t* err);
 cudaError_t chunk_status_address(int** status);
+// SMs of the current device (asked once).
+cudaError_t sm_count(int* sms);
 
 // The calls around a paged cache (see include/kda.h for the arguments).
 struct AppendProblem {
