@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -138,12 +139,6 @@ def _p(t):
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
-
-
-def _on(stream):
-    """Allocate for `stream`: what the caching allocator hands out must belong
-    to the stream that the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _check(code, where):
@@ -467,28 +462,43 @@ class PagedCache:
         self._ref = ctypes.addressof(self._struct)
 
 
-def _token_stride(x, d, name):
-    """The elements between the tokens of x ([T, H, d] or [N, K, H, d], heads
-    packed, sequences of equal length one after the other)."""
-    s = x.stride()
-    if not x.is_cuda or x.shape[-1] != d or (s[-1] != 1 and d > 1) or (s[-2] != d and x.shape[-2] > 1):
-        raise ValueError(f"{name} must be a CUDA tensor of heads of {d} channels, packed within a token")
-    if x.dim() == 3:
+# The calls below take a few microseconds on the GPU for a single token, so what
+# they do on the host is kept short: one look at a tensor's shape and strides,
+# raw pointers, no context manager where the current stream is used.
+
+def _token_stride(x, heads, d, name):
+    """The elements between the tokens of x ([T, heads, d] or [N, K, heads, d],
+    heads packed, sequences of equal length one after the other)."""
+    shape, s = x.shape, x.stride()
+    if not x.is_cuda or shape[-1] != d or shape[-2] != heads or s[-1] != 1 or (s[-2] != d and heads > 1):
+        raise ValueError(f"{name} must be a CUDA tensor of {heads} heads of {d} channels, packed within a token")
+    if len(shape) == 3 or shape[1] == 1:
         return s[0]
-    if x.shape[1] == 1:
-        return s[0]
-    if x.shape[0] > 1 and s[0] != x.shape[1] * s[1]:
+    if shape[0] > 1 and s[0] != shape[1] * s[1]:
         raise ValueError(f"the tokens of {name} must be evenly spaced")
     return s[1]
 
 
-def _counts_ptr(counts, n_seq):
-    if counts is None:
+def _int32_ptr(t, n, name):
+    """The address of a contiguous int32 tensor of n entries; None for None."""
+    if t is None:
         return None
-    _need(counts, torch.int32, "counts")
-    if counts.shape != (n_seq,):
-        raise ValueError(f"counts must have {n_seq} entries")
-    return counts.data_ptr()
+    if not t.is_cuda or t.dtype != torch.int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of {n} entries")
+    return t.data_ptr()
+
+
+def _stream_of(stream, t):
+    """The raw handle of `stream`, or of the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+@functools.lru_cache(maxsize=1024)
+def _attend_workspace(device, N, K, H_q, H_kv, d, max_len):
+    """Bytes of kda_cache_attend's workspace for these sizes on the current device."""
+    return load().kda_cache_attend_workspace_size(N, K, H_q, H_kv, d, max_len)
 
 
 def kda_cache_append(k, v, cache, q=None, inv_freq=None, interleaved=False, cu_seqlens=None,
@@ -498,47 +508,55 @@ def kda_cache_append(k, v, cache, q=None, inv_freq=None, interleaved=False, cu_s
     packed [T,H_kv,d] with cu_seqlens int32 [N+1]; q the same with H_q heads;
     inv_freq fp64 [rot_dim/2] or None (no rotation); counts int32 [N]: how many
     of the K tokens are real.  Returns the rotated queries (q_out), or None."""
-    lib = load()
-    if k.dim() != (4 if cu_seqlens is None else 3) or k.shape != v.shape:
-        raise ValueError("k and v must be [N, K, H_kv, d], or [T, H_kv, d] with cu_seqlens")
-    if k.dtype != v.dtype or k.dtype not in _CODES or (q is not None and q.dtype != k.dtype):
+    lib = _lib or load()
+    shape, dtype = k.shape, k.dtype
+    code = _CODES.get(dtype)
+    if code is None or v.dtype != dtype or (q is not None and q.dtype != dtype):
         raise ValueError("k, v and q must have one dtype, bfloat16 or float16")
-    H, d = cache.heads, cache.d
-    if k.shape[-2] != H:
-        raise ValueError(f"k has {k.shape[-2]} heads, the cache {H}")
+    H, d, N = cache.heads, cache.d, cache.n_seq
+    if len(shape) != (4 if cu_seqlens is None else 3) or v.shape != shape:
+        raise ValueError("k and v must be [N, K, H_kv, d], or [T, H_kv, d] with cu_seqlens")
     if cu_seqlens is None:
-        K, T, cu = k.shape[1], k.shape[0] * k.shape[1], None
-        if k.shape[0] != cache.n_seq:
-            raise ValueError(f"k has {k.shape[0]} sequences, the cache {cache.n_seq}")
+        K = shape[1]
+        T = N * K
+        if shape[0] != N:
+            raise ValueError(f"k has {shape[0]} sequences, the cache {N}")
     else:
-        _need(cu_seqlens, torch.int32, "cu_seqlens")
-        if cu_seqlens.shape != (cache.n_seq + 1,):
-            raise ValueError(f"cu_seqlens must have {cache.n_seq + 1} entries")
-        K, T, cu = 0, k.shape[0], cu_seqlens.data_ptr()
-    rot = 0
+        K, T = 0, shape[0]
+    rot, freqs = 0, None
     if inv_freq is not None:
         _need(inv_freq, torch.float64, "inv_freq")
         rot = 2 * inv_freq.numel()
+        freqs = inv_freq.data_ptr() if rot else None
     qp = qo = None
     qs = qos = Hq = 0
     if q is not None:
-        if q.shape[:-2] != k.shape[:-2]:
+        q_shape = q.shape
+        if q_shape[:-2] != shape[:-2]:
             raise ValueError("q and k must have the same tokens")
-        qs, Hq = _token_stride(q, d, "q"), q.shape[-2]
+        Hq = q_shape[-2]
+        qs = _token_stride(q, Hq, d, "q")
         if q_out is None:
-            with _on(stream):
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+            if stream is None:
+                q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
+            else:
+                with torch.cuda.stream(stream):
+                    q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
+            qos = Hq * d
+        elif q_out.shape != q_shape or q_out.dtype != dtype:
             raise ValueError("q_out must have q's shape and dtype")
-        qos = _token_stride(q_out, d, "q_out")
+        else:
+            qos = _token_stride(q_out, Hq, d, "q_out")
         qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check(lib.kda_cache_append(
-        cache._ref, k.data_ptr(), v.data_ptr(), qp, qo, _CODES[k.dtype], _token_stride(k, d, "k"),
-        _token_stride(v, d, "v"), qs, qos, inv_freq.data_ptr() if rot else None, rot,
-        int(interleaved), cu, _counts_ptr(counts, cache.n_seq), K, T, Hq, _stream(stream)),
-        "kda_cache_append")
+    code = lib.kda_cache_append(
+        cache._ref, k.data_ptr(), v.data_ptr(), qp, qo, code, _token_stride(k, H, d, "k"),
+        _token_stride(v, H, d, "v"), qs, qos, freqs, rot, interleaved,
+        _int32_ptr(cu_seqlens, N + 1, "cu_seqlens"), _int32_ptr(counts, N, "counts"), K, T, Hq,
+        _stream_of(stream, k))
+    if code:
+        raise KDAError(code, "kda_cache_append")
     return q_out
 
 
@@ -550,24 +568,31 @@ def kda_cache_attend(q, cache, scale=None, window=0, counts=None, max_len=0, out
     to 1/sqrt(d); max_len: an upper bound on lens + K (0: what the table
     holds).  Returns out [N,K,H_q,d], and with return_lse also the fp32 log of
     the sum of exponentials [N,K,H_q]."""
-    lib = load()
-    if q.dim() != 4 or q.shape[0] != cache.n_seq or q.dtype not in _CODES:
+    lib = _lib or load()
+    shape, dtype = q.shape, q.dtype
+    code = _CODES.get(dtype)
+    if len(shape) != 4 or shape[0] != cache.n_seq or code is None:
         raise ValueError(f"q must be [{cache.n_seq}, K, H_q, {cache.d}] in bfloat16 or float16")
-    N, K, Hq, d = q.shape
-    qs = _token_stride(q, cache.d, "q")
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous()):
-        raise ValueError("out must be contiguous, with q's shape and dtype")
-    need = lib.kda_cache_attend_workspace_size(N, K, Hq, cache.heads, d, max_len or cache.capacity)
-    with _on(stream):
+    N, K, Hq, d = shape
+    qs = _token_stride(q, Hq, cache.d, "q")
+    if out is not None and (out.shape != shape or out.dtype != dtype or not out.is_cuda or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous CUDA tensor with q's shape and dtype")
+    dev = q.device
+    need = _attend_workspace(dev.index, N, K, Hq, cache.heads, d, max_len or cache.capacity)
+    lse = ws = None
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
         if out is None:
-            out = torch.empty((N, K, Hq, d), dtype=q.dtype, device=q.device)
-        lse = torch.empty((N, K, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _check(lib.kda_cache_attend(
-        cache._ref, q.data_ptr(), _CODES[q.dtype], qs, out.data_ptr(),
-        lse.data_ptr() if return_lse else None, _counts_ptr(counts, N), K, Hq,
-        d ** -0.5 if scale is None else float(scale), int(window), int(max_len),
-        ws.data_ptr() if need else None, need, _stream(stream)), "kda_cache_attend")
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        if return_lse:
+            lse = torch.empty((N, K, Hq), dtype=torch.float32, device=dev)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    code = lib.kda_cache_attend(
+        cache._ref, q.data_ptr(), code, qs, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        _int32_ptr(counts, N, "counts"), K, Hq, d ** -0.5 if scale is None else scale, window, max_len,
+        None if ws is None else ws.data_ptr(), need, _stream_of(stream, q))
+    if code:
+        raise KDAError(code, "kda_cache_attend")
     return (out, lse) if return_lse else out
 
 
@@ -579,40 +604,42 @@ def kda_draft_accept(draft_tokens, draft_probs, target_probs, uniform, draft_len
     (fp32, bf16 or fp16); uniform fp32 [N,K+1] in [0, 1); draft_lens int32 [N]
     (negative: an idle sequence).  Returns (counts int32 [N], the tokens gained
     by each sequence, and tokens int32 [N,K+1], -1 beyond them)."""
-    lib = load()
+    lib = _lib or load()
     N, K1, V = target_probs.shape
     K = K1 - 1
+    dtype = target_probs.dtype
+    code = _CODES.get(dtype)
+    ts = target_probs.stride()
+    if code is None or not target_probs.is_cuda or (ts[2] != 1 and V > 1):
+        raise ValueError("target_probs must be a CUDA tensor of float32, bfloat16 or float16 with contiguous rows")
     _need(draft_tokens, torch.int32, "draft_tokens")
     _need(uniform, torch.float32, "uniform")
     if K < 0 or draft_tokens.shape != (N, K) or uniform.shape != (N, K1):
         raise ValueError("draft_tokens must be [N, K] and uniform [N, K + 1] for target_probs [N, K + 1, V]")
-    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
-        if t is not None and (not t.is_cuda or t.dtype not in _CODES or t.dtype != target_probs.dtype or
-                              (t.stride(2) != 1 and V > 1)):
-            raise ValueError(f"{name} must be a CUDA tensor of float32, bfloat16 or float16 with "
-                             "contiguous rows, of target_probs' dtype")
-    if draft_probs is not None and draft_probs.shape != (N, K, V):
-        raise ValueError(f"draft_probs must be {(N, K, V)}")
-    if draft_lens is not None:
-        _need(draft_lens, torch.int32, "draft_lens")
-        if draft_lens.shape != (N,):
-            raise ValueError(f"draft_lens must have {N} entries")
-    for t, shape, name in ((counts, (N,), "counts"), (tokens, (N, K1), "tokens")):
-        if t is not None:
-            _need(t, torch.int32, name)
-            if t.shape != shape:
-                raise ValueError(f"{name} must be {shape}")
-    with _on(stream):
+    dp, ds = None, (0, 0)
+    if draft_probs is not None:
+        ds = draft_probs.stride()
+        if (draft_probs.dtype != dtype or not draft_probs.is_cuda or draft_probs.shape != (N, K, V) or
+                (ds[2] != 1 and V > 1)):
+            raise ValueError(f"draft_probs must be a CUDA tensor {(N, K, V)} of target_probs' dtype with "
+                             "contiguous rows")
+        dp = draft_probs.data_ptr()
+    dev = target_probs.device
+    if tokens is not None:
+        _need(tokens, torch.int32, "tokens")
+        if tokens.shape != (N, K1):
+            raise ValueError(f"tokens must be {(N, K1)}")
+    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
         if counts is None:
-            counts = torch.empty((N,), dtype=torch.int32, device=target_probs.device)
+            counts = torch.empty(N, dtype=torch.int32, device=dev)
         if tokens is None:
-            tokens = torch.empty((N, K1), dtype=torch.int32, device=target_probs.device)
-    dsn, dsk = (0, 0) if draft_probs is None else draft_probs.stride()[:2]
-    _check(lib.kda_draft_accept(
-        draft_tokens.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
-        target_probs.data_ptr(), _CODES[target_probs.dtype], dsn, dsk, target_probs.stride(0),
-        target_probs.stride(1), uniform.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(),
-        counts.data_ptr(), tokens.data_ptr(), N, K, V, _stream(stream)), "kda_draft_accept")
+            tokens = torch.empty((N, K1), dtype=torch.int32, device=dev)
+    code = lib.kda_draft_accept(
+        draft_tokens.data_ptr(), dp, target_probs.data_ptr(), code, ds[0], ds[1], ts[0], ts[1],
+        uniform.data_ptr(), _int32_ptr(draft_lens, N, "draft_lens"), _int32_ptr(counts, N, "counts"),
+        tokens.data_ptr(), N, K, V, _stream_of(stream, target_probs))
+    if code:
+        raise KDAError(code, "kda_draft_accept")
     return counts, tokens
 
 

@@ -64,29 +64,92 @@ template <typename T> __device__ __forceinline__ void add_one(Sum& s, const Row&
   s.add(x, e);
 }
 
-// This lane's share of the weights of [j0, j1), 16 bytes at a time
-template <typename T> __device__ __forceinline__ Sum sum_vectors(const Row& r, int j0, int j1, int lane) {
-  constexpr int VE = 16 / sizeof(T), AHEAD = 4;
-  Sum s;
-  for (int j = j0 + lane * VE; j < j1; j += 32 * VE * AHEAD) {
-    uint4 a[AHEAD], b[AHEAD];
+// Two fp32 numbers in a register pair, and their sums and differences.
+__device__ __forceinline__ uint64_t pack(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+// Sum, two at a time
+struct Sum2 {
+  uint64_t hi = 0, lo = 0;
+  __device__ __forceinline__ void add(uint64_t x, uint64_t e) {
+    const uint64_t t = add2(hi, x), z = sub2(t, hi);
+    lo = add2(lo, add2(add2(sub2(hi, sub2(t, z)), sub2(x, z)), e));
+    hi = t;
+  }
+  // the weights of two entries
+  __device__ __forceinline__ void add(float p0, float p1, float q0, float q1) {
+    const uint64_t p = pack(p0, p1), q = pack(q0, q1);
+    const uint64_t x = sub2(p, q), z = sub2(x, p), e = sub2(sub2(p, sub2(x, z)), add2(q, z));
+    float x0, x1, e0, e1;
+    unpack(x, x0, x1);
+    unpack(e, e0, e1);
+    // positive and finite: bits 1 to 0x7f7fffff
+    const bool ok0 = __float_as_uint(x0) - 1u < 0x7f7fffffu, ok1 = __float_as_uint(x1) - 1u < 0x7f7fffffu;
+    add(pack(ok0 ? x0 : 0.f, ok1 ? x1 : 0.f), pack(ok0 ? e0 : 0.f, ok1 ? e1 : 0.f));
+  }
+  __device__ __forceinline__ double value() const {
+    float a, b, c, d;
+    unpack(hi, a, b);
+    unpack(lo, c, d);
+    return ((double)a + (double)c) + ((double)b + (double)d);
+  }
+};
+
+// This lane's share of the weights of [j0, j1), 16 bytes at a time; the next
+// bytes are on their way while these are summed.
+template <typename T> __device__ __forceinline__ double sum_vectors(const Row& r, int j0, int j1, int lane) {
+  constexpr int VE = 16 / sizeof(T), AHEAD = 2, STEP = 32 * VE * AHEAD;
+  Sum2 s;
+  uint4 a[2][AHEAD], b[2][AHEAD];
+  const T* top = static_cast<const T*>(r.top);
+  const T* low = static_cast<const T*>(r.low);
+  auto load = [&](int buf, int j) {
 #pragma unroll
     for (int x = 0; x < AHEAD; ++x) {
       const int at = j + x * 32 * VE;
-      a[x] = b[x] = make_uint4(0, 0, 0, 0);
+      a[buf][x] = b[buf][x] = make_uint4(0, 0, 0, 0);
       if (at < j1) {
-        a[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(r.top) + at);
-        if (r.low) b[x] = *reinterpret_cast<const uint4*>(static_cast<const T*>(r.low) + at);
+        a[buf][x] = *reinterpret_cast<const uint4*>(top + at);
+        if (low) b[buf][x] = *reinterpret_cast<const uint4*>(low + at);
       }
     }
+  };
+  auto sum = [&](int buf, int j) {
 #pragma unroll
-    for (int x = 0; x < AHEAD; ++x)
+    for (int x = 0; x < AHEAD; ++x) {
+      T* p = reinterpret_cast<T*>(&a[buf][x]);
+      const T* q = reinterpret_cast<const T*>(&b[buf][x]);
+      const int at = j + x * 32 * VE;
+      const int skip = r.skip - at;  // an entry of these without weight
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        add_one<T>(s, r, j + x * 32 * VE + e, to_f32(reinterpret_cast<const T*>(&a[x])[e]),
-                   to_f32(reinterpret_cast<const T*>(&b[x])[e]));
+      for (int e = 0; e < VE; e += 2)
+        s.add(skip == e ? 0.f : to_f32(p[e]), skip == e + 1 ? 0.f : to_f32(p[e + 1]), to_f32(q[e]), to_f32(q[e + 1]));
+    }
+  };
+  int j = j0 + lane * VE;
+  if (j < j1) load(0, j);
+  for (; j < j1; j += 2 * STEP) {
+    load(1, j + STEP);
+    sum(0, j);
+    load(0, j + 2 * STEP);
+    sum(1, j + STEP);
   }
-  return s;
+  return s.value();
 }
 
 // The same, one entry at a time (rows that do not start on 16 bytes), `step` apart from j0 on
@@ -135,7 +198,7 @@ __device__ __forceinline__ void store_remote(const double* local, uint32_t rank,
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) accept_kernel(const __grid_constant__ AcceptProblem p, int cluster) {
+__global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constant__ AcceptProblem p, int cluster) {
   __shared__ double s_slice[2][MOST * WARPS];  // the slices' sums, for each of two attempts
   __shared__ double s_warp[WARPS];
   __shared__ int s_next;
@@ -193,8 +256,7 @@ __global__ void __launch_bounds__(THREADS) accept_kernel(const __grid_constant__
   int slice = -1;
   for (int attempt = 0; attempt < 2; ++attempt) {
     const int j0 = (int)min((long long)mine * L, (long long)V), j1 = (int)min((long long)j0 + L, (long long)V);
-    const Sum s = vectors ? sum_vectors<T>(row, j0, j1, lane) : sum_entries<T>(row, j0 + lane, j1, 32);
-    double total = s.value();
+    double total = vectors ? sum_vectors<T>(row, j0, j1, lane) : sum_entries<T>(row, j0 + lane, j1, 32).value();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (cluster == 1) {
@@ -280,13 +342,13 @@ __global__ void __launch_bounds__(THREADS) accept_kernel(const __grid_constant__
 }
 
 template <typename T> cudaError_t launch_typed(const AcceptProblem& p, cudaStream_t stream) {
-  // As many CTAs to a sequence as are resident together for all of them (8 of 256 threads on an SM),
+  // As many CTAs to a sequence as are resident together for all of them (4 on an SM),
   // while each has at least 1024 entries.
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   int cluster = MOST;
-  while (cluster > 1 && ((long long)p.N * cluster > 8LL * sms || p.V < 1024 * cluster)) cluster /= 2;
+  while (cluster > 1 && ((long long)p.N * cluster > 4LL * sms || p.V < 1024 * cluster)) cluster /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.N * cluster);
   cfg.blockDim = dim3(THREADS);

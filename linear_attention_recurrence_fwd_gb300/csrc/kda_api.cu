@@ -395,6 +395,7 @@ kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void* k, con
       !aligned_rows(q, q ? q_stride : 0, dtype) || !aligned_rows(q_out, q ? q_out_stride : 0, dtype) ||
       (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
     return KDA_ERR_ALIGNMENT;
+  if (T > (1 << 30)) return KDA_ERR_UNSUPPORTED;
   if (q && H_q > (1 << 16)) return KDA_ERR_UNSUPPORTED;
   if (cache->H_kv > (1 << 16)) return KDA_ERR_UNSUPPORTED;
   if (T == 0) return KDA_OK;

@@ -8,10 +8,10 @@
 // 2^20 * 2^-24 radians).
 //
 // The call moves bytes: it is bound by HBM for prompts and by latency for
-// single tokens.  A CTA has 256 threads and 1 or 4 tokens.  A token's sines
-// and cosines are formed once, for all its heads, and kept in shared memory;
-// the heads' first bytes are on their way meanwhile.  A thread takes 8
-// channels and the 8 that they are turned with, 16 bytes each.
+// single tokens.  A CTA has 256 threads and takes 1 or 4 tokens at a time.  A
+// token's sines and cosines are formed once, for all its heads, and kept in
+// shared memory; the heads' first bytes are on their way meanwhile.  A thread
+// takes 8 channels and the 8 that they are turned with, 16 bytes each.
 #include "kda_internal.h"
 #include "kda_types.cuh"
 
@@ -103,119 +103,130 @@ template <typename C> __device__ __forceinline__ void store8(C* dst, const float
 // c + rot_dim / 2), then 8 channels that are not turned; or, with neighbouring
 // pairs, 8 channels each.
 template <typename T, typename C, int TOKENS>
-__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ AppendProblem p, int jobs) {
-  constexpr int AHEAD = 3;  // pieces of a thread whose loads are in flight together
-  __shared__ __align__(16) float2 s_turn[TOKENS][64];
-  __shared__ long long s_row[TOKENS];
-  __shared__ int s_owned[TOKENS];
+__global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constant__ AppendProblem p, int jobs) {
+  constexpr int AHEAD = 2;  // pieces of a thread whose loads are in flight together
+  __shared__ __align__(16) float2 s_turn[2][TOKENS][64];
+  __shared__ long long s_row[2][TOKENS];
+  __shared__ int s_owned[2][TOKENS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t0 = blockIdx.x * TOKENS, tokens = min(TOKENS, p.T - t0);
   const int d = p.cache.d, half = p.rot_dim / 2, heads = p.H_q + 2 * p.cache.H_kv;
 
   const int slots = THREADS / jobs, j = tid % jobs, slot = tid / jobs;
   const bool pairs_apart = !p.interleaved && half > 0;
   const bool two = pairs_apart && j < half / 8;
   const int at = two || !pairs_apart ? 8 * j : p.rot_dim + 8 * (j - half / 8);
-  const int work = slot < slots ? tokens * heads : 0;
+  const int tt0 = slot / heads, h0 = slot - tt0 * heads;  // a thread's first piece of a group of tokens
+  const int tt_step = slots / heads, h_step = slots - tt_step * heads;
+
+  // the turn of a position by this thread's pair
+  constexpr int WARPS = THREADS / 32, PER = WARPS / TOKENS;  // warps of a token
+  const int my_token = warp / PER, part = warp % PER, pair = part * 32 + lane;
+  const long long step = pair < half ? turn_step(p.inv_freq[pair]) : 0;
 
   uint4 a[AHEAD], b[AHEAD];
-  auto source = [&](int tt, int h) -> const T* {
-    const long long t = t0 + tt;
-    if (h < p.H_q) return static_cast<const T*>(p.q) + t * p.q_stride + h * d + at;
-    h -= p.H_q;
-    if (h < p.cache.H_kv) return static_cast<const T*>(p.k) + t * p.k_stride + h * d + at;
-    return static_cast<const T*>(p.v) + t * p.v_stride + (h - p.cache.H_kv) * d + at;
+  int tt, h;  // the next piece to load
+  auto advance = [&](int& t, int& x) {
+    t += tt_step;
+    x += h_step;
+    if (x >= heads) x -= heads, ++t;
   };
-  auto load = [&](int w0) {
+  auto load = [&](int t0) {
 #pragma unroll
     for (int x = 0; x < AHEAD; ++x) {
-      const int w = w0 + x * slots;
-      if (w < work) {
-        const T* src = source(w / heads, w % heads);
-        a[x] = *reinterpret_cast<const uint4*>(src);
-        if (two) b[x] = *reinterpret_cast<const uint4*>(src + half);
+      const long long t = t0 + tt;
+      if (tt < TOKENS && t < p.T && slot < slots) {
+        const T* src = h < p.H_q ? static_cast<const T*>(p.q) + t * p.q_stride + h * d
+                       : h < p.H_q + p.cache.H_kv
+                           ? static_cast<const T*>(p.k) + t * p.k_stride + (h - p.H_q) * d
+                           : static_cast<const T*>(p.v) + t * p.v_stride + (h - p.H_q - p.cache.H_kv) * d;
+        a[x] = *reinterpret_cast<const uint4*>(src + at);
+        if (two) b[x] = *reinterpret_cast<const uint4*>(src + at + half);
       }
+      advance(tt, h);
     }
   };
-  load(slot);
+  if (p.cu_seqlens && blockIdx.x == 0) check_offsets(p);
 
-  // ---- places and turns: the CTA's warps share its tokens
-  constexpr int WARPS = THREADS / 32, PER = WARPS / TOKENS;  // warps of a token
-  {
-    const int tt = warp / PER, part = warp % PER;
-    if (tt < tokens) {
-      const Place pl = place_of(p, t0 + tt, lane, part == 0);
+  int buf = 0;
+  for (int t0 = blockIdx.x * TOKENS; t0 < p.T; t0 += gridDim.x * TOKENS, buf ^= 1) {
+    tt = tt0, h = h0;
+    load(t0);
+    // ---- places and turns: the CTA's warps share its tokens
+    if (t0 + my_token < p.T) {
+      const Place pl = place_of(p, t0 + my_token, lane, part == 0);
       if (part == 0 && lane == 0) {
-        s_row[tt] = pl.row;
-        s_owned[tt] = pl.owned;
+        s_row[buf][my_token] = pl.row;
+        s_owned[buf][my_token] = pl.owned;
         if (!pl.owned) *p.status = 1;
       }
-      for (int x = part * 32 + lane; x < half; x += PER * 32) s_turn[tt][x] = turn(turn_step(p.inv_freq[x]), pl.pos);
+      if (pair < half) s_turn[buf][my_token][pair] = turn(step, pl.pos);
     }
-  }
-  if (p.cu_seqlens && blockIdx.x == 0) check_offsets(p);
-  __syncthreads();
+    __syncthreads();
 
-  for (int w0 = slot; w0 < work; w0 += AHEAD * slots) {
+    int ct = tt0, ch = h0;  // the piece to store
+    while (ct < TOKENS && t0 + ct < p.T && slot < slots) {
 #pragma unroll
-    for (int x = 0; x < AHEAD; ++x) {
-      const int w = w0 + x * slots;
-      if (w >= work) break;
-      const int tt = w / heads, h = w % heads;
-      if (!s_owned[tt]) continue;
-      const bool is_q = h < p.H_q, is_k = !is_q && h < p.H_q + p.cache.H_kv;
-      const T* u = reinterpret_cast<const T*>(&a[x]);
-      const T* v = reinterpret_cast<const T*>(&b[x]);
-      float lo[8], hi[8];
+      for (int x = 0; x < AHEAD; ++x) {
+        if (ct >= TOKENS || t0 + ct >= p.T) break;
+        const bool is_q = ch < p.H_q, is_k = !is_q && ch < p.H_q + p.cache.H_kv;
+        const T* u = reinterpret_cast<const T*>(&a[x]);
+        const T* v = reinterpret_cast<const T*>(&b[x]);
+        float lo[8], hi[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo[e] = to_f32(u[e]);
-        hi[e] = two ? to_f32(v[e]) : 0.f;
-      }
-      if (is_q || is_k) {
-        if (two) {
-          const float4* cs = reinterpret_cast<const float4*>(&s_turn[tt][8 * j]);
+        for (int e = 0; e < 8; ++e) {
+          lo[e] = to_f32(u[e]);
+          hi[e] = two ? to_f32(v[e]) : 0.f;
+        }
+        if (is_q || is_k) {
+          if (two) {
+            const float4* cs = reinterpret_cast<const float4*>(&s_turn[buf][ct][8 * j]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 z = cs[e];
+            for (int e = 0; e < 4; ++e) {
+              const float4 z = cs[e];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float c = y ? z.z : z.x, s = y ? z.w : z.y;
-              const float r = lo[2 * e + y] * c - hi[2 * e + y] * s;
-              hi[2 * e + y] = lo[2 * e + y] * s + hi[2 * e + y] * c;
-              lo[2 * e + y] = r;
+              for (int y = 0; y < 2; ++y) {
+                const float c = y ? z.z : z.x, s = y ? z.w : z.y;
+                const float r = lo[2 * e + y] * c - hi[2 * e + y] * s;
+                hi[2 * e + y] = lo[2 * e + y] * s + hi[2 * e + y] * c;
+                lo[2 * e + y] = r;
+              }
             }
-          }
-        } else if (p.interleaved) {
-          const float4* cs = reinterpret_cast<const float4*>(&s_turn[tt][at / 2]);
+          } else if (p.interleaved) {
+            const float4* cs = reinterpret_cast<const float4*>(&s_turn[buf][ct][at / 2]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float4 z = cs[e];
+            for (int e = 0; e < 2; ++e) {
+              const float4 z = cs[e];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              if (at / 2 + 2 * e + y >= half) continue;  // not turned
-              const float c = y ? z.z : z.x, s = y ? z.w : z.y;
-              float &f = lo[4 * e + 2 * y], &g = lo[4 * e + 2 * y + 1];
-              const float r = f * c - g * s;
-              g = f * s + g * c;
-              f = r;
+              for (int y = 0; y < 2; ++y) {
+                if (at / 2 + 2 * e + y >= half) continue;  // not turned
+                const float c = y ? z.z : z.x, s = y ? z.w : z.y;
+                float &f = lo[4 * e + 2 * y], &g = lo[4 * e + 2 * y + 1];
+                const float r = f * c - g * s;
+                g = f * s + g * c;
+                f = r;
+              }
             }
           }
         }
+        if (is_q) {
+          if (s_owned[buf][ct]) {
+            T* dst = static_cast<T*>(p.q_out) + (long long)(t0 + ct) * p.q_out_stride + ch * d + at;
+            store8<T>(dst, lo, 1.f);
+            if (two) store8<T>(dst + half, hi, 1.f);
+          }
+        } else if (s_row[buf][ct] >= 0) {
+          const int hk = ch - p.H_q - (is_k ? 0 : p.cache.H_kv);
+          C* dst = static_cast<C*>(is_k ? p.cache.k : p.cache.v) + s_row[buf][ct] + hk * p.cache.head_stride + at;
+          const float scale = is_k ? p.cache.k_scale : p.cache.v_scale;
+          store8<C>(dst, lo, scale);
+          if (two) store8<C>(dst + half, hi, scale);
+        }
+        advance(ct, ch);
       }
-      if (is_q) {
-        T* dst = static_cast<T*>(p.q_out) + (long long)(t0 + tt) * p.q_out_stride + h * d + at;
-        store8<T>(dst, lo, 1.f);
-        if (two) store8<T>(dst + half, hi, 1.f);
-      } else if (s_row[tt] >= 0) {
-        const int hk = h - p.H_q - (is_k ? 0 : p.cache.H_kv);
-        C* dst = static_cast<C*>(is_k ? p.cache.k : p.cache.v) + s_row[tt] + hk * p.cache.head_stride + at;
-        const float scale = is_k ? p.cache.k_scale : p.cache.v_scale;
-        store8<C>(dst, lo, scale);
-        if (two) store8<C>(dst + half, hi, scale);
-      }
+      load(t0);
     }
-    load(w0 + AHEAD * slots);
+    // The next group's places and turns go to the other buffer; its writers have all passed this
+    // group's barrier, and so are done with the one before.
   }
 }
 
@@ -269,11 +280,15 @@ template <typename T, typename C> cudaError_t launch_stored(const AppendProblem&
     return cudaGetLastError();
   }
   const int jobs = p.interleaved ? p.cache.d / 8 : half / 8 + (p.cache.d - p.rot_dim) / 8;
-  // A CTA to a token while that leaves no SM idle; four share the cost of a CTA's start.
-  if (p.T <= 1024)
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  // A CTA to a token while all are resident together; else as many CTAs as are, four tokens at a time.
+  const int resident = 4 * sms;
+  if (p.T <= 2 * resident)
     append_kernel<T, C, 1><<<p.T, THREADS, 0, stream>>>(p, jobs);
   else
-    append_kernel<T, C, 4><<<(p.T + 3) / 4, THREADS, 0, stream>>>(p, jobs);
+    append_kernel<T, C, 4><<<resident, THREADS, 0, stream>>>(p, jobs);
   return cudaGetLastError();
 }
 

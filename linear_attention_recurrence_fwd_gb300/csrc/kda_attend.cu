@@ -56,7 +56,8 @@ struct Params {
   int groups;        // row groups per (sequence, key head)
   int rows;          // query rows of a key head: K H_q / H_kv
   int group_heads;   // H_q / H_kv
-  int box_rows;      // rows of one TMA box; below 8 the producer copies rows itself
+  int box_rows;      // rows of one TMA box
+  bool use_tma;      // else the producer copies rows itself, 16 bytes at a time
   bool token_first;  // the tensor map's second dimension is the token, not the head
   bool whole;        // whole units per CTA: nothing is joined
   bool by_unit;      // records are indexed by unit, else by CTA
@@ -197,13 +198,13 @@ __global__ void __launch_bounds__(Shape<D, E8, WG>::THREADS, Shape<D, E8, WG>::C
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid < STAGES) {
-    mbar_init(&full[tid], s.box_rows >= 8 ? 1 : 33);
+    mbar_init(&full[tid], s.use_tma ? 1 : 33);
     mbar_init(&empty[tid], KW * WG);
     mbar_init(&told[tid], 1);
   }
   if (tid == 0) mbar_init(joined, KW * WG);
   mbar_fence_init();
-  if (tid == 32 * KW * WG && s.box_rows >= 8 && p.cache.num_pages > 0) {
+  if (tid == 32 * KW * WG && s.use_tma && p.cache.num_pages > 0) {
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
@@ -284,10 +285,10 @@ __global__ void __launch_bounds__(Shape<D, E8, WG>::THREADS, Shape<D, E8, WG>::C
     if (WG > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::PRODUCER_REGS));
     if (warp > KW * WG) return;
   // ------------------------------------------------------------ producer
-    const bool use_tma = s.box_rows >= 8;
+    const bool use_tma = s.use_tma;
     // Page numbers are looked up for as many tiles at once as 32 lanes hold, one such batch ahead
     // of the copies, and lens and counts one sequence ahead: neither latency is waited for.
-    const int rows_per = use_tma ? s.box_rows : 1;
+    const int rows_per = s.box_rows;
     constexpr int PL = TILE / 32;  // pages of a lane, where each row of a tile is looked up
     const int boxes = TILE / rows_per, batch = boxes < 32 ? 32 / boxes : 1;
     struct Batch {
@@ -408,23 +409,29 @@ __global__ void __launch_bounds__(Shape<D, E8, WG>::THREADS, Shape<D, E8, WG>::C
       }
       if (use_tma) {
         if (lane == 0) {
-          const uint32_t bytes = (__popc(good[0])) * s.box_rows * S::ROW_BYTES * 2;
+          uint32_t boxes_here = 0;
+#pragma unroll
+          for (int y = 0; y < PL; ++y) boxes_here += __popc(good[y]);
+          const uint32_t bytes = boxes_here * s.box_rows * S::ROW_BYTES * 2;
           if (bytes) mbar_arrive_expect_tx(&full[stage], bytes); else mbar_arrive(&full[stage]);
         }
         __syncwarp();
-        if (page[0] >= 0) {
-          const int row = lane * s.box_rows, at = (pos0 + row) % p.cache.page_size;
+#pragma unroll
+        for (int y = 0; y < PL; ++y) {
+          if (page[y] < 0) continue;
+          const int row = (lane + 32 * y) * s.box_rows, at = (pos0 + row) % p.cache.page_size;
           const int c1 = s.token_first ? at : hk, c2 = s.token_first ? hk : at;
 #pragma unroll
           for (int h = 0; h < S::HALVES; ++h) {
             const uint32_t off = h * TILE * S::BOX_BYTES + row * S::BOX_BYTES;
             const int c0 = h * (S::BOX_BYTES / (E8 ? 1 : 2));
-            tma_load_4d(k_s + off, &map_k, &full[stage], c0, c1, c2, page[0]);
-            tma_load_4d(v_s + off, &map_v, &full[stage], c0, c1, c2, page[0]);
+            tma_load_4d(k_s + off, &map_k, &full[stage], c0, c1, c2, page[y]);
+            tma_load_4d(v_s + off, &map_v, &full[stage], c0, c1, c2, page[y]);
           }
         }
       } else {
-        // page sizes whose pages do not hold 8 rows of a tile: row by row, 16 bytes to a lane
+        // 8-bit heads of 64 in pages of odd size: a box would be one row of 64 bytes, half of TMA's
+        // 128-byte step in shared memory
         constexpr int CH = S::ROW_BYTES / 16;
         for (int x = lane; x < TILE * CH; x += 32) {
           const int row = x / CH, ch = x % CH;
@@ -1057,7 +1064,9 @@ cudaError_t launch_cache_attend(const AttendProblem& p, void* workspace, cudaStr
   while (c.page_size % s.box_rows) s.box_rows >>= 1;
   s.token_first = c.token_stride <= c.head_stride;
   CUtensorMap mk{}, mv{};
-  if (s.box_rows >= 8 && c.num_pages > 0) {
+  // a box starts on 128 bytes of shared memory
+  s.use_tma = s.box_rows * c.d * (c.dtype == KDA_E4M3 ? 1 : 2) >= 128;
+  if (s.use_tma && c.num_pages > 0) {
     if (!make_map(&mk, c, c.k, s.token_first, s.box_rows) || !make_map(&mv, c, c.v, s.token_first, s.box_rows))
       return cudaErrorInvalidValue;
   }
