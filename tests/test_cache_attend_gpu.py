@@ -217,3 +217,135 @@ def test_no_sequences_and_no_tokens():
     assert binding.kda_cache_attend(torch.empty((0, 1, 2, 64), dtype=BF, device="cuda"), cache).shape == (0, 1, 2, 64)
     cache, _, _ = make_cache([5], 0, 2, 64, 16, BF)
     assert binding.kda_cache_attend(torch.empty((1, 0, 2, 64), dtype=BF, device="cuda"), cache).shape == (1, 0, 2, 64)
+
+
+# More query rows to a key head than one row tile: 20, 32, 33, 40, 48, 49 and 100 of them.
+MANY = [(1, 20, 1), (4, 16, 2), (3, 11, 1), (5, 32, 4), (3, 16, 1), (7, 7, 1), (25, 4, 1)]
+
+
+@pytest.mark.parametrize("K,Hq,Hkv", MANY)
+@pytest.mark.parametrize("act,dtype", [(BF, BF), (FP, FP), (BF, E4), (FP, E4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows(K, Hq, Hkv, act, dtype, d):
+    check([0, 1, 63, 127, 128, 129, 700], K=K, Hq=Hq, Hkv=Hkv, d=d, act=act, dtype=dtype, page=32, seed=K,
+          k_scale=0.5 if dtype == E4 else 1.0, v_scale=0.25 if dtype == E4 else 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("window", [1, 5, 64, 129, 1000])
+def test_many_rows_windows_counts_and_layouts(window, dtype):
+    check([0, 30, 200, 511, 1000, 3], K=5, Hq=16, Hkv=2, window=window, counts=[5, 0, 3, 5, 1, 2], page=48,
+          layout="head", dtype=dtype, seed=window)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_many_rows_long_and_negative(dtype):
+    check([20000, -2, 5, 9000, 0, 33], K=4, Hq=10, Hkv=1, page=64, dtype=dtype, seed=3)
+    check([40000], K=5, Hq=32, Hkv=4, page=64, dtype=dtype, seed=4)
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_many_rows_scores_that_keep_growing(dtype):
+    """Keys that grow along the sequence: the running maximum is passed again and again."""
+    lens, K, Hq, d = [1000], 3, 12, 128
+    cache, keys, values = make_cache(lens, K, 1, d, 64, dtype)
+    grow = torch.linspace(0.05, 8.0, lens[0] + K)[:, None, None]
+    new = (keys[0].float() * grow).to(dtype).float()
+    for p in range(lens[0] + K):
+        cache.k_pages[int(cache.block_table[0, p // 64]), p % 64] = new[p].to(dtype).cuda()
+    q = (2 * torch.randn((1, K, Hq, d), generator=torch.Generator().manual_seed(2))).to(BF)
+    out, lse = binding.kda_cache_attend(q.cuda(), cache, return_lse=True)
+    ref, rlse, tol, ltol = attend_reference(q, [new.double()], values, lens, None, d ** -0.5, 0)
+    assert_within(lse, rlse, ltol, "lse")
+    assert_within(out, ref, tol, "out")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [70, 127, 128])
+@pytest.mark.parametrize("dtype", [BF, FP, E4])
+def test_many_rows_infinite_and_nan_in_a_later_draft(dtype, at, d):
+    """As above with 40 rows; positions before, at and after a tile's border."""
+    lens, K, Hq = [at - 1], 5, 8
+    act = FP if dtype == FP else BF
+    cache, keys, values = make_cache(lens, K, 1, d, 16, dtype)
+    pos = lens[0] + 1
+    page = int(cache.block_table[0, pos // 16])
+    q = torch.randn((1, K, Hq, d), generator=torch.Generator().manual_seed(4)).to(act)
+    for bad in (NAN, math.inf) if dtype != E4 else (NAN,):
+        cache.v_pages[page, pos % 16] = torch.full((1, d), bad).to(dtype).cuda()
+        cache.k_pages[page, pos % 16] = torch.zeros((1, d)).to(dtype).cuda()
+        out = binding.kda_cache_attend(q.cuda(), cache)
+        ref, _, tol, _ = attend_reference(q[:, :1], [keys[0][:lens[0] + 1]], [values[0][:lens[0] + 1]],
+                                          lens, None, d ** -0.5, 0)
+        assert_within(out[:, :1], ref, tol, "token 0")
+        assert not torch.isfinite(out[:, 1:].float()).any()
+
+
+def test_one_infinite_value_of_a_later_draft_reaches_its_channel_alone():
+    lens, K, Hq, d = [100], 4, 8, 128
+    cache, keys, values = make_cache(lens, K, 1, d, 16, BF)
+    pos = lens[0] + 2
+    cache.v_pages[int(cache.block_table[0, pos // 16]), pos % 16, 0, 77] = math.inf
+    values[0][pos, 0, 77] = 0  # the other channels' reference
+    q = torch.randn((1, K, Hq, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), cache)
+    ref, _, tol, _ = attend_reference(q, keys, values, lens, None, d ** -0.5, 0)
+    rest = [c for c in range(d) if c != 77]
+    assert_within(out[..., rest], ref[..., rest], tol[..., rest], "other channels")
+    assert (out[:, 2:, :, 77] == math.inf).all()
+    assert torch.isfinite(out[:, :2].float()).all()
+
+
+@pytest.mark.parametrize("rows", [4, 40])
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_pages_at_every_row_count(rows, dtype, d):
+    lens = [300]
+    cache, keys, values = make_cache(lens, 1, 1, d, 16, dtype)
+    binding.kda_last_device_status()
+    for j, bad in ((0, -1), (7, 10 ** 9), (15, cache.k_pages.shape[0])):
+        cache.block_table[0, j] = bad
+    q = torch.randn((1, 1, rows, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), cache)
+    torch.cuda.synchronize()
+    assert binding.kda_last_device_status() == 1
+    kept = [j for j in range(301) if j // 16 not in (0, 7, 15)]
+    ref, _, tol, _ = attend_reference(q, [keys[0][kept]], [values[0][kept]], [len(kept) - 1], None, d ** -0.5, 0)
+    assert_within(out, ref, tol, "out")
+
+
+@pytest.mark.parametrize("page", [1, 3, 5])
+@pytest.mark.parametrize("Hq", [4, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_odd_pages_of_an_8_bit_cache(page, Hq, d):
+    check([0, 62, 300], Hq=Hq, Hkv=1, d=d, page=page, dtype=E4, seed=page)
+
+
+@pytest.mark.parametrize("Hq", [4, 40])
+def test_strides_of_interleaved_keys_and_values(Hq):
+    """Keys and values as the two halves of one pool, pages [page, 2, token, head, d]."""
+    lens, d = [130, 7], 128
+    cache, keys, values = make_cache(lens, 1, 1, d, 16, BF)
+    pool = torch.stack([cache.k_pages, cache.v_pages], 1).contiguous()
+    both = binding.PagedCache(pool[:, 0], pool[:, 1], cache.block_table, cache.lens)
+    q = torch.randn((2, 1, Hq, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), both)
+    ref, _, tol, _ = attend_reference(q, keys, values, lens, None, d ** -0.5, 0)
+    assert_within(out, ref, tol, "out")
+
+
+def test_many_rows_repeat_and_follow_the_lengths_in_a_graph():
+    lens, K = [3000, 17, 600], 3
+    cache, keys, values = make_cache(lens, K, 2, 128, 16, BF)
+    q = torch.randn((3, K, 16, 128), generator=torch.Generator().manual_seed(8)).to(BF).cuda()
+    first = binding.kda_cache_attend(q, cache)
+    for _ in range(3):
+        assert torch.equal(first, binding.kda_cache_attend(q, cache))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = binding.kda_cache_attend(q, cache)
+    cache.lens.copy_(torch.tensor([1999, 16, 0], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    ref, _, tol, _ = attend_reference(q.cpu(), keys, values, [1999, 16, 0], None, 128 ** -0.5, 0)
+    assert_within(out, ref, tol, "replayed")
