@@ -353,9 +353,16 @@ bool aligned_rows(const void* p, long long stride, kda_dtype_t t) {
   return aligned16(p) && (stride * element_bytes(t)) % 16 == 0;
 }
 
+// The cache with the strides of dimensions that have one entry, which no offset contains, made plain.
+kda_paged_cache_t plain_strides(kda_paged_cache_t c) {
+  if (c.H_kv == 1) c.head_stride = c.d;
+  if (c.page_size == 1) c.token_stride = (long long)c.d * c.H_kv;
+  if (c.num_pages <= 1) c.page_stride = (long long)c.d * c.H_kv * c.page_size;
+  return c;
+}
+
 // What both cache calls ask of the cache and of the new tokens' type.
 kda_status_t validate_cache(const kda_paged_cache_t* c, kda_dtype_t dtype) {
-  if (!c) return KDA_ERR_INVALID_ARG;
   if (c->n_seq < 0 || c->num_pages < 0 || c->page_size <= 0 || c->table_width < 0 || c->H_kv <= 0 ||
       c->d <= 0 || c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0 ||
       c->table_stride < 0)
@@ -382,6 +389,9 @@ kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void* k, con
                               const double* inv_freq, int rot_dim, int interleaved,
                               const int* cu_seqlens, const int* counts, int K, int T, int H_q,
                               cudaStream_t stream) {
+  if (!cache) return KDA_ERR_INVALID_ARG;
+  const kda_paged_cache_t plain = plain_strides(*cache);
+  cache = &plain;
   kda_status_t st = validate_cache(cache, dtype);
   if (st != KDA_OK) return st;
   if (T < 0 || K < 0 || (!cu_seqlens && (long long)cache->n_seq * K != T)) return KDA_ERR_INVALID_ARG;
@@ -416,6 +426,9 @@ kda_status_t kda_cache_attend(const kda_paged_cache_t* cache, const void* q, kda
                               long long q_stride, void* out, float* lse, const int* counts, int K,
                               int H_q, float scale, int window, int max_len, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream) {
+  if (!cache) return KDA_ERR_INVALID_ARG;
+  const kda_paged_cache_t plain = plain_strides(*cache);
+  cache = &plain;
   kda_status_t st = validate_cache(cache, dtype);
   if (st != KDA_OK) return st;
   if (K < 0 || H_q <= 0 || H_q % cache->H_kv || window < 0 || max_len < 0 || q_stride < 0)

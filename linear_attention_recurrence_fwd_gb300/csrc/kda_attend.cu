@@ -5,18 +5,24 @@
 //
 // over the positions j that the token sees, in one pass: m and the two sums
 // are carried and rescaled when m grows.  The query rows of one key head (K
-// tokens times H_q / H_kv heads, in groups of up to 64) share one read of its
-// keys and values, so the call is bound by HBM: 4 flop per byte and row.
+// tokens times H_q / H_kv heads, in groups of up to 48) share one read of its
+// keys and values, so the call is bound by HBM: 2 flop per row and byte of a
+// 16-bit cache.
+//
+// This file: up to 16 rows, and more over an 8-bit cache.  17 to 48 rows over a
+// 16-bit cache are kda_attend_wide.cu; how the work is cut is kda_attend.cuh.
 //
 // Work.  A unit is (sequence, key head, row group); its positions are cut into
-// tiles of 64.  The tiles of all units, one after the other, are cut into
-// equal stretches, one for each CTA (two CTAs on every SM), whatever the
-// lengths are; a unit that ends up in several CTAs is joined from their
-// unnormalised parts by a second small kernel.  Where the caller's bound says
-// that units are short, each CTA takes whole units instead and nothing is
-// joined.
+// tiles of 64 or 128.  The tiles of all units, one after the other, are cut
+// into equal stretches, whatever the lengths are; a unit that ends up in
+// several CTAs is joined from their unnormalised parts by a second small
+// kernel.  Where units are short, each CTA takes whole units instead and
+// nothing is joined.  CTAs walk the heads of the same positions in teams of up
+// to 8, since a token's heads lie side by side: DRAM is then read in longer
+// runs (64 requests of 8192 positions, 8 key heads of 64: 195 us without
+// teams, 163 us with).
 //
-// A CTA is one producer warp and 4 or 8 consumer warps around a ring of stages
+// A CTA is one producer warp and 4 to 12 consumer warps around a ring of stages
 // (a tile's keys and values).  The producer looks up pages and issues TMA
 // boxes of the rows that lie in one page.  Each consumer warp takes 16 or 32
 // positions of every tile through scores, softmax and values by itself, with
@@ -26,7 +32,13 @@
 // tile; measured, 1.0 us for a tile of 64 positions against 0.74 us for its
 // share of the HBM bandwidth at two CTAs on an SM.)  The products are
 // warp-level tensor core instructions (m16n8k16): 16 rows are what one token
-// of most layouts fills, and tcgen05's 128 would be mostly padding.
+// of most layouts fills.
+//
+// Measured (32 query heads of 128): 256 requests of 7 to 8191 positions on 8
+// key heads 630 us, 6.8 TB/s, the copy bandwidth; one request of 2^20
+// positions, 16 heads on 2, 170 us (6.3 TB/s); 64 requests of 8192, 8 key heads,
+// 8-bit, 205 us (5.2 TB/s: converting 8-bit fragments is what bounds it), and
+// with 40 rows, 4 key heads, 277 us (2.0 TB/s: each of 3 row groups converts).
 #include <cstdint>
 
 #include "kda_internal.h"
@@ -39,7 +51,8 @@ namespace {
 
 constexpr int KW = 4;  // consumer warps that share a tile's positions
 
-// A CTA has WG row groups of 16 rows (1, 2 or 3), of KW consumer warps each.  A
+// A CTA has WG row groups of 16 rows (1; over an 8-bit cache 2 or 3 where there
+// are more rows), of KW consumer warps each.  A
 // warp's share of a tile is KT positions, 4 KB of keys and as much of values
 // (8-bit heads of 64: 2 KB).
 template <int D, bool E8, int WG> struct Shape {
@@ -628,8 +641,11 @@ Plan plan_for(int n_seq, int K, int H_q, int H_kv, int d, bool e8, int max_len) 
   if (sm_count(&sms) != cudaSuccess) return a;
   a.wide = !e8 && a.per > 16;
   const int resident = (a.per > 16 ? 1 : 2) * sms;
-  // up to 4 tiles (256 positions) a unit is read faster than its parts are joined
-  a.whole = max_len <= 4 * TILE;
+  // Short units are read faster by one CTA than they are joined, the more so where there are enough of
+  // them for all CTAs (8 key heads of 128; whole units against parts): 250 positions, 1 request 9.0
+  // against 10.5 us; 500, 1 request 12.2 against 10.3, 16 requests 12.8 against 14.4, 64 requests 29.2
+  // against 32.5; 1000, 16 requests 18.8 against 17.1, 64 requests 49.1 against 51.7.
+  a.whole = max_len <= 256 || (max_len <= 512 && 4 * a.units >= resident) || (max_len <= 1024 && a.units >= resident);
   const long long want = a.whole ? a.units : tiles;
   // Where a token's heads lie side by side, CTAs that read them at the same time read DRAM in longer
   // runs: teams of up to 8 heads.

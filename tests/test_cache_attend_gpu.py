@@ -349,3 +349,23 @@ def test_many_rows_repeat_and_follow_the_lengths_in_a_graph():
     torch.cuda.synchronize()
     ref, _, tol, _ = attend_reference(q.cpu(), keys, values, [1999, 16, 0], None, 128 ** -0.5, 0)
     assert_within(out, ref, tol, "replayed")
+
+
+@pytest.mark.parametrize("Hq", [4, 40])
+def test_pages_whose_rows_are_interleaved(Hq):
+    """Rows of all pages side by side ([row, page, head, d]), and one page with odd strides of its own."""
+    lens, d = [130, 7], 128
+    cache, keys, values = make_cache(lens, 1, 2, d, 16, BF)
+    q = torch.randn((2, 1, Hq, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    pools = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (cache.k_pages, cache.v_pages)]
+    assert pools[0].stride(0) < pools[0].stride(1)
+    out = binding.kda_cache_attend(q.cuda(), binding.PagedCache(*pools, cache.block_table, cache.lens))
+    ref, _, tol, _ = attend_reference(q, keys, values, lens, None, d ** -0.5, 0)
+    assert_within(out, ref, tol, "out")
+    # one page, one head: the strides of those dimensions say nothing
+    cache, keys, values = make_cache([9], 1, 1, d, 16, BF, spare=0)
+    pools = [x.as_strided((1, 16, 1, d), (3, d, 5, 1)) for x in (cache.k_pages, cache.v_pages)]
+    odd = binding.PagedCache(*pools, cache.block_table, cache.lens)
+    out = binding.kda_cache_attend(q[:1].cuda(), odd)
+    ref, _, tol, _ = attend_reference(q[:1], keys, values, [9], None, d ** -0.5, 0)
+    assert_within(out, ref, tol, "out")
