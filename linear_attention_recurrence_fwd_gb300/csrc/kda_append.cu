@@ -90,13 +90,44 @@ __device__ __forceinline__ void check_offsets(const AppendProblem& p) {
   if (bad) *p.status = 1;
 }
 
-// Eight channels to a row of the cache or of the queries: one rounding each.
-template <typename C> __device__ __forceinline__ void store8(C* dst, const float (&x)[8], float scale) {
-  C y[8];
+// Eight 16-bit channels as fp32, and back: one rounding each.
+template <typename T> __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = from_f32<C>(scale == 1.f ? x[e] : x[e] / scale);
-  if (sizeof(C) == 1) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
-  else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(y);
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (__is_same(T, __nv_bfloat16)) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  }
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (__is_same(T, __nv_bfloat16)) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+// to a row of the cache or of the queries, divided by `scale`
+template <typename C> __device__ __forceinline__ void store8(C* dst, float (&x)[8], float scale) {
+  if (scale != 1.f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] /= scale;
+  }
+  if constexpr (sizeof(C) == 1) {
+    C y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = from_f32<C>(x[e]);
+    *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(y);
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack2<C>(x[0], x[1]), pack2<C>(x[2], x[3]), pack2<C>(x[4], x[5]), pack2<C>(x[6], x[7]));
+  }
 }
 
 // jobs: of a head, the pieces that a thread takes: 8 pairs of channels (c and
@@ -123,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constan
   const int my_token = warp / PER, part = warp % PER, pair = part * 32 + lane;
   const long long step = pair < half ? turn_step(p.inv_freq[pair]) : 0;
 
-  uint4 a[AHEAD], b[AHEAD];
+  uint4 a[AHEAD] = {}, b[AHEAD] = {};
   int tt, h;  // the next piece to load
   auto advance = [&](int& t, int& x) {
     t += tt_step;
@@ -169,14 +200,18 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constan
       for (int x = 0; x < AHEAD; ++x) {
         if (ct >= TOKENS || t0 + ct >= p.T) break;
         const bool is_q = ch < p.H_q, is_k = !is_q && ch < p.H_q + p.cache.H_kv;
-        const T* u = reinterpret_cast<const T*>(&a[x]);
-        const T* v = reinterpret_cast<const T*>(&b[x]);
-        float lo[8], hi[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          lo[e] = to_f32(u[e]);
-          hi[e] = two ? to_f32(v[e]) : 0.f;
+        if (__is_same(T, C) && !is_q && !is_k && p.cache.v_scale == 1.f) {  // values as they are
+          if (s_row[buf][ct] >= 0) {
+            T* dst = static_cast<T*>(p.cache.v) + s_row[buf][ct] + (ch - p.H_q - p.cache.H_kv) * p.cache.head_stride + at;
+            *reinterpret_cast<uint4*>(dst) = a[x];
+            if (two) *reinterpret_cast<uint4*>(dst + half) = b[x];
+          }
+          advance(ct, ch);
+          continue;
         }
+        float lo[8], hi[8];
+        unpack8<T>(a[x], lo);
+        unpack8<T>(b[x], hi);  // (read only where `two`)
         if (is_q || is_k) {
           if (two) {
             const float4* cs = reinterpret_cast<const float4*>(&s_turn[buf][ct][8 * j]);
