@@ -639,7 +639,7 @@ Plan plan_for(int n_seq, int K, int H_q, int H_kv, int d, bool e8, int max_len) 
   const long long tiles = a.units * ((max_len + TILE - 1) / TILE > 1 ? (max_len + TILE - 1) / TILE : 1);
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) return a;
-  a.wide = !e8 && a.per > 16;
+  a.wide = a.per > 16;
   const int resident = (a.per > 16 ? 1 : 2) * sms;
   // Short units are read faster by one CTA than they are joined, the more so where there are enough of
   // them for all CTAs (8 key heads of 128; whole units against parts): 250 positions, 1 request 9.0

@@ -29,20 +29,46 @@ namespace {
 constexpr int TILE = 128;
 constexpr float UNSEEN = 3e38f;  // takes any score of a row without a maximum past the limit
 
-template <int D> struct Wide {
+// E8: an 8-bit cache.  QP and WP: the 8-bit pieces that a query and a weight are written as.
+template <typename A, int D, bool E8> struct Wide {
   static constexpr int THREADS = 192;
-  static constexpr int KV_BYTES = TILE * D * 2;          // keys or values of a stage
+  static constexpr int ES = E8 ? 1 : 2;                  // bytes of a cached element
+  static constexpr int QP = E8 ? (__is_same(A, __nv_bfloat16) ? 2 : 3) : 1, WP = E8 ? QP + 1 : 1;
+  static constexpr int ROW_BYTES = D * ES;
+  static constexpr int KV_BYTES = TILE * ROW_BYTES;      // keys or values of a stage
   static constexpr int STAGE_BYTES = 2 * KV_BYTES;
-  static constexpr int Q_BYTES = 48 * D * 2, P_BYTES = 48 * TILE * 2;
-  static constexpr int MISC_BYTES = 5120;
+  static constexpr int Q_BYTES = 48 * D * QP * ES, P_BYTES = 48 * TILE * WP * ES;
+  static constexpr int MISC_BYTES = 5632;
   static constexpr int FIT = (224 * 1024 - Q_BYTES - P_BYTES - MISC_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int SMEM = STAGES * STAGE_BYTES + Q_BYTES + P_BYTES + MISC_BYTES + 1024;
+  // Columns of tensor memory: two tiles' scores, then the output
+  static constexpr uint32_t T_S = 0, S_COLS = E8 ? QP * 48 : 64, T_O = 2 * S_COLS, T_COLS = E8 ? 512 : 256;
+  // Weights are 2^(f s - m + BIAS) and reach 2^(BIAS + SLACK) before the maximum is moved.
+  static constexpr float BIAS = E8 ? 12.f : 0.f, SLACK = E8 ? 3.f : 8.f;
 };
 
-// Columns of tensor memory
-constexpr uint32_t T_S = 0, T_O = 128, T_COLS = 256;
+// kind::f8f6f4 with 8-bit operands, each e4m3 or e5m2, and an fp32 accumulator; K = 32 per MMA.
+enum F8 : uint32_t { F8_E4M3 = 0, F8_E5M2 = 1 };
+__host__ __device__ constexpr uint32_t make_idesc_f8(int M, int N, bool a_mn_major, bool b_mn_major, F8 a, F8 b) {
+  return (1u << 4) | ((uint32_t)a << 7) | ((uint32_t)b << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+         ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_u16(uint32_t at, uint32_t v) {
   asm volatile("{.reg .b16 l, h; mov.b32 {l, h}, %1; st.shared.b16 [%0], l;}" ::"r"(at), "r"(v) : "memory");
 }
@@ -64,12 +90,13 @@ template <typename Op> __device__ __forceinline__ float across(float (&v)[16], O
 }
 
 // NC: rows of a unit, in sixteens
-template <typename A, int D, int NC>
-__global__ void __launch_bounds__(Wide<D>::THREADS, 1)
+template <typename A, int D, int NC, bool E8>
+__global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
     attend_wide_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const __grid_constant__ Params s) {
-  using W = Wide<D>;
-  constexpr int STAGES = W::STAGES;
+  using W = Wide<A, D, E8>;
+  constexpr int STAGES = W::STAGES, QP = W::QP, WP = W::WP;
+  constexpr uint32_t T_S = W::T_S, T_O = W::T_O;
   constexpr bool BF = __is_same(A, __nv_bfloat16);
   extern __shared__ uint8_t smem_raw[];
   const AttendProblem& p = s.p;
@@ -79,8 +106,9 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   uint8_t* misc = aligned + STAGES * W::STAGE_BYTES + W::Q_BYTES + W::P_BYTES;
   // tables of the unit's rows, for two units in turn
   float* row_m = reinterpret_cast<float*>(misc);    // [2][48] maximum (of scores in log2 units)
-  float* row_neg = row_m + 96;                      // [2][48] minus the maximum; UNSEEN while nothing is seen
-  int* row_tok = reinterpret_cast<int*>(row_neg + 96);  // [2][48] the row's token
+  float* row_neg = row_m + 96;                      // [2][48] BIAS minus the maximum; UNSEEN while nothing is seen
+  float* row_f = row_neg + 96;                      // [2][48] what its scores are multiplied with (8-bit)
+  int* row_tok = reinterpret_cast<int*>(row_f + 96);  // [2][48] the row's token
   float* warp_top = reinterpret_cast<float*>(row_tok + 96);  // [4][48]
   float* warp_sum = warp_top + 192;                 // [4][48]
   float* keep = warp_sum + 192;                     // [48] what O and the sums are rescaled with; 1 / sum at the end
@@ -123,7 +151,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   const Stretch st = find_stretch<TILE, W::THREADS>(s);
   if (st.left == 0) return;
   if (warp == 5) {
-    tmem_alloc(&s_tmem, T_COLS);
+    tmem_alloc(&s_tmem, W::T_COLS);
     tmem_relinquish();
   }
   tc_fence_before_sync();
@@ -172,7 +200,53 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     for (int x = 0; x < 8; ++x)
       at_p[x] = p_s + (tid >> 6) * (N * 128) + ((((tid & 63) >> 3) ^ x) << 4) + (tid & 7) * 2;
 
-    // A unit's rows' tables, then its queries as they are.
+    // Eight channels of a query in 8-bit pieces: the row is scaled by a power of two that brings its
+    // largest entry to [2^7, 2^8), a piece has 4 bits of an entry, and the next one 2^4 times what is
+    // left.  The 8 bits of a bf16 entry (11 of an fp16 one) fit exactly, down to 2^-14 of the largest
+    // (2^-18); what is below is off by 2^-21 of it (2^-25) at most.  Infinities become NaN.
+    auto write_pieces = [&](const uint4& v, int row, int ch, int odd) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float x[8], big = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (BF) {
+          x[2 * e] = __uint_as_float(w[e] << 16);
+          x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        } else {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+          x[2 * e] = y.x;
+          x[2 * e + 1] = y.y;
+        }
+        big = fmaxf(big, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+      }
+#pragma unroll
+      for (int o = 1; o < D / 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      const int power = min(max(134 - (int)(__float_as_uint(big) >> 23), -120), 120);
+      const float by = __uint_as_float((uint32_t)(127 + power) << 23);
+      if (ch == 0) row_f[odd * 48 + row] = p.scale * p.cache.k_scale * 1.44269504088896340736f * __uint_as_float((uint32_t)(127 - power) << 23);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fabsf(x[e]) < INFINITY ? x[e] * by : __uint_as_float(0x7fffffffu);
+#pragma unroll
+      for (int pc = 0; pc < QP; ++pc) {
+        uint32_t out[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          asm("{.reg .b16 l, h; cvt.rn.satfinite.e4m3x2.f32 l, %2, %1; cvt.rn.satfinite.e4m3x2.f32 h, %4, %3; mov.b32 %0, {l, h};}"
+              : "=r"(out[e]) : "f"(x[4 * e]), "f"(x[4 * e + 1]), "f"(x[4 * e + 2]), "f"(x[4 * e + 3]));
+          uint32_t lo, hi;
+          e4m3x4_to_f16(out[e], lo, hi);
+          const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo)), b = __half22float2(*reinterpret_cast<__half2*>(&hi));
+          x[4 * e] = (x[4 * e] - a.x) * 16.f;
+          x[4 * e + 1] = (x[4 * e + 1] - a.y) * 16.f;
+          x[4 * e + 2] = (x[4 * e + 2] - b.x) * 16.f;
+          x[4 * e + 3] = (x[4 * e + 3] - b.y) * 16.f;
+        }
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_s + pc * (N * D) + kv_offset<D, TILE>(row, ch >> 1) + (ch & 1) * 8),
+                     "r"(out[0]), "r"(out[1]) : "memory");
+      }
+    };
+
+    // A unit's rows' tables, then its queries: as they are, or in pieces.
     auto load_queries = [&](int stage, int turn, int odd) {
       if (!wait(&told[stage], turn)) return false;
       const Meta& t = meta[stage];
@@ -194,6 +268,15 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         const long long from = row_from[(tid + z * 128) / (D / 8)];
         q[z] = from < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(static_cast<const A*>(p.q) + from + ch * 8);
       }
+      if constexpr (E8) {
+#pragma unroll 1
+        for (int z = 0; z < EACH; ++z) {
+          const int row = (tid + z * 128) / (D / 8);
+          write_pieces(q[0], row, ch, odd);
+#pragma unroll
+          for (int y = 0; y + 1 < EACH; ++y) q[y] = q[y + 1];
+        }
+      } else
 #pragma unroll
       for (int z = 0; z < EACH; ++z) {
         const int row = (tid + z * 128) / (D / 8);
@@ -216,9 +299,9 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       const uint32_t flags = t.flags;
       const bool first = flags & FIRST, all = flags & FULL;
       const float f = p.scale * p.cache.k_scale * 1.44269504088896340736f;
-      const float* neg = row_neg + odd * 48;
+      const float *neg = row_neg + odd * 48, *fs = row_f + odd * 48;
       const int* tok = row_tok + odd * 48;
-      const uint32_t scores = my_lane + T_S + (it & 1) * 64;
+      const uint32_t scores = my_lane + T_S + (it & 1) * W::S_COLS;
       int at = 0;
       bool exists = true;
       if (!all) {
@@ -236,21 +319,22 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         if (!wait(&full[stage], turn)) return false;
         const bool seen = any_sees(t, at);
         if (!seen) {
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            for (int x = 0; x < 8; ++x) st_shared_v4(v_s + h * (TILE * 128) + tid * 128 + ((x ^ (tid & 7)) << 4), 0, 0, 0, 0);
+          for (int x = 0; x < W::ROW_BYTES / 16; ++x) st_shared_v4(v_s + kv_offset<W::ROW_BYTES, TILE>(tid, x), 0, 0, 0, 0);
         }
         bool none = false;
         const int i0 = t.row0 / s.group_heads, i1 = (min(t.row0 + N, s.rows) - 1) / s.group_heads;
         if (seen && i0 != i1 && !(i1 < t.count && at <= last_seen(t, i0) && at >= first_seen(t, i1))) {
           constexpr uint32_t EXP = BF ? 0x7f80u : 0x7c00u;  // of an infinite or NaN value
 #pragma unroll
-          for (int x = 0; x < D / 8; ++x) {
+          for (int x = 0; x < W::ROW_BYTES / 16; ++x) {
             uint32_t v[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(v_s + (x >> 3) * (TILE * 128) + tid * 128 + (((x & 7) ^ (tid & 7)) << 4)) : "memory");
+                         : "r"(v_s + kv_offset<W::ROW_BYTES, TILE>(tid, x)) : "memory");
 #pragma unroll
-            for (int y = 0; y < 4; ++y) none |= (v[y] & EXP) == EXP || (v[y] & (EXP << 16)) == EXP << 16;
+            for (int y = 0; y < 4; ++y) {
+              if (E8) none |= (((v[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;  // 0x7f: NaN
+              else none |= (v[y] & EXP) == EXP || (v[y] & (EXP << 16)) == EXP << 16;
+            }
           }
         }
         if (tid < N) {
@@ -263,14 +347,22 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       }
       // ---- whether a score passes its row's maximum
       float v[NC][16];
+      auto join_pieces = [](float (&a)[16], const float (&more)[QP][16]) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          if (QP == 2) a[x] = fmaf(more[1][x], 0.0625f, a[x]);
+          if (QP == 3) a[x] = fmaf(fmaf(more[QP - 1][x], 0.0625f, more[QP > 1 ? 1 : 0][x]), 0.0625f, a[x]);
+        }
+      };
       auto scale = [&]() {  // f s - m; -infinity where not seen
 #pragma unroll
         for (int y = 0; y < NC; ++y) {
 #pragma unroll
           for (int x = 0; x < 16; x += 4) {
             const float4 nn = *reinterpret_cast<const float4*>(neg + y * 16 + x);
-            v[y][x] = fmaf(v[y][x], f, nn.x), v[y][x + 1] = fmaf(v[y][x + 1], f, nn.y);
-            v[y][x + 2] = fmaf(v[y][x + 2], f, nn.z), v[y][x + 3] = fmaf(v[y][x + 3], f, nn.w);
+            const float4 ff = E8 ? *reinterpret_cast<const float4*>(fs + y * 16 + x) : make_float4(f, f, f, f);
+            v[y][x] = fmaf(v[y][x], ff.x, nn.x), v[y][x + 1] = fmaf(v[y][x + 1], ff.y, nn.y);
+            v[y][x + 2] = fmaf(v[y][x + 2], ff.z, nn.z), v[y][x + 3] = fmaf(v[y][x + 3], ff.w, nn.w);
           }
           if (!all) {
 #pragma unroll
@@ -293,12 +385,15 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
           tc_fence_after_sync();
 #pragma unroll 1
           for (int y = 0; y < NC; ++y) {
-            float w[16];
+            float w[16], more[QP][16];
             tmem_ld16(scores + y * 16, w);
+#pragma unroll
+            for (int z = 1; z < QP; ++z) tmem_ld16(scores + z * N + y * 16, more[z]);
             tmem_ld_wait();
+            join_pieces(w, more);
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
-              w[x] *= f;
+              w[x] *= E8 ? fs[y * 16 + x] : f;
               if (!all) w[x] = sees(y * 16 + x) ? w[x] : -INFINITY;
             }
             const float top = across(w, [](float a, float b) { return fmaxf(a, b); });
@@ -310,7 +405,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
             const float now = fmaxf(fmaxf(fmaxf(warp_top[tid], warp_top[48 + tid]), fmaxf(warp_top[96 + tid], warp_top[144 + tid])), old);
             keep[tid] = now == -INFINITY || old == -INFINITY ? 1.f : exp2_fast(old - now);
             row_m[odd * 48 + tid] = now;
-            row_neg[odd * 48 + tid] = now == -INFINITY ? UNSEEN : -now;
+            row_neg[odd * 48 + tid] = now == -INFINITY ? UNSEEN : W::BIAS - now;
           }
           if (!sync()) return false;
           if (!first) {
@@ -319,21 +414,39 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 #pragma unroll
               for (int x = 0; x < 16; ++x) sums[y][x] *= keep[y * 16 + x];
 #pragma unroll 1
-            for (int y = 0; y < NC; ++y) {
+            for (int y = 0; y < NC * WP; ++y) {
               float a[16];
               tmem_ld16(my_lane + T_O + y * 16, a);
               tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) a[x] *= keep[y * 16 + x];
+              for (int x = 0; x < 16; ++x) a[x] *= keep[(y % NC) * 16 + x];
               tmem_st16(my_lane + T_O + y * 16, a);
             }
             tmem_st_wait();
           }
           done = true;
         }
+        if (QP < 3) {
+          float more[NC][QP][16];
 #pragma unroll
-        for (int y = 0; y < NC; ++y) tmem_ld16(scores + y * 16, v[y]);
-        tmem_ld_wait();
+          for (int y = 0; y < NC; ++y) {
+            tmem_ld16(scores + y * 16, v[y]);
+            if (QP == 2) tmem_ld16(scores + N + y * 16, more[y][QP - 1]);
+          }
+          tmem_ld_wait();
+#pragma unroll
+          for (int y = 0; y < NC; ++y) join_pieces(v[y], more[y]);
+        } else {
+#pragma unroll
+          for (int y = 0; y < NC; ++y) {
+            float more[QP][16];
+            tmem_ld16(scores + y * 16, v[y]);
+#pragma unroll
+            for (int z = 1; z < QP; ++z) tmem_ld16(scores + z * N + y * 16, more[z]);
+            tmem_ld_wait();
+            join_pieces(v[y], more);
+          }
+        }
         scale();
         if (done) break;
         float top = -INFINITY;
@@ -341,46 +454,100 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         for (int y = 0; y < NC; ++y)
 #pragma unroll
           for (int x = 0; x < 16; ++x) top = fmaxf(top, v[y][x]);
-        if (!vote(top > 8.f, raise)) return false;
+        if (!vote(top > W::BIAS + W::SLACK, raise)) return false;
         if (!raise) break;
       }
       // the previous weights have been read, and O is complete up to the previous tile
       if (it > 0 && !done && !wait(p_empty, (it - 1) & 1)) return false;
       tc_fence_after_sync();
 
-      // ---- weights 2^(f s - m), in 16 bits for the product (half a step of the type each); their sums
-      // are fp32
+      // ---- weights 2^(f s - m): in 16 bits for the product (half a step of the type each), or in
+      // pieces of 8; their sums are fp32.  A piece is the upper byte of an fp16 number, an e5m2 number of
+      // 3 bits: what it leaves is exact.  Three pieces hold 9 bits of a weight (the last is rounded),
+      // four the 11 of fp16.
 #pragma unroll
-      for (int y = 0; y < NC; ++y)
+      for (int y = 0; y < NC; ++y) {
+        if constexpr (E8) {
+          uint32_t pieces[WP][4];
 #pragma unroll
-        for (int x = 0; x < 16; x += 2) {
-          const float a = exp2_fast(v[y][x]), b = exp2_fast(v[y][x + 1]);
-          sums[y][x] += a;
-          sums[y][x + 1] += b;
-          const uint32_t w = BF ? pack_bf16x2(a, b) : pack_f16x2(a, b);
-          st_u16(at_p[x & 7] + (y * 16 + x) * 128, w);
-          st_u16(at_p[(x + 1) & 7] + (y * 16 + x + 1) * 128, w >> 16);
+          for (int x = 0; x < 16; x += 4) {
+            float a[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              a[z] = exp2_fast(v[y][x + z]);
+              sums[y][x + z] += a[z];
+            }
+            uint32_t lo = pack_f16x2(a[0], a[1]), hi = pack_f16x2(a[2], a[3]);
+#pragma unroll
+            for (int z = 0; z < WP; ++z) {
+              if (z == WP - 1) lo += 0x00800080u, hi += 0x00800080u;
+              pieces[z][x / 4] = __byte_perm(lo, hi, 0x7531);
+              if (z < WP - 1) {
+                const uint32_t tl = lo & 0xff00ff00u, th = hi & 0xff00ff00u;
+                const __half2 rl = __hsub2(*reinterpret_cast<const __half2*>(&lo), *reinterpret_cast<const __half2*>(&tl));
+                const __half2 rh = __hsub2(*reinterpret_cast<const __half2*>(&hi), *reinterpret_cast<const __half2*>(&th));
+                lo = *reinterpret_cast<const uint32_t*>(&rl);
+                hi = *reinterpret_cast<const uint32_t*>(&rh);
+              }
+            }
+          }
+#pragma unroll
+          for (int z = 0; z < WP; ++z)
+            st_shared_v4(p_s + (z * NC + y) * (TILE * 16) + tid * 16, pieces[z][0], pieces[z][1], pieces[z][2], pieces[z][3]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 16; x += 2) {
+            const float a = exp2_fast(v[y][x]), b = exp2_fast(v[y][x + 1]);
+            sums[y][x] += a;
+            sums[y][x + 1] += b;
+            const uint32_t w = BF ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+            st_u16(at_p[x & 7] + (y * 16 + x) * 128, w);
+            st_u16(at_p[(x + 1) & 7] + (y * 16 + x + 1) * 128, w >> 16);
+          }
         }
+      }
       if (by_hand) {
         // O^T += V^T P^T over the rows that see a position, one channel to a thread
         if (!sync()) return false;
         const int d = D == 128 ? tid : warp * 16 + (lane & 15);
-        const uint32_t v_at = values_of(stage) + (d >> 6) * (TILE * 128) + (d & 7) * 2;
-        for (int c0 = 0; c0 < N; c0 += 16) {
+        const uint32_t v_s = values_of(stage);
+        auto value_of = [&](int y) -> float {
+          const uint32_t v_at = v_s + kv_offset<W::ROW_BYTES, TILE>(y, d * W::ES / 16) + d * W::ES % 16;
+          if (E8) {
+            uint32_t lo, hi;
+            e4m3x4_to_f16(ld_shared_u8(v_at), lo, hi);
+            return __half2float(__ushort_as_half((unsigned short)lo));
+          }
+          const uint16_t v = ld_shared_u16(v_at);
+          return BF ? to_f32(__ushort_as_bfloat16(v)) : to_f32(__ushort_as_half(v));
+        };
+        auto weight_of = [&](int row, int y) -> float {
+          if (E8) {
+            float sum = 0.f;
+            for (int z = WP - 1; z >= 0; --z)
+              sum += __half2float(__ushort_as_half((unsigned short)(ld_shared_u8(p_s + (z * NC + row / 16) * (TILE * 16) + y * 16 + row % 16) << 8)));
+            return sum;
+          }
+          const uint16_t w = ld_shared_u16(p_s + (y >> 6) * (N * 128) + row * 128 + ((((y & 63) >> 3) ^ (row & 7)) << 4) + (y & 7) * 2);
+          return BF ? to_f32(__ushort_as_bfloat16(w)) : to_f32(__ushort_as_half(w));
+        };
+        for (int c0 = 0; c0 < N * WP; c0 += 16) {
           float o[16];
+          if (c0 >= N) {  // the other pieces' sums
+            if (!first) break;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] = 0.f;
+            tmem_st16(my_lane + T_O + c0, o);
+            continue;
+          }
           tmem_ld16(my_lane + T_O + c0, o);
           tmem_ld_wait();
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             float sum = first ? 0.f : o[x];
             const int hi = row_hi[c0 + x], lo = row_lo[c0 + x];
-            for (int y = max(0, lo - t.pos0); y < TILE && t.pos0 + y <= hi; ++y) {
-              if (!((t.valid[y >> 5] >> (y & 31)) & 1)) continue;
-              const uint16_t v = ld_shared_u16(v_at + y * 128 + ((((d & 63) >> 3) ^ (y & 7)) << 4));
-              const uint16_t w = ld_shared_u16(p_s + (y >> 6) * (N * 128) + (c0 + x) * 128 + ((((y & 63) >> 3) ^ (x & 7)) << 4) + (y & 7) * 2);
-              sum += BF ? to_f32(__ushort_as_bfloat16(v)) * to_f32(__ushort_as_bfloat16(w))
-                        : to_f32(__ushort_as_half(v)) * to_f32(__ushort_as_half(w));
-            }
+            for (int y = max(0, lo - t.pos0); y < TILE && t.pos0 + y <= hi; ++y)
+              if ((t.valid[y >> 5] >> (y & 31)) & 1) sum += value_of(y) * weight_of(c0 + x, y);
             o[x] = sum;
           }
           tmem_st16(my_lane + T_O + c0, o);
@@ -414,7 +581,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         const long long slot = 2LL * c + ((flags & OPENS) ? 1 : 0);
         const int unit_rows = min(N, s.rows - t_row0);
         if (tid < unit_rows) {
-          const float m = row_m[rows + tid];
+          const float m = row_m[rows + tid] - W::BIAS;
           const float sum = (warp_sum[tid] + warp_sum[48 + tid]) + (warp_sum[96 + tid] + warp_sum[144 + tid]);
           const bool none = m == -INFINITY;
           const int i = tok[tid], gh = t_row0 + tid - i * s.group_heads;
@@ -431,9 +598,15 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
         const int d = D == 128 ? tid : warp * 16 + (lane & 15);
 #pragma unroll 1
         for (int y = 0; y < NC; ++y) {
-          float o[16];
+          float o[16], more[WP][16];
           tmem_ld16(my_lane + T_O + y * 16, o);
+#pragma unroll
+          for (int z = 1; z < WP; ++z) tmem_ld16(my_lane + T_O + z * N + y * 16, more[z]);
           tmem_ld_wait();
+#pragma unroll
+          for (int z = 1; z < WP; ++z)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o[x] += more[z][x];
           const int have = mine ? unit_rows - y * 16 : 0;
           if (whole_unit) {
 #pragma unroll
@@ -457,11 +630,17 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
 
   // ---------------------------------------------------------------- products, issued by one thread
   auto issue = [&]() -> bool {
-    constexpr uint32_t id_s = make_idesc(128, N, false, false, false, !BF), id_o = make_idesc(D, N, true, false, false, !BF);
-    // operands' descriptors; a step of 16 along a product adds a constant (in units of 16 bytes)
-    const uint64_t dq = make_sdesc(q_s, 16, 1024, SW_128), dp = make_sdesc(p_s, 16, 1024, SW_128);
-    const uint64_t dk = make_sdesc(base, 16, 1024, SW_128);
-    const uint64_t dv = make_sdesc(base + W::KV_BYTES, TILE * 128, 1024, SW_128);
+    constexpr uint32_t id_s = E8 ? make_idesc_f8(128, N * QP, false, false, F8_E4M3, F8_E4M3) : make_idesc(128, N, false, false, false, !BF);
+    constexpr uint32_t id_o = E8 ? make_idesc_f8(D, N * WP, true, true, F8_E4M3, F8_E5M2) : make_idesc(D, N, true, false, false, !BF);
+    // Operands' descriptors; 32 bytes of a product's depth are a step.  Keys, queries and values lie in
+    // swizzled rows; the weights of an 8-bit cache in atoms of 8 positions by 16 rows.
+    constexpr uint32_t SW = W::ROW_BYTES < 128 ? SW_64 : SW_128, EIGHT = W::ROW_BYTES < 128 ? 512 : 1024;
+    const uint64_t dq = make_sdesc(q_s, 16, EIGHT, SW), dk = make_sdesc(base, 16, EIGHT, SW);
+    const uint64_t dv = make_sdesc(base + W::KV_BYTES, TILE * 128, EIGHT, SW);
+    const uint64_t dp = E8 ? make_sdesc(p_s, 128, TILE * 16, SW_NONE) : make_sdesc(p_s, 16, 1024, SW_128);
+    auto product = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+      if (E8) umma_f8(d, a, b, id, add); else umma_bf16(d, a, b, id, add);
+    };
     int units = 0;
     auto values = [&](int it, int stage, uint32_t flags) {
       if (!mbar_wait(p_full, it & 1)) return false;
@@ -469,8 +648,9 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
       if (*reinterpret_cast<volatile int*>(&mark[it & 1]) != it) {  // else it was done by hand
         const uint64_t a = dv + stage * (W::STAGE_BYTES >> 4);
 #pragma unroll
-        for (int ks = 0; ks < TILE / 16; ++ks)
-          umma_bf16(tmem + T_O, a + ks * 128, dp + ((ks >> 2) * (N * 128) + (ks & 3) * 32) / 16, id_o, ks > 0 || !(flags & FIRST));
+        for (int ks = 0; ks < TILE * W::ES / 32; ++ks)
+          product(tmem + T_O, a + ks * (E8 ? 2 * D : 128), dp + (E8 ? ks * 32 : ((ks >> 2) * (N * 128) + (ks & 3) * 32) / 16), id_o,
+                  ks > 0 || !(flags & FIRST));
       }
       umma_commit(p_empty);
       umma_commit(&empty[stage]);
@@ -480,14 +660,15 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
     uint32_t before_flags = 0;
     for (int it = 0, stage = 0, turn = 0;; ++it) {
       if (!mbar_wait(&full[stage], turn)) return false;
+      if (E8 && !s.use_tma) fence_proxy_async_smem();  // (the producer's own copies)
       const uint32_t flags = meta[stage].flags;
       if ((flags & FIRST) && !mbar_wait(q_full, units++ & 1)) return false;
       if (it >= 2 && !mbar_wait(&s_empty[it & 1], ((it >> 1) - 1) & 1)) return false;
       tc_fence_after_sync();
       const uint64_t a = dk + stage * (W::STAGE_BYTES >> 4);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        umma_bf16(tmem + T_S + (it & 1) * 64, a + ((ks >> 2) * (TILE * 128) + (ks & 3) * 32) / 16,
+      for (int ks = 0; ks < W::ROW_BYTES / 32; ++ks)
+        product(tmem + T_S + (it & 1) * W::S_COLS, a + ((ks >> 2) * (TILE * 128) + (ks & 3) * 32) / 16,
                   dq + ((ks >> 2) * (N * 128) + (ks & 3) * 32) / 16, id_s, ks > 0);
       umma_commit(&s_full[it & 1]);
       umma_commit(&empty[stage]);
@@ -503,7 +684,7 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   if (warp < 4) {
     ok = softmax();
   } else if (warp == 4) {
-    produce<D, false, TILE, STAGES>(s, st, Ring{base, full, empty, told, meta}, map_k, map_v);
+    produce<D, E8, TILE, STAGES>(s, st, Ring{base, full, empty, told, meta}, map_k, map_v);
   } else {
     if (lane == 0) ok = issue();
     __syncwarp();
@@ -513,24 +694,30 @@ __global__ void __launch_bounds__(Wide<D>::THREADS, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 5) tmem_dealloc(tmem, T_COLS);
+  if (warp == 5) tmem_dealloc(tmem, W::T_COLS);
 }
 
-template <typename A, int D, int NC>
-cudaError_t launch_rows(const Params& s, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t stream) {
-  using W = Wide<D>;
-  auto kernel = attend_wide_kernel<A, D, NC>;
+template <typename A, int D, int NC, bool E8>
+cudaError_t launch_shape(const Params& s, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t stream) {
+  using W = Wide<A, D, E8>;
+  auto kernel = attend_wide_kernel<A, D, NC, E8>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::SMEM);
   if (e != cudaSuccess) return e;
   kernel<<<grid, W::THREADS, W::SMEM, stream>>>(mk, mv, s);
   return cudaGetLastError();
 }
 
+template <typename A, int D, bool E8>
+cudaError_t launch_rows(const Params& s, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t stream) {
+  return s.rows_per == 32 ? launch_shape<A, D, 2, E8>(s, mk, mv, grid, stream) : launch_shape<A, D, 3, E8>(s, mk, mv, grid, stream);
+}
+
 template <typename A>
 cudaError_t launch_typed(const Params& s, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t stream) {
+  const bool e8 = s.p.cache.dtype == KDA_E4M3;
   if (s.p.cache.d == 128)
-    return s.rows_per == 32 ? launch_rows<A, 128, 2>(s, mk, mv, grid, stream) : launch_rows<A, 128, 3>(s, mk, mv, grid, stream);
-  return s.rows_per == 32 ? launch_rows<A, 64, 2>(s, mk, mv, grid, stream) : launch_rows<A, 64, 3>(s, mk, mv, grid, stream);
+    return e8 ? launch_rows<A, 128, true>(s, mk, mv, grid, stream) : launch_rows<A, 128, false>(s, mk, mv, grid, stream);
+  return e8 ? launch_rows<A, 64, true>(s, mk, mv, grid, stream) : launch_rows<A, 64, false>(s, mk, mv, grid, stream);
 }
 
 }  // namespace
