@@ -20,7 +20,7 @@
 // keys and values would have to be converted through shared memory, whose
 // bandwidth the products' operands take already (295 us against 278 us).
 //
-// Warps: 0-3 softmax, 4 producer, 5 issues the products.  One CTA on an SM.
+// Warps: 0-7 softmax (a thread has half of the rows), 8 producer, 9 issues the products.  One CTA on an SM.
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -31,7 +31,7 @@ constexpr float UNSEEN = 3e38f;  // takes any score of a row without a maximum p
 
 // E8: an 8-bit cache.  QP and WP: the 8-bit pieces that a query and a weight are written as.
 template <typename A, int D, bool E8> struct Wide {
-  static constexpr int THREADS = 192;
+  static constexpr int THREADS = 320;
   static constexpr int ES = E8 ? 1 : 2;                  // bytes of a cached element
   static constexpr int QP = E8 ? (__is_same(A, __nv_bfloat16) ? 2 : 3) : 1, WP = E8 ? QP + 1 : 1;
   static constexpr int ROW_BYTES = D * ES;
@@ -73,20 +73,35 @@ __device__ __forceinline__ void st_u16(uint32_t at, uint32_t v) {
   asm volatile("{.reg .b16 l, h; mov.b32 {l, h}, %1; st.shared.b16 [%0], l;}" ::"r"(at), "r"(v) : "memory");
 }
 
-// op over the warp's lanes of each of 16 values, by halves: 16 exchanges.  Lane l gets value l >> 1;
+// 8 consecutive columns: thread i of the warp gets lane (base lane + i).
+__device__ __forceinline__ void tmem_ld8(uint32_t at, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(at));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const float (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(__float_as_uint(v[0])),
+               "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])),
+               "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])) : "memory");
+}
+
+// op over the warp's lanes of each of 8 values, by halves: 9 exchanges.  Lane l gets value l >> 2;
 // the values are lost.
-template <typename Op> __device__ __forceinline__ float across(float (&v)[16], Op op) {
+template <typename Op> __device__ __forceinline__ float across(float (&v)[8], Op op) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int half = 8; half > 0; half >>= 1) {
-    const bool upper = lane & (2 * half);
+  for (int half = 4; half > 0; half >>= 1) {
+    const bool upper = lane & (4 * half);
 #pragma unroll
     for (int x = 0; x < half; ++x) {
       const float give = upper ? v[x] : v[x + half], take = upper ? v[x + half] : v[x];
-      v[x] = op(take, __shfl_xor_sync(0xffffffffu, give, 2 * half));
+      v[x] = op(take, __shfl_xor_sync(0xffffffffu, give, 4 * half));
     }
   }
-  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+  const float y = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 2));
+  return op(y, __shfl_xor_sync(0xffffffffu, y, 1));
 }
 
 // NC: rows of a unit, in sixteens
@@ -135,22 +150,22 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
   if (tid == 32) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&s_empty[x], 4);
+      mbar_init(&s_empty[x], 8);
     }
-    mbar_init(p_full, 4);
+    mbar_init(p_full, 8);
     mbar_init(p_empty, 1);
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 8);
     mark[0] = mark[1] = -1;
     *give_up = 0;
   }
   mbar_fence_init();
-  if (tid == 128 && s.use_tma && p.cache.num_pages > 0) {
+  if (tid == 256 && s.use_tma && p.cache.num_pages > 0) {
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
   const Stretch st = find_stretch<TILE, W::THREADS>(s);
   if (st.left == 0) return;
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(&s_tmem, W::T_COLS);
     tmem_relinquish();
   }
@@ -173,13 +188,15 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 
   // ---------------------------------------------------------------- softmax
   auto softmax = [&]() -> bool {
-    const uint32_t my_lane = tmem_addr(tmem, warp * 32, 0);
-    // The four warps' barrier, with a vote.  A warp that meets a limit marks it and comes to one more
+    // a thread has position `pos` of a tile and the rows [r0, r0 + 8 NC)
+    const int pos = tid & 127, quarter = warp & 3, half = warp >> 2, r0 = half * (8 * NC);
+    const uint32_t my_lane = tmem_addr(tmem, quarter * 32, 0);
+    // The eight warps' barrier, with a vote.  A warp that meets a limit marks it and comes to one more
     // barrier, after which the others see the mark and leave as well: no barrier waits for a warp that
     // has left.
     auto vote = [&](bool mine, bool& any) {
       uint32_t r;
-      asm volatile("{.reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 128, p; selp.u32 %0, 1, 0, q;}"
+      asm volatile("{.reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 256, p; selp.u32 %0, 1, 0, q;}"
                    : "=r"(r) : "r"((uint32_t)mine) : "memory");
       any = r != 0;
       return *reinterpret_cast<volatile int*>(give_up) == 0;
@@ -198,7 +215,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
     uint32_t at_p[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x)
-      at_p[x] = p_s + (tid >> 6) * (N * 128) + ((((tid & 63) >> 3) ^ x) << 4) + (tid & 7) * 2;
+      at_p[x] = p_s + (pos >> 6) * (N * 128) + r0 * 128 + ((((pos & 63) >> 3) ^ x) << 4) + (pos & 7) * 2;
 
     // Eight channels of a query in 8-bit pieces: the row is scaled by a power of two that brings its
     // largest entry to [2^7, 2^8), a piece has 4 bits of an entry, and the next one 2^4 times what is
@@ -260,18 +277,20 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         row_from[tid] = real ? ((long long)n * p.K + i) * p.q_stride + (hk * s.group_heads + gr - i * s.group_heads) * D : -1;
       }
       if (!sync()) return false;
-      constexpr int EACH = N * (D / 8) / 128;  // chunks of 8 channels of a thread: all on their way together
+      constexpr int ALL = N * (D / 8), EACH = (ALL + 255) / 256;  // chunks of 8 channels: a thread's are on their way together
       uint4 q[EACH];
       const int ch = tid % (D / 8);
 #pragma unroll
       for (int z = 0; z < EACH; ++z) {
-        const long long from = row_from[(tid + z * 128) / (D / 8)];
+        if (ALL % 256 && tid + z * 256 >= ALL) break;  // (whole warps)
+        const long long from = row_from[(tid + z * 256) / (D / 8)];
         q[z] = from < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(static_cast<const A*>(p.q) + from + ch * 8);
       }
       if constexpr (E8) {
 #pragma unroll 1
         for (int z = 0; z < EACH; ++z) {
-          const int row = (tid + z * 128) / (D / 8);
+          if (ALL % 256 && tid + z * 256 >= ALL) break;
+          const int row = (tid + z * 256) / (D / 8);
           write_pieces(q[0], row, ch, odd);
 #pragma unroll
           for (int y = 0; y + 1 < EACH; ++y) q[y] = q[y + 1];
@@ -279,7 +298,8 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       } else
 #pragma unroll
       for (int z = 0; z < EACH; ++z) {
-        const int row = (tid + z * 128) / (D / 8);
+        if (ALL % 256 && tid + z * 256 >= ALL) break;
+        const int row = (tid + z * 256) / (D / 8);
         st_shared_v4(q_s + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), q[z].x, q[z].y, q[z].z, q[z].w);
       }
       fence_proxy_async_smem();
@@ -288,7 +308,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       return true;
     };
 
-    float sums[NC][16];  // of this position's weights of each row, over the unit's tiles
+    float sums[NC][8];  // of this position's weights of each row, over the unit's tiles
     int odd = 0;
     if (!load_queries(0, 0, odd)) return false;
     for (int it = 0, stage = 0, turn = 0;; ++it) {
@@ -299,17 +319,17 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       const uint32_t flags = t.flags;
       const bool first = flags & FIRST, all = flags & FULL;
       const float f = p.scale * p.cache.k_scale * 1.44269504088896340736f;
-      const float *neg = row_neg + odd * 48, *fs = row_f + odd * 48;
+      const float *neg = row_neg + odd * 48 + r0, *fs = row_f + odd * 48 + r0;  // of this thread's rows
       const int* tok = row_tok + odd * 48;
-      const uint32_t scores = my_lane + T_S + (it & 1) * W::S_COLS;
+      const uint32_t scores = my_lane + T_S + (it & 1) * W::S_COLS + r0;
       int at = 0;
       bool exists = true;
       if (!all) {
-        at = t.pos0 + tid;
-        exists = (t.valid[tid >> 5] >> lane) & 1;
+        at = t.pos0 + pos;
+        exists = (t.valid[quarter] >> lane) & 1;
       }
       int *row_lo = rows_lo + (it & 1) * 48, *row_hi = rows_hi + (it & 1) * 48;
-      auto sees = [&](int row) { return exists & (at <= row_hi[row]) & (at >= row_lo[row]); };  // (no branches)
+      auto sees = [&](int row) { return exists & (at <= row_hi[r0 + row]) & (at >= row_lo[r0 + row]); };  // (no branches)
 
       // ---- values that no row sees are set to zero (0 times an infinite or NaN value is NaN), and
       // values that are none but only some rows see have their product formed by hand
@@ -319,17 +339,18 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         if (!wait(&full[stage], turn)) return false;
         const bool seen = any_sees(t, at);
         if (!seen) {
-          for (int x = 0; x < W::ROW_BYTES / 16; ++x) st_shared_v4(v_s + kv_offset<W::ROW_BYTES, TILE>(tid, x), 0, 0, 0, 0);
+          for (int x = half; x < W::ROW_BYTES / 16; x += 2) st_shared_v4(v_s + kv_offset<W::ROW_BYTES, TILE>(pos, x), 0, 0, 0, 0);
         }
         bool none = false;
         const int i0 = t.row0 / s.group_heads, i1 = (min(t.row0 + N, s.rows) - 1) / s.group_heads;
         if (seen && i0 != i1 && !(i1 < t.count && at <= last_seen(t, i0) && at >= first_seen(t, i1))) {
           constexpr uint32_t EXP = BF ? 0x7f80u : 0x7c00u;  // of an infinite or NaN value
 #pragma unroll
-          for (int x = 0; x < W::ROW_BYTES / 16; ++x) {
+          for (int x2 = 0; x2 < W::ROW_BYTES / 32; ++x2) {
+            const int x = 2 * x2 + half;
             uint32_t v[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(v_s + kv_offset<W::ROW_BYTES, TILE>(tid, x)) : "memory");
+                         : "r"(v_s + kv_offset<W::ROW_BYTES, TILE>(pos, x)) : "memory");
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               if (E8) none |= (((v[y] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;  // 0x7f: NaN
@@ -346,10 +367,10 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         if (by_hand && tid == 0) mark[it & 1] = it;
       }
       // ---- whether a score passes its row's maximum
-      float v[NC][16];
-      auto join_pieces = [](float (&a)[16], const float (&more)[QP][16]) {
+      float v[NC][8];
+      auto join_pieces = [](float (&a)[8], const float (&more)[QP][8]) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
+        for (int x = 0; x < 8; ++x) {
           if (QP == 2) a[x] = fmaf(more[1][x], 0.0625f, a[x]);
           if (QP == 3) a[x] = fmaf(fmaf(more[QP - 1][x], 0.0625f, more[QP > 1 ? 1 : 0][x]), 0.0625f, a[x]);
         }
@@ -358,16 +379,16 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 #pragma unroll
         for (int y = 0; y < NC; ++y) {
 #pragma unroll
-          for (int x = 0; x < 16; x += 4) {
-            const float4 nn = *reinterpret_cast<const float4*>(neg + y * 16 + x);
-            const float4 ff = E8 ? *reinterpret_cast<const float4*>(fs + y * 16 + x) : make_float4(f, f, f, f);
+          for (int x = 0; x < 8; x += 4) {
+            const float4 nn = *reinterpret_cast<const float4*>(neg + y * 8 + x);
+            const float4 ff = E8 ? *reinterpret_cast<const float4*>(fs + y * 8 + x) : make_float4(f, f, f, f);
             v[y][x] = fmaf(v[y][x], ff.x, nn.x), v[y][x + 1] = fmaf(v[y][x + 1], ff.y, nn.y);
             v[y][x + 2] = fmaf(v[y][x + 2], ff.z, nn.z), v[y][x + 3] = fmaf(v[y][x + 3], ff.w, nn.w);
           }
           if (!all) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              v[y][x] = sees(y * 16 + x) ? v[y][x] : -INFINITY;
+            for (int x = 0; x < 8; ++x)
+              v[y][x] = sees(y * 8 + x) ? v[y][x] : -INFINITY;
           }
         }
       };
@@ -375,7 +396,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 #pragma unroll
         for (int y = 0; y < NC; ++y)
 #pragma unroll
-          for (int x = 0; x < 16; ++x) sums[y][x] = 0.f;
+          for (int x = 0; x < 8; ++x) sums[y][x] = 0.f;
       }
       bool raise = first, done = false;  // done: the previous tile's product has been waited for
       while (true) {
@@ -385,19 +406,19 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           tc_fence_after_sync();
 #pragma unroll 1
           for (int y = 0; y < NC; ++y) {
-            float w[16], more[QP][16];
-            tmem_ld16(scores + y * 16, w);
+            float w[8], more[QP][8];
+            tmem_ld8(scores + y * 8, w);
 #pragma unroll
-            for (int z = 1; z < QP; ++z) tmem_ld16(scores + z * N + y * 16, more[z]);
+            for (int z = 1; z < QP; ++z) tmem_ld8(scores + z * N + y * 8, more[z]);
             tmem_ld_wait();
             join_pieces(w, more);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              w[x] *= E8 ? fs[y * 16 + x] : f;
-              if (!all) w[x] = sees(y * 16 + x) ? w[x] : -INFINITY;
+            for (int x = 0; x < 8; ++x) {
+              w[x] *= E8 ? fs[y * 8 + x] : f;
+              if (!all) w[x] = sees(y * 8 + x) ? w[x] : -INFINITY;
             }
             const float top = across(w, [](float a, float b) { return fmaxf(a, b); });
-            if (!(lane & 1)) warp_top[warp * 48 + y * 16 + (lane >> 1)] = top;
+            if (!(lane & 3)) warp_top[quarter * 48 + r0 + y * 8 + (lane >> 2)] = top;
           }
           if (!sync()) return false;
           if (tid < N) {
@@ -412,26 +433,27 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 #pragma unroll
             for (int y = 0; y < NC; ++y)
 #pragma unroll
-              for (int x = 0; x < 16; ++x) sums[y][x] *= keep[y * 16 + x];
+              for (int x = 0; x < 8; ++x) sums[y][x] *= keep[r0 + y * 8 + x];
 #pragma unroll 1
             for (int y = 0; y < NC * WP; ++y) {
-              float a[16];
-              tmem_ld16(my_lane + T_O + y * 16, a);
+              float a[8];
+              const int row = r0 + y % NC * 8;
+              tmem_ld8(my_lane + T_O + y / NC * N + row, a);
               tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) a[x] *= keep[(y % NC) * 16 + x];
-              tmem_st16(my_lane + T_O + y * 16, a);
+              for (int x = 0; x < 8; ++x) a[x] *= keep[row + x];
+              tmem_st8(my_lane + T_O + y / NC * N + row, a);
             }
             tmem_st_wait();
           }
           done = true;
         }
         if (QP < 3) {
-          float more[NC][QP][16];
+          float more[NC][QP][8];
 #pragma unroll
           for (int y = 0; y < NC; ++y) {
-            tmem_ld16(scores + y * 16, v[y]);
-            if (QP == 2) tmem_ld16(scores + N + y * 16, more[y][QP - 1]);
+            tmem_ld8(scores + y * 8, v[y]);
+            if (QP == 2) tmem_ld8(scores + N + y * 8, more[y][QP - 1]);
           }
           tmem_ld_wait();
 #pragma unroll
@@ -439,10 +461,10 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         } else {
 #pragma unroll
           for (int y = 0; y < NC; ++y) {
-            float more[QP][16];
-            tmem_ld16(scores + y * 16, v[y]);
+            float more[QP][8];
+            tmem_ld8(scores + y * 8, v[y]);
 #pragma unroll
-            for (int z = 1; z < QP; ++z) tmem_ld16(scores + z * N + y * 16, more[z]);
+            for (int z = 1; z < QP; ++z) tmem_ld8(scores + z * N + y * 8, more[z]);
             tmem_ld_wait();
             join_pieces(v[y], more);
           }
@@ -453,7 +475,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 #pragma unroll
         for (int y = 0; y < NC; ++y)
 #pragma unroll
-          for (int x = 0; x < 16; ++x) top = fmaxf(top, v[y][x]);
+          for (int x = 0; x < 8; ++x) top = fmaxf(top, v[y][x]);
         if (!vote(top > W::BIAS + W::SLACK, raise)) return false;
         if (!raise) break;
       }
@@ -468,9 +490,9 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 #pragma unroll
       for (int y = 0; y < NC; ++y) {
         if constexpr (E8) {
-          uint32_t pieces[WP][4];
+          uint32_t pieces[WP][2];
 #pragma unroll
-          for (int x = 0; x < 16; x += 4) {
+          for (int x = 0; x < 8; x += 4) {
             float a[4];
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
@@ -493,23 +515,24 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           }
 #pragma unroll
           for (int z = 0; z < WP; ++z)
-            st_shared_v4(p_s + (z * NC + y) * (TILE * 16) + tid * 16, pieces[z][0], pieces[z][1], pieces[z][2], pieces[z][3]);
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_s + (z * NC + ((r0 + y * 8) >> 4)) * (TILE * 16) + pos * 16 + ((r0 + y * 8) & 8)),
+                         "r"(pieces[z][0]), "r"(pieces[z][1]) : "memory");
         } else {
 #pragma unroll
-          for (int x = 0; x < 16; x += 2) {
+          for (int x = 0; x < 8; x += 2) {
             const float a = exp2_fast(v[y][x]), b = exp2_fast(v[y][x + 1]);
             sums[y][x] += a;
             sums[y][x + 1] += b;
             const uint32_t w = BF ? pack_bf16x2(a, b) : pack_f16x2(a, b);
-            st_u16(at_p[x & 7] + (y * 16 + x) * 128, w);
-            st_u16(at_p[(x + 1) & 7] + (y * 16 + x + 1) * 128, w >> 16);
+            st_u16(at_p[x] + (y * 8 + x) * 128, w);
+            st_u16(at_p[x + 1] + (y * 8 + x + 1) * 128, w >> 16);
           }
         }
       }
       if (by_hand) {
         // O^T += V^T P^T over the rows that see a position, one channel to a thread
         if (!sync()) return false;
-        const int d = D == 128 ? tid : warp * 16 + (lane & 15);
+        const int d = D == 128 ? pos : quarter * 16 + (lane & 15);
         const uint32_t v_s = values_of(stage);
         auto value_of = [&](int y) -> float {
           const uint32_t v_at = v_s + kv_offset<W::ROW_BYTES, TILE>(y, d * W::ES / 16) + d * W::ES % 16;
@@ -531,26 +554,24 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           const uint16_t w = ld_shared_u16(p_s + (y >> 6) * (N * 128) + row * 128 + ((((y & 63) >> 3) ^ (row & 7)) << 4) + (y & 7) * 2);
           return BF ? to_f32(__ushort_as_bfloat16(w)) : to_f32(__ushort_as_half(w));
         };
-        for (int c0 = 0; c0 < N * WP; c0 += 16) {
-          float o[16];
-          if (c0 >= N) {  // the other pieces' sums
-            if (!first) break;
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = 0.f;
-            tmem_st16(my_lane + T_O + c0, o);
-            continue;
-          }
-          tmem_ld16(my_lane + T_O + c0, o);
+        for (int c0 = r0; c0 < r0 + 8 * NC; c0 += 8) {
+          float o[8];
+          tmem_ld8(my_lane + T_O + c0, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
+          for (int x = 0; x < 8; ++x) {
             float sum = first ? 0.f : o[x];
             const int hi = row_hi[c0 + x], lo = row_lo[c0 + x];
             for (int y = max(0, lo - t.pos0); y < TILE && t.pos0 + y <= hi; ++y)
               if ((t.valid[y >> 5] >> (y & 31)) & 1) sum += value_of(y) * weight_of(c0 + x, y);
             o[x] = sum;
           }
-          tmem_st16(my_lane + T_O + c0, o);
+          tmem_st8(my_lane + T_O + c0, o);
+          if (first) {  // the other pieces' sums
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x] = 0.f;
+            for (int z = 1; z < WP; ++z) tmem_st8(my_lane + T_O + z * N + c0, o);
+          }
         }
         tmem_st_wait();
       }
@@ -574,7 +595,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 #pragma unroll
         for (int y = 0; y < NC; ++y) {
           const float sum = across(sums[y], [](float a, float b) { return a + b; });
-          if (!(lane & 1)) warp_sum[warp * 48 + y * 16 + (lane >> 1)] = sum;
+          if (!(lane & 3)) warp_sum[quarter * 48 + r0 + y * 8 + (lane >> 2)] = sum;
         }
         if (!sync()) return false;
         const bool whole_unit = (flags & OPENS) && (flags & CLOSES);
@@ -595,29 +616,30 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         if (!wait(p_empty, it & 1)) return false;
         tc_fence_after_sync();
         const bool mine = D == 128 || lane < 16;
-        const int d = D == 128 ? tid : warp * 16 + (lane & 15);
+        const int d = D == 128 ? pos : quarter * 16 + (lane & 15);
 #pragma unroll 1
         for (int y = 0; y < NC; ++y) {
-          float o[16], more[WP][16];
-          tmem_ld16(my_lane + T_O + y * 16, o);
+          float o[8], more[WP][8];
+          const int c0 = r0 + y * 8;
+          tmem_ld8(my_lane + T_O + c0, o);
 #pragma unroll
-          for (int z = 1; z < WP; ++z) tmem_ld16(my_lane + T_O + z * N + y * 16, more[z]);
+          for (int z = 1; z < WP; ++z) tmem_ld8(my_lane + T_O + z * N + c0, more[z]);
           tmem_ld_wait();
 #pragma unroll
           for (int z = 1; z < WP; ++z)
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] += more[z][x];
-          const int have = mine ? unit_rows - y * 16 : 0;
+            for (int x = 0; x < 8; ++x) o[x] += more[z][x];
+          const int have = mine ? unit_rows - c0 : 0;
           if (whole_unit) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float by = keep[y * 16 + x];  // 0: nothing was seen
-              if (x < have) static_cast<A*>(p.out)[row_to[y * 16 + x] * D + d] = from_f32<A>(by == 0.f ? 0.f : o[x] * by);
+            for (int x = 0; x < 8; ++x) {
+              const float by = keep[c0 + x];  // 0: nothing was seen
+              if (x < have) static_cast<A*>(p.out)[row_to[c0 + x] * D + d] = from_f32<A>(by == 0.f ? 0.f : o[x] * by);
             }
           } else {
 #pragma unroll
-            for (int x = 0; x < 16; ++x)
-              if (x < have) s.part_o[row_to[y * 16 + x] * D + d] = keep[y * 16 + x] == 0.f ? 0.f : o[x];
+            for (int x = 0; x < 8; ++x)
+              if (x < have) s.part_o[row_to[c0 + x] * D + d] = keep[c0 + x] == 0.f ? 0.f : o[x];
           }
         }
         tc_fence_before_sync();
@@ -681,9 +703,9 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
   };
 
   bool ok = true;
-  if (warp < 4) {
+  if (warp < 8) {
     ok = softmax();
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     produce<D, E8, TILE, STAGES>(s, st, Ring{base, full, empty, told, meta}, map_k, map_v);
   } else {
     if (lane == 0) ok = issue();
@@ -694,7 +716,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  if (warp == 5) tmem_dealloc(tmem, W::T_COLS);
+  if (warp == 9) tmem_dealloc(tmem, W::T_COLS);
 }
 
 template <typename A, int D, int NC, bool E8>
