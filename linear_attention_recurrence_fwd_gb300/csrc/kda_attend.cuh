@@ -10,11 +10,14 @@
 
 namespace kda {
 
-enum : uint32_t { FIRST = 1, LAST = 2, STOP = 4, FULL = 8, OPENS = 16, CLOSES = 32 };
+// Of a tile: a unit's first or last one here, the CTA's last one, seen by all rows; and of its unit: whether
+// its first and last tile are here (CLOSES: known at the last one; UNIT_CLOSES, UNIT_STOPS: at the first).
+enum : uint32_t { FIRST = 1, LAST = 2, STOP = 4, FULL = 8, OPENS = 16, CLOSES = 32, UNIT_CLOSES = 64, UNIT_STOPS = 128 };
 
 struct Meta {  // what the consumers need to know of a stage's tile
   int n, hk, row0, pos0, len, count, end;
   uint32_t flags;
+  int tiles;          // of the unit, from this one on, in this CTA
   uint32_t valid[4];  // bit j: position pos0 + j lies in a page that exists
 };
 
@@ -261,6 +264,8 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
     const bool first = it == 0 || j == 0;
     if (first) opened_here = j == 0;
     const bool closes = j == r.tiles - 1;
+    const int unit_tiles = s.whole ? r.tiles - j : min(r.tiles - j, left);
+    const bool unit_stops = s.whole ? left == 1 : left == unit_tiles;
     if (!s.whole) --left; else if (closes) --left;
     stop = left == 0;
     if (!s.whole && first && opened_here && lane == 0) {
@@ -322,7 +327,9 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
       const bool all = !bad && pos0 + TILE <= r.end && i1 < r.count && pos0 + TILE - 1 <= r.len + i0 &&
                        !(p.window && r.len + i1 >= p.window && pos0 < r.len + i1 - p.window + 1);
       m.flags = (first ? FIRST : 0) | (closes || stop ? LAST : 0) | (stop ? STOP : 0) | (all ? FULL : 0) |
-                (opened_here ? OPENS : 0) | (closes ? CLOSES : 0);
+                (opened_here ? OPENS : 0) | (closes ? CLOSES : 0) |
+                (j + unit_tiles == r.tiles ? UNIT_CLOSES : 0) | (unit_stops ? UNIT_STOPS : 0);
+      m.tiles = unit_tiles;
       mbar_arrive(&told[stage]);
     }
     if (use_tma) {

@@ -20,7 +20,7 @@
 // keys and values would have to be converted through shared memory, whose
 // bandwidth the products' operands take already (295 us against 278 us).
 //
-// Warps: 0-7 softmax (a thread has half of the rows), 8 producer, 9 issues the products.  One CTA on an SM.
+// Warps: 0-7 softmax (a thread has half of the rows), 8 producer, 9 and 10 issue the products.  One CTA on an SM.
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -31,19 +31,28 @@ constexpr float UNSEEN = 3e38f;  // takes any score of a row without a maximum p
 
 // E8: an 8-bit cache.  QP and WP: the 8-bit pieces that a query and a weight are written as.
 template <typename A, int D, bool E8> struct Wide {
-  static constexpr int THREADS = 320;
+  // Softmax warps: two groups that take tiles in turn, or one of which each half has half of the rows
+  static constexpr int GROUPS = E8 ? 2 : 1;
+  // The launch's registers are split anew where a thread has all rows; the sum stays what it was.
+  static constexpr int THREADS = E8 ? 384 : 352;
+  static constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 200, OTHER_REGS = 104;
+  static_assert(!E8 || 8 * SOFTMAX_REGS + 4 * OTHER_REGS <= 12 * LAUNCH_REGS, "registers");
   static constexpr int ES = E8 ? 1 : 2;                  // bytes of a cached element
   static constexpr int QP = E8 ? (__is_same(A, __nv_bfloat16) ? 2 : 3) : 1, WP = E8 ? QP + 1 : 1;
+  // Of a weight's pieces, WN lie side by side in one product (each with columns of its own in O; the
+  // values, whose reading bounds a product this narrow, are read once), in WP / WN products.
+  static constexpr int WN = WP == 4 ? 2 : WP;
   static constexpr int ROW_BYTES = D * ES;
   static constexpr int KV_BYTES = TILE * ROW_BYTES;      // keys or values of a stage
   static constexpr int STAGE_BYTES = 2 * KV_BYTES;
-  static constexpr int Q_BYTES = 48 * D * QP * ES, P_BYTES = 48 * TILE * WP * ES;
-  static constexpr int MISC_BYTES = 5632;
-  static constexpr int FIT = (224 * 1024 - Q_BYTES - P_BYTES - MISC_BYTES) / STAGE_BYTES;
+  static constexpr int Q_BYTES = 48 * D * QP * ES, P_BYTES = 48 * TILE * WP * ES;  // P: of a group
+  static constexpr int MISC_BYTES = 7680;
+  static constexpr int FIT = (227 * 1024 - 1280 - Q_BYTES - GROUPS * P_BYTES - MISC_BYTES) / STAGE_BYTES;
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
-  static constexpr int SMEM = STAGES * STAGE_BYTES + Q_BYTES + P_BYTES + MISC_BYTES + 1024;
-  // Columns of tensor memory: two tiles' scores, then the output
-  static constexpr uint32_t T_S = 0, S_COLS = E8 ? QP * 48 : 64, T_O = 2 * S_COLS, T_COLS = E8 ? 512 : 256;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + Q_BYTES + GROUPS * P_BYTES + MISC_BYTES + 1024;
+  // Columns of tensor memory: two tiles' scores, then each group's output
+  static constexpr uint32_t T_S = 0, S_COLS = E8 ? QP * 48 : 64, T_O = 2 * S_COLS, O_COLS = 48 * WN, T_COLS = E8 ? 512 : 256;
+  static_assert(T_O + GROUPS * O_COLS <= T_COLS, "tensor memory");
   // Weights are 2^(f s - m + BIAS) and reach 2^(BIAS + SLACK) before the maximum is moved.
   static constexpr float BIAS = E8 ? 12.f : 0.f, SLACK = E8 ? 3.f : 8.f;
 };
@@ -110,7 +119,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
     attend_wide_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const __grid_constant__ Params s) {
   using W = Wide<A, D, E8>;
-  constexpr int STAGES = W::STAGES, QP = W::QP, WP = W::WP;
+  constexpr int STAGES = W::STAGES, QP = W::QP, WP = W::WP, WN = W::WN, GROUPS = W::GROUPS;
   constexpr uint32_t T_S = W::T_S, T_O = W::T_O;
   constexpr bool BF = __is_same(A, __nv_bfloat16);
   extern __shared__ uint8_t smem_raw[];
@@ -118,25 +127,24 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const aligned = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t q_s = base + STAGES * W::STAGE_BYTES, p_s = q_s + W::Q_BYTES;
-  uint8_t* misc = aligned + STAGES * W::STAGE_BYTES + W::Q_BYTES + W::P_BYTES;
+  uint8_t* misc = aligned + STAGES * W::STAGE_BYTES + W::Q_BYTES + GROUPS * W::P_BYTES;
   // tables of the unit's rows, for two units in turn
-  float* row_m = reinterpret_cast<float*>(misc);    // [2][48] maximum (of scores in log2 units)
-  float* row_neg = row_m + 96;                      // [2][48] BIAS minus the maximum; UNSEEN while nothing is seen
-  float* row_f = row_neg + 96;                      // [2][48] what its scores are multiplied with (8-bit)
+  float* row_m = reinterpret_cast<float*>(misc);    // [group][2][48] maximum (of scores in log2 units)
+  float* row_neg = row_m + 192;                     // [group][2][48] BIAS minus the maximum; UNSEEN while nothing is seen
+  float* row_f = row_neg + 192;                     // [2][48] what its scores are multiplied with (8-bit)
   int* row_tok = reinterpret_cast<int*>(row_f + 96);  // [2][48] the row's token
-  float* warp_top = reinterpret_cast<float*>(row_tok + 96);  // [4][48]
-  float* warp_sum = warp_top + 192;                 // [4][48]
-  float* keep = warp_sum + 192;                     // [48] what O and the sums are rescaled with; 1 / sum at the end
-  int* rows_lo = reinterpret_cast<int*>(keep + 48);  // [2][48] first and last position that a row sees,
-  int* rows_hi = rows_lo + 96;                       // [2][48] for two tiles in turn
-  long long* row_to = reinterpret_cast<long long*>(rows_hi + 96);  // [48] where a row's output goes
+  float* warp_top = reinterpret_cast<float*>(row_tok + 96);  // [group][4][48] maxima over a warp's positions; a unit's sums
+  float* keep = warp_top + 384;                     // [group][48] what O and the sums are rescaled with; what O is multiplied with
+  int* rows_lo = reinterpret_cast<int*>(keep + 96);  // [4][48] first and last position that a row sees,
+  int* rows_hi = rows_lo + 192;                      // [4][48] for four tiles in turn
+  long long* row_to = reinterpret_cast<long long*>(rows_hi + 192);  // [48] where a row's output goes
   long long* row_from = row_to + 48;                // [48] where its query is, or -1
-  int* mark = reinterpret_cast<int*>(row_from + 48);  // [2]: the tile whose values are multiplied by hand, two in turn
-  int* give_up = mark + 2;                          // a softmax warp met a limit
-  uint64_t* bars = reinterpret_cast<uint64_t*>(mark + 4);
+  int* mark = reinterpret_cast<int*>(row_from + 48);  // [4]: the tile whose values are multiplied by hand, four in turn
+  int* give_up = mark + 4;                          // [group] a softmax warp met a limit
+  uint64_t* bars = reinterpret_cast<uint64_t*>(give_up + 4);
   uint64_t *full = bars, *empty = bars + 6, *told = bars + 12;
-  uint64_t *s_full = bars + 18, *s_empty = bars + 20, *p_full = bars + 22, *p_empty = bars + 23, *q_full = bars + 24;
-  Meta* meta = reinterpret_cast<Meta*>(bars + 25);  // [6]
+  uint64_t *s_full = bars + 18, *s_empty = bars + 20, *p_full = bars + 22, *p_empty = bars + 24, *q_full = bars + 26, *joint = bars + 27;
+  Meta* meta = reinterpret_cast<Meta*>(bars + 28);  // [6]
   __shared__ uint32_t s_tmem;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -150,13 +158,14 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
   if (tid == 32) {
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&s_empty[x], 8);
+      mbar_init(&s_empty[x], 8 / GROUPS);
+      mbar_init(&p_full[x], 8 / GROUPS);
+      mbar_init(&p_empty[x], 1);
+      give_up[x] = 0;
     }
-    mbar_init(p_full, 8);
-    mbar_init(p_empty, 1);
     mbar_init(q_full, 8);
-    mark[0] = mark[1] = -1;
-    *give_up = 0;
+    mbar_init(joint, 8);
+    for (int x = 0; x < 4; ++x) mark[x] = -1;
   }
   mbar_fence_init();
   if (tid == 256 && s.use_tma && p.cache.num_pages > 0) {
@@ -188,18 +197,22 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 
   // ---------------------------------------------------------------- softmax
   auto softmax = [&]() -> bool {
-    // a thread has position `pos` of a tile and the rows [r0, r0 + 8 NC)
-    const int pos = tid & 127, quarter = warp & 3, half = warp >> 2, r0 = half * (8 * NC);
+    // Group grp takes the tiles it with it % GROUPS == grp.  A thread has position `pos` of them, and the
+    // 8 CH rows from r0 on.
+    constexpr int HALVES = 2 / GROUPS, CH = 2 * NC / HALVES, GROUP = 256 / GROUPS;
+    const int pos = tid & 127, quarter = warp & 3, upper = warp >> 2;
+    const int grp = GROUPS == 2 ? upper : 0, half = GROUPS == 2 ? 0 : upper, r0 = half * (8 * CH), gt = tid - grp * GROUP;
     const uint32_t my_lane = tmem_addr(tmem, quarter * 32, 0);
-    // The eight warps' barrier, with a vote.  A warp that meets a limit marks it and comes to one more
-    // barrier, after which the others see the mark and leave as well: no barrier waits for a warp that
-    // has left.
+    const uint32_t my_p = p_s + grp * W::P_BYTES, my_o = my_lane + T_O + grp * W::O_COLS;
+    // A group's barrier, with a vote.  A warp that meets a limit marks it and comes to one more barrier
+    // of its group, after which the others see the mark and leave as well: no barrier waits for a warp
+    // that has left.
     auto vote = [&](bool mine, bool& any) {
       uint32_t r;
-      asm volatile("{.reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, 1, 256, p; selp.u32 %0, 1, 0, q;}"
-                   : "=r"(r) : "r"((uint32_t)mine) : "memory");
+      asm volatile("{.reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, %3, p; selp.u32 %0, 1, 0, q;}"
+                   : "=r"(r) : "r"((uint32_t)mine), "r"(1 + grp), "n"(GROUP) : "memory");
       any = r != 0;
-      return *reinterpret_cast<volatile int*>(give_up) == 0;
+      return *reinterpret_cast<volatile int*>(&give_up[grp]) == 0;
     };
     auto sync = [&]() {
       bool any;
@@ -207,15 +220,23 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
     };
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (__all_sync(0xffffffffu, mbar_wait(bar, parity))) return true;
-      *give_up = 1;
+      give_up[grp] = 1;
       sync();
       return false;
+    };
+    // all softmax warps
+    uint32_t joints = 0;
+    auto sync_all = [&]() {
+      if (GROUPS == 1) return sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(joint);
+      return wait(joint, joints++ & 1);
     };
     // this position's place in the weights: rows of 128 bytes, 64 positions each
     uint32_t at_p[8];
 #pragma unroll
     for (int x = 0; x < 8; ++x)
-      at_p[x] = p_s + (pos >> 6) * (N * 128) + r0 * 128 + ((((pos & 63) >> 3) ^ x) << 4) + (pos & 7) * 2;
+      at_p[x] = my_p + (pos >> 6) * (N * 128) + r0 * 128 + ((((pos & 63) >> 3) ^ x) << 4) + (pos & 7) * 2;
 
     // Eight channels of a query in 8-bit pieces: the row is scaled by a power of two that brings its
     // largest entry to [2^7, 2^8), a piece has 4 bits of an entry, and the next one 2^4 times what is
@@ -263,20 +284,25 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       }
     };
 
-    // A unit's rows' tables, then its queries: as they are, or in pieces.
+    // A unit, from its first tile's stage: its rows' tables, then its queries: as they are, or in pieces.
+    int u_n, u_hk, u_row0, u_tiles;
+    uint32_t u_flags;
     auto load_queries = [&](int stage, int turn, int odd) {
       if (!wait(&told[stage], turn)) return false;
       const Meta& t = meta[stage];
       const int n = t.n, hk = t.hk, row0 = t.row0;
+      u_n = n, u_hk = hk, u_row0 = row0, u_tiles = t.tiles, u_flags = t.flags;
       if (tid < N) {
         const int gr = row0 + tid, i = gr / s.group_heads;
         const bool real = gr < s.rows;
-        row_m[odd * 48 + tid] = -INFINITY;
-        row_neg[odd * 48 + tid] = UNSEEN;
+        for (int x = 0; x < GROUPS; ++x) {
+          row_m[x * 96 + odd * 48 + tid] = -INFINITY;
+          row_neg[x * 96 + odd * 48 + tid] = UNSEEN;
+        }
         row_tok[odd * 48 + tid] = real ? i : 0x3fffffff;
         row_from[tid] = real ? ((long long)n * p.K + i) * p.q_stride + (hk * s.group_heads + gr - i * s.group_heads) * D : -1;
       }
-      if (!sync()) return false;
+      if (!sync_all()) return false;
       constexpr int ALL = N * (D / 8), EACH = (ALL + 255) / 256;  // chunks of 8 channels: a thread's are on their way together
       uint4 q[EACH];
       const int ch = tid % (D / 8);
@@ -308,19 +334,34 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       return true;
     };
 
-    float sums[NC][8];  // of this position's weights of each row, over the unit's tiles
+    float sums[CH][8];  // of this position's weights of each row, over the unit's tiles
     int odd = 0;
-    if (!load_queries(0, 0, odd)) return false;
-    for (int it = 0, stage = 0, turn = 0;; ++it) {
+    int it = 0, stage = 0, turn = 0;
+    auto advance = [&]() {
+      ++it;
+      if (++stage == STAGES) stage = 0, turn ^= 1;
+    };
+    if (!load_queries(0, 0, 0)) return false;
+    while (true) {
+    const int n = u_n, hk = u_hk, row0 = u_row0, tiles = u_tiles;
+    const uint32_t unit = u_flags;
+    const float *neg = row_neg + grp * 96 + odd * 48 + r0, *fs = row_f + odd * 48 + r0;  // of this thread's rows
+    const int* tok = row_tok + odd * 48;
+#pragma unroll
+    for (int y = 0; y < CH; ++y)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) sums[y][x] = 0.f;
+    // ---- the unit's tiles, or every second of them
+    for (int z = 0; z < tiles; ++z, advance()) {
+      if (GROUPS == 2 && (it & 1) != grp) continue;
       if (!wait(&s_full[it & 1], (it >> 1) & 1)) return false;
       if (!wait(&told[stage], turn)) return false;
       tc_fence_after_sync();
       const Meta& t = meta[stage];  // the stage is given back after this tile's last look at it
-      const uint32_t flags = t.flags;
-      const bool first = flags & FIRST, all = flags & FULL;
+      const bool first = z < GROUPS, all = t.flags & FULL;
+      const int done_before = it / GROUPS;  // the group's tiles before this one
+      uint64_t* const o_done = &p_empty[GROUPS == 2 ? grp : 0];
       const float f = p.scale * p.cache.k_scale * 1.44269504088896340736f;
-      const float *neg = row_neg + odd * 48 + r0, *fs = row_f + odd * 48 + r0;  // of this thread's rows
-      const int* tok = row_tok + odd * 48;
       const uint32_t scores = my_lane + T_S + (it & 1) * W::S_COLS + r0;
       int at = 0;
       bool exists = true;
@@ -328,7 +369,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         at = t.pos0 + pos;
         exists = (t.valid[quarter] >> lane) & 1;
       }
-      int *row_lo = rows_lo + (it & 1) * 48, *row_hi = rows_hi + (it & 1) * 48;
+      int *row_lo = rows_lo + (it & 3) * 48, *row_hi = rows_hi + (it & 3) * 48;
       auto sees = [&](int row) { return exists & (at <= row_hi[r0 + row]) & (at >= row_lo[r0 + row]); };  // (no branches)
 
       // ---- values that no row sees are set to zero (0 times an infinite or NaN value is NaN), and
@@ -339,15 +380,15 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         if (!wait(&full[stage], turn)) return false;
         const bool seen = any_sees(t, at);
         if (!seen) {
-          for (int x = half; x < W::ROW_BYTES / 16; x += 2) st_shared_v4(v_s + kv_offset<W::ROW_BYTES, TILE>(pos, x), 0, 0, 0, 0);
+          for (int x = half; x < W::ROW_BYTES / 16; x += HALVES) st_shared_v4(v_s + kv_offset<W::ROW_BYTES, TILE>(pos, x), 0, 0, 0, 0);
         }
         bool none = false;
         const int i0 = t.row0 / s.group_heads, i1 = (min(t.row0 + N, s.rows) - 1) / s.group_heads;
         if (seen && i0 != i1 && !(i1 < t.count && at <= last_seen(t, i0) && at >= first_seen(t, i1))) {
           constexpr uint32_t EXP = BF ? 0x7f80u : 0x7c00u;  // of an infinite or NaN value
 #pragma unroll
-          for (int x2 = 0; x2 < W::ROW_BYTES / 32; ++x2) {
-            const int x = 2 * x2 + half;
+          for (int x2 = 0; x2 < W::ROW_BYTES / 16 / HALVES; ++x2) {
+            const int x = HALVES * x2 + half;
             uint32_t v[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                          : "r"(v_s + kv_offset<W::ROW_BYTES, TILE>(pos, x)) : "memory");
@@ -358,16 +399,16 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
             }
           }
         }
-        if (tid < N) {
-          const int hi = last_seen(t, tok[tid]);
-          row_hi[tid] = hi;
-          row_lo[tid] = hi >= 0 ? first_seen(t, tok[tid]) : 0;
+        if (gt < N) {
+          const int hi = last_seen(t, tok[gt]);
+          row_hi[gt] = hi;
+          row_lo[gt] = hi >= 0 ? first_seen(t, tok[gt]) : 0;
         }
         if (!vote(none, by_hand)) return false;
-        if (by_hand && tid == 0) mark[it & 1] = it;
+        if (by_hand && gt == 0) mark[it & 3] = it;
       }
       // ---- whether a score passes its row's maximum
-      float v[NC][8];
+      float v[CH][8];
       auto join_pieces = [](float (&a)[8], const float (&more)[QP][8]) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
@@ -377,7 +418,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       };
       auto scale = [&]() {  // f s - m; -infinity where not seen
 #pragma unroll
-        for (int y = 0; y < NC; ++y) {
+        for (int y = 0; y < CH; ++y) {
 #pragma unroll
           for (int x = 0; x < 8; x += 4) {
             const float4 nn = *reinterpret_cast<const float4*>(neg + y * 8 + x);
@@ -392,20 +433,14 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           }
         }
       };
-      if (first) {
-#pragma unroll
-        for (int y = 0; y < NC; ++y)
-#pragma unroll
-          for (int x = 0; x < 8; ++x) sums[y][x] = 0.f;
-      }
-      bool raise = first, done = false;  // done: the previous tile's product has been waited for
+      bool raise = first, raised = false, done = done_before == 0;  // done: the previous weights' product has been waited for
       while (true) {
         if (raise) {
           // ---- new maxima: over the warp's positions, then over the warps
-          if (it > 0 && !done && !wait(p_empty, (it - 1) & 1)) return false;
+          if (!done && !wait(o_done, (done_before - 1) & 1)) return false;
           tc_fence_after_sync();
 #pragma unroll 1
-          for (int y = 0; y < NC; ++y) {
+          for (int y = 0; y < CH; ++y) {
             float w[8], more[QP][8];
             tmem_ld8(scores + y * 8, w);
 #pragma unroll
@@ -418,49 +453,51 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
               if (!all) w[x] = sees(y * 8 + x) ? w[x] : -INFINITY;
             }
             const float top = across(w, [](float a, float b) { return fmaxf(a, b); });
-            if (!(lane & 3)) warp_top[quarter * 48 + r0 + y * 8 + (lane >> 2)] = top;
+            if (!(lane & 3)) warp_top[grp * 192 + quarter * 48 + r0 + y * 8 + (lane >> 2)] = top;
           }
           if (!sync()) return false;
-          if (tid < N) {
-            const float old = row_m[odd * 48 + tid];
-            const float now = fmaxf(fmaxf(fmaxf(warp_top[tid], warp_top[48 + tid]), fmaxf(warp_top[96 + tid], warp_top[144 + tid])), old);
-            keep[tid] = now == -INFINITY || old == -INFINITY ? 1.f : exp2_fast(old - now);
-            row_m[odd * 48 + tid] = now;
-            row_neg[odd * 48 + tid] = now == -INFINITY ? UNSEEN : W::BIAS - now;
+          if (gt < N) {
+            const int at_m = grp * 96 + odd * 48 + gt;
+            const float* tops = warp_top + grp * 192 + gt;
+            const float old = row_m[at_m];
+            const float now = fmaxf(fmaxf(fmaxf(tops[0], tops[48]), fmaxf(tops[96], tops[144])), old);
+            keep[grp * 48 + gt] = now == -INFINITY || old == -INFINITY ? 1.f : exp2_fast(old - now);
+            row_m[at_m] = now;
+            row_neg[at_m] = now == -INFINITY ? UNSEEN : W::BIAS - now;
           }
           if (!sync()) return false;
           if (!first) {
 #pragma unroll
-            for (int y = 0; y < NC; ++y)
+            for (int y = 0; y < CH; ++y)
 #pragma unroll
-              for (int x = 0; x < 8; ++x) sums[y][x] *= keep[r0 + y * 8 + x];
+              for (int x = 0; x < 8; ++x) sums[y][x] *= keep[grp * 48 + r0 + y * 8 + x];
 #pragma unroll 1
-            for (int y = 0; y < NC * WP; ++y) {
+            for (int y = 0; y < CH * WN; ++y) {
               float a[8];
-              const int row = r0 + y % NC * 8;
-              tmem_ld8(my_lane + T_O + y / NC * N + row, a);
+              const int row = r0 + y % CH * 8;
+              tmem_ld8(my_o + y / CH * N + row, a);
               tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 8; ++x) a[x] *= keep[row + x];
-              tmem_st8(my_lane + T_O + y / NC * N + row, a);
+              for (int x = 0; x < 8; ++x) a[x] *= keep[grp * 48 + row + x];
+              tmem_st8(my_o + y / CH * N + row, a);
             }
             tmem_st_wait();
           }
-          done = true;
+          raised = done = true;
         }
         if (QP < 3) {
-          float more[NC][QP][8];
+          float more[CH][QP][8];
 #pragma unroll
-          for (int y = 0; y < NC; ++y) {
+          for (int y = 0; y < CH; ++y) {
             tmem_ld8(scores + y * 8, v[y]);
             if (QP == 2) tmem_ld8(scores + N + y * 8, more[y][QP - 1]);
           }
           tmem_ld_wait();
 #pragma unroll
-          for (int y = 0; y < NC; ++y) join_pieces(v[y], more[y]);
+          for (int y = 0; y < CH; ++y) join_pieces(v[y], more[y]);
         } else {
 #pragma unroll
-          for (int y = 0; y < NC; ++y) {
+          for (int y = 0; y < CH; ++y) {
             float more[QP][8];
             tmem_ld8(scores + y * 8, v[y]);
 #pragma unroll
@@ -470,17 +507,20 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           }
         }
         scale();
-        if (done) break;
+        if (raised) break;
         float top = -INFINITY;
 #pragma unroll
-        for (int y = 0; y < NC; ++y)
+        for (int y = 0; y < CH; ++y)
 #pragma unroll
           for (int x = 0; x < 8; ++x) top = fmaxf(top, v[y][x]);
         if (!vote(top > W::BIAS + W::SLACK, raise)) return false;
         if (!raise) break;
       }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[it & 1]);
       // the previous weights have been read, and O is complete up to the previous tile
-      if (it > 0 && !done && !wait(p_empty, (it - 1) & 1)) return false;
+      if (!done && !wait(o_done, (done_before - 1) & 1)) return false;
       tc_fence_after_sync();
 
       // ---- weights 2^(f s - m): in 16 bits for the product (half a step of the type each), or in
@@ -488,7 +528,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       // 3 bits: what it leaves is exact.  Three pieces hold 9 bits of a weight (the last is rounded),
       // four the 11 of fp16.
 #pragma unroll
-      for (int y = 0; y < NC; ++y) {
+      for (int y = 0; y < CH; ++y) {
         if constexpr (E8) {
           uint32_t pieces[WP][2];
 #pragma unroll
@@ -515,7 +555,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           }
 #pragma unroll
           for (int z = 0; z < WP; ++z)
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_s + (z * NC + ((r0 + y * 8) >> 4)) * (TILE * 16) + pos * 16 + ((r0 + y * 8) & 8)),
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(my_p + (z * NC + ((r0 + y * 8) >> 4)) * (TILE * 16) + pos * 16 + ((r0 + y * 8) & 8)),
                          "r"(pieces[z][0]), "r"(pieces[z][1]) : "memory");
         } else {
 #pragma unroll
@@ -548,15 +588,15 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           if (E8) {
             float sum = 0.f;
             for (int z = WP - 1; z >= 0; --z)
-              sum += __half2float(__ushort_as_half((unsigned short)(ld_shared_u8(p_s + (z * NC + row / 16) * (TILE * 16) + y * 16 + row % 16) << 8)));
+              sum += __half2float(__ushort_as_half((unsigned short)(ld_shared_u8(my_p + (z * NC + row / 16) * (TILE * 16) + y * 16 + row % 16) << 8)));
             return sum;
           }
-          const uint16_t w = ld_shared_u16(p_s + (y >> 6) * (N * 128) + row * 128 + ((((y & 63) >> 3) ^ (row & 7)) << 4) + (y & 7) * 2);
+          const uint16_t w = ld_shared_u16(my_p + (y >> 6) * (N * 128) + row * 128 + ((((y & 63) >> 3) ^ (row & 7)) << 4) + (y & 7) * 2);
           return BF ? to_f32(__ushort_as_bfloat16(w)) : to_f32(__ushort_as_half(w));
         };
-        for (int c0 = r0; c0 < r0 + 8 * NC; c0 += 8) {
+        for (int c0 = r0; c0 < r0 + 8 * CH; c0 += 8) {
           float o[8];
-          tmem_ld8(my_lane + T_O + c0, o);
+          tmem_ld8(my_o + c0, o);
           tmem_ld_wait();
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
@@ -566,120 +606,112 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
               if ((t.valid[y >> 5] >> (y & 31)) & 1) sum += value_of(y) * weight_of(c0 + x, y);
             o[x] = sum;
           }
-          tmem_st8(my_lane + T_O + c0, o);
+          tmem_st8(my_o + c0, o);
           if (first) {  // the other pieces' sums
 #pragma unroll
             for (int x = 0; x < 8; ++x) o[x] = 0.f;
-            for (int z = 1; z < WP; ++z) tmem_st8(my_lane + T_O + z * N + c0, o);
+            for (int z = 1; z < WN; ++z) tmem_st8(my_o + z * N + c0, o);
           }
         }
         tmem_st_wait();
       }
-      const int t_n = t.n, t_hk = t.hk, t_row0 = t.row0;
       fence_proxy_async_smem();
       tc_fence_before_sync();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s_empty[it & 1]);
-        mbar_arrive(p_full);
-      }
-
-      if (flags & LAST) {
-        // the next unit's queries first: its first product need not wait for what follows
-        const bool stop = flags & STOP;
-        int next_stage = stage + 1, next_turn = turn;
-        if (next_stage == STAGES) next_stage = 0, next_turn ^= 1;
-        if (!stop && !load_queries(next_stage, next_turn, odd ^ 1)) return false;
-        // the rows' sums: over the warp's positions, then the warps
-        const int rows = odd * 48;
+      if (lane == 0) mbar_arrive(&p_full[GROUPS == 2 ? grp : 0]);
+    }
+    // ---- the unit's end.  The next unit's queries first: its first product need not wait for what follows
+    const bool stop = unit & UNIT_STOPS;
+    if (!sync_all()) return false;  // all scores have been formed
+    if (!stop && !load_queries(stage, turn, odd ^ 1)) return false;
+    // the rows' sums: over the warp's positions, then the warps
 #pragma unroll
-        for (int y = 0; y < NC; ++y) {
-          const float sum = across(sums[y], [](float a, float b) { return a + b; });
-          if (!(lane & 3)) warp_sum[quarter * 48 + r0 + y * 8 + (lane >> 2)] = sum;
-        }
-        if (!sync()) return false;
-        const bool whole_unit = (flags & OPENS) && (flags & CLOSES);
-        const long long slot = 2LL * c + ((flags & OPENS) ? 1 : 0);
-        const int unit_rows = min(N, s.rows - t_row0);
-        if (tid < unit_rows) {
-          const float m = row_m[rows + tid] - W::BIAS;
-          const float sum = (warp_sum[tid] + warp_sum[48 + tid]) + (warp_sum[96 + tid] + warp_sum[144 + tid]);
-          const bool none = m == -INFINITY;
-          const int i = tok[tid], gh = t_row0 + tid - i * s.group_heads;
-          const long long to = whole_unit ? ((long long)t_n * p.K + i) * p.H_q + t_hk * s.group_heads + gh : slot * N + tid;
-          row_to[tid] = to;
-          keep[tid] = none ? 0.f : whole_unit ? p.cache.v_scale / sum : 1.f;
-          if (!whole_unit) s.part_ml[to] = make_float2(m, sum);
-          else if (p.lse) p.lse[to] = none ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
-        }
-        if (!sync()) return false;
-        if (!wait(p_empty, it & 1)) return false;
-        tc_fence_after_sync();
-        const bool mine = D == 128 || lane < 16;
-        const int d = D == 128 ? pos : quarter * 16 + (lane & 15);
+    for (int y = 0; y < CH; ++y) {
+      const float sum = across(sums[y], [](float a, float b) { return a + b; });
+      if (!(lane & 3)) warp_top[grp * 192 + quarter * 48 + r0 + y * 8 + (lane >> 2)] = sum;
+    }
+    if (!sync_all()) return false;
+    const bool whole_unit = (unit & OPENS) && (unit & UNIT_CLOSES);
+    const long long slot = 2LL * c + ((unit & OPENS) ? 1 : 0);
+    const int unit_rows = min(N, s.rows - row0);
+    if (tid < unit_rows) {
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int x = 0; x < GROUPS; ++x) top = fmaxf(top, row_m[x * 96 + odd * 48 + tid]);
+#pragma unroll
+      for (int x = 0; x < GROUPS; ++x) {
+        const float m = row_m[x * 96 + odd * 48 + tid], by = m == -INFINITY ? 0.f : exp2_fast(m - top);
+        const float* of = warp_top + x * 192 + tid;
+        const float l = (of[0] + of[48]) + (of[96] + of[144]);
+        sum += m == -INFINITY ? l : by * l;  // (nothing, or NaN, without a maximum)
+        keep[x * 48 + tid] = by;
+      }
+      const bool none = top == -INFINITY && sum == 0.f;
+      const int i = tok[tid], gh = row0 + tid - i * s.group_heads;
+      const long long to = whole_unit ? ((long long)n * p.K + i) * p.H_q + hk * s.group_heads + gh : slot * N + tid;
+      row_to[tid] = to;
+      if (whole_unit) {
+        const float mul = none ? 0.f : p.cache.v_scale / sum;
+#pragma unroll
+        for (int x = 0; x < GROUPS; ++x) keep[x * 48 + tid] *= mul;
+      }
+      top -= W::BIAS;
+      if (!whole_unit) s.part_ml[to] = make_float2(top, sum);
+      else if (p.lse) p.lse[to] = none ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+    }
+    if (!sync_all()) return false;
+    // every group's last product
+#pragma unroll
+    for (int x = 0; x < GROUPS; ++x) {
+      const int products = (it + GROUPS - 1 - x) / GROUPS;
+      if (products > 0 && !wait(&p_empty[x], (products - 1) & 1)) return false;
+    }
+    tc_fence_after_sync();
+    const bool mine = D == 128 || lane < 16;
+    const int d = D == 128 ? pos : quarter * 16 + (lane & 15);
 #pragma unroll 1
-        for (int y = 0; y < NC; ++y) {
-          float o[8], more[WP][8];
-          const int c0 = r0 + y * 8;
-          tmem_ld8(my_lane + T_O + c0, o);
+    for (int y = 0; y < NC; ++y) {
+      const int c0 = upper * (8 * NC) + y * 8;
+      float o[GROUPS * WN][8];
 #pragma unroll
-          for (int z = 1; z < WP; ++z) tmem_ld8(my_lane + T_O + z * N + c0, more[z]);
-          tmem_ld_wait();
+      for (int x = 0; x < GROUPS * WN; ++x) tmem_ld8(my_lane + T_O + x / WN * W::O_COLS + x % WN * N + c0, o[x]);
+      tmem_ld_wait();
+      const int have = mine ? unit_rows - c0 : 0;
 #pragma unroll
-          for (int z = 1; z < WP; ++z)
+      for (int x = 0; x < 8; ++x) {
+        if (x >= have) break;
+        float sum = 0.f;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) o[x] += more[z][x];
-          const int have = mine ? unit_rows - c0 : 0;
-          if (whole_unit) {
+        for (int g = 0; g < GROUPS; ++g) {
+          const float by = keep[g * 48 + c0 + x];  // 0: the group has seen nothing
+          float all = o[g * WN][x];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const float by = keep[c0 + x];  // 0: nothing was seen
-              if (x < have) static_cast<A*>(p.out)[row_to[c0 + x] * D + d] = from_f32<A>(by == 0.f ? 0.f : o[x] * by);
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-              if (x < have) s.part_o[row_to[c0 + x] * D + d] = keep[c0 + x] == 0.f ? 0.f : o[x];
-          }
+          for (int z = 1; z < WN; ++z) all += o[g * WN + z][x];
+          if (by != 0.f) sum += all * by;
         }
-        tc_fence_before_sync();
-        odd ^= 1;
-        if (stop) return sync();
+        if (whole_unit) static_cast<A*>(p.out)[row_to[c0 + x] * D + d] = from_f32<A>(sum);
+        else s.part_o[row_to[c0 + x] * D + d] = sum;
       }
-      if (++stage == STAGES) stage = 0, turn ^= 1;
+    }
+    tc_fence_before_sync();
+    odd ^= 1;
+    if (stop) return sync_all();
+    // the other group's next product writes over what this one has read
+    if (GROUPS == 2 && !sync_all()) return false;
     }
   };
 
-  // ---------------------------------------------------------------- products, issued by one thread
-  auto issue = [&]() -> bool {
-    constexpr uint32_t id_s = E8 ? make_idesc_f8(128, N * QP, false, false, F8_E4M3, F8_E4M3) : make_idesc(128, N, false, false, false, !BF);
-    constexpr uint32_t id_o = E8 ? make_idesc_f8(D, N * WP, true, true, F8_E4M3, F8_E5M2) : make_idesc(D, N, true, false, false, !BF);
-    // Operands' descriptors; 32 bytes of a product's depth are a step.  Keys, queries and values lie in
-    // swizzled rows; the weights of an 8-bit cache in atoms of 8 positions by 16 rows.
-    constexpr uint32_t SW = W::ROW_BYTES < 128 ? SW_64 : SW_128, EIGHT = W::ROW_BYTES < 128 ? 512 : 1024;
+  // ---------------------------------------------------------------- products, each issued by one thread
+  // Operands' descriptors; 32 bytes of a product's depth are a step.  Keys, queries and values lie in
+  // swizzled rows; the weights of an 8-bit cache in atoms of 8 positions by 16 rows.
+  constexpr uint32_t SW = W::ROW_BYTES < 128 ? SW_64 : SW_128, EIGHT = W::ROW_BYTES < 128 ? 512 : 1024;
+  auto product = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
+    if (E8) umma_f8(d, a, b, id, add); else umma_bf16(d, a, b, id, add);
+  };
+  auto issue_scores = [&]() -> bool {
+    constexpr uint32_t id = E8 ? make_idesc_f8(128, N * QP, false, false, F8_E4M3, F8_E4M3) : make_idesc(128, N, false, false, false, !BF);
     const uint64_t dq = make_sdesc(q_s, 16, EIGHT, SW), dk = make_sdesc(base, 16, EIGHT, SW);
-    const uint64_t dv = make_sdesc(base + W::KV_BYTES, TILE * 128, EIGHT, SW);
-    const uint64_t dp = E8 ? make_sdesc(p_s, 128, TILE * 16, SW_NONE) : make_sdesc(p_s, 16, 1024, SW_128);
-    auto product = [](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
-      if (E8) umma_f8(d, a, b, id, add); else umma_bf16(d, a, b, id, add);
-    };
     int units = 0;
-    auto values = [&](int it, int stage, uint32_t flags) {
-      if (!mbar_wait(p_full, it & 1)) return false;
-      tc_fence_after_sync();
-      if (*reinterpret_cast<volatile int*>(&mark[it & 1]) != it) {  // else it was done by hand
-        const uint64_t a = dv + stage * (W::STAGE_BYTES >> 4);
-#pragma unroll
-        for (int ks = 0; ks < TILE * W::ES / 32; ++ks)
-          product(tmem + T_O, a + ks * (E8 ? 2 * D : 128), dp + (E8 ? ks * 32 : ((ks >> 2) * (N * 128) + (ks & 3) * 32) / 16), id_o,
-                  ks > 0 || !(flags & FIRST));
-      }
-      umma_commit(p_empty);
-      umma_commit(&empty[stage]);
-      return true;
-    };
-    int before_stage = 0;
-    uint32_t before_flags = 0;
     for (int it = 0, stage = 0, turn = 0;; ++it) {
       if (!mbar_wait(&full[stage], turn)) return false;
       if (E8 && !s.use_tma) fence_proxy_async_smem();  // (the producer's own copies)
@@ -691,24 +723,54 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
 #pragma unroll
       for (int ks = 0; ks < W::ROW_BYTES / 32; ++ks)
         product(tmem + T_S + (it & 1) * W::S_COLS, a + ((ks >> 2) * (TILE * 128) + (ks & 3) * 32) / 16,
-                  dq + ((ks >> 2) * (N * 128) + (ks & 3) * 32) / 16, id_s, ks > 0);
+                dq + ((ks >> 2) * (N * 128) + (ks & 3) * 32) / 16, id, ks > 0);
       umma_commit(&s_full[it & 1]);
       umma_commit(&empty[stage]);
-      if (it > 0 && !values(it - 1, before_stage, before_flags)) return false;
-      if (flags & STOP) return values(it, stage, flags);
-      before_stage = stage;
-      before_flags = flags;
+      if (flags & STOP) return true;
       if (++stage == STAGES) stage = 0, turn ^= 1;
+    }
+  };
+  auto issue_values = [&]() -> bool {
+    constexpr uint32_t id = E8 ? make_idesc_f8(D, N * WN, true, true, F8_E4M3, F8_E5M2) : make_idesc(D, N, true, false, false, !BF);
+    const uint64_t dv = make_sdesc(base + W::KV_BYTES, TILE * 128, EIGHT, SW);
+    const uint64_t dp = E8 ? make_sdesc(p_s, 128, TILE * 16, SW_NONE) : make_sdesc(p_s, 16, 1024, SW_128);
+    int of_unit = 0;  // the unit's tiles so far
+    for (int it = 0, stage = 0;; ++it) {
+      const int g = GROUPS == 2 ? it & 1 : 0;
+      if (!mbar_wait(&p_full[g], (it / GROUPS) & 1)) return false;
+      if (E8 && !s.use_tma) fence_proxy_async_smem();
+      const uint32_t flags = meta[stage].flags;
+      tc_fence_after_sync();
+      if (flags & FIRST) of_unit = 0;
+      const bool fresh = of_unit++ < GROUPS;  // the group's first tile of a unit
+      if (*reinterpret_cast<volatile int*>(&mark[it & 3]) != it) {  // else it was done by hand
+        const uint64_t a = dv + stage * (W::STAGE_BYTES >> 4), b = dp + g * (W::P_BYTES >> 4);
+#pragma unroll
+        for (int z = 0; z < WP / WN; ++z)
+#pragma unroll
+          for (int ks = 0; ks < TILE * W::ES / 32; ++ks)
+            product(tmem + T_O + g * W::O_COLS, a + ks * (E8 ? 2 * D : 128),
+                    b + (E8 ? z * (WN * NC * TILE) + ks * 32 : ((ks >> 2) * (N * 128) + (ks & 3) * 32) / 16), id,
+                    ks > 0 || z > 0 || !fresh);
+      }
+      umma_commit(&p_empty[g]);
+      umma_commit(&empty[stage]);
+      if (flags & STOP) return true;
+      if (++stage == STAGES) stage = 0;
     }
   };
 
   bool ok = true;
+  if (E8) {
+    if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(W::SOFTMAX_REGS));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(W::OTHER_REGS));
+  }
   if (warp < 8) {
     ok = softmax();
   } else if (warp == 8) {
     produce<D, E8, TILE, STAGES>(s, st, Ring{base, full, empty, told, meta}, map_k, map_v);
-  } else {
-    if (lane == 0) ok = issue();
+  } else if (warp < 11) {
+    if (lane == 0) ok = warp == 9 ? issue_scores() : issue_values();
     __syncwarp();
   }
   if (!ok) *p.status = 6;
