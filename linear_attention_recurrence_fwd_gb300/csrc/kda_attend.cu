@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(Shape<D, E8, WG>::THREADS, Shape<D, E8, WG>::C
   uint64_t* empty = full + 8;
   uint64_t* told = empty + 8;                              // a stage's Meta is written
   uint64_t* joined = told + 8;                             // the consumer warps' own barrier
-  Meta* meta = reinterpret_cast<Meta*>(joined + 1);       // [8]
+  Meta* meta = reinterpret_cast<Meta*>(joined + 2);       // [8]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

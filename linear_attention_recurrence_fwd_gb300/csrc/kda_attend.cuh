@@ -14,11 +14,11 @@ namespace kda {
 // its first and last tile are here (CLOSES: known at the last one; UNIT_CLOSES, UNIT_STOPS: at the first).
 enum : uint32_t { FIRST = 1, LAST = 2, STOP = 4, FULL = 8, OPENS = 16, CLOSES = 32, UNIT_CLOSES = 64, UNIT_STOPS = 128 };
 
-struct Meta {  // what the consumers need to know of a stage's tile
+struct alignas(16) Meta {  // what the consumers need to know of a stage's tile
   int n, hk, row0, pos0, len, count, end;
   uint32_t flags;
-  int tiles;          // of the unit, from this one on, in this CTA
   uint32_t valid[4];  // bit j: position pos0 + j lies in a page that exists
+  int tiles;          // of the unit, from this one on, in this CTA
 };
 
 struct Record {  // a unit that several CTAs hold parts of
@@ -191,10 +191,11 @@ struct Ring {
   Meta* meta;
 };
 
-// The producer warp's work: page look-ups, each stage's Meta, and the copies.
-template <int D, bool E8, int TILE, int STAGES>
+// A producer warp's work: page look-ups, each stage's Meta, and the copies.  Of PRODUCERS warps, this
+// one (`which`) takes every PRODUCERS-th tile.
+template <int D, bool E8, int TILE, int STAGES, int PRODUCERS = 1>
 __device__ __forceinline__ void produce(const Params& s, const Stretch& st, const Ring& ring, const CUtensorMap& map_k,
-                                        const CUtensorMap& map_v) {
+                                        const CUtensorMap& map_v, int which = 0) {
   constexpr int ROW_BYTES = D * (E8 ? 1 : 2), BOX_BYTES = ROW_BYTES < 128 ? ROW_BYTES : 128;
   constexpr int HALVES = ROW_BYTES / BOX_BYTES, KV_BYTES = TILE * ROW_BYTES, STAGE_BYTES = 2 * KV_BYTES;
   const AttendProblem& p = s.p;
@@ -216,6 +217,7 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
     int n, sub, j;     // tiles j .. of a unit
     Range r;
     int page[PL];       // as loaded: nothing waits for it here
+    int at[PL];         // the box's first row in its page
     uint32_t need[PL];  // lanes whose page is needed
   };
   auto look_up = [&](Batch& b) {
@@ -226,10 +228,14 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
       const bool need = (x == 0 || 32 * x < boxes) && b.j + (lane + 32 * x) / boxes < b.r.tiles &&
                         pos < b.r.end && pos + rows_per > first_seen;
       b.need[x] = __ballot_sync(0xffffffffu, need);
-      if (need) b.page[x] = p.cache.block_table[b.n * p.cache.table_stride + pos / p.cache.page_size];
+      if (need) {
+        const int entry = pos / p.cache.page_size;
+        b.page[x] = p.cache.block_table[b.n * p.cache.table_stride + entry];
+        b.at[x] = pos - entry * p.cache.page_size;
+      }
     }
   };
-  Batch cur{st.n0, st.sub0, st.tile_in, st.range, {}, {}};
+  Batch cur{st.n0, st.sub0, st.tile_in, st.range, {}, {}, {}};
   look_up(cur);
   int ahead_len = 0, ahead_count = p.K;
   auto read_ahead = [&](int n) {
@@ -256,11 +262,14 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
     if (next.n < N) look_up(next);
     const int n = cur.n, sub = cur.sub * s.team + member, tiles_here = min(batch, cur.r.tiles - cur.j);
     const Range& r = cur.r;
+    // of the unit: its key head, first row, and first and last token
+    const int hk = sub / s.groups, row0 = (sub - hk * s.groups) * s.rows_per;
+    const int i0 = row0 / s.group_heads, i1 = min(s.rows - 1, row0 + s.rows_per - 1) / s.group_heads;
+    const bool over = r.count && r.len + r.count > r.end && r.len + r.count > 0;
     for (int x = 0; x < tiles_here && !stop; ++x, ++it) {
     const int j = cur.j + x;
     const int stage = it % STAGES;
     const int pos0 = (r.tile0 + j) * TILE;
-    const int hk = sub / s.groups, row0 = (sub - hk * s.groups) * s.rows_per;
     const bool first = it == 0 || j == 0;
     if (first) opened_here = j == 0;
     const bool closes = j == r.tiles - 1;
@@ -268,7 +277,7 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
     const bool unit_stops = s.whole ? left == 1 : left == unit_tiles;
     if (!s.whole) --left; else if (closes) --left;
     stop = left == 0;
-    if (!s.whole && first && opened_here && lane == 0) {
+    if (!s.whole && first && opened_here && lane == 0 && which == 0) {
       // parts of this unit that other CTAs will hold
       const int last = a0 + it + r.tiles - 1, longer = extra * (each + 1);  // its last tile
       const int last_team = last < longer ? last / (each + 1) : extra + (last - longer) / each;
@@ -284,22 +293,26 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
         recorded = true;
       }
     }
+    if (PRODUCERS > 1 && it % PRODUCERS != which) continue;
     // lane b: the page of rows [b rows_per, (b + 1) rows_per) of the tile; of single rows b, b + 32, ...
     const int from = (x * boxes + lane) & 31;
-    int page[PL];
+    int page[PL], at[PL];
     uint32_t good[PL];
-    bool bad = false;
+    uint32_t wrong = 0;
 #pragma unroll
     for (int y = 0; y < PL; ++y) {
+      page[y] = -1;
+      good[y] = 0;
+      if (32 * y >= boxes) continue;  // the same for all lanes
       page[y] = y == 0 ? __shfl_sync(0xffffffffu, cur.page[0], from) : cur.page[y];
+      at[y] = y == 0 ? __shfl_sync(0xffffffffu, cur.at[0], from) : cur.at[y];
       const bool need = y == 0 ? lane < boxes && ((cur.need[0] >> from) & 1) : (cur.need[y] >> lane) & 1;
       const bool ok = need && page[y] >= 0 && page[y] < p.cache.num_pages;
-      bad |= need != ok;
       if (!ok) page[y] = -1;
       good[y] = __ballot_sync(0xffffffffu, ok);
+      wrong |= __ballot_sync(0xffffffffu, need) & ~good[y];
     }
-    bad = __any_sync(0xffffffffu, bad);
-    const bool over = r.count && r.len + r.count > r.end && r.len + r.count > 0;
+    const bool bad = wrong != 0;
     if (lane == 0 && (bad || (over && first))) *p.status = 1;
     if (it >= STAGES && !mbar_wait(&empty[stage], ((it / STAGES) - 1) & 1)) {
       *p.status = 6;
@@ -323,7 +336,6 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
           if ((good[b >> 5] >> (b & 31)) & 1) m.valid[y >> 5] |= 1u << (y & 31);
         }
       }
-      const int i0 = row0 / s.group_heads, i1 = min(s.rows - 1, row0 + s.rows_per - 1) / s.group_heads;
       const bool all = !bad && pos0 + TILE <= r.end && i1 < r.count && pos0 + TILE - 1 <= r.len + i0 &&
                        !(p.window && r.len + i1 >= p.window && pos0 < r.len + i1 - p.window + 1);
       m.flags = (first ? FIRST : 0) | (closes || stop ? LAST : 0) | (stop ? STOP : 0) | (all ? FULL : 0) |
@@ -337,15 +349,15 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
         uint32_t boxes_here = 0;
 #pragma unroll
         for (int y = 0; y < PL; ++y) boxes_here += __popc(good[y]);
-        const uint32_t bytes = boxes_here * s.box_rows * ROW_BYTES * 2;
+        const uint32_t bytes = boxes_here * rows_per * ROW_BYTES * 2;
         if (bytes) mbar_arrive_expect_tx(&full[stage], bytes); else mbar_arrive(&full[stage]);
       }
       __syncwarp();
 #pragma unroll
       for (int y = 0; y < PL; ++y) {
         if (page[y] < 0) continue;
-        const int row = (lane + 32 * y) * s.box_rows, at = (pos0 + row) % p.cache.page_size;
-        const int c1 = s.token_first ? at : hk, c2 = s.token_first ? hk : at;
+        const int row = (lane + 32 * y) * rows_per;
+        const int c1 = s.token_first ? at[y] : hk, c2 = s.token_first ? hk : at[y];
 #pragma unroll
         for (int h = 0; h < HALVES; ++h) {
           const uint32_t off = h * TILE * BOX_BYTES + row * BOX_BYTES;
@@ -382,7 +394,7 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
     }
     cur = next;
   }
-  if (!s.whole && !s.by_unit && !recorded && lane == 0) s.records[c].more = 0;
+  if (!s.whole && !s.by_unit && !recorded && lane == 0 && which == 0) s.records[c].more = 0;
 }
 
 // More than 16 query rows to a key head, or an 8-bit cache (kda_attend_wide.cu).

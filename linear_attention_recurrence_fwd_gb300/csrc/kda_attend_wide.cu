@@ -20,7 +20,7 @@
 // keys and values would have to be converted through shared memory, whose
 // bandwidth the products' operands take already (295 us against 278 us).
 //
-// Warps: 0-7 softmax (a thread has half of the rows), 8 producer, 9 and 10 issue the products.  One CTA on an SM.
+// Warps: 0-7 softmax (a thread has half of the rows), 8 and 11 load, 9 and 10 issue the products.  One CTA on an SM.
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -34,8 +34,8 @@ template <typename A, int D, bool E8> struct Wide {
   // Softmax warps: two groups that take tiles in turn, or one of which each half has half of the rows
   static constexpr int GROUPS = E8 ? 2 : 1;
   // The launch's registers are split anew where a thread has all rows; the sum stays what it was.
-  static constexpr int THREADS = E8 ? 384 : 352;
-  static constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 200, OTHER_REGS = 104;
+  static constexpr int THREADS = 384;
+  static constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 192, OTHER_REGS = 120;
   static_assert(!E8 || 8 * SOFTMAX_REGS + 4 * OTHER_REGS <= 12 * LAUNCH_REGS, "registers");
   static constexpr int ES = E8 ? 1 : 2;                  // bytes of a cached element
   static constexpr int QP = E8 ? (__is_same(A, __nv_bfloat16) ? 2 : 3) : 1, WP = E8 ? QP + 1 : 1;
@@ -767,8 +767,8 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
   }
   if (warp < 8) {
     ok = softmax();
-  } else if (warp == 8) {
-    produce<D, E8, TILE, STAGES>(s, st, Ring{base, full, empty, told, meta}, map_k, map_v);
+  } else if (warp == 8 || warp == 11) {
+    produce<D, E8, TILE, STAGES, 2>(s, st, Ring{base, full, empty, told, meta}, map_k, map_v, warp == 11);
   } else if (warp < 11) {
     if (lane == 0) ok = warp == 9 ? issue_scores() : issue_values();
     __syncwarp();
