@@ -138,8 +138,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
   int* rows_lo = reinterpret_cast<int*>(keep + 96);  // [4][48] first and last position that a row sees,
   int* rows_hi = rows_lo + 192;                      // [4][48] for four tiles in turn
   long long* row_to = reinterpret_cast<long long*>(rows_hi + 192);  // [48] where a row's output goes
-  long long* row_from = row_to + 48;                // [48] where its query is, or -1
-  int* mark = reinterpret_cast<int*>(row_from + 48);  // [4]: the tile whose values are multiplied by hand, four in turn
+  int* mark = reinterpret_cast<int*>(row_to + 48);  // [4]: the tile whose values are multiplied by hand, four in turn
   int* give_up = mark + 4;                          // [group] a softmax warp met a limit
   uint64_t* bars = reinterpret_cast<uint64_t*>(give_up + 4);
   uint64_t *full = bars, *empty = bars + 6, *told = bars + 12;
@@ -284,54 +283,55 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       }
     };
 
-    // A unit, from its first tile's stage: its rows' tables, then its queries: as they are, or in pieces.
+    // A unit, from its first tile's stage, and its queries on their way: a thread's chunks of 8 channels.
     int u_n, u_hk, u_row0, u_tiles;
     uint32_t u_flags;
-    auto load_queries = [&](int stage, int turn, int odd) {
+    constexpr int ALL = N * (D / 8), EACH = (ALL + 255) / 256;
+    uint4 q[EACH];
+    auto fetch_queries = [&](int stage, int turn) {
       if (!wait(&told[stage], turn)) return false;
       const Meta& t = meta[stage];
-      const int n = t.n, hk = t.hk, row0 = t.row0;
-      u_n = n, u_hk = hk, u_row0 = row0, u_tiles = t.tiles, u_flags = t.flags;
+      u_n = t.n, u_hk = t.hk, u_row0 = t.row0, u_tiles = t.tiles, u_flags = t.flags;
+#pragma unroll
+      for (int z = 0; z < EACH; ++z) {
+        q[z] = make_uint4(0, 0, 0, 0);
+        const int gr = u_row0 + (tid + z * 256) / (D / 8), i = gr / s.group_heads;
+        if (gr < s.rows && tid + z * 256 < ALL)
+          q[z] = *reinterpret_cast<const uint4*>(static_cast<const A*>(p.q) + ((long long)u_n * p.K + i) * p.q_stride +
+                                                 (u_hk * s.group_heads + gr - i * s.group_heads) * D + tid % (D / 8) * 8);
+      }
+      return true;
+    };
+    // Its rows' tables, then its queries to shared memory: as they are, or in pieces.
+    auto place_queries = [&](int odd) {
       if (tid < N) {
-        const int gr = row0 + tid, i = gr / s.group_heads;
-        const bool real = gr < s.rows;
+        const int gr = u_row0 + tid;
         for (int x = 0; x < GROUPS; ++x) {
           row_m[x * 96 + odd * 48 + tid] = -INFINITY;
           row_neg[x * 96 + odd * 48 + tid] = UNSEEN;
         }
-        row_tok[odd * 48 + tid] = real ? i : 0x3fffffff;
-        row_from[tid] = real ? ((long long)n * p.K + i) * p.q_stride + (hk * s.group_heads + gr - i * s.group_heads) * D : -1;
+        row_tok[odd * 48 + tid] = gr < s.rows ? gr / s.group_heads : 0x3fffffff;
       }
-      if (!sync_all()) return false;
-      constexpr int ALL = N * (D / 8), EACH = (ALL + 255) / 256;  // chunks of 8 channels: a thread's are on their way together
-      uint4 q[EACH];
       const int ch = tid % (D / 8);
-#pragma unroll
-      for (int z = 0; z < EACH; ++z) {
-        if (ALL % 256 && tid + z * 256 >= ALL) break;  // (whole warps)
-        const long long from = row_from[(tid + z * 256) / (D / 8)];
-        q[z] = from < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(static_cast<const A*>(p.q) + from + ch * 8);
-      }
       if constexpr (E8) {
 #pragma unroll 1
         for (int z = 0; z < EACH; ++z) {
-          if (ALL % 256 && tid + z * 256 >= ALL) break;
-          const int row = (tid + z * 256) / (D / 8);
-          write_pieces(q[0], row, ch, odd);
+          if (ALL % 256 && tid + z * 256 >= ALL) break;  // (whole warps)
+          write_pieces(q[0], (tid + z * 256) / (D / 8), ch, odd);
 #pragma unroll
           for (int y = 0; y + 1 < EACH; ++y) q[y] = q[y + 1];
         }
-      } else
+      } else {
 #pragma unroll
-      for (int z = 0; z < EACH; ++z) {
-        if (ALL % 256 && tid + z * 256 >= ALL) break;
-        const int row = (tid + z * 256) / (D / 8);
-        st_shared_v4(q_s + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), q[z].x, q[z].y, q[z].z, q[z].w);
+        for (int z = 0; z < EACH; ++z) {
+          if (ALL % 256 && tid + z * 256 >= ALL) break;
+          const int row = (tid + z * 256) / (D / 8);
+          st_shared_v4(q_s + (ch >> 3) * (N * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), q[z].x, q[z].y, q[z].z, q[z].w);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      return true;
     };
 
     float sums[CH][8];  // of this position's weights of each row, over the unit's tiles
@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
       ++it;
       if (++stage == STAGES) stage = 0, turn ^= 1;
     };
-    if (!load_queries(0, 0, 0)) return false;
+    if (!fetch_queries(0, 0)) return false;
+    place_queries(0);
+    if (!sync_all()) return false;
     while (true) {
     const int n = u_n, hk = u_hk, row0 = u_row0, tiles = u_tiles;
     const uint32_t unit = u_flags;
@@ -622,8 +624,9 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
     }
     // ---- the unit's end.  The next unit's queries first: its first product need not wait for what follows
     const bool stop = unit & UNIT_STOPS;
+    if (!stop && !fetch_queries(stage, turn)) return false;
     if (!sync_all()) return false;  // all scores have been formed
-    if (!stop && !load_queries(stage, turn, odd ^ 1)) return false;
+    if (!stop) place_queries(odd ^ 1);
     // the rows' sums: over the warp's positions, then the warps
 #pragma unroll
     for (int y = 0; y < CH; ++y) {
