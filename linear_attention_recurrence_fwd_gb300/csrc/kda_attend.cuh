@@ -397,7 +397,7 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
   if (!s.whole && !s.by_unit && !recorded && lane == 0 && which == 0) s.records[c].more = 0;
 }
 
-// More than 16 query rows to a key head, or an 8-bit cache (kda_attend_wide.cu).
+// More than 16 query rows to a key head (kda_attend_wide.cu).
 cudaError_t launch_attend_wide(const Params& s, const CUtensorMap& map_k, const CUtensorMap& map_v, int grid,
                                cudaStream_t stream);
 

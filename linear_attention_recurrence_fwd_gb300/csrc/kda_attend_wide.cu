@@ -1,26 +1,43 @@
 // kda_cache_attend where 17 to 48 query rows share a key head (several tokens,
-// many heads to a key head) over a 16-bit cache: both products on the tcgen05
-// tensor cores, with positions and output channels on their lanes.
+// many heads to a key head): both products on the tcgen05 tensor cores, with
+// positions and output channels on their lanes.
 //
 //     S^T [128 positions x N rows] = K Q^T      (A: keys as TMA lays them, B: Q)
 //     O^T [d channels x N rows]   += V^T P^T    (A: values, read transposed, B: P)
 //
 // N is 32 or 48: with the rows on the 128 lanes most would be padding.  A
-// thread of the four softmax warps has one position: it turns that position's
-// N scores into weights with no exchange between lanes, since the rows' maxima
-// are kept from earlier tiles as long as no score passes one by 2^8, and the
-// sums of the weights are kept by thread until the unit ends.  When a score
-// does pass (and at a unit's start), the maxima are found across the lanes and
-// O and the sums are rescaled.  What runs once a unit is written as loops, not
-// unrolled: its time is that of fetching instructions.
+// thread of the softmax warps has one position: it turns that position's
+// scores into weights with no exchange between lanes, since the rows' maxima
+// are kept from earlier tiles as long as no score passes one by 2^8 (2^3 for
+// an 8-bit cache), and the sums of the weights are kept by thread until the
+// unit ends.  When a score does pass (and at a unit's start), the maxima are
+// found across the lanes and O and the sums are rescaled.  What runs once a
+// unit is written as loops, not unrolled: its time is that of fetching
+// instructions.
 //
-// Against warp-level instructions (kda_attend.cu, 16 rows to a group of warps),
-// which run at an eighth of tcgen05's rate: 64 requests of 8192 positions with
-// 40 rows, 347 us there and 203 us here.  An 8-bit cache stays there: here its
-// keys and values would have to be converted through shared memory, whose
-// bandwidth the products' operands take already (295 us against 278 us).
+// An 8-bit cache's keys and values are operands as they are (kind::f8f6f4): no
+// byte is converted.  The other operand comes in 8-bit pieces instead.  A query
+// q is q_1 + q_2 / 16 (+ q_3 / 256), e4m3 numbers of 4 bits each, their scores
+// side by side in N; a weight is the sum of 3 (fp16 queries: 4) e5m2 numbers of
+// 3 bits each, whose products lie side by side in O and are added at the
+// unit's end.  The accumulators are fp32.  The weights are 2^(s - m + 12), so
+// that their pieces are normal numbers down to 2^-26 of the largest.  (e4m3
+// pieces of the weights would leave absolute errors of 2^-18 of the largest,
+// which a million small weights add up.)
 //
-// Warps: 0-7 softmax (a thread has half of the rows), 8 and 11 load, 9 and 10 issue the products.  One CTA on an SM.
+// Against warp-level instructions, which run at an eighth of tcgen05's rate (64
+// requests of 8192 positions, 4 key heads of 128, 40 rows): 347 us there and
+// 180 us here, 6.0 TB/s.  8-bit: 277 us there (each group of 16 rows converts
+// all keys and values), 258 us here with keys and values converted through
+// shared and tensor memory, 139 us in pieces (3.9 TB/s; a tile takes 1620
+// clocks, of which its bytes need 1400, and a unit's end and start 14000).
+//
+// Warps: 0-7 softmax, 8 and 11 load, 9 and 10 issue the scores and the values.
+// The softmax warps are one group of which each half has half of the rows; or,
+// over an 8-bit cache, two groups that take tiles in turn, each with maxima,
+// sums, weights and an O of its own (as one group 146 us: the latencies of one
+// tile's steps add up to 2100 clocks).  One loading warp spends 2000 clocks on
+// a tile, more than its bytes take.  One CTA on an SM.
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -441,7 +458,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           // ---- new maxima: over the warp's positions, then over the warps
           if (!done && !wait(o_done, (done_before - 1) & 1)) return false;
           tc_fence_after_sync();
-#pragma unroll 1
+#pragma unroll (E8 ? 2 : 1)
           for (int y = 0; y < CH; ++y) {
             float w[8], more[QP][8];
             tmem_ld8(scores + y * 8, w);

@@ -369,3 +369,54 @@ def test_pages_whose_rows_are_interleaved(Hq):
     out = binding.kda_cache_attend(q[:1].cuda(), odd)
     ref, _, tol, _ = attend_reference(q[:1], keys, values, [9], None, d ** -0.5, 0)
     assert_within(out, ref, tol, "out")
+
+
+@pytest.mark.parametrize("length", [40, 5000])
+@pytest.mark.parametrize("rows", [4, 40])
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_nan_in_a_query_reaches_its_own_row_alone(dtype, rows, length):
+    """A row all of whose scores are NaN has no maximum; it must not pass for one that sees nothing."""
+    K, Hq, d = (1, 4, 128) if rows == 4 else (5, 8, 128)
+    cache, keys, values = make_cache([length], K, 1, d, 64, dtype)
+    q = torch.randn((1, K, Hq, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    q[0, 0, 1, 3] = NAN
+    out, lse = binding.kda_cache_attend(q.cuda(), cache, return_lse=True)
+    assert torch.isnan(out[0, 0, 1].float()).all() and torch.isnan(lse[0, 0, 1])
+    q[0, 0, 1] = 0
+    ref, rlse, tol, ltol = attend_reference(q, keys, values, [length], None, d ** -0.5, 0)
+    out[0, 0, 1], lse[0, 0, 1] = ref[0, 0, 1], rlse[0, 0, 1]
+    assert_within(lse, rlse, ltol, "lse")
+    assert_within(out, ref, tol + 2.0 ** -8 * ref.abs(), "out")
+
+
+@pytest.mark.parametrize("act", [BF, FP])
+def test_many_rows_8_bit_queries_of_all_sizes(act):
+    """Rows whose entries lie far apart, and rows far above and below the others."""
+    K, Hq, d, lens = 5, 8, 128, [700]
+    cache, keys, values = make_cache(lens, K, 1, d, 64, E4)
+    g = torch.Generator().manual_seed(9)
+    q = torch.randn((1, K, Hq, d), generator=g) * 2.0 ** torch.randint(-12, 1, (1, K, Hq, d), generator=g)
+    q = (q * 2.0 ** torch.randint(-10, 4, (1, K, Hq, 1), generator=g)).to(act)
+    out, lse = binding.kda_cache_attend(q.cuda(), cache, return_lse=True)
+    ref, rlse, tol, ltol = attend_reference(q, keys, values, lens, None, d ** -0.5, 0)
+    assert_within(lse, rlse, ltol, "lse")
+    assert_within(out, ref, tol, "out")
+
+
+def test_many_rows_8_bit_many_small_weights_beside_a_large_one():
+    """One score 2^20 times the weight of each of 60000 others: together they still count."""
+    K, Hq, d, length = 5, 8, 128, 60000
+    cache, keys, values = make_cache([length], K, 1, d, 64, E4)
+    k = torch.zeros_like(cache.k_pages, dtype=torch.float32)
+    page = int(cache.block_table[0, 0])
+    k[page, 5, 0, 0] = 16.0
+    cache.k_pages.copy_(k.to(E4))
+    keys[0].zero_()
+    keys[0][5, 0, 0] = 16.0
+    q = torch.zeros((1, K, Hq, d))
+    q[..., 0] = 13.875 / 16 * d ** 0.5
+    q = q.to(BF)
+    out, lse = binding.kda_cache_attend(q.cuda(), cache, return_lse=True)
+    ref, rlse, tol, ltol = attend_reference(q, keys, values, [length], None, d ** -0.5, 0)
+    assert_within(lse, rlse, ltol, "lse")
+    assert_within(out, ref, tol, "out")
