@@ -14,9 +14,10 @@
 //
 // Sums: an fp32 running sum over 10^5 weights is off by about 10^-7 of the
 // total, enough to change a token in every few hundred draws, and fp64 runs at
-// a 64th of fp32's rate here.  Threads therefore sum pairs of fp32 numbers
-// (hi + lo, with the exact error of every difference and sum; Knuth's two-sum),
-// which holds 48 bits; sums of threads are fp64.
+// a 64th of fp32's rate here (40 such instructions in every warp were a third
+// of the call).  All sums are therefore pairs of fp32 numbers (hi + lo, with
+// the exact error of every difference and sum; Knuth's two-sum), which hold 48
+// bits.
 #include "kda_internal.h"
 #include "kda_types.cuh"
 
@@ -25,43 +26,46 @@ namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32, MOST = 8;  // CTAs of a cluster
 
-struct Sum {
-  float hi = 0.f, lo = 0.f;
-  // adds x + e, |e| far below |x|
-  __device__ __forceinline__ void add(float x, float e) {
-    const float t = hi + x, z = t - hi;
-    lo += ((hi - (t - z)) + (x - z)) + e;
-    hi = t;
-  }
-  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
-};
-
-// The weight max(p - q, 0) as x + e, exactly; 0 where it is not finite.
-__device__ __forceinline__ void difference(float p, float q, float& x, float& e) {
-  x = p - q;
-  const float z = x - p;
-  e = (p - (x - z)) - (q + z);
-  if (!(x > 0.f && x < INFINITY)) x = e = 0.f;
-}
-
 struct Row {
   const void* top;  // the target's probabilities
   const void* low;  // the draft model's, or null
   int skip;         // an entry without weight, or -1
 };
 
-// a weight in fp64
-template <typename T> __device__ __forceinline__ double weight(const Row& r, int j) {
-  double w = (double)to_f32(static_cast<const T*>(r.top)[j]);
-  if (r.low) w -= (double)to_f32(static_cast<const T*>(r.low)[j]);
-  return w > 0. && w < (double)INFINITY && j != r.skip ? w : 0.;
+// A number as hi + lo, hi the sum rounded to fp32.
+struct Pair {
+  float hi = 0.f, lo = 0.f;
+};
+__device__ __forceinline__ Pair normal(float hi, float lo) {
+  const float s = hi + lo;
+  return Pair{s, lo - (s - hi)};
+}
+__device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) {
+  const float s = a.hi + b.hi, z = s - a.hi;
+  return normal(s, ((a.hi - (s - z)) + (b.hi - z)) + (a.lo + b.lo));
+}
+__device__ __forceinline__ Pair operator*(float u, const Pair& a) {
+  const float x = u * a.hi;
+  return normal(x, fmaf(u, a.lo, fmaf(u, a.hi, -x)));
+}
+__device__ __forceinline__ bool operator>(const Pair& a, const Pair& b) {
+  return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+}
+__device__ __forceinline__ Pair shfl(const Pair& a, int lane) {
+  return Pair{__shfl_sync(0xffffffffu, a.hi, lane), __shfl_sync(0xffffffffu, a.lo, lane)};
+}
+__device__ __forceinline__ Pair shfl_up(const Pair& a, int by) {
+  return Pair{__shfl_up_sync(0xffffffffu, a.hi, by), __shfl_up_sync(0xffffffffu, a.lo, by)};
+}
+__device__ __forceinline__ Pair shfl_xor(const Pair& a, int by) {
+  return Pair{__shfl_xor_sync(0xffffffffu, a.hi, by), __shfl_xor_sync(0xffffffffu, a.lo, by)};
 }
 
-template <typename T> __device__ __forceinline__ void add_one(Sum& s, const Row& r, int j, float p, float q) {
-  float x, e;
-  difference(p, q, x, e);
-  if (j == r.skip) x = e = 0.f;
-  s.add(x, e);
+// The weight of an entry: max(p - q, 0), exactly; 0 where it is not finite.
+template <typename T> __device__ __forceinline__ Pair weight(const Row& r, int j) {
+  const float p = to_f32(static_cast<const T*>(r.top)[j]), q = r.low ? to_f32(static_cast<const T*>(r.low)[j]) : 0.f;
+  const float x = p - q, z = x - p;
+  return x > 0.f && x < INFINITY && j != r.skip ? Pair{x, (p - (x - z)) - (q + z)} : Pair{};
 }
 
 // Two fp32 numbers in a register pair, and their sums and differences.
@@ -83,7 +87,7 @@ __device__ __forceinline__ uint64_t sub2(uint64_t x, uint64_t y) {
   asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
   return r;
 }
-// Sum, two at a time
+// Two sums, each of two fp32 numbers; what is added is x + e, |e| far below |x|.
 struct Sum2 {
   uint64_t hi = 0, lo = 0;
   __device__ __forceinline__ void add(uint64_t x, uint64_t e) {
@@ -91,7 +95,7 @@ struct Sum2 {
     lo = add2(lo, add2(add2(sub2(hi, sub2(t, z)), sub2(x, z)), e));
     hi = t;
   }
-  // the weights of two entries
+  // the weights max(p - q, 0) of two entries, exactly; 0 where one is not finite
   __device__ __forceinline__ void add(float p0, float p1, float q0, float q1) {
     const uint64_t p = pack(p0, p1), q = pack(q0, q1);
     const uint64_t x = sub2(p, q), z = sub2(x, p), e = sub2(sub2(p, sub2(x, z)), add2(q, z));
@@ -102,17 +106,17 @@ struct Sum2 {
     const bool ok0 = __float_as_uint(x0) - 1u < 0x7f7fffffu, ok1 = __float_as_uint(x1) - 1u < 0x7f7fffffu;
     add(pack(ok0 ? x0 : 0.f, ok1 ? x1 : 0.f), pack(ok0 ? e0 : 0.f, ok1 ? e1 : 0.f));
   }
-  __device__ __forceinline__ double value() const {
+  __device__ __forceinline__ Pair value() const {
     float a, b, c, d;
     unpack(hi, a, b);
     unpack(lo, c, d);
-    return ((double)a + (double)c) + ((double)b + (double)d);
+    return normal(a, c) + normal(b, d);
   }
 };
 
 // This lane's share of the weights of [j0, j1), 16 bytes at a time; the next
 // bytes are on their way while these are summed.
-template <typename T> __device__ __forceinline__ double sum_vectors(const Row& r, int j0, int j1, int lane) {
+template <typename T> __device__ __forceinline__ Pair sum_vectors(const Row& r, int j0, int j1, int lane) {
   constexpr int VE = 16 / sizeof(T), AHEAD = 2, STEP = 32 * VE * AHEAD;
   Sum2 s;
   uint4 a[2][AHEAD], b[2][AHEAD];
@@ -152,10 +156,10 @@ template <typename T> __device__ __forceinline__ double sum_vectors(const Row& r
   return s.value();
 }
 
-// The same, one entry at a time (rows that do not start on 16 bytes), `step` apart from j0 on
-template <typename T> __device__ __forceinline__ Sum sum_entries(const Row& r, int j0, int j1, int step) {
-  constexpr int AHEAD = 8;
-  Sum s;
+// The same, one entry at a time (rows that do not start on 16 bytes), `step` apart from j0 on; AHEAD
+// loads are on their way together.
+template <int AHEAD, typename T> __device__ __forceinline__ Pair sum_entries(const Row& r, int j0, int j1, int step) {
+  Sum2 s;
   for (int j = j0; j < j1; j += step * AHEAD) {
     float a[AHEAD], b[AHEAD];
 #pragma unroll
@@ -165,19 +169,20 @@ template <typename T> __device__ __forceinline__ Sum sum_entries(const Row& r, i
       if (at < j1) {
         a[x] = to_f32(static_cast<const T*>(r.top)[at]);
         if (r.low) b[x] = to_f32(static_cast<const T*>(r.low)[at]);
+        if (at == r.skip) a[x] = 0.f;
       }
     }
 #pragma unroll
-    for (int x = 0; x < AHEAD; ++x) add_one<T>(s, r, j + x * step, a[x], b[x]);
+    for (int x = 0; x < AHEAD; x += 2) s.add(a[x], a[x + 1], b[x], b[x + 1]);
   }
-  return s;
+  return s.value();
 }
 
-__device__ __forceinline__ double warp_scan(double s, int lane) {
+__device__ __forceinline__ Pair warp_scan(Pair s, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
+    const Pair y = shfl_up(s, o);
+    if (lane >= o) s = s + y;
   }
   return s;
 }
@@ -191,17 +196,19 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // stores x at the place of `local` in the shared memory of the cluster's CTA `rank`
-__device__ __forceinline__ void store_remote(const double* local, uint32_t rank, double x) {
+__device__ __forceinline__ void store_remote(const Pair* local, uint32_t rank, const Pair& x) {
   uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
-  asm volatile("{.reg .u32 r; mapa.shared::cluster.u32 r, %0, %1; st.shared::cluster.f64 [r], %2;}" ::"r"(at), "r"(rank),
-               "d"(x) : "memory");
+  asm volatile("{.reg .u32 r; mapa.shared::cluster.u32 r, %0, %1; st.shared::cluster.v2.f32 [r], {%2, %3};}" ::"r"(at), "r"(rank),
+               "f"(x.hi), "f"(x.lo) : "memory");
 }
 
 template <typename T>
 __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constant__ AcceptProblem p, int cluster) {
-  __shared__ double s_slice[2][MOST * WARPS];  // the slices' sums, for each of two attempts
-  __shared__ double s_warp[WARPS];
+  __shared__ __align__(8) float2 s_slices[2][MOST * WARPS];  // the slices' sums, for each of two attempts
+  __shared__ float2 s_warps[WARPS];
   __shared__ int s_next;
+  Pair(*const s_slice)[MOST * WARPS] = reinterpret_cast<Pair(*)[MOST * WARPS]>(s_slices);
+  Pair* const s_warp = reinterpret_cast<Pair*>(s_warps);
   const int rank = cluster == 1 ? 0 : (int)cluster_rank();
   const int n = blockIdx.x / cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = p.K, V = p.V;
@@ -223,8 +230,11 @@ __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constan
       const int t = toks[i];
       outside = t < 0 || t >= V;
       if (!outside) {
-        const double qt = draft ? (double)to_f32(draft[i * p.draft_stride_k + t]) : 1.;
-        ok = (double)u[i] * qt < (double)to_f32(target[i * p.target_stride_k + t]);
+        const float qt = draft ? to_f32(draft[i * p.draft_stride_k + t]) : 1.f, pt = to_f32(target[i * p.target_stride_k + t]);
+        // u q < p for the exact product: its rounding error is exact too, unless it falls below 2^-149
+        const float uq = u[i] * qt;
+        ok = uq < pt || (uq == pt && fmaf(u[i], qt, -uq) < 0.f);
+        if (uq < 0x1p-100f) ok = (double)u[i] * (double)qt < (double)pt;
       }
     }
     const unsigned stop = __ballot_sync(0xffffffffu, !ok || i >= len);
@@ -252,13 +262,13 @@ __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constan
   const int L = E * THREADS;
   const auto odd = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15u) != 0; };
   const bool vectors = !odd(row.top) && !(row.low && odd(row.low)) && V % (16 / sizeof(T)) == 0;
-  double goal = 0., before = 0.;
+  Pair goal, before;
   int slice = -1;
   for (int attempt = 0; attempt < 2; ++attempt) {
     const int j0 = (int)min((long long)mine * L, (long long)V), j1 = (int)min((long long)j0 + L, (long long)V);
-    double total = vectors ? sum_vectors<T>(row, j0, j1, lane) : sum_entries<T>(row, j0 + lane, j1, 32).value();
+    Pair total = vectors ? sum_vectors<T>(row, j0, j1, lane) : sum_entries<8, T>(row, j0 + lane, j1, 32);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    for (int o = 16; o > 0; o >>= 1) total = total + shfl_xor(total, o);
     if (cluster == 1) {
       if (lane == 0) s_slice[attempt][mine] = total;
       __syncthreads();
@@ -267,30 +277,30 @@ __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constan
       cluster_sync();
     }
     // every warp finds the slice that holds the border: the first whose running sum passes the goal
-    double x = lane * 2 < slices ? s_slice[attempt][lane * 2] : 0., y = lane * 2 + 1 < slices ? s_slice[attempt][lane * 2 + 1] : 0.;
-    const double end = warp_scan(x + y, lane);       // after slice 2 lane + 1
-    const double start = __shfl_up_sync(0xffffffffu, end, 1);
-    const double first = lane ? start : 0.;          // before slice 2 lane
-    const double middle = first + x;
-    const double all = __shfl_sync(0xffffffffu, end, 31);
-    if (!(all > 0.)) {
+    const Pair x = lane * 2 < slices ? s_slice[attempt][lane * 2] : Pair{}, y = lane * 2 + 1 < slices ? s_slice[attempt][lane * 2 + 1] : Pair{};
+    const Pair end = warp_scan(x + y, lane);       // after slice 2 lane + 1
+    const Pair start = shfl_up(end, 1);
+    const Pair first = lane ? start : Pair{};      // before slice 2 lane
+    const Pair middle = first + x;
+    const Pair all = shfl(end, 31);
+    if (!(all.hi > 0.f)) {
       if (!row.low && row.skip < 0) break;
       row.low = nullptr;  // no weight is positive: the target's own probabilities
       row.skip = -1;
       continue;
     }
-    goal = (double)u_last * all;
-    const unsigned in_x = __ballot_sync(0xffffffffu, x > 0. && middle > goal);
-    const unsigned in_y = __ballot_sync(0xffffffffu, y > 0. && end > goal);
+    goal = u_last * all;
+    const unsigned in_x = __ballot_sync(0xffffffffu, x.hi > 0.f && middle > goal);
+    const unsigned in_y = __ballot_sync(0xffffffffu, y.hi > 0.f && end > goal);
     const int kx = in_x ? __ffs(in_x) - 1 : 32, ky = in_y ? __ffs(in_y) - 1 : 32;
     if (kx == 32 && ky == 32) {  // rounding (or u = 1): the last slice that has weight
-      const unsigned has_x = __ballot_sync(0xffffffffu, x > 0.), has_y = __ballot_sync(0xffffffffu, y > 0.);
+      const unsigned has_x = __ballot_sync(0xffffffffu, x.hi > 0.f), has_y = __ballot_sync(0xffffffffu, y.hi > 0.f);
       const int lx = has_x ? 31 - __clz(has_x) : -1, ly = has_y ? 31 - __clz(has_y) : -1;
       slice = ly >= lx ? 2 * ly + 1 : 2 * lx;
     } else {
       slice = kx <= ky ? 2 * kx : 2 * ky + 1;
     }
-    before = __shfl_sync(0xffffffffu, slice & 1 ? middle : first, slice >> 1);
+    before = shfl(slice & 1 ? middle : first, slice >> 1);
     break;
   }
   // all of the cluster's shared memory has been written: its CTAs go on alone
@@ -301,31 +311,34 @@ __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constan
   if (slice >= 0) {
     const long long s0 = (long long)slice * L;
     const int j0 = (int)min(s0 + tid * E, (long long)V), j1 = (int)min((long long)j0 + E, (long long)V);
-    const double mine_sum = sum_entries<T>(row, j0, j1, 1).value();
-    double scan = warp_scan(mine_sum, lane);
+    // (pieces of few entries: loads past a piece's end are not free)
+    const Pair mine_sum = E <= 2   ? sum_entries<2, T>(row, j0, j1, 1)
+                          : E <= 4 ? sum_entries<4, T>(row, j0, j1, 1)
+                                   : sum_entries<8, T>(row, j0, j1, 1);
+    const Pair scan = warp_scan(mine_sum, lane);
     if (tid == 0) s_next = -1;
     if (lane == 31) s_warp[warp] = scan;
     __syncthreads();
-    double base = before;
-    for (int w = 0; w < warp; ++w) base += s_warp[w];
+    Pair base = before;
+    for (int w = 0; w < warp; ++w) base = base + s_warp[w];
+    const Pair to_here = shfl_up(scan, 1), from = lane ? base + to_here : base;  // before this piece
     // the first piece that passes the goal, or else (rounding) the last that has weight: candidates
     // are numbered so that one maximum decides
-    const bool passes = mine_sum > 0. && base + scan > goal;
-    if (mine_sum > 0.) atomicMax(&s_next, passes ? 2 * THREADS - tid : tid);
+    const bool passes = mine_sum.hi > 0.f && base + scan > goal;
+    if (mine_sum.hi > 0.f) atomicMax(&s_next, passes ? 2 * THREADS - tid : tid);
     __syncthreads();
     const int piece = s_next >= THREADS ? 2 * THREADS - s_next : s_next;
     if (piece >= 0 && piece / 32 == warp) {
-      const double at = __shfl_sync(0xffffffffu, base + scan - mine_sum, piece & 31);
+      Pair run = shfl(from, piece & 31);
       const int p0 = (int)min(s0 + (long long)piece * E, (long long)V), p1 = (int)min((long long)p0 + E, (long long)V);
-      double run = at;
       int last = -1;
       for (int q0 = p0; q0 < p1 && next < 0; q0 += 32) {
-        const double w = q0 + lane < p1 ? weight<T>(row, q0 + lane) : 0.;
-        const double sum = run + warp_scan(w, lane);
-        const unsigned pass = __ballot_sync(0xffffffffu, w > 0. && sum > goal), has = __ballot_sync(0xffffffffu, w > 0.);
+        const Pair w = q0 + lane < p1 ? weight<T>(row, q0 + lane) : Pair{};
+        const Pair sum = run + warp_scan(w, lane);
+        const unsigned pass = __ballot_sync(0xffffffffu, w.hi > 0.f && sum > goal), has = __ballot_sync(0xffffffffu, w.hi > 0.f);
         if (pass) next = q0 + __ffs(pass) - 1;
         if (has) last = q0 + 31 - __clz(has);
-        run = __shfl_sync(0xffffffffu, sum, 31);
+        run = shfl(sum, 31);
       }
       if (next < 0) next = last;
       if (lane == 0) {
