@@ -38,6 +38,8 @@
 // sums, weights and an O of its own (as one group 146 us: the latencies of one
 // tile's steps add up to 2100 clocks).  One loading warp spends 2000 clocks on
 // a tile, more than its bytes take.  One CTA on an SM.
+#include <atomic>
+
 #include "kda_attend.cuh"
 
 namespace kda {
@@ -805,8 +807,18 @@ template <typename A, int D, int NC, bool E8>
 cudaError_t launch_shape(const Params& s, const CUtensorMap& mk, const CUtensorMap& mv, int grid, cudaStream_t stream) {
   using W = Wide<A, D, E8>;
   auto kernel = attend_wide_kernel<A, D, NC, E8>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, W::SMEM);
   if (e != cudaSuccess) return e;
+  if (E8) {
+    // the new split of the registers waits for registers that a launch with fewer would not have
+    static std::atomic<bool> enough{false};
+    if (!enough.load(std::memory_order_relaxed)) {
+      cudaFuncAttributes a;
+      if ((e = cudaFuncGetAttributes(&a, kernel)) != cudaSuccess) return e;
+      if (a.numRegs < W::LAUNCH_REGS) return cudaErrorLaunchOutOfResources;
+      enough.store(true, std::memory_order_relaxed);
+    }
+  }
   kernel<<<grid, W::THREADS, W::SMEM, stream>>>(mk, mv, s);
   return cudaGetLastError();
 }
