@@ -162,27 +162,25 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constan
     x += h_step;
     if (x >= heads) x -= heads, ++t;
   };
-  auto load = [&](int t0) {
-#pragma unroll
-    for (int x = 0; x < AHEAD; ++x) {
-      const long long t = t0 + tt;
-      if (tt < TOKENS && t < p.T && slot < slots) {
-        const T* src = h < p.H_q ? static_cast<const T*>(p.q) + t * p.q_stride + h * d
-                       : h < p.H_q + p.cache.H_kv
-                           ? static_cast<const T*>(p.k) + t * p.k_stride + (h - p.H_q) * d
-                           : static_cast<const T*>(p.v) + t * p.v_stride + (h - p.H_q - p.cache.H_kv) * d;
-        a[x] = *reinterpret_cast<const uint4*>(src + at);
-        if (two) b[x] = *reinterpret_cast<const uint4*>(src + at + half);
-      }
-      advance(tt, h);
+  auto load = [&](int t0, uint4& lo, uint4& hi) {
+    const long long t = t0 + tt;
+    if (tt < TOKENS && t < p.T && slot < slots) {
+      const T* src = h < p.H_q ? static_cast<const T*>(p.q) + t * p.q_stride + h * d
+                     : h < p.H_q + p.cache.H_kv
+                         ? static_cast<const T*>(p.k) + t * p.k_stride + (h - p.H_q) * d
+                         : static_cast<const T*>(p.v) + t * p.v_stride + (h - p.H_q - p.cache.H_kv) * d;
+      lo = *reinterpret_cast<const uint4*>(src + at);
+      if (two) hi = *reinterpret_cast<const uint4*>(src + at + half);
     }
+    advance(tt, h);
   };
   if (p.cu_seqlens && blockIdx.x == 0) check_offsets(p);
 
   int buf = 0;
   for (int t0 = blockIdx.x * TOKENS; t0 < p.T; t0 += gridDim.x * TOKENS, buf ^= 1) {
     tt = tt0, h = h0;
-    load(t0);
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) load(t0, a[x], b[x]);
     // ---- places and turns: the CTA's warps share its tokens
     if (t0 + my_token < p.T) {
       const Place pl = place_of(p, t0 + my_token, lane, part == 0);
@@ -208,11 +206,13 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constan
             if (two) *reinterpret_cast<uint4*>(dst + half) = b[x];
           }
           advance(ct, ch);
+          load(t0, a[x], b[x]);
           continue;
         }
         float lo[8], hi[8];
         unpack8<T>(a[x], lo);
         unpack8<T>(b[x], hi);  // (read only where `two`)
+        load(t0, a[x], b[x]);
         if (is_q || is_k) {
           if (two) {
             const float4* cs = reinterpret_cast<const float4*>(&s_turn[buf][ct][8 * j]);
@@ -259,7 +259,6 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constan
         }
         advance(ct, ch);
       }
-      load(t0);
     }
     // The next group's places and turns go to the other buffer; its writers have all passed this
     // group's barrier, and so are done with the one before.
