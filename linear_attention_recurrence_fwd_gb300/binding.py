@@ -7,7 +7,6 @@ The Python names match the C entry points (include/kda.h).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -469,7 +468,10 @@ class PagedCache:
 def _token_stride(x, heads, d, name):
     """The elements between the tokens of x ([T, heads, d] or [N, K, heads, d],
     heads packed, sequences of equal length one after the other)."""
-    shape, s = x.shape, x.stride()
+    shape = x.shape
+    if x.is_contiguous() and x.is_cuda and shape[-1] == d and shape[-2] == heads:
+        return heads * d
+    s = x.stride()
     if not x.is_cuda or shape[-1] != d or shape[-2] != heads or s[-1] != 1 or (s[-2] != d and heads > 1):
         raise ValueError(f"{name} must be a CUDA tensor of {heads} heads of {d} channels, packed within a token")
     if len(shape) == 3 or shape[1] == 1:
@@ -493,6 +495,14 @@ def _stream_of(stream, t):
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to `stream`, or to the current one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -537,11 +547,7 @@ def kda_cache_append(k, v, cache, q=None, inv_freq=None, interleaved=False, cu_s
         Hq = q_shape[-2]
         qs = _token_stride(q, Hq, d, "q")
         if q_out is None:
-            if stream is None:
-                q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
-            else:
-                with torch.cuda.stream(stream):
-                    q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
+            q_out = _empty(q_shape, dtype, q.device, stream)
             qos = Hq * d
         elif q_out.shape != q_shape or q_out.dtype != dtype:
             raise ValueError("q_out must have q's shape and dtype")
@@ -580,13 +586,12 @@ def kda_cache_attend(q, cache, scale=None, window=0, counts=None, max_len=0, out
     dev = q.device
     need = _attend_workspace(dev.index, N, K, Hq, cache.heads, d, max_len or cache.capacity)
     lse = ws = None
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
-        if return_lse:
-            lse = torch.empty((N, K, Hq), dtype=torch.float32, device=dev)
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    if return_lse:
+        lse = _empty((N, K, Hq), torch.float32, dev, stream)
+    if need:
+        ws = _empty(need, torch.uint8, dev, stream)
     code = lib.kda_cache_attend(
         cache._ref, q.data_ptr(), code, qs, out.data_ptr(), None if lse is None else lse.data_ptr(),
         _int32_ptr(counts, N, "counts"), K, Hq, d ** -0.5 if scale is None else scale, window, max_len,
@@ -629,11 +634,10 @@ def kda_draft_accept(draft_tokens, draft_probs, target_probs, uniform, draft_len
         _need(tokens, torch.int32, "tokens")
         if tokens.shape != (N, K1):
             raise ValueError(f"tokens must be {(N, K1)}")
-    with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-        if counts is None:
-            counts = torch.empty(N, dtype=torch.int32, device=dev)
-        if tokens is None:
-            tokens = torch.empty((N, K1), dtype=torch.int32, device=dev)
+    if counts is None:
+        counts = _empty(N, torch.int32, dev, stream)
+    if tokens is None:
+        tokens = _empty((N, K1), torch.int32, dev, stream)
     code = lib.kda_draft_accept(
         draft_tokens.data_ptr(), dp, target_probs.data_ptr(), code, ds[0], ds[1], ts[0], ts[1],
         uniform.data_ptr(), _int32_ptr(draft_lens, N, "draft_lens"), _int32_ptr(counts, N, "counts"),

@@ -8,11 +8,14 @@
 // 2^20 * 2^-24 radians).
 //
 // The call moves bytes: it is bound by HBM for prompts (65536 packed tokens of
-// 32 query and 8 key heads of 128, 1.61 GB: 278 us, 5.8 TB/s) and by latency
-// for single tokens (256 tokens: 5.0 us).  A CTA has 256 threads and takes 1 or 4 tokens at a time.  A
-// token's sines and cosines are formed once, for all its heads, and kept in
-// shared memory; the heads' first bytes are on their way meanwhile.  A thread
-// takes 8 channels and the 8 that they are turned with, 16 bytes each.
+// 32 query and 8 key heads of 128, 1.61 GB: 251 us, 6.4 TB/s) and by latency
+// for single tokens (256 tokens: 5.0 us).  A CTA has 256 threads and takes 1 or
+// 4 tokens at a time.  A token's sines and cosines are formed once, for all its
+// heads, and kept in shared memory; the heads' first bytes are on their way
+// meanwhile.  A thread takes 8 channels and the 8 that they are turned with, 16
+// bytes each, and loads into their registers again at once: two such pieces are
+// always on their way (loaded two by two instead: 277 us; three, with spills:
+// 293; three with three CTAs on an SM instead of four: 276).
 #include "kda_internal.h"
 #include "kda_types.cuh"
 
@@ -320,7 +323,7 @@ template <typename T, typename C> cudaError_t launch_stored(const AppendProblem&
   if (e != cudaSuccess) return e;
   // A CTA to a token while all are resident together; else as many CTAs as are, four tokens at a time.
   // 48 heads of 128: 608 tokens 5.6 us one by one and 8.1 us by four, 912 tokens 9.0 and 8.2 us, 4096
-  // tokens 28 and 21 us; 65536 tokens 378 and 279 us.
+  // tokens 28 and 21 us.
   const int resident = 4 * sms;
   if (p.T <= resident)
     append_kernel<T, C, 1><<<p.T, THREADS, 0, stream>>>(p, jobs);
