@@ -615,13 +615,18 @@ Plan plan_for(int n_seq, int K, int H_q, int H_kv, int d, int max_len) {
   constexpr int TILE = 64;  // the smallest
   Plan a{};
   a.rows = K * (H_q / H_kv);
-  // at most 48 rows to a unit; more are split evenly (their units run side by side, in one team)
-  a.groups = (a.rows + 47) / 48;
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) return a;
+  // at most 48 rows to a unit; more are split evenly (their units run side by side, in one team).  Few
+  // and short ones are sooner done 16 rows at a time, by two CTAs on an SM (40 rows on each of 4 key
+  // heads of 128): one request of 250 positions 10.9 us against 11.6, 500 positions 11.5 against 14.1,
+  // 8-bit 11.2 against 13.6 and 13.1 against 16.0; but 64 requests of 250, 26.5 against 19.2.
+  const int by16 = (a.rows + 15) / 16;
+  const int most = max_len <= 512 && (long long)n_seq * H_kv * by16 <= 2 * sms ? 16 : 48;
+  a.groups = (a.rows + most - 1) / most;
   a.per = ((a.rows + a.groups - 1) / a.groups + 15) / 16 * 16;
   a.units = (long long)n_seq * H_kv * a.groups;
   const long long tiles = a.units * ((max_len + TILE - 1) / TILE > 1 ? (max_len + TILE - 1) / TILE : 1);
-  int sms = 0;
-  if (sm_count(&sms) != cudaSuccess) return a;
   // 64 requests of 8192 positions, 4 key heads of 128, on tcgen05 against the warp-level products with as
   // many row groups as it takes: 16-bit, 32 rows 175 us against 218, 40 rows 180 against 347; 8-bit, 32
   // rows 113 against 167, 40 rows 139 against 277.
