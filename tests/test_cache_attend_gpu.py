@@ -420,3 +420,42 @@ def test_many_rows_8_bit_many_small_weights_beside_a_large_one():
     ref, rlse, tol, ltol = attend_reference(q, keys, values, [length], None, d ** -0.5, 0)
     assert_within(lse, rlse, ltol, "lse")
     assert_within(out, ref, tol, "out")
+
+
+# A large bound on the lengths keeps short sequences on the units of up to 48 rows.
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("act,dtype", [(BF, BF), (FP, FP), (BF, E4), (FP, E4)])
+@pytest.mark.parametrize("K,Hq", [(5, 8), (4, 8), (13, 4), (8, 8)])
+def test_many_rows_short_sequences_with_a_large_bound(K, Hq, act, dtype, d):
+    check([0, 1, 70, 127, 128, 200], K=K, Hq=Hq, Hkv=1, d=d, act=act, dtype=dtype, max_len=9000)
+    check([5, 300], K=K, Hq=Hq, Hkv=1, d=d, act=act, dtype=dtype, max_len=9000, window=33, counts=[K, 2], page=3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [70, 127, 128])
+@pytest.mark.parametrize("dtype", [BF, FP, E4])
+def test_many_rows_nan_in_a_later_draft_with_a_large_bound(dtype, at, d):
+    lens, K, Hq = [at - 1], 5, 8
+    cache, keys, values = make_cache(lens, K, 1, d, 16, dtype)
+    pos = lens[0] + 1
+    page = int(cache.block_table[0, pos // 16])
+    q = torch.randn((1, K, Hq, d), generator=torch.Generator().manual_seed(4)).to(FP if dtype == FP else BF)
+    for bad in (NAN, math.inf) if dtype != E4 else (NAN,):
+        cache.v_pages[page, pos % 16] = torch.full((1, d), bad).to(dtype).cuda()
+        cache.k_pages[page, pos % 16] = torch.zeros((1, d)).to(dtype).cuda()
+        out = binding.kda_cache_attend(q.cuda(), cache, max_len=9000)
+        ref, _, tol, _ = attend_reference(q[:, :1], [keys[0][:lens[0] + 1]], [values[0][:lens[0] + 1]],
+                                          lens, None, d ** -0.5, 0)
+        assert_within(out[:, :1], ref, tol, "token 0")
+        assert not torch.isfinite(out[:, 1:].float()).any()
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+def test_nan_in_a_query_with_a_large_bound(dtype):
+    cache, _, _ = make_cache([40], 5, 1, 128, 64, dtype)
+    q = torch.randn((1, 5, 8, 128), generator=torch.Generator().manual_seed(4)).to(BF)
+    q[0, 0, 1, 3] = NAN
+    out, lse = binding.kda_cache_attend(q.cuda(), cache, return_lse=True, max_len=9000)
+    assert torch.isnan(out[0, 0, 1].float()).all() and torch.isnan(lse[0, 0, 1])
+    lse[0, 0, 1] = 0
+    assert torch.isfinite(lse).all() and torch.isfinite(out[:, 1:].float()).all()
