@@ -193,9 +193,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // stores x at the place of `local` in the shared memory of the cluster's CTA `rank`
 __device__ __forceinline__ void store_remote(const Pair* local, uint32_t rank, const Pair& x) {
   uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(local));
@@ -211,6 +210,9 @@ __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constan
   Pair(*const s_slice)[MOST * WARPS] = reinterpret_cast<Pair(*)[MOST * WARPS]>(s_slices);
   Pair* const s_warp = reinterpret_cast<Pair*>(s_warps);
   const int rank = cluster == 1 ? 0 : (int)cluster_rank();
+  // Another CTA's shared memory exists once that CTA has started: all arrive here, and wait before
+  // their first store to it (the drafts' test and the sums lie in between).
+  if (cluster > 1) cluster_arrive();
   const int n = blockIdx.x / cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = p.K, V = p.V;
   int* tokens = p.tokens + (long long)n * (K + 1);
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constan
     if (stop) break;
   }
   if (len < 0) {  // an idle sequence: the same for the whole cluster
+    if (cluster > 1) cluster_wait();
     if (rank == 0) {
       for (int i = tid; i <= K; i += THREADS) tokens[i] = -1;
       if (tid == 0) p.counts[n] = 0;
@@ -274,8 +277,11 @@ __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constan
       if (lane == 0) s_slice[attempt][mine] = total;
       __syncthreads();
     } else {
+      if (attempt == 0) cluster_wait();  // all of the cluster's CTAs have started
       if (lane < cluster) store_remote(&s_slice[attempt][mine], lane, total);
-      cluster_sync();
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
     }
     // every warp finds the slice that holds the border: the first whose running sum passes the goal
     const Pair x = lane * 2 < slices ? s_slice[attempt][lane * 2] : Pair{}, y = lane * 2 + 1 < slices ? s_slice[attempt][lane * 2 + 1] : Pair{};

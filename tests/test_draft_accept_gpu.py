@@ -233,3 +233,15 @@ def test_no_sequences():
     c, t = binding.kda_draft_accept(torch.empty((0, 2), dtype=torch.int32, device="cuda"), None,
                                     torch.empty((0, 3, 10), device="cuda"), torch.empty((0, 3), device="cuda"))
     assert c.shape == (0,) and t.shape == (0, 3)
+
+
+@pytest.mark.parametrize("V", [2048, 2049, 3000, 4096, 6144, 8192])
+@pytest.mark.parametrize("N", [1, 300])
+def test_sequences_of_several_blocks_with_nothing_before_their_sums(N, V):
+    """No drafts to look at and slices of few or no entries: the blocks of a
+    sequence exchange their sums as soon as they have started."""
+    toks, q, p, u = make(N, 0, V, seed=V + N)
+    for lens in (None, (torch.arange(N) % 3 - 1).int()):  # idle sequences among them
+        check(toks, None, p, u, lens)
+    toks, q, p, u = make(N, 2, V, seed=V + N + 1)
+    check(toks, q, p, u, (torch.arange(N) % 4 - 1).int())
