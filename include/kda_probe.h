@@ -67,6 +67,21 @@ KDA_API int kda_probe_tma(const void* src, void* out, int T, int H, int d, int h
  */
 KDA_API int kda_probe_wait_timeout(int limit_us, int* status, cudaStream_t stream);
 
+/*
+ * Runs the loading warps of the split attention (tiles of 64 positions, two
+ * stages, two warps, `grid` CTAs over the tiles of all n_seq * heads units)
+ * with nobody to give a stage back, so that their waits run out after
+ * limit_us microseconds (1..100000).  They set *status to 6 and still write
+ * every record that the joining kernel would read: records (device int32, 4
+ * entries each: unit, first CTA, number of further CTAs, unused) are indexed
+ * by unit where n_seq * heads <= grid, else by CTA.  pages: bf16
+ * [num_pages][16][heads][64]; table: device int32 [n_seq][table_width].
+ * Returns 0 / 1 / 4 as above.
+ */
+KDA_API int kda_probe_attend_loaders(const void* pages, int num_pages, const int* table, int table_width,
+                             const int* lens, int n_seq, int heads, int grid, int limit_us,
+                             int* records, int* status, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

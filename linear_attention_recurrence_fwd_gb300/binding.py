@@ -127,6 +127,8 @@ def load_probe(path: str = PROBE_LIB_PATH):
         lib.kda_probe_umma_ta.restype = _i
         lib.kda_probe_wait_timeout.argtypes = [_i, _vp, _vp]
         lib.kda_probe_wait_timeout.restype = _i
+        lib.kda_probe_attend_loaders.argtypes = [_vp, _i, _vp, _i, _vp] + [_i] * 4 + [_vp, _vp, _vp]
+        lib.kda_probe_attend_loaders.restype = _i
         _probe = lib
     return _probe
 

@@ -192,10 +192,12 @@ struct Ring {
 };
 
 // A producer warp's work: page look-ups, each stage's Meta, and the copies.  Of PRODUCERS warps, this
-// one (`which`) takes every PRODUCERS-th tile.
+// one (`which`) takes every PRODUCERS-th tile.  Where a wait runs out it copies nothing more, but still
+// writes the records of all its units, which the joining kernel forms addresses from; it returns when
+// its copies have landed.
 template <int D, bool E8, int TILE, int STAGES, int PRODUCERS = 1>
 __device__ __forceinline__ void produce(const Params& s, const Stretch& st, const Ring& ring, const CUtensorMap& map_k,
-                                        const CUtensorMap& map_v, int which = 0) {
+                                        const CUtensorMap& map_v, int which = 0, uint64_t limit_ns = WAIT_NS) {
   constexpr int ROW_BYTES = D * (E8 ? 1 : 2), BOX_BYTES = ROW_BYTES < 128 ? ROW_BYTES : 128;
   constexpr int HALVES = ROW_BYTES / BOX_BYTES, KV_BYTES = TILE * ROW_BYTES, STAGE_BYTES = 2 * KV_BYTES;
   const AttendProblem& p = s.p;
@@ -245,7 +247,7 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
   };
   read_ahead(st.n0 + 1);
   bool opened_here = false, recorded = false, stop = false;
-  int it = 0;
+  int it = 0, sent = -1;  // sent: tiles copied when a wait ran out
   while (!stop) {
     Batch next = cur;
     next.j += batch;
@@ -293,7 +295,7 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
         recorded = true;
       }
     }
-    if (PRODUCERS > 1 && it % PRODUCERS != which) continue;
+    if (sent >= 0 || (PRODUCERS > 1 && it % PRODUCERS != which)) continue;
     // lane b: the page of rows [b rows_per, (b + 1) rows_per) of the tile; of single rows b, b + 32, ...
     const int from = (x * boxes + lane) & 31;
     int page[PL], at[PL];
@@ -314,9 +316,10 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
     }
     const bool bad = wrong != 0;
     if (lane == 0 && (bad || (over && first))) *p.status = 1;
-    if (it >= STAGES && !mbar_wait(&empty[stage], ((it / STAGES) - 1) & 1)) {
+    if (it >= STAGES && !mbar_wait(&empty[stage], ((it / STAGES) - 1) & 1, limit_ns)) {
       *p.status = 6;
-      return;
+      sent = it;
+      continue;
     }
     const uint32_t k_s = base + stage * STAGE_BYTES, v_s = k_s + KV_BYTES;
     if (lane == 0) {
@@ -395,6 +398,9 @@ __device__ __forceinline__ void produce(const Params& s, const Stretch& st, cons
     cur = next;
   }
   if (!s.whole && !s.by_unit && !recorded && lane == 0 && which == 0) s.records[c].more = 0;
+  if (sent < 0) sent = it;
+  for (int t = max(0, sent - STAGES); t < sent; ++t)
+    if (t % PRODUCERS == which && !mbar_wait(&full[t % STAGES], (t / STAGES) & 1, limit_ns)) *p.status = 6;
 }
 
 // More than 16 query rows to a key head (kda_attend_wide.cu).

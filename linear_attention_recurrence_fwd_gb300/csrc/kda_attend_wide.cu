@@ -747,8 +747,8 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         product(tmem + T_S + (it & 1) * W::S_COLS, a + ((ks >> 2) * (TILE * 128) + (ks & 3) * 32) / 16,
                 dq + ((ks >> 2) * (N * 128) + (ks & 3) * 32) / 16, id, ks > 0);
       umma_commit(&s_full[it & 1]);
+      if (flags & STOP) return mbar_wait(&s_full[it & 1], (it >> 1) & 1);  // nothing in flight is left behind
       umma_commit(&empty[stage]);
-      if (flags & STOP) return true;
       if (++stage == STAGES) stage = 0, turn ^= 1;
     }
   };
@@ -776,8 +776,8 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
                     ks > 0 || z > 0 || !fresh);
       }
       umma_commit(&p_empty[g]);
+      if (flags & STOP) return mbar_wait(&p_empty[g], (it / GROUPS) & 1);
       umma_commit(&empty[stage]);
-      if (flags & STOP) return true;
       if (++stage == STAGES) stage = 0;
     }
   };

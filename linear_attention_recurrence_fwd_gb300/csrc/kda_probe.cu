@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/kda_probe.h"
+#include "kda_attend.cuh"
 #include "tma_host.h"
 #include "umma.cuh"
 
@@ -227,7 +228,53 @@ __global__ void __launch_bounds__(128) probe_timeout_kernel(uint64_t limit_ns, i
   if (warp == 0) tmem_dealloc(tbase, 32);
 }
 
+// The loading warps of the split attention without anyone who gives their stages back: after STAGES
+// tiles their waits run out.
+constexpr int LOAD_TILE = 64, LOAD_STAGES = 2, LOAD_WARPS = 2;
+__global__ void __launch_bounds__(32 * LOAD_WARPS) probe_loaders_kernel(const __grid_constant__ Params s, uint64_t limit_ns) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[LOAD_STAGES], empty[LOAD_STAGES], told[LOAD_STAGES];
+  __shared__ Meta meta[LOAD_STAGES];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  if (threadIdx.x < LOAD_STAGES) {
+    mbar_init(&full[threadIdx.x], 33);
+    mbar_init(&empty[threadIdx.x], 1);
+    mbar_init(&told[threadIdx.x], 1);
+  }
+  mbar_fence_init();
+  const Stretch st = find_stretch<LOAD_TILE, 32 * LOAD_WARPS>(s);
+  if (st.left == 0) return;
+  CUtensorMap none;  // not used: rows are copied 16 bytes at a time
+  produce<64, false, LOAD_TILE, LOAD_STAGES, LOAD_WARPS>(s, st, Ring{base, full, empty, told, meta}, none, none,
+                                                         threadIdx.x / 32, limit_ns);
+}
+
 }  // namespace
+
+extern "C" KDA_API int kda_probe_attend_loaders(const void* pages, int num_pages, const int* table, int table_width,
+                                                const int* lens, int n_seq, int heads, int grid, int limit_us,
+                                                int* records, int* status, cudaStream_t stream) {
+  if (!pages || !table || !lens || !records || !status || n_seq < 1 || heads < 1 || grid < 1 || limit_us <= 0 ||
+      limit_us > 100000)
+    return 1;
+  constexpr int PAGE = 16, D = 64, SMEM = LOAD_STAGES * 2 * LOAD_TILE * D * 2 + 1024;
+  Params s{};
+  kda_paged_cache_t& c = s.p.cache;
+  c.k = c.v = const_cast<void*>(pages);
+  c.block_table = table;
+  c.lens = lens;
+  c.page_stride = PAGE * heads * D, c.token_stride = heads * D, c.head_stride = D, c.table_stride = table_width;
+  c.dtype = KDA_BF16;
+  c.n_seq = n_seq, c.num_pages = num_pages, c.page_size = PAGE, c.table_width = table_width, c.H_kv = heads, c.d = D;
+  s.p.K = 1, s.p.H_q = heads, s.p.status = status;
+  s.groups = 1, s.rows = 1, s.group_heads = 1, s.rows_per = 16, s.box_rows = 1;
+  s.by_unit = n_seq * heads <= grid;
+  s.min_tiles = 2, s.team = 1;
+  s.records = reinterpret_cast<Record*>(records);
+  if (cudaFuncSetAttribute(probe_loaders_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) return 4;
+  probe_loaders_kernel<<<grid, 32 * LOAD_WARPS, SMEM, stream>>>(s, (uint64_t)limit_us * 1000ull);
+  return cudaGetLastError() == cudaSuccess ? 0 : 4;
+}
 
 extern "C" KDA_API int kda_probe_wait_timeout(int limit_us, int* status, cudaStream_t stream) {
   if (limit_us <= 0 || limit_us > 100000 || !status) return 1;

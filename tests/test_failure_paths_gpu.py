@@ -187,3 +187,48 @@ def test_nan_poisoned_workspace_changes_nothing(B, T, H):
     ref_out, ref_fin = binding.kda_chunk_fwd(*[g[k] for k in KEYS], g["initial_state"])
     torch.cuda.synchronize()
     assert torch.equal(out, ref_out) and torch.equal(fin, ref_fin)
+
+
+@pytest.mark.parametrize("lens,heads,grid", [([5000, 10, 900], 2, 7), ([5000, 10, 900], 2, 5), ([40000], 1, 13),
+                                             ([0, 0, 3, 700, 1500, 64, 63], 3, 4), ([100] * 30, 2, 11)])
+def test_loaders_of_split_attention_whose_waits_run_out_still_write_every_record(lens, heads, grid):
+    """What the joining kernel forms addresses from must not be what the
+    workspace held before: each record equals the cut of the tiles."""
+    probe = binding.load_probe()
+    need = [n // 16 + 1 for n in lens]
+    width, n_pages = max(need), sum(need)
+    table = torch.full((len(lens), width), -1, dtype=torch.int32)
+    at = 0
+    for n, m in enumerate(need):
+        table[n, :m] = torch.arange(at, at + m)
+        at += m
+    pages = torch.zeros((n_pages, 16, heads, 64), dtype=torch.bfloat16, device="cuda")
+    table, held = table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    units = len(lens) * heads
+    by_unit = units <= grid
+    garbage = 0x7f7f7f7f
+    records = torch.full((units if by_unit else grid, 4), garbage, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert probe.kda_probe_attend_loaders(pages.data_ptr(), n_pages, table.data_ptr(), width, held.data_ptr(), len(lens),
+                                          heads, grid, 1000, records.data_ptr(), status.data_ptr(),
+                                          torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert status.item() == 6
+    # the cut: tiles of all units, one after the other, in equal stretches
+    tiles = [(n + 1 + 63) // 64 for n in lens for _ in range(heads)]
+    total = sum(tiles)
+    live = min(grid, max(1, total // 2))
+    owner = [c for c in range(live) for _ in range(total // live + (c < total % live))]
+    want = torch.full_like(records.cpu(), garbage)
+    if not by_unit:
+        want[:, 2] = 0
+    at = 0
+    for u, n in enumerate(tiles):
+        first, more = owner[at], owner[at + n - 1] - owner[at]
+        at += n
+        if by_unit or more:
+            want[u if by_unit else first, :3] = torch.tensor([u, first, more], dtype=torch.int32)
+    got = records.cpu()
+    live_record = want[:, 2] != 0
+    assert torch.equal(got[:, 2], want[:, 2])
+    assert torch.equal(got[live_record, :3], want[live_record, :3])
