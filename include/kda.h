@@ -481,8 +481,8 @@ KDA_API kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void
  * nothing stored at a position that a token does not see reaches its output,
  * whatever it holds.  The scores, the softmax and its sums are fp32; for the
  * product with the values the weights are rounded to the type of q or, over an
- * 8-bit cache, to 9 bits (11 with KDA_F16), and small ones to 2^-29 of the
- * largest.  Over an 8-bit cache a row of q that holds an infinity gives NaN.
+ * 8-bit cache, to 9 bits or more (11 with KDA_F16), and small ones to 2^-29 of
+ * the largest.  Over an 8-bit cache a row of q that holds an infinity gives NaN.
  * Results do not depend on anything but the arguments (no atomics).
  *   workspace : kda_cache_attend_workspace_size() bytes, 16-byte aligned, for
  *             the parts of a sequence's softmax that different blocks compute

@@ -141,7 +141,9 @@ __global__ void __launch_bounds__(Shape<D, E8>::THREADS, 2)
   constexpr int NT = D / 8;                // n-tiles of output columns
   constexpr int KP = D / (E8 ? 32 : 16);   // fragment loads over a row's channels
   constexpr int PITCH = S::BOX_BYTES;      // of a row of keys or values in shared memory
-  constexpr float SLACK = 8.f;             // weights reach 2^8 before the maximum is moved
+  // Weights are 2^(f s - m), m the running maximum less BIAS, and reach 2^(BIAS + SLACK) before m is
+  // moved.  In fp16 the bias keeps small ones to 2^-32 of the largest (its least step is 2^-24).
+  constexpr float BIAS = BF ? 0.f : 7.f, SLACK = 8.f;
   float o[NT][4], m[2], l[2], f[2];
   int ri[2];                               // the token of each of the thread's two rows
   uint32_t qf[D / 16][4];
@@ -330,11 +332,11 @@ __global__ void __launch_bounds__(Shape<D, E8>::THREADS, 2)
         for (int nt = 0; nt < NS; ++nt) x = fmaxf(x, fmaxf(sc[0][nt][h * 2], sc[0][nt][h * 2 + 1]));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        top[h] = x;
-        move |= x > m[h] + SLACK;
+        top[h] = x - BIAS;
+        move |= top[h] > m[h] + SLACK;
       }
       // The output and the sum are rescaled only where a row's maximum has grown by more than 2^8:
-      // until then the weights are just larger than 1, which costs no precision.
+      // until then the weights are just larger, which costs no precision.
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

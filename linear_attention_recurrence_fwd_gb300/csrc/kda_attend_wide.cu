@@ -72,8 +72,9 @@ template <typename A, int D, bool E8> struct Wide {
   // Columns of tensor memory: two tiles' scores, then each group's output
   static constexpr uint32_t T_S = 0, S_COLS = E8 ? QP * 48 : 64, T_O = 2 * S_COLS, O_COLS = 48 * WN, T_COLS = E8 ? 512 : 256;
   static_assert(T_O + GROUPS * O_COLS <= T_COLS, "tensor memory");
-  // Weights are 2^(f s - m + BIAS) and reach 2^(BIAS + SLACK) before the maximum is moved.
-  static constexpr float BIAS = E8 ? 12.f : 0.f, SLACK = E8 ? 3.f : 8.f;
+  // Weights are 2^(f s - m + BIAS) and reach 2^(BIAS + SLACK) before the maximum is moved.  (In fp16 the
+  // bias keeps small ones to 2^-32 of the largest; its least step is 2^-24.)
+  static constexpr float BIAS = E8 ? 12.f : __is_same(A, __nv_bfloat16) ? 0.f : 7.f, SLACK = E8 ? 3.f : 8.f;
 };
 
 // kind::f8f6f4 with 8-bit operands, each e4m3 or e5m2, and an fp32 accumulator; K = 32 per MMA.

@@ -459,3 +459,33 @@ def test_nan_in_a_query_with_a_large_bound(dtype):
     assert torch.isnan(out[0, 0, 1].float()).all() and torch.isnan(lse[0, 0, 1])
     lse[0, 0, 1] = 0
     assert torch.isfinite(lse).all() and torch.isfinite(out[:, 1:].float()).all()
+
+
+@pytest.mark.parametrize("rows", [4, 40])
+@pytest.mark.parametrize("act,dtype", [(BF, BF), (FP, FP), (BF, E4), (FP, E4)])
+def test_small_weights_beside_a_large_one_without_a_value(act, dtype, rows):
+    """The first position takes nearly all the weight and holds zeros; the others, 2^-26 of it each,
+    are the whole output.  Enough units for every block to hold whole sequences."""
+    N, Hkv, d, length = 40, 8, 128, 999
+    cache, keys, values = make_cache([length] * N, 1, Hkv, d, 16, dtype)
+    for x in (cache.k_pages, cache.v_pages):
+        x.copy_(torch.zeros(x.shape).to(dtype))
+    g = torch.Generator().manual_seed(3)
+    for n in range(N):
+        v = (64 * torch.randn((length + 1, Hkv, d), generator=g).abs()).to(dtype)
+        v[0] = 0
+        held = cache.block_table[n].long()
+        at = torch.arange(length + 1, device="cuda")
+        flat = cache.v_pages.view(torch.uint8) if dtype == E4 else cache.v_pages
+        flat[held[at // 16], at % 16] = (v.view(torch.uint8) if dtype == E4 else v).cuda()
+        cache.k_pages[int(held[0]), 0, :, 0] = 16.0
+        keys[n].zero_()
+        keys[n][0, :, 0] = 16.0
+        values[n] = v.double()
+    q = torch.zeros((N, 1, Hkv * rows, d))
+    q[..., 0] = 1.0
+    scale = 26 * math.log(2) / 16  # the first score is 26 in powers of two, the others 0
+    out, lse = binding.kda_cache_attend(q.to(act).cuda(), cache, scale=scale, return_lse=True)
+    ref, rlse, tol, ltol = attend_reference(q.to(act), keys, values, [length] * N, None, scale, 0)
+    assert_within(lse, rlse, ltol, "lse")
+    assert_within(out, ref, tol, "out")
