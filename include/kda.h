@@ -479,7 +479,8 @@ KDA_API kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void
  * p = lens[n] + i (lens[n] may be negative).  Where nothing is seen (a token
  * beyond counts[n], an empty sequence), out is 0 and lse is -infinity;
  * nothing stored at a position that a token does not see reaches its output,
- * whatever it holds.  The scores, the softmax and its sums are fp32; for the
+ * whatever it holds.  Where all that a token sees scores -infinity, out is NaN
+ * and lse -infinity.  The scores, the softmax and its sums are fp32; for the
  * product with the values the weights are rounded to the type of q or, over an
  * 8-bit cache, to 9 bits or more (11 with KDA_F16), and small ones to 2^-29 of
  * the largest.  Over an 8-bit cache a row of q that holds an infinity gives NaN.

@@ -515,9 +515,10 @@ __global__ void __launch_bounds__(Shape<D, E8>::THREADS, 2)
             const float4 z = *reinterpret_cast<const float4*>(from + y * PART);
             v.x += z.x, v.y += z.y, v.z += z.z, v.w += z.w;
           }
-          const bool none = big == -INFINITY && sum == 0.f;
+          bool none = big == -INFINITY && sum == 0.f;
+          const int i = gr / s.group_heads, gh = gr - i * s.group_heads;
+          if (none && sees_any(s, n, i, flags & OPENS ? 0 : t.pos0 - it * TILE, t.pos0 + TILE)) none = false, big = LOWEST;
           if (whole_unit) {
-            const int i = gr / s.group_heads, gh = gr - i * s.group_heads;
             const long long at = ((long long)n * p.K + i) * p.H_q + hk * s.group_heads + gh;
             const float by = p.cache.v_scale / sum;
             uint2 w = make_uint2(pack2<A>(v.x * by, v.y * by), pack2<A>(v.z * by, v.w * by));

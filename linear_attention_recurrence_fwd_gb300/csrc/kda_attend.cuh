@@ -88,6 +88,26 @@ template <int TILE> __device__ __forceinline__ Range range_of(const Params& s, i
   return range_from<TILE>(s, s.p.cache.lens[n], s.p.counts ? s.p.counts[n] : s.p.K);
 }
 
+// The maximum of a row all of whose scores are -infinity: not -infinity, which is that of a row that sees
+// nothing.  Its weights are 0, and 0 / 0 is the result.
+constexpr float LOWEST = -3.402823466e38f;
+
+// Whether token i of sequence n sees a position from `begin` to before `end` that lies in a page that
+// exists.  Asked only of rows without a weight: the tiles' loops need not keep track of it.
+__device__ __forceinline__ bool sees_any(const Params& s, int n, int i, int begin, int end) {
+  const AttendProblem& p = s.p;
+  const Range r = range_of<64>(s, n);
+  if (i >= r.count) return false;
+  const int first = p.window && r.len + i >= p.window ? r.len + i - p.window + 1 : 0;
+  const int a = max(first, begin), b = min(min(r.len + i, r.end - 1), end - 1);
+  if (a > b) return false;
+  for (int x = a / p.cache.page_size; x <= b / p.cache.page_size; ++x) {
+    const int page = p.cache.block_table[n * p.cache.table_stride + x];
+    if (page >= 0 && page < p.cache.num_pages) return true;
+  }
+  return false;
+}
+
 // Byte of 16-byte chunk `c` of row `row` in a [TILE][ROW_BYTES] region, as TMA's swizzle lays it
 template <int ROW_BYTES, int TILE> __device__ __forceinline__ uint32_t kv_offset(int row, int c) {
   if (ROW_BYTES >= 128)

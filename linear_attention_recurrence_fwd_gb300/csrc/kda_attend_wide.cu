@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
   uint64_t *s_full = bars + 18, *s_empty = bars + 20, *p_full = bars + 22, *p_empty = bars + 24, *q_full = bars + 26, *joint = bars + 27;
   Meta* meta = reinterpret_cast<Meta*>(bars + 28);  // [6]
   __shared__ uint32_t s_tmem;
+  __shared__ int unit_pos0[2];  // the first position of the unit's tiles here, for two units in turn
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int N = 16 * NC;  // query rows of a unit
@@ -304,14 +305,14 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
     };
 
     // A unit, from its first tile's stage, and its queries on their way: a thread's chunks of 8 channels.
-    int u_n, u_hk, u_row0, u_tiles;
+    int u_n, u_hk, u_row0, u_tiles, u_pos0;
     uint32_t u_flags;
     constexpr int ALL = N * (D / 8), EACH = (ALL + 255) / 256;
     uint4 q[EACH];
     auto fetch_queries = [&](int stage, int turn) {
       if (!wait(&told[stage], turn)) return false;
       const Meta& t = meta[stage];
-      u_n = t.n, u_hk = t.hk, u_row0 = t.row0, u_tiles = t.tiles, u_flags = t.flags;
+      u_n = t.n, u_hk = t.hk, u_row0 = t.row0, u_tiles = t.tiles, u_flags = t.flags, u_pos0 = t.pos0;
 #pragma unroll
       for (int z = 0; z < EACH; ++z) {
         q[z] = make_uint4(0, 0, 0, 0);
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
           row_neg[x * 96 + odd * 48 + tid] = UNSEEN;
         }
         row_tok[odd * 48 + tid] = gr < s.rows ? gr / s.group_heads : 0x3fffffff;
+        if (tid == 0) unit_pos0[odd] = u_pos0;
       }
       const int ch = tid % (D / 8);
       if constexpr (E8) {
@@ -669,8 +671,9 @@ __global__ void __launch_bounds__(Wide<A, D, E8>::THREADS, 1)
         sum += m == -INFINITY ? l : by * l;  // (nothing, or NaN, without a maximum)
         keep[x * 48 + tid] = by;
       }
-      const bool none = top == -INFINITY && sum == 0.f;
+      bool none = top == -INFINITY && sum == 0.f;
       const int i = tok[tid], gh = row0 + tid - i * s.group_heads;
+      if (none && sees_any(s, n, i, unit_pos0[odd], unit_pos0[odd] + tiles * TILE)) none = false, top = LOWEST;
       const long long to = whole_unit ? ((long long)n * p.K + i) * p.H_q + hk * s.group_heads + gh : slot * N + tid;
       row_to[tid] = to;
       if (whole_unit) {

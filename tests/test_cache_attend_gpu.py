@@ -489,3 +489,46 @@ def test_small_weights_beside_a_large_one_without_a_value(act, dtype, rows):
     ref, rlse, tol, ltol = attend_reference(q.to(act), keys, values, [length] * N, None, scale, 0)
     assert_within(lse, rlse, ltol, "lse")
     assert_within(out, ref, tol, "out")
+
+
+@pytest.mark.parametrize("lens,window,max_len", [([40], 0, 0), ([40], 0, 9000), ([5000], 0, 0), ([625, 1137], 500, 0),
+                                                 ([625, 1137], 500, 9000)])
+@pytest.mark.parametrize("rows", [4, 13])
+@pytest.mark.parametrize("act,dtype", [(BF, BF), (FP, FP), (BF, E4), (FP, E4)])
+def test_scores_of_minus_infinity_are_not_positions_that_are_not_seen(act, dtype, rows, lens, window, max_len):
+    """A row all of whose scores overflow to -infinity is 0 / 0, with a sum of 0; the rows beside it see
+    equal scores.  (With the window, the first tile is seen by the first two tokens alone.)"""
+    K, d = 3, 128
+    cache, keys, values = make_cache(lens, K, 1, d, 16, dtype)
+    for n in range(len(lens)):
+        at = torch.arange(lens[n] + K, device="cuda")
+        k = torch.zeros((lens[n] + K, 1, d))
+        k[..., 0] = -8
+        flat = cache.k_pages.view(torch.uint8) if dtype == E4 else cache.k_pages
+        flat[cache.block_table[n].long()[at // 16], at % 16] = (k.to(dtype).view(torch.uint8) if dtype == E4 else k.to(dtype)).cuda()
+        keys[n] = k.double()
+    q = torch.zeros((len(lens), K, rows, d))
+    q[:, :, 1, 0] = 8.0
+    out, lse = binding.kda_cache_attend(q.to(act).cuda(), cache, scale=1e38, window=window, max_len=max_len, return_lse=True)
+    assert torch.isnan(out[:, :, 1].float()).all()
+    assert (lse[:, :, 1] == -math.inf).all()
+    q[:, :, 1] = 0
+    ref, rlse, tol, ltol = attend_reference(q.to(act), keys, values, lens, None, 1e38, window)
+    rest = [r for r in range(rows) if r != 1]
+    assert_within(lse[:, :, rest], rlse[:, :, rest], ltol[:, :, rest], "lse")
+    assert_within(out[:, :, rest], ref[:, :, rest], tol[:, :, rest], "out")
+
+
+@pytest.mark.parametrize("length", [40, 5000])
+@pytest.mark.parametrize("rows", [4, 40])
+def test_an_infinite_query_over_an_8_bit_cache_gives_nan(rows, length):
+    """Also where it would make every score -infinity."""
+    d = 128
+    cache, _, _ = make_cache([length], 1, 1, d, 16, E4)
+    cache.k_pages.copy_(torch.full(cache.k_pages.shape, -1.0).to(E4))
+    q = torch.zeros((1, 1, rows, d))
+    q[0, 0, 2, 5] = math.inf
+    out = binding.kda_cache_attend(q.to(BF).cuda(), cache, max_len=9000)
+    assert torch.isnan(out[0, 0, 2].float()).all()
+    rest = [r for r in range(rows) if r != 2]
+    assert torch.isfinite(out[0, 0, rest].float()).all()
