@@ -430,10 +430,17 @@ class PagedCache:
     lens: int32 [N], the tokens held before a call's new ones.  The tensors
     stay the caller's: pages, table and lens are read by every call as they
     are then, and lens is advanced by the caller (`cache.lens.add_(counts)`).
-    k_scale, v_scale: what a stored 1.0 stands for.
+    k_scale, v_scale: what a stored 1.0 stands for.  All six may be assigned
+    later; an assignment is checked like the constructor's arguments and holds
+    for the calls after it (a graph keeps the tensors of its capture).
     """
 
     def __init__(self, k_pages, v_pages, block_table, lens, k_scale=1.0, v_scale=1.0):
+        self._struct = _CacheStruct()
+        self._ref = ctypes.addressof(self._struct)
+        self._set(k_pages, v_pages, block_table, lens, float(k_scale), float(v_scale))
+
+    def _set(self, k_pages, v_pages, block_table, lens, k_scale, v_scale):
         for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
             if not t.is_cuda or t.dim() != 4 or t.dtype not in _CODES or t.dtype == torch.float32:
                 raise ValueError(f"{name} must be a CUDA tensor [num_pages, page_size, H_kv, d] of "
@@ -449,18 +456,26 @@ class PagedCache:
         _need(lens, torch.int32, "lens")
         if lens.shape != (block_table.shape[0],):
             raise ValueError("lens must have one entry for each row of block_table")
-        self.k_pages, self.v_pages, self.block_table, self.lens = k_pages, v_pages, block_table, lens
-        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self._held = k_pages, v_pages, block_table, lens, k_scale, v_scale
         pages, page_size, heads, d = k_pages.shape
         self.n_seq, self.heads, self.d, self.page_size = lens.numel(), heads, d, page_size
         self.capacity = block_table.shape[1] * page_size  # tokens a row of the table holds
         self.device = k_pages.device
-        self._struct = _CacheStruct(
+        # the calls hold the address of this struct: it is filled anew, not replaced
+        self._struct.__init__(
             k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
             k_pages.stride(0), k_pages.stride(1), k_pages.stride(2), block_table.stride(0),
-            self.k_scale, self.v_scale, _CODES[k_pages.dtype], self.n_seq, pages, page_size,
+            k_scale, v_scale, _CODES[k_pages.dtype], self.n_seq, pages, page_size,
             block_table.shape[1], heads, d)
-        self._ref = ctypes.addressof(self._struct)
+
+    def _field(i, convert=lambda x: x):
+        def assign(self, value):
+            self._set(*self._held[:i], convert(value), *self._held[i + 1:])
+        return property(lambda self: self._held[i], assign)
+
+    k_pages, v_pages, block_table, lens = _field(0), _field(1), _field(2), _field(3)
+    k_scale, v_scale = _field(4, float), _field(5, float)
+    del _field
 
 
 # The calls below take a few microseconds on the GPU for a single token, so what

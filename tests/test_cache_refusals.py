@@ -105,6 +105,72 @@ def test_host_tensors_are_refused():
         binding.kda_draft_accept(torch.zeros((1, 1), dtype=torch.int32), None, torch.zeros((1, 2, 4)), torch.zeros((1, 2)))
 
 
+class Claimed:
+    """A host tensor that says it is on a GPU: for what is looked at before any launch."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self._t = t
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+def claimed_cache(N=3, width=4):
+    pages = [Claimed(torch.zeros((5, 16, 2, 64), dtype=torch.bfloat16)) for _ in range(2)]
+    return binding.PagedCache(*pages, Claimed(torch.zeros((N, width), dtype=torch.int32)),
+                              Claimed(torch.zeros(N, dtype=torch.int32)))
+
+
+def test_assignments_to_a_cache_are_followed():
+    """What a call gets is the struct behind cache._ref."""
+    c = claimed_cache()
+    seen = binding._CacheStruct.from_address(c._ref)
+    lens = Claimed(torch.ones(3, dtype=torch.int32))
+    c.lens = lens
+    assert c.lens is lens and seen.lens == lens.data_ptr()
+    table = Claimed(torch.zeros((3, 9), dtype=torch.int32))
+    c.block_table = table  # a grown table
+    assert seen.block_table == table.data_ptr() and seen.table_width == 9 and seen.table_stride == 9
+    assert c.capacity == 9 * 16
+    c.k_scale, c.v_scale = 0.5, 0.25
+    assert (seen.k_scale, seen.v_scale) == (0.5, 0.25) and (c.k_scale, c.v_scale) == (0.5, 0.25)
+    pages = Claimed(torch.zeros((5, 16, 2, 64), dtype=torch.bfloat16))
+    c.v_pages = pages
+    assert seen.v == pages.data_ptr() and seen.k == c.k_pages.data_ptr() != seen.v
+
+
+def test_assignments_that_do_not_fit_are_refused_and_change_nothing():
+    c = claimed_cache()
+    before = bytes(c._struct)
+    for name, value in (("lens", Claimed(torch.ones(4, dtype=torch.int32))), ("lens", Claimed(torch.ones(3))),
+                        ("lens", torch.ones(3, dtype=torch.int32)),  # on the host
+                        ("block_table", Claimed(torch.zeros((4, 4), dtype=torch.int32))),
+                        ("k_pages", Claimed(torch.zeros((6, 16, 2, 64), dtype=torch.bfloat16))),
+                        ("v_pages", Claimed(torch.zeros((5, 16, 2, 64), dtype=torch.float16)))):
+        held = getattr(c, name)
+        with pytest.raises(ValueError):
+            setattr(c, name, value)
+        assert getattr(c, name) is held and bytes(c._struct) == before
+    with pytest.raises((TypeError, ValueError)):
+        c.k_scale = "none"
+    assert bytes(c._struct) == before
+
+
+@pytest.mark.gpu
+def test_a_cache_follows_lens_that_are_assigned(cuda_device):
+    build.build()
+    d, bf = 64, torch.bfloat16
+    pages = [torch.zeros((2, 16, 1, d), dtype=bf, device="cuda") for _ in range(2)]
+    c = binding.PagedCache(*pages, torch.tensor([[1]], dtype=torch.int32).cuda(), torch.tensor([3], dtype=torch.int32).cuda())
+    k = torch.ones((1, 1, 1, d), dtype=bf, device="cuda")
+    c.lens = c.lens + 2
+    binding.kda_cache_append(k, k, c)
+    c.lens += 4  # in place, and assigned
+    binding.kda_cache_append(k, k, c)
+    assert pages[0][1, :, 0, 0].nonzero().flatten().tolist() == [5, 9]
+
+
 @pytest.mark.gpu
 def test_tensors_that_do_not_fit_are_refused(cuda_device):
     build.build()
