@@ -456,11 +456,13 @@ class PagedCache:
         _need(lens, torch.int32, "lens")
         if lens.shape != (block_table.shape[0],):
             raise ValueError("lens must have one entry for each row of block_table")
+        if not k_pages.device == v_pages.device == block_table.device == lens.device:
+            raise ValueError("k_pages, v_pages, block_table and lens must be on one device")
         self._held = k_pages, v_pages, block_table, lens, k_scale, v_scale
         pages, page_size, heads, d = k_pages.shape
         self.n_seq, self.heads, self.d, self.page_size = lens.numel(), heads, d, page_size
         self.capacity = block_table.shape[1] * page_size  # tokens a row of the table holds
-        self.device = k_pages.device
+        self.device, self.device_index = k_pages.device, k_pages.get_device()
         # the calls hold the address of this struct: it is filled anew, not replaced
         self._struct.__init__(
             k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), lens.data_ptr(),
@@ -482,14 +484,16 @@ class PagedCache:
 # they do on the host is kept short: one look at a tensor's shape and strides,
 # raw pointers, no context manager where the current stream is used.
 
-def _token_stride(x, heads, d, name):
+def _token_stride(x, heads, d, name, dev):
     """The elements between the tokens of x ([T, heads, d] or [N, K, heads, d],
-    heads packed, sequences of equal length one after the other)."""
+    heads packed, sequences of equal length one after the other) on GPU dev."""
     shape = x.shape
-    if x.is_contiguous() and x.is_cuda and shape[-1] == d and shape[-2] == heads:
+    if x.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if x.is_contiguous() and shape[-1] == d and shape[-2] == heads:
         return heads * d
     s = x.stride()
-    if not x.is_cuda or shape[-1] != d or shape[-2] != heads or s[-1] != 1 or (s[-2] != d and heads > 1):
+    if shape[-1] != d or shape[-2] != heads or s[-1] != 1 or (s[-2] != d and heads > 1):
         raise ValueError(f"{name} must be a CUDA tensor of {heads} heads of {d} channels, packed within a token")
     if len(shape) == 3 or shape[1] == 1:
         return s[0]
@@ -498,20 +502,20 @@ def _token_stride(x, heads, d, name):
     return s[1]
 
 
-def _int32_ptr(t, n, name):
-    """The address of a contiguous int32 tensor of n entries; None for None."""
+def _int32_ptr(t, n, name, dev):
+    """The address of a contiguous int32 tensor of n entries on GPU dev; None for None."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != torch.int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of {n} entries")
+    if t.get_device() != dev or t.dtype != torch.int32 or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on cuda:{dev}")
     return t.data_ptr()
 
 
-def _stream_of(stream, t):
-    """The raw handle of `stream`, or of the current one of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+def _stream_of(stream, dev):
+    """The raw handle of `stream`, or of the current one, on GPU dev, which must be the current one."""
+    if dev != torch.cuda.current_device() or (stream is not None and stream.device_index != dev):
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device or the stream's")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -551,8 +555,11 @@ def kda_cache_append(k, v, cache, q=None, inv_freq=None, interleaved=False, cu_s
     else:
         K, T = 0, shape[0]
     rot, freqs = 0, None
+    dev = cache.device_index
     if inv_freq is not None:
         _need(inv_freq, torch.float64, "inv_freq")
+        if inv_freq.get_device() != dev:
+            raise ValueError(f"inv_freq must be on cuda:{dev}")
         rot = 2 * inv_freq.numel()
         freqs = inv_freq.data_ptr() if rot else None
     qp = qo = None
@@ -562,22 +569,22 @@ def kda_cache_append(k, v, cache, q=None, inv_freq=None, interleaved=False, cu_s
         if q_shape[:-2] != shape[:-2]:
             raise ValueError("q and k must have the same tokens")
         Hq = q_shape[-2]
-        qs = _token_stride(q, Hq, d, "q")
+        qs = _token_stride(q, Hq, d, "q", dev)
         if q_out is None:
             q_out = _empty(q_shape, dtype, q.device, stream)
             qos = Hq * d
         elif q_out.shape != q_shape or q_out.dtype != dtype:
             raise ValueError("q_out must have q's shape and dtype")
         else:
-            qos = _token_stride(q_out, Hq, d, "q_out")
+            qos = _token_stride(q_out, Hq, d, "q_out", dev)
         qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     code = lib.kda_cache_append(
-        cache._ref, k.data_ptr(), v.data_ptr(), qp, qo, code, _token_stride(k, H, d, "k"),
-        _token_stride(v, H, d, "v"), qs, qos, freqs, rot, interleaved,
-        _int32_ptr(cu_seqlens, N + 1, "cu_seqlens"), _int32_ptr(counts, N, "counts"), K, T, Hq,
-        _stream_of(stream, k))
+        cache._ref, k.data_ptr(), v.data_ptr(), qp, qo, code, _token_stride(k, H, d, "k", dev),
+        _token_stride(v, H, d, "v", dev), qs, qos, freqs, rot, interleaved,
+        _int32_ptr(cu_seqlens, N + 1, "cu_seqlens", dev), _int32_ptr(counts, N, "counts", dev), K, T, Hq,
+        _stream_of(stream, dev))
     if code:
         raise KDAError(code, "kda_cache_append")
     return q_out
@@ -597,11 +604,13 @@ def kda_cache_attend(q, cache, scale=None, window=0, counts=None, max_len=0, out
     if len(shape) != 4 or shape[0] != cache.n_seq or code is None:
         raise ValueError(f"q must be [{cache.n_seq}, K, H_q, {cache.d}] in bfloat16 or float16")
     N, K, Hq, d = shape
-    qs = _token_stride(q, Hq, cache.d, "q")
-    if out is not None and (out.shape != shape or out.dtype != dtype or not out.is_cuda or not out.is_contiguous()):
-        raise ValueError("out must be a contiguous CUDA tensor with q's shape and dtype")
-    dev = q.device
-    need = _attend_workspace(dev.index, N, K, Hq, cache.heads, d, max_len or cache.capacity)
+    index, dev = cache.device_index, cache.device
+    qs = _token_stride(q, Hq, cache.d, "q", index)
+    if out is not None and (out.shape != shape or out.dtype != dtype or out.get_device() != index or
+                            not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous tensor on cuda:{index} with q's shape and dtype")
+    real, raw_stream = _int32_ptr(counts, N, "counts", index), _stream_of(stream, index)
+    need = _attend_workspace(index, N, K, Hq, cache.heads, d, max_len or cache.capacity)
     lse = ws = None
     if out is None:
         out = _empty(shape, dtype, dev, stream)
@@ -611,8 +620,8 @@ def kda_cache_attend(q, cache, scale=None, window=0, counts=None, max_len=0, out
         ws = _empty(need, torch.uint8, dev, stream)
     code = lib.kda_cache_attend(
         cache._ref, q.data_ptr(), code, qs, out.data_ptr(), None if lse is None else lse.data_ptr(),
-        _int32_ptr(counts, N, "counts"), K, Hq, d ** -0.5 if scale is None else scale, window, max_len,
-        None if ws is None else ws.data_ptr(), need, _stream_of(stream, q))
+        real, K, Hq, d ** -0.5 if scale is None else scale, window, max_len,
+        None if ws is None else ws.data_ptr(), need, raw_stream)
     if code:
         raise KDAError(code, "kda_cache_attend")
     return (out, lse) if return_lse else out
@@ -634,31 +643,34 @@ def kda_draft_accept(draft_tokens, draft_probs, target_probs, uniform, draft_len
     ts = target_probs.stride()
     if code is None or not target_probs.is_cuda or (ts[2] != 1 and V > 1):
         raise ValueError("target_probs must be a CUDA tensor of float32, bfloat16 or float16 with contiguous rows")
+    dev = target_probs.device
+    index = dev.index
     _need(draft_tokens, torch.int32, "draft_tokens")
     _need(uniform, torch.float32, "uniform")
+    if draft_tokens.get_device() != index or uniform.get_device() != index:
+        raise ValueError(f"draft_tokens and uniform must be on cuda:{index}, as target_probs")
     if K < 0 or draft_tokens.shape != (N, K) or uniform.shape != (N, K1):
         raise ValueError("draft_tokens must be [N, K] and uniform [N, K + 1] for target_probs [N, K + 1, V]")
     dp, ds = None, (0, 0)
     if draft_probs is not None:
         ds = draft_probs.stride()
-        if (draft_probs.dtype != dtype or not draft_probs.is_cuda or draft_probs.shape != (N, K, V) or
+        if (draft_probs.dtype != dtype or draft_probs.get_device() != index or draft_probs.shape != (N, K, V) or
                 (ds[2] != 1 and V > 1)):
-            raise ValueError(f"draft_probs must be a CUDA tensor {(N, K, V)} of target_probs' dtype with "
+            raise ValueError(f"draft_probs must be a tensor {(N, K, V)} on cuda:{index}, of target_probs' dtype with "
                              "contiguous rows")
         dp = draft_probs.data_ptr()
-    dev = target_probs.device
     if tokens is not None:
         _need(tokens, torch.int32, "tokens")
-        if tokens.shape != (N, K1):
-            raise ValueError(f"tokens must be {(N, K1)}")
+        if tokens.shape != (N, K1) or tokens.get_device() != index:
+            raise ValueError(f"tokens must be {(N, K1)} on cuda:{index}")
     if counts is None:
         counts = _empty(N, torch.int32, dev, stream)
     if tokens is None:
         tokens = _empty((N, K1), torch.int32, dev, stream)
     code = lib.kda_draft_accept(
         draft_tokens.data_ptr(), dp, target_probs.data_ptr(), code, ds[0], ds[1], ts[0], ts[1],
-        uniform.data_ptr(), _int32_ptr(draft_lens, N, "draft_lens"), _int32_ptr(counts, N, "counts"),
-        tokens.data_ptr(), N, K, V, _stream_of(stream, target_probs))
+        uniform.data_ptr(), _int32_ptr(draft_lens, N, "draft_lens", index), _int32_ptr(counts, N, "counts", index),
+        tokens.data_ptr(), N, K, V, _stream_of(stream, index))
     if code:
         raise KDAError(code, "kda_draft_accept")
     return counts, tokens

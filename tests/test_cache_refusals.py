@@ -109,8 +109,12 @@ class Claimed:
     """A host tensor that says it is on a GPU: for what is looked at before any launch."""
     is_cuda = True
 
-    def __init__(self, t):
-        self._t = t
+    def __init__(self, t, index=0):
+        self._t, self._index = t, index
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self._index
 
     def __getattr__(self, name):
         return getattr(self._t, name)
@@ -155,6 +159,72 @@ def test_assignments_that_do_not_fit_are_refused_and_change_nothing():
     with pytest.raises((TypeError, ValueError)):
         c.k_scale = "none"
     assert bytes(c._struct) == before
+
+
+def test_a_cache_lies_on_one_device():
+    def parts():
+        return [Claimed(torch.zeros((5, 16, 2, 64), dtype=torch.bfloat16)) for _ in range(2)] + [
+            Claimed(torch.zeros((3, 4), dtype=torch.int32)), Claimed(torch.zeros(3, dtype=torch.int32))]
+    for i in range(4):
+        p = parts()
+        p[i] = Claimed(p[i]._t, 1)
+        with pytest.raises(ValueError):
+            binding.PagedCache(*p)
+    c = binding.PagedCache(*parts())
+    with pytest.raises(ValueError):
+        c.lens = Claimed(torch.zeros(3, dtype=torch.int32), 1)
+
+
+def elsewhere(good, names, call):
+    """call(**good) with each of the named tensors on another GPU, or on the host, in turn."""
+    for name in names:
+        for t in (Claimed(good[name]._t, 1), good[name]._t):
+            with pytest.raises(ValueError):
+                call(**{**good, name: t})
+
+
+class NoLaunch:
+    """Stands for the library: a call that gets there has not been refused."""
+
+    def __getattr__(self, name):
+        def call(*args):
+            raise AssertionError(f"{name} was called")
+        return call
+
+
+def test_tensors_on_another_device_than_the_cache_are_refused(monkeypatch):
+    c, bf, i32 = claimed_cache(), torch.bfloat16, torch.int32
+    monkeypatch.setattr(binding, "_lib", NoLaunch())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    new = dict(k=Claimed(torch.zeros((3, 2, 2, 64), dtype=bf)), v=Claimed(torch.zeros((3, 2, 2, 64), dtype=bf)),
+               q=Claimed(torch.zeros((3, 2, 4, 64), dtype=bf)), q_out=Claimed(torch.zeros((3, 2, 4, 64), dtype=bf)),
+               inv_freq=Claimed(torch.zeros(8, dtype=torch.float64)), counts=Claimed(torch.zeros(3, dtype=i32)))
+    elsewhere(new, list(new), lambda **kw: binding.kda_cache_append(cache=c, **kw))
+    packed = dict(k=Claimed(torch.zeros((6, 2, 64), dtype=bf)), v=Claimed(torch.zeros((6, 2, 64), dtype=bf)),
+                  cu_seqlens=Claimed(torch.zeros(4, dtype=i32)))
+    elsewhere(packed, list(packed), lambda **kw: binding.kda_cache_append(cache=c, **kw))
+    monkeypatch.setattr(binding, "_attend_workspace", lambda *a: 0)
+    rows = dict(q=Claimed(torch.zeros((3, 2, 4, 64), dtype=bf)), out=Claimed(torch.zeros((3, 2, 4, 64), dtype=bf)),
+                counts=Claimed(torch.zeros(3, dtype=i32)))
+    elsewhere(rows, list(rows), lambda **kw: binding.kda_cache_attend(cache=c, **kw))
+    drafts = dict(draft_tokens=Claimed(torch.zeros((2, 3), dtype=i32)), draft_probs=Claimed(torch.zeros((2, 3, 9))),
+                  target_probs=Claimed(torch.zeros((2, 4, 9))), uniform=Claimed(torch.zeros((2, 4))),
+                  draft_lens=Claimed(torch.zeros(2, dtype=i32)), counts=Claimed(torch.zeros(2, dtype=i32)),
+                  tokens=Claimed(torch.zeros((2, 4), dtype=i32)))
+    elsewhere(drafts, list(drafts), binding.kda_draft_accept)
+
+
+def test_calls_away_from_the_current_device_or_the_streams_are_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        binding._stream_of(None, 0)
+
+    class Stream:
+        device_index, cuda_stream = 1, 7
+    assert binding._stream_of(Stream, 1) == 7
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError):
+        binding._stream_of(Stream, 0)
 
 
 @pytest.mark.gpu
