@@ -629,7 +629,8 @@ Plan plan_for(int n_seq, int K, int H_q, int H_kv, int d, int max_len) {
   a.groups = (a.rows + most - 1) / most;
   a.per = ((a.rows + a.groups - 1) / a.groups + 15) / 16 * 16;
   a.units = (long long)n_seq * H_kv * a.groups;
-  const long long tiles = a.units * ((max_len + TILE - 1) / TILE > 1 ? (max_len + TILE - 1) / TILE : 1);
+  const long long unit_tiles = ((long long)max_len + TILE - 1) / TILE;
+  const long long tiles = a.units * (unit_tiles > 1 ? unit_tiles : 1);
   // 64 requests of 8192 positions, 4 key heads of 128, on tcgen05 against the warp-level products with as
   // many row groups as it takes: 16-bit, 32 rows 175 us against 218, 40 rows 180 against 347; 8-bit, 32
   // rows 113 against 167, 40 rows 139 against 277.

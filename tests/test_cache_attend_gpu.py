@@ -532,3 +532,12 @@ def test_an_infinite_query_over_an_8_bit_cache_gives_nan(rows, length):
     assert torch.isnan(out[0, 0, 2].float()).all()
     rest = [r for r in range(rows) if r != 2]
     assert torch.isfinite(out[0, 0, rest].float()).all()
+
+
+@pytest.mark.parametrize("rows", [4, 40])
+def test_the_largest_bound_on_the_lengths_is_one(rows):
+    """2^31 - 1, as for 'no bound': the launch and the workspace are those of any long sequence."""
+    size = binding.load().kda_cache_attend_workspace_size
+    most = (1 << 31) - 1
+    assert size(3, 1, rows, 1, 128, most) == size(3, 1, rows, 1, 128, 1 << 30) == size(3, 1, rows, 1, 128, 1 << 20) > 0
+    check([100, 2000, 7], Hq=rows, Hkv=1, max_len=most)
