@@ -1,5 +1,6 @@
 // C-ABI boundary of libkda: argument validation, status codes and dispatch
 // to the kernels.  No allocation, no printing, no exception crosses it.
+#include <algorithm>
 #include <cstdint>
 #include <cstdlib>
 
@@ -415,9 +416,20 @@ kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void* k, con
   return from_cuda(e == cudaSuccess ? kda::launch_cache_append(p, stream) : e);
 }
 
+namespace {
+
+// Query rows of a call of kda_cache_attend; more than it takes are one more than that.
+constexpr long long MOST_ROWS = 0x3fffffffLL;
+long long attend_rows(int n_seq, int K, int H_q) {
+  const long long of_seq = std::min((long long)K * H_q, MOST_ROWS + 1);
+  return std::min(n_seq * of_seq, MOST_ROWS + 1);
+}
+
+}  // namespace
+
 size_t kda_cache_attend_workspace_size(int n_seq, int K, int H_q, int H_kv, int d, int max_len) {
   if (n_seq <= 0 || K <= 0 || H_kv <= 0 || H_q <= 0 || H_q % H_kv || !(d == 64 || d == 128) ||
-      max_len < 0)
+      max_len < 0 || attend_rows(n_seq, K, H_q) > MOST_ROWS)
     return 0;
   return kda::attend_workspace_bytes(n_seq, K, H_q, H_kv, d, max_len);
 }
@@ -433,11 +445,11 @@ kda_status_t kda_cache_attend(const kda_paged_cache_t* cache, const void* q, kda
   if (st != KDA_OK) return st;
   if (K < 0 || H_q <= 0 || H_q % cache->H_kv || window < 0 || max_len < 0 || q_stride < 0)
     return KDA_ERR_INVALID_ARG;
-  const long long rows = (long long)cache->n_seq * K * H_q;
+  const long long rows = attend_rows(cache->n_seq, K, H_q);
   if (rows > 0 && (!q || !out)) return KDA_ERR_INVALID_ARG;
   if (!aligned_rows(q, q_stride, dtype) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return KDA_ERR_ALIGNMENT;
-  if (rows > 0x3fffffffLL) return KDA_ERR_UNSUPPORTED;
+  if (rows > MOST_ROWS) return KDA_ERR_UNSUPPORTED;
   if (rows == 0) return KDA_OK;
   const int capacity = cache->table_width * cache->page_size;
   if (!kda::attend_tiles_fit(cache->n_seq, K, H_q, cache->H_kv, capacity)) return KDA_ERR_UNSUPPORTED;

@@ -84,6 +84,15 @@ def test_attend_workspace_size_of_nonsense_is_zero(lib):
     assert size(1, 1, 4, 2, 96, 100) == 0 and size(1, 1, 4, 2, 128, -1) == 0
 
 
+def test_attend_row_counts_past_32_bits(lib):
+    big = (1 << 31) - 1
+    assert attend(lib, cache(n_seq=1 << 22), K=1 << 22, Hq=1 << 20) == 2  # 2^64 rows
+    assert attend(lib, cache(n_seq=big), K=big, Hq=big - 1) == 2
+    assert attend(lib, cache(n_seq=1 << 15), K=1 << 10, Hq=64) == 2
+    assert lib.kda_cache_attend_workspace_size(big, big, big, 1, 128, 100) == 0
+    assert lib.kda_cache_attend_workspace_size(1, 1 << 20, 1 << 20, 1, 128, 100) == 0
+
+
 def test_accept_arguments(lib):
     def call(toks=F, draft=F, target=F, dtype=F32, strides=(400, 100, 500, 100), u=F, lens=None, counts=F,
              out=F, N=2, K=4, V=100):
