@@ -609,6 +609,8 @@ def kda_cache_attend(q, cache, scale=None, window=0, counts=None, max_len=0, out
     if out is not None and (out.shape != shape or out.dtype != dtype or out.get_device() != index or
                             not out.is_contiguous()):
         raise ValueError(f"out must be a contiguous tensor on cuda:{index} with q's shape and dtype")
+    # no length passes 2^30; ctypes would cut larger numbers to their lower 32 bits
+    window, max_len = max(-1, min(window, 0x7fffffff)), max(-1, min(max_len, 0x7fffffff))
     real, raw_stream = _int32_ptr(counts, N, "counts", index), _stream_of(stream, index)
     need = _attend_workspace(index, N, K, Hq, cache.heads, d, max_len or cache.capacity)
     lse = ws = None

@@ -223,6 +223,22 @@ def test_tensors_on_another_device_than_the_cache_are_refused(monkeypatch):
     elsewhere(drafts, list(drafts), binding.kda_draft_accept)
 
 
+@pytest.mark.parametrize("value,given", [(5, 5), (1 << 31, (1 << 31) - 1), ((1 << 32) + 5, (1 << 31) - 1),
+                                         (-1, -1), (-(1 << 32), -1), (-(1 << 32) + 5, -1)])
+def test_windows_and_bounds_past_32_bits_are_not_cut_to_their_lower_bits(monkeypatch, value, given):
+    """No length passes 2^30, so a larger window or bound is the same as 2^31 - 1."""
+    class Library:
+        def kda_cache_attend(self, *args):
+            self.window, self.max_len = args[10], args[11]
+            return 0
+    monkeypatch.setattr(binding, "_lib", Library())
+    monkeypatch.setattr(binding, "_attend_workspace", lambda *a: 0)
+    monkeypatch.setattr(binding, "_stream_of", lambda *a: 0)
+    q, out = (Claimed(torch.zeros((3, 2, 4, 64), dtype=torch.bfloat16)) for _ in range(2))
+    binding.kda_cache_attend(q, claimed_cache(), out=out, window=value, max_len=value)
+    assert (binding._lib.window, binding._lib.max_len) == (given, given)
+
+
 def test_calls_away_from_the_current_device_or_the_streams_are_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError):
