@@ -541,3 +541,86 @@ def test_the_largest_bound_on_the_lengths_is_one(rows):
     most = (1 << 31) - 1
     assert size(3, 1, rows, 1, 128, most) == size(3, 1, rows, 1, 128, 1 << 30) == size(3, 1, rows, 1, 128, 1 << 20) > 0
     check([100, 2000, 7], Hq=rows, Hkv=1, max_len=most)
+
+
+# Bad pages, strides and single infinities where the large bound puts 40 rows on the units of up to 48.
+@pytest.mark.parametrize("bad", [(0, 7, 15), tuple(range(8, 16)), tuple(range(19))])
+@pytest.mark.parametrize("act,dtype", [(BF, BF), (FP, FP), (BF, E4)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_bad_pages_with_a_large_bound(act, dtype, d, bad):
+    """Single pages, a whole tile of 128 positions, and every page but the last one's drafts."""
+    lens, K, Hq = [300], 5, 8
+    cache, keys, values = make_cache(lens, K, 1, d, 16, dtype)
+    binding.kda_last_device_status()
+    for x, j in enumerate(bad):
+        cache.block_table[0, j] = (-1, 10 ** 9, cache.k_pages.shape[0])[x % 3]
+    q = torch.randn((1, K, Hq, d), generator=torch.Generator().manual_seed(4)).to(act)
+    out, lse = binding.kda_cache_attend(q.cuda(), cache, max_len=9000, return_lse=True)
+    torch.cuda.synchronize()
+    assert binding.kda_last_device_status() == 1
+    kept = [j for j in range(lens[0] + K) if j // 16 not in bad]
+    ref, rlse, tol, ltol = attend_reference(q, [keys[0][kept]], [values[0][kept]], [len(kept) - K], None, d ** -0.5, 0)
+    assert_within(lse, rlse, ltol, "lse")
+    assert_within(out, ref, tol, "out")
+
+
+@pytest.mark.parametrize("dtype", [BF, E4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_rows_bad_page_and_nan_in_a_later_draft_with_a_large_bound(dtype, d):
+    """Both in one tile: the product formed row by row leaves the bad page out."""
+    lens, K, Hq = [300], 5, 8
+    cache, keys, values = make_cache(lens, K, 1, d, 16, dtype)
+    binding.kda_last_device_status()
+    cache.block_table[0, 17] = -1  # positions 272 to 287, in the tile of the drafts
+    pos = lens[0] + 1
+    page = int(cache.block_table[0, pos // 16])
+    cache.v_pages[page, pos % 16] = torch.full((1, d), NAN).to(dtype).cuda()
+    cache.k_pages[page, pos % 16] = torch.zeros((1, d)).to(dtype).cuda()
+    q = torch.randn((1, K, Hq, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), cache, max_len=9000)
+    torch.cuda.synchronize()
+    assert binding.kda_last_device_status() == 1
+    kept = [j for j in range(lens[0] + 1) if j // 16 != 17]
+    ref, _, tol, _ = attend_reference(q[:, :1], [keys[0][kept]], [values[0][kept]], [len(kept) - 1], None, d ** -0.5, 0)
+    assert_within(out[:, :1], ref, tol, "token 0")
+    assert not torch.isfinite(out[:, 1:].float()).any()
+
+
+def test_many_rows_pages_that_no_entry_names_with_a_large_bound():
+    """Every page bad: nothing is seen, in every row."""
+    cache, _, _ = make_cache([200], 1, 1, 128, 16, BF)
+    binding.kda_last_device_status()
+    cache.block_table.fill_(-1)
+    for rows in (4, 40):
+        q = torch.randn((1, 1, rows, 128), generator=torch.Generator().manual_seed(4)).to(BF).cuda()
+        out, lse = binding.kda_cache_attend(q, cache, max_len=9000, return_lse=True)
+        torch.cuda.synchronize()
+        assert binding.kda_last_device_status() == 1
+        assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_many_rows_strides_with_a_large_bound():
+    lens, d, Hq = [130, 7], 128, 80
+    cache, keys, values = make_cache(lens, 1, 2, d, 16, BF)
+    q = torch.randn((2, 1, Hq, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    ref, _, tol, _ = attend_reference(q, keys, values, lens, None, d ** -0.5, 0)
+    pool = torch.stack([cache.k_pages, cache.v_pages], 1).contiguous()  # keys and values of a page side by side
+    rows = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (cache.k_pages, cache.v_pages)]  # [row, page, head, d]
+    for pools in ((pool[:, 0], pool[:, 1]), rows):
+        out = binding.kda_cache_attend(q.cuda(), binding.PagedCache(*pools, cache.block_table, cache.lens), max_len=9000)
+        assert_within(out, ref, tol, "out")
+
+
+def test_many_rows_one_infinite_value_of_a_later_draft_with_a_large_bound():
+    lens, K, Hq, d = [100], 5, 8, 128
+    cache, keys, values = make_cache(lens, K, 1, d, 16, BF)
+    pos = lens[0] + 2
+    cache.v_pages[int(cache.block_table[0, pos // 16]), pos % 16, 0, 77] = math.inf
+    values[0][pos, 0, 77] = 0  # the other channels' reference
+    q = torch.randn((1, K, Hq, d), generator=torch.Generator().manual_seed(4)).to(BF)
+    out = binding.kda_cache_attend(q.cuda(), cache, max_len=9000)
+    ref, _, tol, _ = attend_reference(q, keys, values, lens, None, d ** -0.5, 0)
+    rest = [c for c in range(d) if c != 77]
+    assert_within(out[..., rest], ref[..., rest], tol[..., rest], "other channels")
+    assert (out[:, 2:, :, 77] == math.inf).all()
+    assert torch.isfinite(out[:, :2].float()).all()
