@@ -436,8 +436,9 @@ typedef struct {
  *                 v_stride elements apart, heads of a token d apart (slices
  *                 of one projection's output are taken as they are)
  *   q, q_out    : [same tokens, H_q, d] in dtype, token rows q_stride and
- *                 q_out_stride apart, or both NULL; q_out may be q.  Every
- *                 token's query is written, also beyond counts[n].
+ *                 q_out_stride apart (q_out's must not overlap), or both NULL;
+ *                 q_out may be q.  Every token's query is written, also beyond
+ *                 counts[n].
  *   inv_freq    : DEVICE fp64 [rot_dim / 2], radians per position: pair j of a
  *                 head is turned by position * inv_freq[j]; NULL with
  *                 rot_dim 0 (no rotation)

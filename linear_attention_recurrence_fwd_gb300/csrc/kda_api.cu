@@ -402,6 +402,7 @@ kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void* k, con
   if (rot_dim < 0 || rot_dim % 2 || rot_dim > cache->d || (rot_dim > 0 && !inv_freq))
     return KDA_ERR_INVALID_ARG;
   if (k_stride < 0 || v_stride < 0 || q_stride < 0 || q_out_stride < 0) return KDA_ERR_INVALID_ARG;
+  if (q && T > 1 && q_out_stride < (long long)H_q * cache->d) return KDA_ERR_INVALID_ARG;  // tokens on top of one another
   if (!aligned_rows(k, k_stride, dtype) || !aligned_rows(v, v_stride, dtype) ||
       !aligned_rows(q, q ? q_stride : 0, dtype) || !aligned_rows(q_out, q ? q_out_stride : 0, dtype) ||
       (reinterpret_cast<uintptr_t>(inv_freq) & 7u))

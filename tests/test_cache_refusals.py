@@ -67,6 +67,11 @@ def test_append_arguments(lib):
     assert append(lib, K=0, T=0) == 0  # nothing to do
 
 
+def test_append_rotated_queries_that_overlap(lib):
+    assert append(lib, qos=0) == 1 and append(lib, qos=504) == 1
+    assert append(lib, qos=0, K=0, T=0) == 0  # no two tokens
+
+
 def test_attend_arguments(lib):
     assert attend(lib, False) == 1
     assert attend(lib, q=None) == 1 and attend(lib, out=None) == 1
