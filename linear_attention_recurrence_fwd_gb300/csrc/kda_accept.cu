@@ -193,6 +193,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// (relaxed: nothing written before is for the others)
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // stores x at the place of `local` in the shared memory of the cluster's CTA `rank`
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(THREADS, 4) accept_kernel(const __grid_constan
   const int rank = cluster == 1 ? 0 : (int)cluster_rank();
   // Another CTA's shared memory exists once that CTA has started: all arrive here, and wait before
   // their first store to it (the drafts' test and the sums lie in between).
-  if (cluster > 1) cluster_arrive();
+  if (cluster > 1) cluster_started();
   const int n = blockIdx.x / cluster, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int K = p.K, V = p.V;
   int* tokens = p.tokens + (long long)n * (K + 1);
