@@ -387,13 +387,16 @@ KDA_API kda_status_t kda_decode_commit(const void* q, const void* k, const void*
                                        int d_v, cudaStream_t stream);
 
 /*
- * The attention layers of a hybrid stack (one to every three recurrent ones:
+ * A stack may mix recurrent layers with attention layers (one to every three:
  * orkas.ai, "Kimi K3 architecture", section "Sequenz: Drei Viertel der
- * Schichten lesen nicht mehr alles") keep every token's key and value.  The
- * cache of a request is then per-token pages plus the fixed states above
- * (same page, section "Die Rechnung landet in der
- * Bereitstellungsinfrastruktur").  kda_paged_cache_t describes the pages of
- * one attention layer; the caller owns every buffer it points to.
+ * Schichten lesen nicht mehr alles"); a request's cache is then per-token
+ * pages plus the fixed states above (same page, section "Die Rechnung landet
+ * in der Bereitstellungsinfrastruktur").  The calls below are for attention
+ * layers of the grouped-query kind, which keep a key and a value per token and
+ * key head, with or without a turn by position.  (The attention layers of that
+ * page are latent, one row per token for all heads; these pages do not hold
+ * them.)  kda_paged_cache_t describes the pages of one attention layer; the
+ * caller owns every buffer it points to.
  *   k, v        : pages; channel c of head h of row t of page p is element
  *                 p * page_stride + t * token_stride + h * head_stride + c
  *                 (strides in elements, the same for k and v; each a multiple
@@ -475,7 +478,8 @@ KDA_API kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void
  *   window  : 0, or the number of newest positions, its own among them, that a
  *             token sees
  *   max_len : an upper bound on lens[n] + K, or 0 for what the table holds; it
- *             sizes the launch (a sequence beyond it is read to its end)
+ *             sizes the launch and the workspace (a sequence beyond it is read
+ *             to its end)
  * Token i of sequence n sees positions max(0, p - window + 1) .. p with
  * p = lens[n] + i (lens[n] may be negative).  Where nothing is seen (a token
  * beyond counts[n], an empty sequence), out is 0 and lse is -infinity;
@@ -484,7 +488,10 @@ KDA_API kda_status_t kda_cache_append(const kda_paged_cache_t* cache, const void
  * and lse -infinity.  The scores, the softmax and its sums are fp32; for the
  * product with the values the weights are rounded to the type of q or, over an
  * 8-bit cache, to 9 bits or more (11 with KDA_F16), and small ones to 2^-29 of
- * the largest.  Over an 8-bit cache a row of q that holds an infinity gives NaN.
+ * the largest.  Over an 8-bit cache with 17 or more query rows to a key head
+ * (K times H_q / H_kv), entries of q below 2^-14 of their row's largest are off
+ * by up to 2^-21 of it (KDA_F16: 2^-18 and 2^-25).  Over an 8-bit cache a row
+ * of q that holds an infinity gives NaN.
  * Results do not depend on anything but the arguments (no atomics).
  *   workspace : kda_cache_attend_workspace_size() bytes, 16-byte aligned, for
  *             the parts of a sequence's softmax that different blocks compute
@@ -523,7 +530,8 @@ KDA_API size_t kda_cache_attend_workspace_size(int n_seq, int K, int H_q, int H_
  * are max(target[a] - draft[a], 0) (without draft_probs: target[a] without the
  * draft's entry), after the last one target[a], also where no weight is
  * positive.  The token drawn is the first whose running sum of weights is
- * more than uniform[K] times their total.  Sums are in 64 bits.  Weights that
+ * more than uniform[K] times their total.  Sums hold 48 bits (pairs of fp32
+ * numbers with exact differences).  Weights that
  * are not positive and finite count as zero; where all are, the token is -1.
  * A draft outside [0, V) is not kept and sets KDA_ERR_INVALID_ARG in the
  * device status word.

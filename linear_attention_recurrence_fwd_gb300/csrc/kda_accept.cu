@@ -11,7 +11,7 @@
 // The slices' sums meet in every CTA's shared memory; the CTA whose slice
 // holds the border sums that slice again in 256 contiguous pieces, and one
 // warp looks through the piece that holds it, out of L2.  256 sequences of
-// 131072 fp32 entries: 48 us, 4.6 TB/s; one of 32768: 6.2 us.
+// 131072 fp32 entries: 48 us, 4.5 TB/s; one of 32768: 5.8 us.
 //
 // Sums: an fp32 running sum over 10^5 weights is off by about 10^-7 of the
 // total, enough to change a token in every few hundred draws, and fp64 runs at

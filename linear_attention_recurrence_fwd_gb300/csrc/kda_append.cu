@@ -8,8 +8,8 @@
 // 2^20 * 2^-24 radians).
 //
 // The call moves bytes: it is bound by HBM for prompts (65536 packed tokens of
-// 32 query and 8 key heads of 128, 1.61 GB: 251 us, 6.4 TB/s) and by latency
-// for single tokens (256 tokens: 5.0 us).  A CTA has 256 threads and takes 1 or
+// 32 query and 8 key heads of 128, 1.61 GB: 249 us, 6.5 TB/s) and by latency
+// for single tokens (256 tokens: 4.5 us).  A CTA has 256 threads and takes 1 or
 // 4 tokens at a time.  A token's sines and cosines are formed once, for all its
 // heads, and kept in shared memory; the heads' first bytes are on their way
 // meanwhile.  A thread takes 8 channels and the 8 that they are turned with, 16

@@ -36,8 +36,8 @@
 //
 // Measured (32 query heads of 128): 256 requests of 7 to 8191 positions on 8
 // key heads 630 us, 6.8 TB/s, the copy bandwidth; one request of 2^20
-// positions, 16 heads on 2, 170 us (6.3 TB/s); 64 requests of 8192, 8 key heads,
-// 316 us (6.8 TB/s), and 8-bit 195 us (5.5 TB/s: converting 8-bit fragments to
+// positions, 16 heads on 2, 167 us (6.4 TB/s); 64 requests of 8192, 8 key heads,
+// 316 us (6.8 TB/s), and 8-bit 189 us (5.7 TB/s: converting 8-bit fragments to
 // fp16 is what bounds it).
 #include <cstdint>
 

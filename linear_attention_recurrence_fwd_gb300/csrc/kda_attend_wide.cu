@@ -27,9 +27,9 @@
 //
 // Against warp-level instructions, which run at an eighth of tcgen05's rate (64
 // requests of 8192 positions, 4 key heads of 128, 40 rows): 347 us there and
-// 180 us here, 6.0 TB/s.  8-bit: 277 us there (each group of 16 rows converts
+// 177 us here, 6.1 TB/s.  8-bit: 277 us there (each group of 16 rows converts
 // all keys and values), 258 us here with keys and values converted through
-// shared and tensor memory, 139 us in pieces (3.9 TB/s; a tile takes 1620
+// shared and tensor memory, 133 us in pieces (4.0 TB/s; a tile takes 1620
 // clocks, of which its bytes need 1400, and a unit's end and start 14000).
 //
 // Warps: 0-7 softmax, 8 and 11 load, 9 and 10 issue the scores and the values.

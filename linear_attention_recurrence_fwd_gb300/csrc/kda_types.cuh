@@ -1,5 +1,5 @@
 // Element types of the paged cache and the draft calls: conversions to and
-// from fp32, and 16-byte groups of values.
+// from fp32.
 #pragma once
 
 #include <cstdint>
