@@ -30,6 +30,11 @@ def test_comment_edit_keeps_code_and_code_edit_changes_it():
     assert bench.source_code(edited) != bench.source_code(SRC)
 
 
+def test_traffic_record_is_of_the_current_source():
+    """A change of the prefill's code loses the bench's traffic figure until the record is taken again."""
+    assert bench.recorded_traffic() is not None
+
+
 def test_traffic_record_matches_current_source_or_is_ignored():
     rec = json.load(open(os.path.join(ROOT, "profiles", "chunk_prefill_traffic.json")))
     traffic = bench.recorded_traffic()
