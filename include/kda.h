@@ -543,6 +543,165 @@ KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft
                                       const float* uniform, const int* draft_lens, int* counts,
                                       int* tokens, int N, int K, int V, cudaStream_t stream);
 
+/*
+ * Linear attention with one decay per head: a second kind of recurrent layer,
+ * without the delta rule,
+ *
+ *     S_t = alpha_t S_{t-1} + k_t v_t^T,    o_t = scale * S_t^T q_t,
+ *     alpha_t = exp(log_alpha_t), one number for a token and head.
+ *
+ * For the calls below
+ *   q, k, v     : bf16, token rows *_stride elements apart (multiples of 16
+ *                 bytes), heads of a token d apart, so that slices of one
+ *                 projection's output are taken as they are
+ *   log_alpha   : la_dtype (KDA_BF16 or KDA_F32), that of row t and head h at
+ *                 t * la_token_stride + h * la_head_stride (0 and 1: a fixed
+ *                 decay per head).  At most 0; -infinity (and in the chunked
+ *                 calls anything below -104, whose exponential is 0 in fp32)
+ *                 drops the state.  Larger values are not checked.
+ *   states      : [N, H, d_k, d_v] fp32, contiguous
+ *   d_k = d_v   : 64 or 128
+ *   cu_seqlens  : DEVICE int32 [N + 1], offsets of T packed rows (as in
+ *                 kda_varlen_fwd), or NULL: N sequences of T / N rows each.
+ *                 Offsets that decrease or leave [0, T] are clamped, and those,
+ *                 cu[0] != 0 and cu[N] != T set KDA_ERR_INVALID_ARG in the
+ *                 device status word; rows without a sequence are not written.
+ * Sequences do not reach one another, whatever their rows hold.
+ */
+
+/*
+ * kda_linear_fwd -- prompts: all tokens of N sequences, in chunks of 128.
+ *   q, k, v       : [T, H, d];  out : [T, H, d] in out_dtype (KDA_BF16 or
+ *                   KDA_F32), contiguous, no alias of an input
+ *   initial_state : or NULL for zeros;  final_state : or NULL (not written);
+ *                   may be the same buffer
+ *   workspace     : kda_linear_fwd_workspace_size() bytes, 16-byte aligned.
+ *                   Calls that share it must not overlap on the GPU.
+ * Decays between tokens are exponentials of differences of log_alpha's fp32
+ * running sum within a chunk.  Products are sums in fp32.  Operands that are
+ * not given in bf16 (weighted values, weights, states) enter them as two bf16
+ * numbers each (16 bits), but with KDA_BF16 outputs the weights and the states
+ * that only outputs see enter as one.  A value that is not finite makes its
+ * channel NaN from its token on; earlier tokens do not see it.
+ */
+KDA_API kda_status_t kda_linear_fwd(const void* q, const void* k, const void* v, long long q_stride,
+                                    long long k_stride, long long v_stride, const void* log_alpha,
+                                    kda_dtype_t la_dtype, long long la_token_stride,
+                                    long long la_head_stride, const int* cu_seqlens,
+                                    const float* initial_state, void* out, kda_dtype_t out_dtype,
+                                    float* final_state, int N, int T, int H, int d_k, int d_v,
+                                    float scale, void* workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+/* packed: whether the call has cu_seqlens.  The answer depends on the current
+ * device's SM count. */
+KDA_API size_t kda_linear_fwd_workspace_size(int N, int T, int H, int d_k, int d_v, int packed);
+
+/*
+ * kda_linear_bwd -- gradients of <d_out, out> + <d_final_state, final_state>
+ * with respect to kda_linear_fwd's q, k, v, log_alpha and initial_state.
+ *   d_out           : [T, H, d] bf16, rows d_out_stride apart
+ *   d_final_state   : fp32, or NULL (zero)
+ *   dq, dk, dv      : [T, H, d] bf16, contiguous
+ *   dlog_alpha      : [T, H] in la_dtype, contiguous, or NULL; with
+ *                     sum_log_alpha != 0 [H], the sum over all rows (the
+ *                     gradient of decays that are fixed per head)
+ *   d_initial_state : fp32, or NULL (not written)
+ *   workspace       : kda_linear_bwd_workspace_size() bytes, 16-byte aligned
+ * Results do not depend on anything but the arguments (no atomics).
+ */
+KDA_API kda_status_t kda_linear_bwd(const void* q, const void* k, const void* v, const void* d_out,
+                                    long long q_stride, long long k_stride, long long v_stride,
+                                    long long d_out_stride, const void* log_alpha,
+                                    kda_dtype_t la_dtype, long long la_token_stride,
+                                    long long la_head_stride, const int* cu_seqlens,
+                                    const float* initial_state, const float* d_final_state, void* dq,
+                                    void* dk, void* dv, void* dlog_alpha, int sum_log_alpha,
+                                    float* d_initial_state, int N, int T, int H, int d_k, int d_v,
+                                    float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+KDA_API size_t kda_linear_bwd_workspace_size(int N, int T, int H, int d_k, int d_v, int packed);
+
+/*
+ * kda_linear_step -- one new token for each of N sequences, states updated in
+ * place.  q, k, v : [N, H, d]; out : [N, H, d] in out_dtype.
+ * kda_linear_verify, kda_linear_commit -- the speculative pair, as
+ * kda_decode_verify and kda_decode_commit: outputs of K drafted tokens
+ * [N, K, H, d] from states that are only read, and the states advanced in
+ * place by the first accepted[n] (clamped to [0, K]) of the same tokens.
+ */
+KDA_API kda_status_t kda_linear_step(const void* q, const void* k, const void* v, long long q_stride,
+                                     long long k_stride, long long v_stride, const void* log_alpha,
+                                     kda_dtype_t la_dtype, long long la_token_stride,
+                                     long long la_head_stride, float* state, void* out,
+                                     kda_dtype_t out_dtype, int N, int H, int d_k, int d_v,
+                                     float scale, cudaStream_t stream);
+KDA_API kda_status_t kda_linear_verify(const void* q, const void* k, const void* v,
+                                       long long q_stride, long long k_stride, long long v_stride,
+                                       const void* log_alpha, kda_dtype_t la_dtype,
+                                       long long la_token_stride, long long la_head_stride,
+                                       const float* state, void* out, kda_dtype_t out_dtype, int N,
+                                       int K, int H, int d_k, int d_v, float scale,
+                                       cudaStream_t stream);
+KDA_API kda_status_t kda_linear_commit(const void* k, const void* v, long long k_stride,
+                                       long long v_stride, const void* log_alpha,
+                                       kda_dtype_t la_dtype, long long la_token_stride,
+                                       long long la_head_stride, float* state, const int* accepted,
+                                       int N, int K, int H, int d_k, int d_v, cudaStream_t stream);
+
+/*
+ * kda_logits_probs -- probabilities from logits, as kda_draft_accept takes
+ * them: penalties for what has been said, biases, masks and temperature, then
+ * the softmax.  For each entry x = logit and then, in this order,
+ *   said before (history, and the drafts before the row):
+ *                x = x > 0 ? x / repetition : x * repetition
+ *   said in the reply (history without the prompt, drafts), count times:
+ *                x = x - frequency * count - presence
+ *   x = x + each bias given for it; a masked entry gets probability 0;
+ *   p = softmax(x / temperature); temperature <= 0 (or NaN): 1 at the largest
+ *   entry, the first of equal ones, 0 elsewhere.
+ * Of kda_logits_rules_t every pointer may be NULL (that rule is left out):
+ *   tokens       : int32 [N, L], rows tokens_stride apart: each request's
+ *                  history, of which the first lens[n] tokens are real
+ *                  (clamped to [0, L]; NULL: all) and the first prompt_lens[n]
+ *                  of those its prompt (NULL: none)
+ *   drafts       : int32 [N, R - 1]: drafts 0 .. r - 1 have been said before
+ *                  row r
+ *   repetition, presence, frequency : fp32 [N]
+ *   bias_ids     : int32 [N, J]; bias : fp32 [N, J].  An id that comes twice
+ *                  gets both.
+ *   mask         : 32 entries to an int32, the lowest bit the first; rows of
+ *                  requests mask_stride_n and rows mask_stride_r int32 apart
+ *                  (0: shared); a bit that is not set masks its entry
+ *   temperature  : fp32 [N]
+ * Token ids outside [0, V) are left out everywhere.
+ *   logits : [N, R, V] in dtype (KDA_F32, KDA_BF16 or KDA_F16), vocabulary
+ *            contiguous, rows stride_r and requests stride_n elements apart
+ *   out    : [N, R, V] in out_dtype (KDA_F32 or dtype), contiguous; may be
+ *            logits where that is contiguous and of out_dtype
+ * A row all of whose entries are masked or -infinity becomes all 0; one with a
+ * NaN or +infinity that is not masked becomes all NaN.  All sums are fp32.
+ * With a penalty V is at most 425984 (a row's counts are held on chip).
+ * Results do not depend on anything but the arguments.
+ */
+typedef struct {
+    const int* tokens;
+    const int* lens;
+    const int* prompt_lens;
+    const int* drafts;
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    const int* bias_ids;
+    const float* bias;
+    const int* mask;
+    const float* temperature;
+    long long tokens_stride, mask_stride_n, mask_stride_r;
+    int L, J;
+} kda_logits_rules_t;
+KDA_API kda_status_t kda_logits_probs(const void* logits, kda_dtype_t dtype, long long stride_n,
+                                      long long stride_r, const kda_logits_rules_t* rules, void* out,
+                                      kda_dtype_t out_dtype, int N, int R, int V,
+                                      cudaStream_t stream);
+
 /* Static description of a status code (never NULL). */
 KDA_API const char* kda_status_string(kda_status_t status);
 

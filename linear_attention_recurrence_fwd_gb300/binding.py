@@ -34,6 +34,9 @@ EXPORTS = ["kda_chunk_fwd", "kda_chunk_fwd_workspace_size", "kda_chunk_fwd_noall
            "kda_varlen_fwd",
            "kda_varlen_fwd_workspace_size", "kda_decode_step", "kda_cache_append",
            "kda_cache_attend", "kda_cache_attend_workspace_size", "kda_draft_accept",
+           "kda_linear_fwd", "kda_linear_fwd_workspace_size", "kda_linear_bwd",
+           "kda_linear_bwd_workspace_size", "kda_linear_step", "kda_linear_verify",
+           "kda_linear_commit", "kda_logits_probs",
            "kda_status_string",
            "kda_last_device_status", "kda_version"]
 
@@ -103,6 +106,23 @@ def load(path: str = LIB_PATH):
         lib.kda_cache_attend_workspace_size.restype = _sz
         lib.kda_draft_accept.argtypes = [_vp, _vp, _vp, _i] + [_ll] * 4 + [_vp] * 4 + [_i] * 3 + [_vp]
         lib.kda_draft_accept.restype = _i
+        decay = [_vp, _i, _ll, _ll]  # log_alpha, its type and strides
+        lib.kda_linear_fwd.argtypes = ([_vp] * 3 + [_ll] * 3 + decay + [_vp, _vp, _vp, _i, _vp] + [_i] * 5 +
+                                       [_f, _vp, _sz, _vp])
+        lib.kda_linear_fwd.restype = _i
+        lib.kda_linear_bwd.argtypes = ([_vp] * 4 + [_ll] * 4 + decay + [_vp] * 7 + [_i, _vp] + [_i] * 5 + [_f, _vp, _sz, _vp])
+        lib.kda_linear_bwd.restype = _i
+        for name in ("kda_linear_fwd_workspace_size", "kda_linear_bwd_workspace_size"):
+            getattr(lib, name).argtypes = [_i] * 6
+            getattr(lib, name).restype = _sz
+        lib.kda_linear_step.argtypes = [_vp] * 3 + [_ll] * 3 + decay + [_vp, _vp] + [_i] * 5 + [_f, _vp]
+        lib.kda_linear_step.restype = _i
+        lib.kda_linear_verify.argtypes = [_vp] * 3 + [_ll] * 3 + decay + [_vp, _vp] + [_i] * 6 + [_f, _vp]
+        lib.kda_linear_verify.restype = _i
+        lib.kda_linear_commit.argtypes = [_vp] * 2 + [_ll] * 2 + decay + [_vp, _vp] + [_i] * 5 + [_vp]
+        lib.kda_linear_commit.restype = _i
+        lib.kda_logits_probs.argtypes = [_vp, _i, _ll, _ll, _vp, _vp, _i, _i, _i, _i, _vp]
+        lib.kda_logits_probs.restype = _i
         lib.kda_status_string.argtypes = [_i]
         lib.kda_status_string.restype = ctypes.c_char_p
         lib.kda_last_device_status.argtypes = [_vp]
@@ -676,6 +696,278 @@ def kda_draft_accept(draft_tokens, draft_probs, target_probs, uniform, draft_len
     if code:
         raise KDAError(code, "kda_draft_accept")
     return counts, tokens
+
+
+def _linear_tokens(k, lead, **others):
+    """Heads, head dim, GPU and token strides of k and of the others, all [*lead, H, d] in bf16."""
+    shape = k.shape
+    if len(shape) != lead + 2:
+        raise ValueError(f"k must have {lead + 2} dimensions here")
+    H, d = shape[-2:]
+    dev = k.get_device()
+    if dev < 0:
+        raise ValueError("q, k and v must be CUDA tensors")
+    one = shape[:-2].numel() <= 1  # no stride between tokens
+    strides = []
+    for name, x in (("k", k), *others.items()):
+        if x.shape != shape or x.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bfloat16 of k's shape {tuple(shape)}")
+        s = _token_stride(x, H, d, name, dev)
+        strides.append(H * d if one else s)
+    return H, d, dev, strides
+
+
+def _linear_decay(log_alpha, lead, H, dev):
+    """What the C calls take of log_alpha [*lead, H], or [H] for fixed decays: address, type, strides."""
+    code = _CODES.get(log_alpha.dtype)
+    if code not in (KDA_BF16, KDA_F32) or log_alpha.get_device() != dev:
+        raise ValueError(f"log_alpha must be bfloat16 or float32 on cuda:{dev}")
+    s = log_alpha.stride()
+    if log_alpha.shape == (H,):
+        return log_alpha.data_ptr(), code, 0, s[0]
+    if log_alpha.shape != tuple(lead) + (H,):
+        raise ValueError(f"log_alpha must be {tuple(lead) + (H,)} or ({H},)")
+    if len(lead) == 2:
+        if lead[0] > 1 and lead[1] > 1 and s[0] != lead[1] * s[1]:
+            raise ValueError("the tokens of log_alpha must be evenly spaced")
+        return log_alpha.data_ptr(), code, s[1] if lead[1] > 1 else s[0], s[2]
+    return log_alpha.data_ptr(), code, s[0], s[1]
+
+
+def _linear_state(state, shape, name, dev):
+    """The address of a contiguous fp32 tensor of this shape on GPU dev; None for None."""
+    if state is None:
+        return None
+    if state.get_device() != dev or state.dtype != torch.float32 or state.shape != shape or not state.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor {shape} on cuda:{dev}")
+    return state.data_ptr()
+
+
+def _linear_out(out, shape, dtype, device, dev, stream):
+    """A contiguous output of this shape: `out`, checked, or a new one."""
+    if out is None:
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"unsupported output dtype {dtype}")
+        return _empty(shape, dtype, device, stream)
+    if out.shape != shape or out.get_device() != dev or not out.is_contiguous() or out.dtype not in (
+            torch.bfloat16, torch.float32):
+        raise ValueError(f"out must be a contiguous bfloat16 or float32 tensor {tuple(shape)} on cuda:{dev}")
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _linear_workspace(back, device, N, T, H, d, packed):
+    """Bytes of kda_linear_fwd's (kda_linear_bwd's) workspace for these sizes on the current device."""
+    lib = load()
+    size = lib.kda_linear_bwd_workspace_size if back else lib.kda_linear_fwd_workspace_size
+    return size(N, T, H, d, d, packed)
+
+
+def _linear_sequences(shape, cu_seqlens):
+    """(sequences, token rows, [*lead]) of k [B, T, H, d], or [T, H, d] with cu_seqlens."""
+    if cu_seqlens is None:
+        if len(shape) != 4:
+            raise ValueError("q, k and v must be [B, T, H, d], or [T, H, d] with cu_seqlens")
+        return shape[0], shape[0] * shape[1], shape[:2]
+    if len(shape) != 3:
+        raise ValueError("with cu_seqlens q, k and v must be [T, H, d]")
+    return cu_seqlens.numel() - 1, shape[0], shape[:1]
+
+
+def kda_linear_fwd(q, k, v, log_alpha, initial_state=None, scale=1.0, out_dtype=torch.float32,
+                   output_final_state=True, cu_seqlens=None, out=None, final_state=None, stream=None):
+    """Linear attention with one decay per head, all tokens of the sequences:
+    S = exp(log_alpha) S + k v^T, o = scale S^T q.  q, k, v [B,T,H,d] bf16, or
+    packed [T,H,d] with cu_seqlens int32 [N+1]; heads packed within a token,
+    tokens evenly spaced (slices of a projection are taken as they are);
+    log_alpha [B,T,H] ([T,H]) bf16 or fp32, or [H]: a fixed decay per head;
+    initial_state [N,H,d,d] fp32 or None.  Returns (out, final_state fp32 or None)."""
+    lib = _lib or load()
+    shape = k.shape
+    N, T, lead = _linear_sequences(shape, cu_seqlens)
+    H, d, dev, (ks, qs, vs) = _linear_tokens(k, len(lead), q=q, v=v)
+    decay = _linear_decay(log_alpha, lead, H, dev)
+    states = (N, H, d, d)
+    s0 = _linear_state(initial_state, states, "initial_state", dev)
+    cu = _int32_ptr(cu_seqlens, N + 1, "cu_seqlens", dev)
+    raw_stream = _stream_of(stream, dev)
+    out = _linear_out(out, shape, out_dtype, k.device, dev, stream)
+    if final_state is None and output_final_state:
+        final_state = _empty(states, torch.float32, k.device, stream)
+    s1 = _linear_state(final_state, states, "final_state", dev)
+    need = _linear_workspace(False, dev, N, T, H, d, cu is not None)
+    ws = _empty(need, torch.uint8, k.device, stream) if need else None
+    code = lib.kda_linear_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, *decay, cu, s0, out.data_ptr(),
+                              _CODES[out.dtype], s1, N, T, H, d, d, scale, None if ws is None else ws.data_ptr(), need,
+                              raw_stream)
+    if code:
+        raise KDAError(code, "kda_linear_fwd")
+    return out, final_state
+
+
+def kda_linear_bwd(q, k, v, log_alpha, d_out, initial_state=None, d_final_state=None, scale=1.0, cu_seqlens=None,
+                   want_log_alpha_grad=True, want_initial_state_grad=True, stream=None):
+    """Gradients of <d_out, out> + <d_final_state, final_state> for what
+    kda_linear_fwd computes; d_out bf16 like q, k, v.  Returns a dict: q, k, v
+    (bf16), log_alpha (of its shape and dtype; for fixed decays [H] the sum over
+    all tokens; None when not asked for) and initial_state (fp32, None when not
+    asked for)."""
+    lib = _lib or load()
+    shape = k.shape
+    N, T, lead = _linear_sequences(shape, cu_seqlens)
+    H, d, dev, (ks, qs, vs, os_) = _linear_tokens(k, len(lead), q=q, v=v, d_out=d_out)
+    decay = _linear_decay(log_alpha, lead, H, dev)
+    states = (N, H, d, d)
+    s0 = _linear_state(initial_state, states, "initial_state", dev)
+    d1 = _linear_state(d_final_state, states, "d_final_state", dev)
+    cu = _int32_ptr(cu_seqlens, N + 1, "cu_seqlens", dev)
+    raw_stream = _stream_of(stream, dev)
+    g = {n: _empty(shape, torch.bfloat16, k.device, stream) for n in ("q", "k", "v")}
+    g["log_alpha"] = _empty(log_alpha.shape, log_alpha.dtype, k.device, stream) if want_log_alpha_grad else None
+    g["initial_state"] = _empty(states, torch.float32, k.device, stream) if want_initial_state_grad else None
+    need = _linear_workspace(True, dev, N, T, H, d, cu is not None)
+    ws = _empty(need, torch.uint8, k.device, stream) if need else None
+    code = lib.kda_linear_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), d_out.data_ptr(), qs, ks, vs, os_, *decay, cu, s0, d1,
+        *(g[n].data_ptr() for n in ("q", "k", "v")), g["log_alpha"].data_ptr() if want_log_alpha_grad else None,
+        log_alpha.dim() == 1, g["initial_state"].data_ptr() if want_initial_state_grad else None, N, T, H, d, d, scale,
+        None if ws is None else ws.data_ptr(), need, raw_stream)
+    if code:
+        raise KDAError(code, "kda_linear_bwd")
+    return g
+
+
+def kda_linear_step(q, k, v, log_alpha, state, scale=1.0, out=None, out_dtype=torch.float32, stream=None):
+    """One token per sequence of the linear attention; `state` [N,H,d,d] fp32 is
+    updated in place.  q, k, v [N,H,d] bf16; log_alpha [N,H] or [H].  Returns out [N,H,d]."""
+    lib = _lib or load()
+    H, d, dev, (ks, qs, vs) = _linear_tokens(k, 1, q=q, v=v)
+    N = k.shape[0]
+    decay = _linear_decay(log_alpha, (N,), H, dev)
+    s = _linear_state(state, (N, H, d, d), "state", dev)
+    raw_stream = _stream_of(stream, dev)
+    out = _linear_out(out, k.shape, out_dtype, k.device, dev, stream)
+    code = lib.kda_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, *decay, s, out.data_ptr(),
+                               _CODES[out.dtype], N, H, d, d, scale, raw_stream)
+    if code:
+        raise KDAError(code, "kda_linear_step")
+    return out
+
+
+def kda_linear_verify(q, k, v, log_alpha, state, scale=1.0, out_dtype=torch.float32, out=None, stream=None):
+    """Outputs of K drafted tokens per sequence of the linear attention from
+    `state` (only read).  q, k, v [N,K,H,d] bf16; log_alpha [N,K,H] or [H].
+    Returns out [N,K,H,d]."""
+    lib = _lib or load()
+    H, d, dev, (ks, qs, vs) = _linear_tokens(k, 2, q=q, v=v)
+    N, K = k.shape[:2]
+    decay = _linear_decay(log_alpha, (N, K), H, dev)
+    s = _linear_state(state, (N, H, d, d), "state", dev)
+    raw_stream = _stream_of(stream, dev)
+    out = _linear_out(out, k.shape, out_dtype, k.device, dev, stream)
+    code = lib.kda_linear_verify(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, *decay, s, out.data_ptr(),
+                                 _CODES[out.dtype], N, K, H, d, d, scale, raw_stream)
+    if code:
+        raise KDAError(code, "kda_linear_verify")
+    return out
+
+
+def kda_linear_commit(k, v, log_alpha, state, accepted, stream=None):
+    """Advance `state` in place by the first accepted[n] of each sequence's K
+    drafted tokens (accepted: int32 [N] on the device)."""
+    lib = _lib or load()
+    H, d, dev, (ks, vs) = _linear_tokens(k, 2, v=v)
+    N, K = k.shape[:2]
+    decay = _linear_decay(log_alpha, (N, K), H, dev)
+    if accepted is None:
+        raise ValueError("accepted is needed")
+    code = lib.kda_linear_commit(k.data_ptr(), v.data_ptr(), ks, vs, *decay,
+                                 _linear_state(state, (N, H, d, d), "state", dev),
+                                 _int32_ptr(accepted, N, "accepted", dev), N, K, H, d, d, _stream_of(stream, dev))
+    if code:
+        raise KDAError(code, "kda_linear_commit")
+    return state
+
+
+class _LogitsRules(ctypes.Structure):
+    """kda_logits_rules_t (include/kda.h)."""
+    _fields_ = ([(n, _vp) for n in ("tokens", "lens", "prompt_lens", "drafts", "repetition", "presence", "frequency",
+                                    "bias_ids", "bias", "mask", "temperature")] +
+                [(n, _ll) for n in ("tokens_stride", "mask_stride_n", "mask_stride_r")] + [("L", _i), ("J", _i)])
+
+
+def _typed_ptr(t, dtype, shape, name, dev):
+    """The address of a contiguous tensor of this dtype and shape on GPU dev; None for None."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on cuda:{dev}")
+    return t.data_ptr()
+
+
+def kda_logits_probs(logits, tokens=None, lens=None, prompt_lens=None, drafts=None, repetition=None, presence=None,
+                     frequency=None, bias_ids=None, bias=None, mask=None, temperature=None, out_dtype=torch.float32,
+                     out=None, stream=None):
+    """Probabilities [N,R,V] from logits [N,R,V] (fp32, bf16 or fp16), as
+    kda_draft_accept takes them: penalties, biases, masks and temperature, then
+    the softmax.  Every rule may be left out.  tokens int32 [N,L]: each
+    request's history, lens[n] tokens of it real, the first prompt_lens[n] of
+    those its prompt (it counts for `repetition`, not for `presence` and
+    `frequency`); drafts int32 [N,R-1]: said before the rows after them;
+    repetition, presence, frequency, temperature fp32 [N] (temperature 0: 1 at
+    the largest entry); bias_ids int32 [N,J] with bias fp32 [N,J]; mask int32
+    [N,R,ceil(V/32)] (or [N,1,.], [1,R,.], [1,1,.] shared), bit i of word w for
+    entry 32 w + i, 0 masks it.  out_dtype: float32 or the logits' dtype."""
+    lib = _lib or load()
+    if logits.dim() != 3 or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor [N, R, V]")
+    N, R, V = shape = logits.shape
+    code, s, dev = _CODES.get(logits.dtype), logits.stride(), logits.get_device()
+    if code is None or code == KDA_E4M3 or (s[2] != 1 and V > 1):
+        raise ValueError("logits must be float32, bfloat16 or float16 with contiguous rows")
+    if out is None:
+        if out_dtype != torch.float32 and out_dtype != logits.dtype:
+            raise ValueError("out_dtype must be float32 or the logits' dtype")
+    elif out.shape != shape or out.dtype not in (torch.float32, logits.dtype) or out.get_device() != dev or (
+            not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous tensor {tuple(shape)} on cuda:{dev}, float32 or of the logits' dtype")
+    f32, i32, each = torch.float32, torch.int32, (N,)
+    u = _LogitsRules()
+    if tokens is not None:
+        if tokens.get_device() != dev or tokens.dtype != i32 or tokens.dim() != 2 or tokens.shape[0] != N or (
+                tokens.shape[1] > 1 and tokens.stride(1) != 1):
+            raise ValueError(f"tokens must be an int32 tensor [{N}, L] on cuda:{dev} with contiguous rows")
+        u.tokens, u.tokens_stride, u.L = tokens.data_ptr(), tokens.stride(0), tokens.shape[1]
+    elif lens is not None or prompt_lens is not None:
+        raise ValueError("lens and prompt_lens without tokens")
+    u.lens, u.prompt_lens = _typed_ptr(lens, i32, each, "lens", dev), _typed_ptr(prompt_lens, i32, each, "prompt_lens", dev)
+    u.drafts = _typed_ptr(drafts, i32, (N, R - 1), "drafts", dev) if R > 1 else None
+    for name, t in (("repetition", repetition), ("presence", presence), ("frequency", frequency),
+                    ("temperature", temperature)):
+        if t is not None:
+            setattr(u, name, _typed_ptr(t, f32, each, name, dev))
+    if bias_ids is not None or bias is not None:
+        if bias_ids is None or bias is None or bias_ids.dim() != 2:
+            raise ValueError("bias_ids and bias must be given together, [N, J] each")
+        u.J = bias_ids.shape[1]
+        u.bias_ids = _typed_ptr(bias_ids, i32, (N, u.J), "bias_ids", dev)
+        u.bias = _typed_ptr(bias, f32, (N, u.J), "bias", dev)
+    if mask is not None:
+        m = mask.shape
+        if mask.get_device() != dev or mask.dtype != i32 or len(m) != 3 or m[0] not in (1, N) or m[1] not in (1, R) or (
+                m[2] != (V + 31) // 32 or (m[2] > 1 and mask.stride(2) != 1)):
+            raise ValueError(f"mask must be an int32 tensor [{N} or 1, {R} or 1, {(V + 31) // 32}] on cuda:{dev}")
+        u.mask = mask.data_ptr()
+        u.mask_stride_n = 0 if m[0] == 1 else mask.stride(0)
+        u.mask_stride_r = 0 if m[1] == 1 else mask.stride(1)
+    raw_stream = _stream_of(stream, dev)
+    if out is None:
+        out = _empty(shape, out_dtype, logits.device, stream)
+    code = lib.kda_logits_probs(logits.data_ptr(), code, s[0], s[1], ctypes.addressof(u), out.data_ptr(),
+                                _CODES[out.dtype], N, R, V, raw_stream)
+    if code:
+        raise KDAError(code, "kda_logits_probs")
+    return out
 
 
 def kda_chunk_fwd_launches(B, T, H):

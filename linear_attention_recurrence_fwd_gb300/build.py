@@ -23,7 +23,8 @@ PROBE_LIB = os.path.join(PKG, "libkda_probe.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 PRODUCT_SOURCES = ["kda_api.cu", "kda_decode.cu", "kda_chunk.cu", "kda_bwd.cu", "kda_host.cu",
-                   "kda_append.cu", "kda_attend.cu", "kda_attend_wide.cu", "kda_accept.cu"]
+                   "kda_append.cu", "kda_attend.cu", "kda_attend_wide.cu", "kda_accept.cu",
+                   "kda_linear.cu", "kda_linear_bwd.cu", "kda_linear_step.cu", "kda_logits.cu"]
 PROBE_SOURCES = ["kda_probe.cu"]
 
 

@@ -490,6 +490,169 @@ kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft_probs,
   return from_cuda(e == cudaSuccess ? kda::launch_draft_accept(p, stream) : e);
 }
 
+namespace {
+
+// What the linear attention's calls share: the tensors' rows and the decays.
+kda_status_t validate_linear(const void* q, const void* k, const void* v, long long q_stride,
+                             long long k_stride, long long v_stride, const void* log_alpha,
+                             kda_dtype_t la_dtype, long long la_token_stride, long long la_head_stride,
+                             const int* cu_seqlens, const void* state, int N, long long T, int H, int d_k,
+                             int d_v) {
+  if (N < 0 || T < 0 || H <= 0 || d_k <= 0 || d_v <= 0) return KDA_ERR_INVALID_ARG;
+  if (q_stride < 0 || k_stride < 0 || v_stride < 0 || la_token_stride < 0 || la_head_stride < 0)
+    return KDA_ERR_INVALID_ARG;
+  if (T > 0 && (!q || !k || !v || !log_alpha)) return KDA_ERR_INVALID_ARG;
+  if (d_k != d_v || !(d_k == 64 || d_k == 128)) return KDA_ERR_UNSUPPORTED;
+  if (la_dtype != KDA_BF16 && la_dtype != KDA_F32) return KDA_ERR_UNSUPPORTED;
+  // rows, and (sequences x heads) x 2 column blocks, are counted in 32 bits; so are the coordinates of a copy
+  if (T > (1 << 30) || H > (1 << 16) || (long long)N * H > (1 << 29) || T * H > (1LL << 36))
+    return KDA_ERR_UNSUPPORTED;
+  if (!aligned_rows(q, q_stride, KDA_BF16) || !aligned_rows(k, k_stride, KDA_BF16) ||
+      !aligned_rows(v, v_stride, KDA_BF16) || !aligned16(state) || (reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) ||
+      (reinterpret_cast<uintptr_t>(log_alpha) & (element_bytes(la_dtype) - 1)))
+    return KDA_ERR_ALIGNMENT;
+  return KDA_OK;
+}
+
+kda_status_t run_linear_tokens(const void* q, const void* k, const void* v, long long q_stride,
+                               long long k_stride, long long v_stride, const void* log_alpha,
+                               kda_dtype_t la_dtype, long long la_token_stride, long long la_head_stride,
+                               const float* state_in, float* state_out, const int* counts, void* out,
+                               kda_dtype_t out_dtype, int N, int K, int H, int d_k, int d_v, float scale,
+                               cudaStream_t stream) {
+  if (K < 0) return KDA_ERR_INVALID_ARG;
+  const kda_status_t st = validate_linear(q, k, v, q_stride, k_stride, v_stride, log_alpha, la_dtype, la_token_stride,
+                                          la_head_stride, nullptr, state_in, N, (long long)N * K, H, d_k, d_v);
+  if (st != KDA_OK) return st;
+  if (out_dtype != KDA_BF16 && out_dtype != KDA_F32) return KDA_ERR_UNSUPPORTED;
+  if ((long long)N * K == 0) return KDA_OK;
+  if (!state_in) return KDA_ERR_INVALID_ARG;
+  if (!aligned16(out)) return KDA_ERR_ALIGNMENT;
+  const kda::LinearProblem p{q, k, v, q_stride, k_stride, v_stride, log_alpha, la_dtype == KDA_F32, la_token_stride,
+                             la_head_stride, nullptr, state_in, out, out_dtype == KDA_F32, state_out, N, N * K, K, H,
+                             d_k, scale, counts, nullptr};
+  return from_cuda(kda::launch_linear_tokens(p, stream));
+}
+
+}  // namespace
+
+size_t kda_linear_fwd_workspace_size(int N, int T, int H, int d_k, int d_v, int packed) {
+  if (N <= 0 || T <= 0 || H <= 0 || d_k != d_v || !(d_k == 64 || d_k == 128) || (long long)N * H > (1 << 29)) return 0;
+  return kda::linear_fwd_workspace_bytes(N, T, H, d_k, packed != 0);
+}
+
+kda_status_t kda_linear_fwd(const void* q, const void* k, const void* v, long long q_stride,
+                            long long k_stride, long long v_stride, const void* log_alpha,
+                            kda_dtype_t la_dtype, long long la_token_stride, long long la_head_stride,
+                            const int* cu_seqlens, const float* initial_state, void* out,
+                            kda_dtype_t out_dtype, float* final_state, int N, int T, int H, int d_k,
+                            int d_v, float scale, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream) {
+  const kda_status_t st = validate_linear(q, k, v, q_stride, k_stride, v_stride, log_alpha, la_dtype, la_token_stride,
+                                          la_head_stride, cu_seqlens, initial_state, N, T, H, d_k, d_v);
+  if (st != KDA_OK) return st;
+  if (out_dtype != KDA_BF16 && out_dtype != KDA_F32) return KDA_ERR_UNSUPPORTED;
+  if ((T > 0 && !out) || (N == 0 ? T > 0 : !cu_seqlens && T % N)) return KDA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(final_state)) return KDA_ERR_ALIGNMENT;
+  if (N == 0) return KDA_OK;
+  const size_t need = kda_linear_fwd_workspace_size(N, T, H, d_k, d_v, cu_seqlens != nullptr);
+  if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return KDA_ERR_ALIGNMENT;
+  kda::LinearProblem p{q, k, v, q_stride, k_stride, v_stride, log_alpha, la_dtype == KDA_F32, la_token_stride,
+                       la_head_stride, cu_seqlens, initial_state, out, out_dtype == KDA_F32, final_state, N, T,
+                       cu_seqlens ? T : T / N, H, d_k, scale, nullptr, nullptr};
+  cudaError_t e = kda::chunk_status_address(&p.status);
+  return from_cuda(e == cudaSuccess ? kda::launch_linear_fwd(p, workspace, stream) : e);
+}
+
+size_t kda_linear_bwd_workspace_size(int N, int T, int H, int d_k, int d_v, int packed) {
+  if (N <= 0 || T <= 0 || H <= 0 || d_k != d_v || !(d_k == 64 || d_k == 128) || (long long)N * H > (1 << 29)) return 0;
+  return kda::linear_bwd_workspace_bytes(N, T, H, d_k, packed != 0);
+}
+
+kda_status_t kda_linear_bwd(const void* q, const void* k, const void* v, const void* d_out, long long q_stride,
+                            long long k_stride, long long v_stride, long long d_out_stride, const void* log_alpha,
+                            kda_dtype_t la_dtype, long long la_token_stride, long long la_head_stride,
+                            const int* cu_seqlens, const float* initial_state, const float* d_final_state, void* dq,
+                            void* dk, void* dv, void* dlog_alpha, int sum_log_alpha, float* d_initial_state, int N, int T,
+                            int H, int d_k, int d_v, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const kda_status_t st = validate_linear(q, k, v, q_stride, k_stride, v_stride, log_alpha, la_dtype, la_token_stride,
+                                          la_head_stride, cu_seqlens, initial_state, N, T, H, d_k, d_v);
+  if (st != KDA_OK) return st;
+  if (d_out_stride < 0 || (T > 0 && (!d_out || !dq || !dk || !dv)) || (N == 0 ? T > 0 : !cu_seqlens && T % N))
+    return KDA_ERR_INVALID_ARG;
+  if (!aligned_rows(d_out, d_out_stride, KDA_BF16) || !aligned16(d_final_state) || !aligned16(dq) || !aligned16(dk) ||
+      !aligned16(dv) || !aligned16(d_initial_state) ||
+      (reinterpret_cast<uintptr_t>(dlog_alpha) & (element_bytes(la_dtype) - 1)))
+    return KDA_ERR_ALIGNMENT;
+  if (N == 0) return KDA_OK;
+  const size_t need = kda_linear_bwd_workspace_size(N, T, H, d_k, d_v, cu_seqlens != nullptr);
+  if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  if (need && !aligned16(workspace)) return KDA_ERR_ALIGNMENT;
+  kda::LinearProblem p{q, k, v, q_stride, k_stride, v_stride, log_alpha, la_dtype == KDA_F32, la_token_stride,
+                       la_head_stride, cu_seqlens, initial_state, nullptr, false, nullptr, N, T,
+                       cu_seqlens ? T : T / N, H, d_k, scale, nullptr, nullptr};
+  const kda::LinearGrads g{d_out, d_out_stride, d_final_state, dq, dk, dv, dlog_alpha, sum_log_alpha != 0, d_initial_state};
+  cudaError_t e = kda::chunk_status_address(&p.status);
+  return from_cuda(e == cudaSuccess ? kda::launch_linear_bwd(p, g, workspace, stream) : e);
+}
+
+kda_status_t kda_linear_step(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                             long long v_stride, const void* log_alpha, kda_dtype_t la_dtype,
+                             long long la_token_stride, long long la_head_stride, float* state, void* out,
+                             kda_dtype_t out_dtype, int N, int H, int d_k, int d_v, float scale,
+                             cudaStream_t stream) {
+  if (N > 0 && !out) return KDA_ERR_INVALID_ARG;
+  return run_linear_tokens(q, k, v, q_stride, k_stride, v_stride, log_alpha, la_dtype, la_token_stride, la_head_stride,
+                           state, state, nullptr, out, out_dtype, N, 1, H, d_k, d_v, scale, stream);
+}
+
+kda_status_t kda_linear_verify(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                               long long v_stride, const void* log_alpha, kda_dtype_t la_dtype,
+                               long long la_token_stride, long long la_head_stride, const float* state, void* out,
+                               kda_dtype_t out_dtype, int N, int K, int H, int d_k, int d_v, float scale,
+                               cudaStream_t stream) {
+  if (N > 0 && K > 0 && !out) return KDA_ERR_INVALID_ARG;
+  return run_linear_tokens(q, k, v, q_stride, k_stride, v_stride, log_alpha, la_dtype, la_token_stride, la_head_stride,
+                           state, nullptr, nullptr, out, out_dtype, N, K, H, d_k, d_v, scale, stream);
+}
+
+kda_status_t kda_linear_commit(const void* k, const void* v, long long k_stride, long long v_stride,
+                               const void* log_alpha, kda_dtype_t la_dtype, long long la_token_stride,
+                               long long la_head_stride, float* state, const int* accepted, int N, int K, int H,
+                               int d_k, int d_v, cudaStream_t stream) {
+  if (N > 0 && !accepted) return KDA_ERR_INVALID_ARG;
+  return run_linear_tokens(k, k, v, k_stride, k_stride, v_stride, log_alpha, la_dtype, la_token_stride, la_head_stride,
+                           state, state, accepted, nullptr, KDA_F32, N, K, H, d_k, d_v, 1.f, stream);
+}
+
+kda_status_t kda_logits_probs(const void* logits, kda_dtype_t dtype, long long stride_n, long long stride_r,
+                              const kda_logits_rules_t* rules, void* out, kda_dtype_t out_dtype, int N, int R, int V,
+                              cudaStream_t stream) {
+  if (N < 0 || R < 0 || V <= 0 || stride_n < 0 || stride_r < 0) return KDA_ERR_INVALID_ARG;
+  const bool any = (long long)N * R > 0;
+  if (any && (!logits || !out)) return KDA_ERR_INVALID_ARG;
+  if (dtype != KDA_F32 && dtype != KDA_BF16 && dtype != KDA_F16) return KDA_ERR_UNSUPPORTED;
+  if (out_dtype != KDA_F32 && out_dtype != dtype) return KDA_ERR_UNSUPPORTED;
+  if (V > (1 << 30) || (long long)N * R > (1 << 27)) return KDA_ERR_UNSUPPORTED;
+  kda_logits_rules_t u = {};
+  if (rules) u = *rules;
+  if (u.L < 0 || u.J < 0 || u.tokens_stride < 0 || u.mask_stride_n < 0 || u.mask_stride_r < 0)
+    return KDA_ERR_INVALID_ARG;
+  if (!u.bias_ids != !u.bias && u.J > 0) return KDA_ERR_INVALID_ARG;
+  if (u.J == 0) u.bias_ids = nullptr;
+  if ((u.repetition || u.presence || u.frequency) && V > kda::logits_most_counted()) return KDA_ERR_UNSUPPORTED;
+  for (const void* x : {(const void*)u.tokens, (const void*)u.lens, (const void*)u.prompt_lens, (const void*)u.drafts,
+                        (const void*)u.repetition, (const void*)u.presence, (const void*)u.frequency,
+                        (const void*)u.bias_ids, (const void*)u.bias, (const void*)u.mask, (const void*)u.temperature})
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return KDA_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(logits) & (element_bytes(dtype) - 1)) ||
+      (reinterpret_cast<uintptr_t>(out) & (element_bytes(out_dtype) - 1)))
+    return KDA_ERR_ALIGNMENT;
+  if (!any) return KDA_OK;
+  return from_cuda(kda::launch_logits_probs({logits, dtype, stride_n, stride_r, u, out, out_dtype, N, R, V}, stream));
+}
+
 kda_status_t kda_last_device_status(cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   const int s = kda::read_and_clear_chunk_status(stream, &e);

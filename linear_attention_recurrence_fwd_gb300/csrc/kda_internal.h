@@ -155,4 +155,51 @@ struct AcceptProblem {
 };
 cudaError_t launch_draft_accept(const AcceptProblem& p, cudaStream_t stream);
 
+// Linear attention with one decay per head (see include/kda.h for the arguments).
+struct LinearProblem {
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  const void* log_alpha;
+  bool la_f32;
+  long long la_token_stride, la_head_stride;
+  const int* cu_seqlens;
+  const float* s_in;  // states before, or null (zeros)
+  void* out;          // or null
+  bool out_f32;
+  float* s_out;       // states after, or null
+  int n_seq, T, len, H, d;  // T rows in total; len of them in a sequence (without cu_seqlens)
+  float scale;
+  const int* counts;  // of each sequence's tokens, those that are applied; null: all (linear_tokens only)
+  int* status;
+};
+// Token after token, the state in registers: decode steps, drafts, short prompts.
+cudaError_t launch_linear_tokens(const LinearProblem& p, cudaStream_t stream);
+size_t linear_fwd_workspace_bytes(int n_seq, int T, int H, int d, bool packed);
+cudaError_t launch_linear_fwd(const LinearProblem& p, void* workspace, cudaStream_t stream);
+
+// Gradients; p's out and s_out are ignored.
+struct LinearGrads {
+  const void* d_out;
+  long long d_out_stride;
+  const float* d_final;
+  void *dq, *dk, *dv, *dla;
+  bool sum_la;  // dla is [H]
+  float* ds0;
+};
+size_t linear_bwd_workspace_bytes(int n_seq, int T, int H, int d, bool packed);
+cudaError_t launch_linear_bwd(const LinearProblem& p, const LinearGrads& g, void* workspace,
+                              cudaStream_t stream);
+
+struct LogitsProblem {
+  const void* logits;
+  kda_dtype_t dtype;
+  long long stride_n, stride_r;
+  kda_logits_rules_t rules;
+  void* out;
+  kda_dtype_t out_dtype;
+  int N, R, V;
+};
+int logits_most_counted();  // the largest vocabulary of a call with a penalty
+cudaError_t launch_logits_probs(const LogitsProblem& p, cudaStream_t stream);
+
 }  // namespace kda

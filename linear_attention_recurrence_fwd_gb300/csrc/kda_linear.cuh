@@ -1,0 +1,31 @@
+// What the linear attention's kernels share: a sequence's rows and a token's decay.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+// The rows of packed sequence n: their number, and the first one.  Offsets are clamped to [0, T] and
+// to an order, so that no row outside the tensors is touched whatever cu_seqlens holds.
+__device__ __forceinline__ int sequence_rows(const LinearProblem& p, int n, long long* row0) {
+  const int a = min(max(p.cu_seqlens[n], 0), p.T), b = min(max(p.cu_seqlens[n + 1], a), p.T);
+  *row0 = a;
+  return b - a;
+}
+
+// Whether the offsets of sequence n are ones that the interface allows.
+__device__ __forceinline__ bool offsets_good(const LinearProblem& p, int n) {
+  const int a = p.cu_seqlens[n], b = p.cu_seqlens[n + 1];
+  return a >= 0 && b >= a && b <= p.T && (n > 0 || a == 0) && (n < p.n_seq - 1 || b == p.T);
+}
+
+__device__ __forceinline__ float load_decay(const LinearProblem& p, long long row, int h) {
+  const long long at = row * p.la_token_stride + h * p.la_head_stride;
+  return p.la_f32 ? static_cast<const float*>(p.log_alpha)[at]
+                  : __bfloat162float(static_cast<const __nv_bfloat16*>(p.log_alpha)[at]);
+}
+
+}  // namespace kda

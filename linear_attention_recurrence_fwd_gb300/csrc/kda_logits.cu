@@ -1,0 +1,364 @@
+// Probabilities from logits.  For each row, x = logit and then, in order,
+//
+//     said before:   x = x > 0 ? x / repetition : x * repetition
+//     said in reply: x = x - frequency * count - presence
+//     x = x + bias,   masked entries leave,   p = softmax(x / temperature)
+//
+// One pass: a row's entries are read once, wait in registers for the row's
+// maximum and sum, and are written once as probabilities, so HBM bounds it
+// (2 x 4 bytes an entry in fp32).  A cluster of up to 8 CTAs takes the rows of
+// a request; CTA c holds entries [c slice, (c + 1) slice) of each.  Each CTA
+// takes its exponentials against its own maximum and leaves (maximum, sum) in
+// every other CTA's shared memory: one cluster barrier a row.
+//
+// What has been said is counted once for a request, in shared memory, one
+// 32-bit word an entry of the slice: 2 * (how often in the reply) + (whether
+// in the prompt).  The counts are whole numbers, so the order of the adding
+// does not matter; a request's biases are kept in their order.  A row's
+// drafts are added as the rows go by.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "kda_internal.h"
+#include "kda_types.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int MOST = 8;      // CTAs to a cluster
+constexpr int PER = 32;      // entries a thread holds
+constexpr int LIST = 1024;   // biases held at a time
+constexpr float LOG2E = 1.4426950408889634f;
+
+struct Part { float top, sum; int at; };  // of a slice: the largest entry, the sum against it, its lowest index
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Vectors of 16 bytes of the logits' type.
+template <typename T> struct Vec { static constexpr int E = 16 / sizeof(T); };
+
+template <typename T> __device__ __forceinline__ void unpack(const uint4& w, float* x) {
+  if constexpr (sizeof(T) == 4) {
+    x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
+  } else {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      T lo, hi;
+      const uint16_t a = (uint16_t)u[i], b = (uint16_t)(u[i] >> 16);
+      memcpy(&lo, &a, 2);
+      memcpy(&hi, &b, 2);
+      x[2 * i] = to_f32(lo);
+      x[2 * i + 1] = to_f32(hi);
+    }
+  }
+}
+
+// E values to consecutive entries of the output, 16 bytes at a time.
+template <typename O, int E> __device__ __forceinline__ void store_vec(O* to, const float* x) {
+  if constexpr (sizeof(O) == 4) {
+#pragma unroll
+    for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+  } else {
+    uint32_t u[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      const O lo = from_f32<O>(x[2 * i]), hi = from_f32<O>(x[2 * i + 1]);
+      uint16_t a, b;
+      memcpy(&a, &lo, 2);
+      memcpy(&b, &hi, 2);
+      u[i] = a | (uint32_t)b << 16;
+    }
+    *reinterpret_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+template <typename T, typename O, int THREADS, bool VEC>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsProblem p, int cluster, int slice, int rows) {
+  namespace cg = cooperative_groups;
+  constexpr int E = VEC ? Vec<T>::E : 1, TILE = THREADS * PER, WARPS = THREADS / 32;
+  extern __shared__ __align__(16) uint32_t s_said[];  // [slice], only where something is counted
+  __shared__ Part s_warp[WARPS], s_parts[2][MOST];
+  __shared__ int s_id[LIST];
+  __shared__ float s_bias[LIST];
+  __shared__ int s_listed, s_more;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % cluster, item = blockIdx.x / cluster;
+  const int groups = (p.R + rows - 1) / rows;
+  const int n = item / groups, r0 = item % groups * rows, r1 = min(r0 + rows, p.R);
+  const int lo = min(rank * slice, p.V), hi = min(lo + slice, p.V);
+  const kda_logits_rules_t& u = p.rules;
+
+  // ---- what this request has said, and its biases
+  const bool counted = u.repetition || u.presence || u.frequency;
+  if (counted) {
+    for (int i = tid; i < hi - lo; i += THREADS) s_said[i] = 0;
+    __syncthreads();
+    const int L = u.tokens ? (u.lens ? min(max(u.lens[n], 0), u.L) : u.L) : 0;
+    const int prompt = u.prompt_lens ? u.prompt_lens[n] : 0;
+    const int* said = u.tokens + n * u.tokens_stride;
+    for (int i = tid; i < L; i += THREADS) {
+      const int t = said[i];
+      if (t < lo || t >= hi) continue;
+      if (i < prompt) atomicOr(&s_said[t - lo], 1u);
+      else atomicAdd(&s_said[t - lo], 2u);
+    }
+    for (int i = tid; u.drafts && i < r0; i += THREADS) {
+      const int t = u.drafts[(size_t)n * (p.R - 1) + i];
+      if (t >= lo && t < hi) atomicAdd(&s_said[t - lo], 2u);
+    }
+  }
+  const float repetition = u.repetition ? u.repetition[n] : 1.f, presence = u.presence ? u.presence[n] : 0.f;
+  const float frequency = u.frequency ? u.frequency[n] : 0.f, temperature = u.temperature ? u.temperature[n] : 1.f;
+  const bool greedy = !(temperature > 0.f);
+  const float factor = greedy ? 0.f : LOG2E / temperature;
+  // the biases of this slice in their order, as many as the list holds; the rest is looked up in memory
+  if (warp == 0) {
+    int have = 0, j0 = 0;
+    for (; u.bias_ids && j0 < u.J && have <= LIST - 32; j0 += 32) {
+      const int t = j0 + lane < u.J ? u.bias_ids[(size_t)n * u.J + j0 + lane] : -1;
+      const bool in = t >= lo && t < hi;
+      const unsigned who = __ballot_sync(~0u, in);
+      if (in) {
+        const int at = have + __popc(who & ((1u << lane) - 1));
+        s_id[at] = t;
+        s_bias[at] = u.bias[(size_t)n * u.J + j0 + lane];
+      }
+      have += __popc(who);
+    }
+    if (lane == 0) {
+      s_listed = have;
+      s_more = u.bias_ids ? min(j0, u.J) : 0;
+    }
+  }
+  __syncthreads();
+
+  // adds b to the entry t where this thread holds it in x (tile at `from`)
+  auto add_bias = [&](float (&x)[PER], int from, int t, float b) {
+    const int at = t - from;
+    if (at < 0 || at >= TILE || at / E % THREADS != tid) return;
+    const int mine = at / (E * THREADS) * E + at % E;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i == mine) x[i] += b;
+  };
+  // the entries of the tile that starts at `from`, with everything but the temperature; those that are
+  // masked or past the end are -infinity
+  auto load = [&](float (&x)[PER], int r, int from) {
+    const T* row = static_cast<const T*>(p.logits) + n * p.stride_n + r * p.stride_r;
+#pragma unroll
+    for (int i = 0; i < PER; i += E) {
+      const int at = from + (i / E * THREADS + tid) * E;
+      if (at < hi) {
+        if constexpr (VEC) unpack<T>(*reinterpret_cast<const uint4*>(row + at), x + i);
+        else x[i] = to_f32(row[at]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i + e] = -INFINITY;
+      }
+    }
+    if (counted) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int at = from + (i / E * THREADS + tid) * E + i % E;
+        const uint32_t c = at < hi ? s_said[at - lo] : 0;
+        if (c) {
+          x[i] = x[i] > 0.f ? x[i] / repetition : x[i] * repetition;
+          if (c > 1) x[i] -= frequency * (float)(c >> 1) + presence;
+        }
+      }
+    }
+    if (u.bias_ids) {
+      for (int j = 0; j < s_listed; ++j) add_bias(x, from, s_id[j], s_bias[j]);
+      for (int j = s_more; j < u.J; ++j) add_bias(x, from, u.bias_ids[(size_t)n * u.J + j], u.bias[(size_t)n * u.J + j]);
+    }
+    if (u.mask) {
+      const int* bits = u.mask + n * u.mask_stride_n + r * u.mask_stride_r;
+#pragma unroll
+      for (int i = 0; i < PER; i += E) {
+        const int at = from + (i / E * THREADS + tid) * E;
+        const uint32_t word = at < hi ? (uint32_t)bits[at >> 5] >> (at & 31) : 0;  // E entries never straddle a word
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (!(word >> e & 1)) x[i + e] = -INFINITY;
+      }
+    }
+  };
+  // 2^((x - top) factor), 1 at the top whatever the factor is
+  auto weight = [&](float x, float top) {
+    const float d = x - top;
+    return x == -INFINITY || d == 0.f ? (x == -INFINITY ? 0.f : 1.f) : exp2_fast(d * factor);
+  };
+
+  cg::cluster_group all = cg::this_cluster();
+  all.sync();  // no CTA stores to one that has not started
+  for (int r = r0; r < r1; ++r) {
+    float x[PER];
+    Part mine{-INFINITY, 0.f, 0x7fffffff};
+    for (int from = lo; from < hi || from == lo; from += TILE) {
+      load(x, r, from);
+      // ---- the tile's largest entry, over the CTA
+      float top = -INFINITY;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        top = fmaxf(top, x[i]);
+        nan |= x[i] != x[i];
+      }
+      int at = 0x7fffffff;
+      if (greedy) {
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+          if (x[i] == top && top > -INFINITY) at = min(at, from + (i / E * THREADS + tid) * E + i % E);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const float t = __shfl_xor_sync(~0u, top, o);
+        const int a = __shfl_xor_sync(~0u, at, o);
+        at = t > top ? a : t == top ? min(a, at) : at;
+        top = fmaxf(top, t);
+      }
+      if (lane == 0) s_warp[warp] = {top, 0.f, at};
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const Part q = s_warp[w];
+        at = q.top > top ? q.at : q.top == top ? min(q.at, at) : at;
+        top = fmaxf(top, q.top);
+      }
+      // ---- the sum against it
+      float sum = nan ? NAN : 0.f;
+      if (!greedy) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          x[i] = weight(x[i], top);
+          sum += x[i];
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+      __syncthreads();
+      if (lane == 0) s_warp[warp].sum = sum;
+      __syncthreads();
+      sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += s_warp[w].sum;
+      // ---- joined with the tiles before
+      const float both = fmaxf(mine.top, top);
+      mine.sum = mine.sum * weight(mine.top, both) + sum * weight(top, both);
+      mine.at = top > mine.top ? at : mine.at;
+      mine.top = both;
+      __syncthreads();  // s_warp is written again
+    }
+    // ---- and with the other CTAs' slices
+    const int turn = r & 1;
+    if (tid < cluster) *all.map_shared_rank(&s_parts[turn][rank], tid) = mine;
+    all.sync();
+    Part whole = s_parts[turn][0];
+    for (int c = 1; c < cluster; ++c) {
+      const Part q = s_parts[turn][c];
+      const float both = fmaxf(whole.top, q.top);
+      whole.sum = whole.sum * weight(whole.top, both) + q.sum * weight(q.top, both);
+      whole.at = q.top > whole.top ? q.at : whole.at;
+      whole.top = both;
+    }
+    O* to = static_cast<O*>(p.out) + ((size_t)n * p.R + r) * p.V;
+    const float mul = greedy ? whole.sum : whole.sum > 0.f ? weight(mine.top, whole.top) / whole.sum : whole.sum;
+    for (int from = lo; from < hi; from += TILE) {
+      if (slice > TILE) {
+        load(x, r, from);
+        if (!greedy) {
+#pragma unroll
+          for (int i = 0; i < PER; ++i) x[i] = weight(x[i], mine.top);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PER; i += E) {
+        const int at = from + (i / E * THREADS + tid) * E;
+        if (at >= hi) continue;
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = greedy ? (at + e == whole.at ? 1.f + mul : mul) : x[i + e] * mul;
+        if constexpr (VEC) store_vec<O, E>(to + at, y);
+        else to[at] = from_f32<O>(y[0]);
+      }
+    }
+    if (counted && u.drafts && r + 1 < r1) {  // this row's draft has been said before the next row
+      __syncthreads();
+      const int t = u.drafts[(size_t)n * (p.R - 1) + r];
+      if (tid == 0 && t >= lo && t < hi) s_said[t - lo] += 2;
+      __syncthreads();
+    }
+  }
+}
+
+template <typename T, typename O, int THREADS, bool VEC>
+cudaError_t launch_kernel(const LogitsProblem& p, int cluster, int slice, int rows, cudaStream_t stream) {
+  const bool counted = p.rules.repetition || p.rules.presence || p.rules.frequency;
+  const size_t smem = counted ? (size_t)slice * 4 : 0;
+  auto kernel = logits_kernel<T, O, THREADS, VEC>;
+  if (smem > 32 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)p.N * ((p.R + rows - 1) / rows) * cluster));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)cluster, 1u, 1u};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, slice, rows);
+}
+
+template <typename T, typename O> cudaError_t launch_typed(const LogitsProblem& p, cudaStream_t stream) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  constexpr int E = Vec<T>::E;
+  auto in16 = [](const void* x, long long stride) {
+    return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (stride * (long long)sizeof(T)) % 16 == 0;
+  };
+  const bool vec = in16(p.logits, p.stride_n) && in16(nullptr, p.stride_r) && p.V % E == 0 &&
+                   (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  // the fewest CTAs that hold a row in registers, more while some SMs have none
+  int cluster = 1;
+  while (cluster < MOST && (p.V > cluster * 512 * PER ||
+                            ((long long)p.N * p.R * cluster < sms && p.V >= cluster * 4096)))
+    cluster *= 2;
+  const int slice = ((p.V + cluster - 1) / cluster + 31) / 32 * 32;
+  // a request's rows one after the other, its history counted once, unless that leaves SMs without work
+  const int rows = (long long)p.N * p.R * cluster <= 2 * sms ? 1 : p.R;
+  if (slice <= 512 * PER) {
+    if (vec) return launch_kernel<T, O, 512, true>(p, cluster, slice, rows, stream);
+    return launch_kernel<T, O, 512, false>(p, cluster, slice, rows, stream);
+  }
+  if (vec) return launch_kernel<T, O, 1024, true>(p, cluster, slice, rows, stream);
+  return launch_kernel<T, O, 1024, false>(p, cluster, slice, rows, stream);
+}
+
+}  // namespace
+
+// The counts of a row fit the shared memory of a cluster up to here.
+int logits_most_counted() { return MOST * 53248; }
+
+cudaError_t launch_logits_probs(const LogitsProblem& p, cudaStream_t stream) {
+  if (p.N == 0 || p.R == 0) return cudaSuccess;
+  const bool wide = p.out_dtype == KDA_F32;
+  switch (p.dtype) {
+    case KDA_F32: return launch_typed<float, float>(p, stream);
+    case KDA_BF16:
+      return wide ? launch_typed<__nv_bfloat16, float>(p, stream) : launch_typed<__nv_bfloat16, __nv_bfloat16>(p, stream);
+    default: return wide ? launch_typed<__half, float>(p, stream) : launch_typed<__half, __half>(p, stream);
+  }
+}
+
+}  // namespace kda
