@@ -1,21 +1,58 @@
-// Prompts of the linear attention (simple form): token after token.
-#include "kda_linear.cuh"
+// Prompts of the linear attention: the walk in kda_linear_walk.cuh.
+#include <algorithm>
+
+#include "kda_linear_walk.cuh"
 
 namespace kda {
 namespace {
+
+using namespace linear;
 
 __global__ void check_offsets_kernel(LinearProblem p) {
   for (int n = blockIdx.x * blockDim.x + threadIdx.x; n < p.n_seq; n += gridDim.x * blockDim.x)
     if (!offsets_good(p, n)) atomicExch(p.status, (int)KDA_ERR_INVALID_ARG);
 }
 
+struct Plan {
+  int seg_len, slots;
+  bool cut;
+  size_t decay_at, bytes;
+};
+
+Plan plan_for(int n_seq, int T, int H, int d, bool packed) {
+  Plan a{};
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) sms = 152;
+  a.seg_len = segment_tokens(n_seq, T, H, packed, sms);
+  a.slots = segment_slots(n_seq, T, a.seg_len, packed);
+  a.cut = a.slots > n_seq;
+  if (a.cut) {
+    a.decay_at = (size_t)a.slots * H * d * d * 4;
+    a.bytes = a.decay_at + ((size_t)a.slots * H * 4 + 255) / 256 * 256;
+  }
+  return a;
+}
+
+template <int D> cudaError_t run(const LinearProblem& p, void* workspace, cudaStream_t stream) {
+  const Plan a = plan_for(p.n_seq, p.T, p.H, D, p.cu_seqlens != nullptr);
+  Walk w{p, a.seg_len, std::max((p.len + a.seg_len - 1) / a.seg_len, 1), a.slots, static_cast<float*>(workspace), nullptr, nullptr};
+  if (a.cut) {
+    w.decay = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.decay_at);
+    cudaError_t e = launch_walk<D, ENDS, false, false>(w, p.k, p.k_stride, p.v, p.v_stride, stream);
+    if (e == cudaSuccess) e = launch_scan<false>(w, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return p.out_f32 ? launch_walk<D, OUTPUTS, false, true>(w, p.k, p.k_stride, p.v, p.v_stride, stream)
+                   : launch_walk<D, OUTPUTS, false, false>(w, p.k, p.k_stride, p.v, p.v_stride, stream);
+}
+
 }  // namespace
 
-size_t linear_fwd_workspace_bytes(int, int, int, int, bool) { return 0; }
+size_t linear_fwd_workspace_bytes(int n_seq, int T, int H, int d, bool packed) { return plan_for(n_seq, T, H, d, packed).bytes; }
 
-cudaError_t launch_linear_fwd(const LinearProblem& p, void*, cudaStream_t stream) {
+cudaError_t launch_linear_fwd(const LinearProblem& p, void* workspace, cudaStream_t stream) {
   if (p.cu_seqlens) check_offsets_kernel<<<1, 256, 0, stream>>>(p);
-  return launch_linear_tokens(p, stream);
+  return p.d == 128 ? run<128>(p, workspace, stream) : run<64>(p, workspace, stream);
 }
 
 }  // namespace kda
