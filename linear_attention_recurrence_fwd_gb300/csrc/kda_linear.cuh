@@ -1,6 +1,8 @@
 // What the linear attention's kernels share: a sequence's rows and a token's decay.
 #pragma once
 
+#include <cstdint>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,6 +24,14 @@ __device__ __forceinline__ bool offsets_good(const LinearProblem& p, int n) {
   return a >= 0 && b >= a && b <= p.T && (n > 0 || a == 0) && (n < p.n_seq - 1 || b == p.T);
 }
 
+// A token's decay as it is stored, so that a load can be on its way for long, and what it stands for.
+__device__ __forceinline__ uint32_t load_decay_bits(const LinearProblem& p, long long row, int h) {
+  const long long at = row * p.la_token_stride + h * p.la_head_stride;
+  return p.la_f32 ? static_cast<const uint32_t*>(p.log_alpha)[at] : static_cast<const uint16_t*>(p.log_alpha)[at];
+}
+__device__ __forceinline__ float decay_of_bits(const LinearProblem& p, uint32_t bits) {
+  return __uint_as_float(p.la_f32 ? bits : bits << 16);
+}
 __device__ __forceinline__ float load_decay(const LinearProblem& p, long long row, int h) {
   const long long at = row * p.la_token_stride + h * p.la_head_stride;
   return p.la_f32 ? static_cast<const float*>(p.log_alpha)[at]

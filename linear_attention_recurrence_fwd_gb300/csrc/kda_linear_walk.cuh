@@ -6,13 +6,17 @@
 //     O  = scale (2^{g_i} Q S + P V),   P_ij = (q_i . k_j) 2^{g_i - g_j} for j <= i
 //     S <- 2^G S + K^T V',              v'_j = 2^{G - g_j} v_j
 //
-// Four products of 128 x 128 x d, with tokens (or the state's rows) on the 128
+// Products of 128 x 128 x d, with tokens (or the state's rows) on the 128
 // lanes: Q, K and V as TMA lays them (keys as rows and, read transposed, as
-// columns), P from tensor memory, where it takes the place of the scores, the
-// state in tensor memory in fp32 and, as an operand, in shared memory.
-// Differences of g are never positive, so no exponential overflows whatever
-// the decays are.  V' is two bf16 numbers (16 bits), since the state that the
-// caller gets is fp32; so are, for fp32 outputs, P and the operand S.
+// columns), P from tensor memory, where it takes the place of the scores.  The
+// state stays in registers in fp32: K^T V' comes to it from tensor memory, and
+// a bf16 copy goes to shared memory as an operand, so nothing but four warps'
+// arithmetic joins one chunk to the next.  Differences of g are never
+// positive, so no exponential overflows whatever the decays are.
+//
+// V' is two bf16 numbers (16 bits) where the state is a result (what the
+// caller gets, segments' ends, all of a call with fp32 outputs) and one where
+// only bf16 outputs see it; for fp32 outputs so are P and the operand S.
 //
 // A sequence is cut into segments of seg_len tokens where there are fewer
 // (sequence, head) pairs than SMs.  ENDS finds each segment's contribution to
@@ -26,12 +30,14 @@
 // IMAGES leaves each chunk's entering state in memory, as the bf16 operand
 // image that the gradient kernel copies into its shared memory.
 //
-// Warps: 0-7 compute (two to each quarter of the lanes; each has half of the
-// columns), 8 loads, 9 issues.  They meet at mbarriers only, with bounded
-// waits.  Shared memory holds seven tiles: V' and the operand S (whose place
-// the lower half of V' takes when its product is done), and five for the
-// inputs, which follow one another into whichever tile is free first.  One CTA
-// on an SM.
+// Warps: 0-3 keep the state, 4-11 turn scores into weights, 12-15 form V' (in
+// the other modes 4-11 do), 16-23 write the outputs, 24 loads, 25 issues, 26
+// sums up the decays (a token's lie a row apart: 32 sectors to a load, too many
+// for every warp to read them by itself, which held up all others).  They meet
+// at mbarriers only, with bounded waits.  Shared memory holds seven tiles: V',
+// the operand S, and five for the inputs, which follow one another into
+// whichever tile is free first; outputs pass through the values' tile, so that
+// they leave in whole lines.  One CTA on an SM.
 #pragma once
 
 #include "kda_linear.cuh"
@@ -131,12 +137,64 @@ __device__ __forceinline__ uint32_t split_bf16x2(float a, float b, uint32_t* res
   *rest = pack_bf16x2(a - lo_f32(u), b - hi_f32(u));
   return u;
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t at, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(at));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
       "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
       "r"(v[14]), "r"(v[15]) : "memory");
+}
+
+// Two fp32 numbers in a register pair, and what sm_100 does with both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float* a, float* b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t u) {
+  __nv_bfloat162 v;
+  memcpy(&v, &u, 4);
+  return v;
+}
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
+  uint32_t u;
+  memcpy(&u, &v, 4);
+  return u;
+}
+
+// Waits for a phase, 2 s at most; looks at the clock now and then only.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (int i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (i % 64 == 63) {
+      if (!t0) t0 = globaltimer_ns();
+      else if (globaltimer_ns() - t0 > WAIT_NS) return false;
+    }
+  }
 }
 
 // Descriptors of 128-byte-swizzled operands: rows along K (a tile's channels), or rows along the other
@@ -146,19 +204,19 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t at, uint32_t block) { retur
 
 // log2 of the decays of a chunk's tokens, summed up to each: lane l of the warp has tokens 4 l .. 4 l + 3.
 struct Decays {
-  float raw[4];  // log_alpha of the next chunk
+  uint32_t raw[4];  // log_alpha of the next chunk
   __device__ __forceinline__ void load(const LinearProblem& p, long long row, int rows, int h) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i] = 4 * lane + i < rows ? load_decay(p, row + 4 * lane + i, h) : 0.f;
+    for (int i = 0; i < 4; ++i) raw[i] = 4 * lane + i < rows ? load_decay_bits(p, row + 4 * lane + i, h) : 0u;
   }
-  __device__ __forceinline__ float4 sum() const {
+  __device__ __forceinline__ float4 sum(const LinearProblem& p) const {
     const int lane = threadIdx.x & 31;
     float g[4], run = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x = raw[i] < LEAST ? LEAST : raw[i];  // (a NaN stays)
-      run += x * LOG2E;
+      const float x = decay_of_bits(p, raw[i]);
+      run += (x < LEAST ? LEAST : x) * LOG2E;  // (a NaN stays)
       g[i] = run;
     }
     float before = run;
@@ -179,10 +237,38 @@ template <int D, Mode MODE, bool BACK, bool FINE> struct WalkShape : Shape<D> {
   static constexpr uint32_t X = IN * TILE, Y = X + TILE, MISC = Y + TILE, SMEM_USED = MISC + 3072;
   // one CTA on an SM: each takes all of tensor memory
   static constexpr uint32_t SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
-  static constexpr uint32_t T_A = 0, T_O1 = 128, T_O2 = 128 + D, T_S = 128 + 2 * D;
+  // scores and weights; what the state gives; what the weights give; the chunk's part of the state
+  static constexpr uint32_t T_A = 0, T_O1 = 128, T_O2 = 128 + D, T_Z = 128 + 2 * D;
+  static constexpr int VALUE_WARPS = MODE == OUTPUTS ? 4 : 8;
 };
 
-constexpr int WALK_THREADS = 320;
+constexpr int WALK_THREADS = 896;
+// The launch's registers, split anew by warpgroup (in every mode: one group waits for what others give back).
+constexpr int LAUNCH_REGS = 72, STATE_REGS = 160, WEIGHT_REGS = 56, VALUE_REGS = 48, OUTPUT_REGS = 64, OTHER_REGS = 56;
+static_assert(4 * STATE_REGS + 8 * WEIGHT_REGS + 4 * VALUE_REGS + 8 * OUTPUT_REGS + 4 * OTHER_REGS <= 28 * LAUNCH_REGS, "registers");
+
+// The tiles of a chunk's inputs.  Where there are queries: the next chunk's keys and queries are already on
+// their way; its values take the place of this one's keys, and the keys and queries of the chunk after it
+// those of the queries and values.  `phase` has a bit for each tile.
+template <Mode MODE> struct Tiles {
+  int k = 0, q = 1, v = 2, k2 = 3, q2 = 4;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int c) {
+    if constexpr (MODE == OUTPUTS) {
+      phase ^= 1u << k | 1u << q | 1u << v;
+      const int k0 = k, q0 = q, v0 = v;
+      k = k2;
+      q = q2;
+      v = k0;
+      k2 = q0;
+      q2 = v0;
+    } else {
+      phase ^= 1u << k | 1u << v;
+      k = (c + 1) & 1;
+      v = 2 + ((c + 1) & 1);
+    }
+  }
+};
 
 // FINE: fp32 outputs, P and S as two bf16 numbers each.
 template <int D, Mode MODE, bool BACK, bool FINE>
@@ -204,24 +290,44 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
   const bool last_seg = BACK ? seg.index == 0 : seg.index == seg.count - 1;  // in the order of the walk
   const bool first_seg = BACK ? seg.index == seg.count - 1 : seg.index == 0;
   if (MODE == ENDS && last_seg) return;  // what it would find nobody asks for
+  const bool exact = MODE != OUTPUTS || FINE || (last_seg && p.s_out);  // V' as two numbers
   const int nch = max((seg.tokens + CHUNK - 1) / CHUNK, 0);
   constexpr bool UP = MODE == ENDS ? BACK : !BACK;  // from the segment's first chunk to its last
-  const long long row0 = seg.row0 + (long long)seg.index * w.seg_len;
+  const int row0 = (int)(seg.row0 + (long long)seg.index * w.seg_len);
   auto chunk_of = [&](int c) { return UP ? c : nch - 1 - c; };
   auto rows_of = [&](int ci) { return min(CHUNK, seg.tokens - ci * CHUNK); };
 
-  float* s_g = reinterpret_cast<float*>(smem + W::MISC);              // [2][128]
+  float* s_g = reinterpret_cast<float*>(smem + W::MISC);              // [2][128]: -g
   int* s_first = reinterpret_cast<int*>(smem + W::MISC + 1024);       // [3][128]: the first token of a channel that is not finite
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + W::MISC + 2560);  // [5] an input tile has landed
   uint64_t *s_ready = full + 5, *v_ready = full + 6, *p_ready = full + 7, *l_ready = full + 8, *f_ready = full + 9;
-  uint64_t *a_done = full + 10, *qs_done = full + 11, *pv_done = full + 12, *kv_done = full + 13, *f_done = full + 14;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 15);
-  int* s_bad = reinterpret_cast<int*>(full + 16);                     // [3] some value of the chunk is not finite
+  uint64_t *z_free = full + 10, *o_read = full + 11, *a_done = full + 12, *pv_done = full + 13, *zh_done = full + 14;
+  // for odd and even chunks: a wait tells a phase from the next one, not from the one after that, and
+  // those who wait for these may be a chunk behind
+  uint64_t *qs_done = full + 15, *z_done = full + 17, *f_done = full + 19, *o_done = full + 21, *g_ready = full + 23, *g_free = full + 25;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 27);
+  int* s_bad = reinterpret_cast<int*>(full + 28);                     // [3] some value of the chunk is not finite
 
   if (tid == 0) {
     for (int i = 0; i < 5; ++i) mbar_init(full + i, 1);
-    for (uint64_t* b : {s_ready, v_ready, p_ready, l_ready, f_ready}) mbar_init(b, 8);
-    for (uint64_t* b : {a_done, qs_done, pv_done, kv_done, f_done}) mbar_init(b, 1);
+    mbar_init(s_ready, 4);
+    mbar_init(v_ready, W::VALUE_WARPS);
+    mbar_init(l_ready, W::VALUE_WARPS);
+    mbar_init(p_ready, 8);
+    mbar_init(f_ready, 4);
+    mbar_init(z_free, 4);
+    mbar_init(o_read, 8);
+    mbar_init(a_done, 1);
+    mbar_init(pv_done, 1);
+    mbar_init(zh_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(qs_done + i, 1);
+      mbar_init(z_done + i, 1);
+      mbar_init(f_done + i, 1);
+      mbar_init(o_done + i, 8);
+      mbar_init(g_ready + i, 1);
+      mbar_init(g_free + i, MODE == ENDS ? 8 : MODE == IMAGES ? 12 : 24);
+    }
     mbar_fence_init();
     for (int i = 0; i < 3; ++i) s_bad[i] = 0;
   }
@@ -234,94 +340,415 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tb = *s_tmem;
+  const int quarter = warp & 3;
+  const uint32_t my = tb + ((uint32_t)(32 * quarter) << 16);
   bool ok = true;
 
-  // The tiles of a chunk's inputs.  Where there are queries: those of the next chunk's keys and queries are
-  // already on their way; its values take the queries' place, and the chunk after it those of the values
-  // and the keys.  `phase` has a bit for each tile.
-  struct Tiles {
-    int k = 0, q = 1, v = 2, k2 = 3, q2 = 4;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next(int c) {
-      if constexpr (MODE == OUTPUTS) {
-        phase ^= 1u << k | 1u << q | 1u << v;
-        const int k0 = k, q0 = q, v0 = v;
-        k = k2;
-        q = q2;
-        v = q0;
-        k2 = v0;
-        q2 = k0;
-      } else {
-        phase ^= 1u << k | 1u << v;
-        k = (c + 1) & 1;
-        v = 2 + ((c + 1) & 1);
+  // ---- V' of chunk c from the values' tile, by W::VALUE_WARPS warps: a thread has a token and, where there
+  // are eight warps, half of its channels.  The weight is two bf16 numbers, w1 + w2: the first number of v w is
+  // v w1 rounded, what that leaves of v w1 is exact, and v w2 is added to it (16 bits together).
+  auto form_values = [&]() {
+    constexpr int PIECES = D / 8 / (W::VALUE_WARPS / 4);  // of 16 bytes, to a thread
+    const int part = W::VALUE_WARPS == 8 ? warp >> 2 & 1 : 0, trow = 32 * quarter + lane;
+    const uint32_t sw = (uint32_t)(trow & 7);
+    auto piece = [&](int i) {
+      const int x = part * PIECES + i;
+      return (uint32_t)(x / 8) * W::BLOCK + trow * 128 + (((uint32_t)(x % 8) ^ sw) << 4);
+    };
+    const float gain = BACK ? p.scale : 1.f;
+    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+    float reach = 0.f;  // ENDS: log2 of the decay from the chunk to the segment's end (start)
+    Tiles<MODE> t;
+    for (int c = 0; c < nch && ok; ++c) {
+      const uint32_t par = c & 1;
+      const int rows = rows_of(chunk_of(c));
+      const uint32_t v_at = sb + t.v * W::TILE, k_at = sb + t.k * W::TILE;
+      if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
+      const float g_mine = -s_g[par * 128 + trow], end = -s_g[par * 128 + 127];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(g_free + par);
+      if (MODE == OUTPUTS) {
+        if (c > 1 && !(ok = wait_for(o_done + par, (c >> 1 & 1) ^ 1))) break;
+        s_first[(c + 1) % 3 * 128 + trow] = 0x7fffffff;
+        if (trow == 0) s_bad[(c + 1) % 3] = 0;
+      }
+      const bool real = trow < rows;
+      const float weight = gain * ex2(MODE == ENDS ? reach + (BACK ? g_mine : end - g_mine) : BACK ? g_mine : end - g_mine);
+      const __nv_bfloat162 w1 = __float2bfloat162_rn(weight), w2 = __float2bfloat162_rn(weight - __low2float(w1));
+      if constexpr (MODE == ENDS) reach += end;
+      if (!(ok = wait_for(full + t.v, t.phase >> t.v & 1))) break;
+      const bool tail = rows < CHUNK;
+      if (tail && !(ok = wait_for(full + t.k, t.phase >> t.k & 1))) break;
+      if (c > 0 && !(ok = wait_for(z_done + (par ^ 1), c - 1 >> 1 & 1))) break;
+      __nv_bfloat162 odd = zero;
+#pragma unroll
+      for (int i = 0; i < PIECES; i += 4) {
+        uint32_t u[4][4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) lds_v4(v_at + piece(i + z), u[z]);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          uint32_t y[4], rest[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 x = as_bf16x2(u[z][j]), first = __hmul2_rn(x, w1);
+            if (MODE == OUTPUTS) odd = __hfma2(x, zero, odd);  // NaN if one of them is not finite
+            y[j] = real ? as_u32(first) : 0u;
+            if constexpr (MODE != OUTPUTS) rest[j] = real ? as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(first)))) : 0u;
+          }
+          st_shared_v4(sb + W::X + piece(i + z), y[0], y[1], y[2], y[3]);
+          if constexpr (MODE != OUTPUTS) st_shared_v4(sb + W::Y + piece(i + z), rest[0], rest[1], rest[2], rest[3]);
+        }
+      }
+      if (!real) {  // rows of other sequences
+        for (int i = 0; i < PIECES; ++i) {
+          st_shared_v4(v_at + piece(i), 0u, 0u, 0u, 0u);
+          st_shared_v4(k_at + piece(i), 0u, 0u, 0u, 0u);
+        }
+      } else if (MODE == OUTPUTS && !__hbeq2(odd, zero)) {
+        // such a value is taken out of the product with the weights, where zeros would meet it
+        for (int i = 0; i < PIECES; ++i) {
+          uint32_t u[4];
+          lds_v4(v_at + piece(i), u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int ch = 8 * (part * PIECES + i) + 2 * j;
+            if ((u[j] & 0x7f80u) == 0x7f80u) {
+              u[j] &= 0xffff0000u;
+              atomicMin(s_first + c % 3 * 128 + ch, trow);
+            }
+            if ((u[j] & 0x7f800000u) == 0x7f800000u) {
+              u[j] &= 0xffffu;
+              atomicMin(s_first + c % 3 * 128 + ch + 1, trow);
+            }
+          }
+          st_shared_v4(v_at + piece(i), u[0], u[1], u[2], u[3]);
+        }
+        s_bad[c % 3] = 1;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_ready);
+      if (MODE == OUTPUTS && exact) {  // the second numbers take the place of the first ones
+        if (!(ok = wait_for(zh_done, par))) break;
+#pragma unroll
+        for (int i = 0; i < PIECES; i += 4) {
+          uint32_t u[4][4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) lds_v4(v_at + piece(i + z), u[z]);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 x = as_bf16x2(u[z][j]);
+              u[z][j] = real ? as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(__hmul2_rn(x, w1))))) : 0u;
+            }
+            st_shared_v4(sb + W::X + piece(i + z), u[z][0], u[z][1], u[z][2], u[z][3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(l_ready);
+      }
+      t.next(c);
+    }
+    if constexpr (MODE == ENDS) {  // the segment's contribution
+      if (ok && nch > 0) ok = wait_for(z_done + ((nch - 1) & 1), nch - 1 >> 1 & 1);
+      if (ok) {
+        tc_fence_after_sync();
+        const int srow = D == 128 ? 32 * quarter + lane : 16 * quarter + (lane & 15);
+        float* to = w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)srow * D + part * (D / 2);
+#pragma unroll
+        for (int b = 0; b < D / 2; b += 16) {
+          float s[16];
+          tmem_ld16(my + W::T_Z + part * (D / 2) + b, s);
+          tmem_ld_wait();
+          if (D == 128 || lane < 16) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(to + b + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+          }
+        }
+        if (part == 0 && trow == 0) w.decay[(size_t)slot * p.H + h] = reach;
       }
     }
   };
 
-  if (warp == 8) {
-    // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      auto load = [&](const CUtensorMap* map, int tile, int c) {
-        const int row = (int)(row0 + chunk_of(c) * CHUNK);
-        mbar_arrive_expect_tx(full + tile, W::TILE);
-        for (int b = 0; b < D / 64; ++b)
-          tma_load_3d(smem + tile * W::TILE + b * W::BLOCK, map, full + tile, 64 * b, h, row);
-      };
-      Tiles t;
-      uint32_t loads = 0, landed = 0;  // parity of each tile's number of loads
-      if constexpr (MODE != OUTPUTS) { t.q = 0; t.v = 2; }
-      for (int c = -2; c < nch && ok; ++c) {
-        // before chunk 0: what the first two chunks find on their way
-        if constexpr (MODE == OUTPUTS) {
-          if (c == -2) {
-            if (nch > 0) { load(&map_k, 0, 0); load(&map_q, 1, 0); load(&map_v, 2, 0); loads ^= 7; }
-          } else if (c == -1) {
-            if (nch > 1) { load(&map_k, 3, 1); load(&map_q, 4, 1); loads ^= 24; }
-          } else {
-            const uint32_t par = c & 1;
-            if (c + 1 < nch) {
-              ok = mbar_wait(FINE ? f_done : qs_done, par);
-              if (ok) { load(&map_v, t.q, c + 1); loads ^= 1u << t.q; }
-            }
-            if (ok && c + 2 < nch) {
-              ok = mbar_wait(pv_done, par);
-              if (ok) { load(&map_k, t.v, c + 2); loads ^= 1u << t.v; }
-              ok = ok && mbar_wait(kv_done, par);
-              if (ok) { load(&map_q, t.k, c + 2); loads ^= 1u << t.k; }
-            }
-            t.next(c);
-          }
-        } else {
-          if (c >= 0 && c + 2 < nch) ok = mbar_wait(kv_done, c & 1);
-          if (ok && c + 2 < nch) {
-            load(&map_k, c & 1, c + 2);
-            load(&map_v, 2 + (c & 1), c + 2);
-            loads ^= 5u << (c & 1);
-          }
+  if (warp < 4) {
+    // ---------------------------------------------------------------- the state: a lane has one of its rows
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(STATE_REGS));
+    if constexpr (MODE != ENDS) {
+      const int srow = D == 128 ? 32 * quarter + lane : 16 * quarter + (lane & 15);
+      const bool has_row = D == 128 || lane < 16;
+      const size_t state_at = ((size_t)seg.n * p.H + h) * D * D + (size_t)srow * D;
+      uint64_t s[D / 2];  // two columns each
+      {
+        const float* from = !first_seg ? w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)srow * D : p.s_in ? p.s_in + state_at : nullptr;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) {
+          const float4 x = from ? *reinterpret_cast<const float4*>(from + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+          s[2 * i] = pair(x.x, x.y);
+          s[2 * i + 1] = pair(x.z, x.w);
         }
       }
-      (void)landed;
+      // eight columns to their place in the operand, as the first (second) of their two numbers
+      auto place = [&](int i, bool second, auto to) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x, y;
+          unpair(s[4 * i + j], &x, &y);
+          u[j] = pack_bf16x2(x, y);
+          if (second) u[j] = pack_bf16x2(x - lo_f32(u[j]), y - hi_f32(u[j]));
+        }
+        to((uint32_t)(i / 8) * W::IMAGE_BLOCK + (uint32_t)srow * 128 + (((uint32_t)(i % 8) ^ (uint32_t)(srow & 7)) << 4), u);
+      };
+      auto to_tile = [&](uint32_t at, const uint32_t (&u)[4]) {
+        if (has_row) st_shared_v4(sb + W::Y + at, u[0], u[1], u[2], u[3]);
+      };
+      for (int c = 0; c < nch && ok; ++c) {
+        const uint32_t par = c & 1;
+        if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
+        const float keep = ex2(-s_g[par * 128 + 127]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(g_free + par);
+        if constexpr (MODE == OUTPUTS) {
+          if (c > 0 && !(ok = wait_for((FINE ? f_done : qs_done) + (par ^ 1), c - 1 >> 1 & 1))) break;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) place(i, false, to_tile);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_ready);
+          if constexpr (FINE) {
+            if (!(ok = wait_for(qs_done + par, c >> 1 & 1))) break;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) place(i, true, to_tile);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(f_ready);
+          }
+        } else {
+          uint8_t* image = w.images + ((first_chunk(p, seg) + seg.index * (w.seg_len / CHUNK) + chunk_of(c)) * p.H + h) * W::IMAGE;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            place(i, false, [&](uint32_t at, const uint32_t (&u)[4]) {
+              if (has_row) *reinterpret_cast<uint4*>(image + at) = make_uint4(u[0], u[1], u[2], u[3]);
+            });
+        }
+        if (!(ok = wait_for(z_done + par, c >> 1 & 1))) break;
+        tc_fence_after_sync();
+#pragma unroll
+        for (int b = 0; b < D; b += 16) {
+          float z[16];
+          tmem_ld16(my + W::T_Z + b, z);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) s[(b + i) / 2] = fma2(s[(b + i) / 2], pair(keep, keep), pair(z[i], z[i + 1]));
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(z_free);
+      }
+      if (ok && last_seg && p.s_out && has_row) {
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) {
+          float4 x;
+          unpair(s[2 * i], &x.x, &x.y);
+          unpair(s[2 * i + 1], &x.z, &x.w);
+          *reinterpret_cast<float4*>(p.s_out + state_at + 4 * i) = x;
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ---------------------------------------------------------------- the weights, in place of the scores
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(WEIGHT_REGS));
+    if constexpr (MODE != OUTPUTS) {
+      form_values();
+    } else {
+      const int half = warp >> 2 & 1, trow = 32 * quarter + lane;
+      for (int c = 0; c < nch && ok; ++c) {
+        const uint32_t par = c & 1;
+        const float* minus_g = s_g + par * 128;
+        if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
+        const float g_mine = -minus_g[trow];
+        if (!(ok = wait_for(a_done, par))) break;
+        tc_fence_after_sync();
+        uint32_t u[32], rest[FINE ? 32 : 1];
+#pragma unroll
+        for (int b = 0; b < 64; b += 16) {
+          const int j0 = 64 * half + b;
+          if (j0 <= 32 * quarter + 31) {
+            float a[16];
+            tmem_ld16(my + W::T_A + j0, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const uint64_t to = add2(pair(g_mine, g_mine), *reinterpret_cast<const uint64_t*>(minus_g + j0 + j));
+              float x, y;
+              unpair(to, &x, &y);
+              unpair(mul2(pair(a[j], a[j + 1]), pair(ex2(x), ex2(y))), &a[j], &a[j + 1]);
+            }
+            if (j0 + 15 > 32 * quarter) {  // what comes after some of the warp's tokens
+#pragma unroll
+              for (int j = 0; j < 16; ++j) a[j] = j0 + j <= trow ? a[j] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (FINE) u[b / 2 + j] = split_bf16x2(a[2 * j], a[2 * j + 1], &rest[b / 2 + j]);
+              else u[b / 2 + j] = pack_bf16x2(a[2 * j], a[2 * j + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              u[b / 2 + j] = 0u;
+              if constexpr (FINE) rest[b / 2 + j] = 0u;
+            }
+          }
+        }
+        // (a half's pieces lie where its own scores were, all of which it has read)
+        tmem_st16u(my + W::T_A + 64 * half, u);
+        tmem_st16u(my + W::T_A + 64 * half + 16, u + 16);
+        if constexpr (FINE) {
+          tmem_st16u(my + W::T_A + 64 * half + 32, rest);
+          tmem_st16u(my + W::T_A + 64 * half + 48, rest + 16);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(p_ready);
+          mbar_arrive(g_free + par);
+        }
+      }
+    }
+  } else if (warp < 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(VALUE_REGS));
+    if constexpr (MODE == OUTPUTS) form_values();
+  } else if (warp < 24) {
+    // ---------------------------------------------------------------- the outputs: 32 rows and 128 bytes
+    // (d = 64: 64) of each at a time, turned in this warp's part of the values' tile so that 8 lanes write a
+    // row's piece
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OUTPUT_REGS));
+    if constexpr (MODE == OUTPUTS) {
+      constexpr int SC = D / 2, ES = FINE ? 4 : 2, TURN = W::TILE / 256 / ES, LANES = W::TILE / 256 / 16;  // columns; lanes to a row's piece
+      const int half = warp >> 2 & 1, trow = 32 * quarter + lane;
+      const size_t row_bytes = (size_t)p.H * D * ES;
+      Tiles<MODE> t;
+      for (int c = 0; c < nch && ok; ++c) {
+        const uint32_t par = c & 1;
+        const int rows = rows_of(chunk_of(c));
+        const uint32_t turn = sb + t.v * W::TILE + (warp - 16) * (W::TILE / 8);
+        if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
+        const float lead = p.scale * ex2(-s_g[par * 128 + trow]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(g_free + par);
+        if (!(ok = wait_for(pv_done, par))) break;
+        tc_fence_after_sync();
+        const bool bad = s_bad[c % 3] != 0;
+        uint8_t* to = static_cast<uint8_t*>(p.out) + (size_t)(row0 + chunk_of(c) * CHUNK + 32 * quarter) * row_bytes + (h * D + half * SC) * ES;
+#pragma unroll
+        for (int b = 0; b < SC; b += TURN) {
+          uint32_t o[TURN * ES / 4];
+#pragma unroll
+          for (int z = 0; z < TURN; z += 8) {
+            float x[8], y[8];
+            tmem_ld8(my + W::T_O1 + half * SC + b + z, x);
+            tmem_ld8(my + W::T_O2 + half * SC + b + z, y);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; i += 2)
+              unpair(fma2(pair(lead, lead), pair(x[i], x[i + 1]), mul2(pair(p.scale, p.scale), pair(y[i], y[i + 1]))), &y[i], &y[i + 1]);
+            if (bad) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (s_first[c % 3 * 128 + half * SC + b + z + i] <= trow) y[i] = NAN;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if constexpr (FINE) o[z + i] = __float_as_uint(y[i]);
+              else if (i % 2) o[(z + i) / 2] = pack_bf16x2(y[i - 1], y[i]);
+            }
+          }
+          if (b + TURN == SC) {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_read);
+          } else if (b) {
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < LANES; ++i)
+            st_shared_v4(turn + lane * (LANES * 16) + ((i ^ (lane * LANES / 8 % LANES)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < LANES; ++i) {
+            const int r = i * (32 / LANES) + lane / LANES, at = lane % LANES;
+            lds_v4(turn + r * (LANES * 16) + ((at ^ (r * LANES / 8 % LANES)) << 4), *reinterpret_cast<uint32_t(*)[4]>(o + 4 * i));
+          }
+#pragma unroll
+          for (int i = 0; i < LANES; ++i) {
+            const int r = i * (32 / LANES) + lane / LANES, at = lane % LANES;
+            if (32 * quarter + r < rows)
+              *reinterpret_cast<uint4*>(to + r * row_bytes + b * ES + at * 16) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        fence_proxy_async_smem();  // the tile's next content comes by TMA
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_done + par);
+        t.next(c);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
+    if (warp == 24 && lane == 0) {
+      // -------------------------------------------------------------- loads
+      auto load = [&](const CUtensorMap* map, int tile, int c) {
+        mbar_arrive_expect_tx(full + tile, W::TILE);
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(smem + tile * W::TILE + b * W::BLOCK, map, full + tile, 64 * b, h, row0 + chunk_of(c) * CHUNK);
+      };
+      uint32_t loads = 0;  // parity of each tile's number of loads
+      if constexpr (MODE == OUTPUTS) {
+        Tiles<MODE> t;
+        if (nch > 0) { load(&map_k, 0, 0); load(&map_q, 1, 0); load(&map_v, 2, 0); loads = 7; }
+        if (nch > 1) { load(&map_k, 3, 1); load(&map_q, 4, 1); loads = 31; }
+        for (int c = 0; c + 1 < nch && ok; ++c) {
+          const int odd = c & 1;
+          const uint32_t par = c >> 1 & 1;
+          if (!(ok = wait_for(z_done + odd, par))) break;
+          load(&map_v, t.k, c + 1);
+          loads ^= 1u << t.k;
+          if (c + 2 < nch) {
+            if (!(ok = wait_for((FINE ? f_done : qs_done) + odd, par))) break;
+            load(&map_k, t.q, c + 2);
+            loads ^= 1u << t.q;
+            if (!(ok = wait_for(o_done + odd, par))) break;
+            load(&map_q, t.v, c + 2);
+            loads ^= 1u << t.v;
+          }
+          t.next(c);
+        }
+      } else {
+        for (int c = 0; c < nch && ok; ++c) {
+          if (c > 1 && !(ok = wait_for(z_done + (c & 1), (c >> 1 & 1) ^ 1))) break;
+          load(&map_k, c & 1, c);
+          load(&map_v, 2 + (c & 1), c);
+          loads ^= 5u << (c & 1);
+        }
+      }
       // no copy is in flight when the CTA ends: the last one into each tile has landed
       for (int i = 0; i < W::IN; ++i) {
-        const uint32_t odd = loads >> i & 1;  // loads so far are odd: phases 0, 1, .. the last is even
         const bool any = MODE == OUTPUTS ? nch > (i < 3 ? 0 : 1) : nch > (i & 1);
-        if (any) ok = mbar_wait(full + i, odd ^ 1) && ok;
+        if (any) ok = wait_for(full + i, (loads >> i & 1) ^ 1) && ok;
       }
-      if (!ok) atomicExch(p.status, (int)KDA_ERR_TIMEOUT);
-    }
-  } else if (warp == 9) {
-    // ---------------------------------------------------------------- products
-    if (lane == 0) {
+    } else if (warp == 25 && lane == 0) {
+      // -------------------------------------------------------------- products
       constexpr uint32_t ID_A = make_idesc_bf16(128, 128, false, false), ID_O = make_idesc_bf16(128, D, false, true),
-                         ID_S = make_idesc_bf16(D, D, true, true);
-      Tiles t;
-      if constexpr (MODE != OUTPUTS) t.v = 2;
-      auto state_update = [&](uint32_t k_at, uint32_t v_at, bool add) {
+                         ID_Z = make_idesc_bf16(D, D, true, true);
+      Tiles<MODE> t;
+      auto state_part = [&](uint32_t k_at, uint32_t v_at, bool add) {
         const uint64_t a = desc_mn(k_at, W::BLOCK), b = desc_mn(v_at, W::BLOCK);
 #pragma unroll
-        for (int i = 0; i < 128; i += 16)
-          umma_bf16(tb + W::T_S, desc_adv(a, i, true), desc_adv(b, i, true), ID_S, add || i ? 1u : 0u);
+        for (int i = 0; i < 128; i += 16) umma_bf16(tb + W::T_Z, desc_adv(a, i, true), desc_adv(b, i, true), ID_Z, add || i ? 1u : 0u);
       };
       auto from_state = [&](uint32_t q_at, bool add) {
         const uint64_t a = desc_k(q_at), b = desc_mn(sb + W::Y, W::IMAGE_BLOCK);
@@ -332,31 +759,37 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
       for (int c = 0; c < nch && ok; ++c) {
         const uint32_t par = c & 1;
         const uint32_t k_at = sb + t.k * W::TILE, v_at = sb + t.v * W::TILE, q_at = sb + t.q * W::TILE;
-        ok = mbar_wait(full + t.k, t.phase >> t.k & 1);
+        if (!(ok = wait_for(full + t.k, t.phase >> t.k & 1))) break;
         if constexpr (MODE == OUTPUTS) {
-          ok = ok && mbar_wait(full + t.q, t.phase >> t.q & 1);
-          if (!ok) break;
+          if (!(ok = wait_for(full + t.q, t.phase >> t.q & 1))) break;
           const uint64_t a = desc_k(q_at), b = desc_k(k_at);
 #pragma unroll
           for (int i = 0; i < D; i += 16)
             umma_bf16(tb + W::T_A, desc_adv(a, i, false, W::BLOCK), desc_adv(b, i, false, W::BLOCK), ID_A, i ? 1u : 0u);
           umma_commit(a_done);
-          if (!(ok = mbar_wait(s_ready, par))) break;
+        }
+        if (!(ok = wait_for(v_ready, par))) break;
+        if (MODE != ENDS && c > 0 && !(ok = wait_for(z_free, par ^ 1))) break;
+        tc_fence_after_sync();
+        state_part(k_at, sb + W::X, MODE == ENDS && c > 0);
+        if constexpr (MODE == OUTPUTS) {
+          if (exact) {
+            umma_commit(zh_done);
+            if (!(ok = wait_for(l_ready, par))) break;
+            state_part(k_at, sb + W::X, true);
+          }
+          umma_commit(z_done + par);
+          if (!(ok = wait_for(s_ready, par))) break;
+          if (c > 0 && !(ok = wait_for(o_read, par ^ 1))) break;
           tc_fence_after_sync();
           from_state(q_at, false);
-          umma_commit(qs_done);
+          umma_commit(qs_done + par);
           if (FINE) {
-            if (!(ok = mbar_wait(f_ready, par))) break;
-            tc_fence_after_sync();
+            if (!(ok = wait_for(f_ready, par))) break;
             from_state(q_at, true);
-            umma_commit(f_done);
+            umma_commit(f_done + par);
           }
-        }
-        if (!ok || !(ok = mbar_wait(v_ready, par))) break;
-        tc_fence_after_sync();
-        state_update(k_at, sb + W::X, MODE != ENDS || c > 0);
-        if constexpr (MODE == OUTPUTS) {
-          if (!(ok = mbar_wait(p_ready, par))) break;
+          if (!(ok = wait_for(p_ready, par))) break;
           tc_fence_after_sync();
           const uint64_t b = desc_mn(v_at, W::BLOCK);
 #pragma unroll
@@ -366,302 +799,34 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
               umma_f16_ta(tb + W::T_O2, tb + W::T_A + (i >= 64 ? 64 : 0) + (i % 64) / 2 + 32 * x, desc_adv(b, i, true), ID_O,
                           x || i ? 1u : 0u);
           umma_commit(pv_done);
-          if (!(ok = mbar_wait(l_ready, par))) break;
-          tc_fence_after_sync();
+        } else {
+          state_part(k_at, sb + W::Y, true);
+          umma_commit(z_done + par);
         }
-        state_update(k_at, sb + W::Y, true);
-        umma_commit(kv_done);
         t.next(c);
       }
       if (!ok) {  // what has been issued ends before the CTA does
-        atomicExch(p.status, (int)KDA_ERR_TIMEOUT);
-        umma_commit(kv_done);
-        umma_commit(kv_done);
-        (void)mbar_wait(kv_done, 0);
-        (void)mbar_wait(kv_done, 1);
+        umma_commit(pv_done);
+        umma_commit(pv_done);
+        (void)wait_for(pv_done, 0);
+        (void)wait_for(pv_done, 1);
       }
-    }
-  } else {
-    // ---------------------------------------------------------------- weights, states, outputs
-    const int quarter = warp & 3, half = warp >> 2;
-    const uint32_t my = tb + ((uint32_t)(32 * quarter) << 16);
-    // the state: a lane has one of its rows, a warp half of its columns
-    const int srow = D == 128 ? 32 * quarter + lane : 16 * quarter + (lane & 15);
-    const bool has_srow = D == 128 || lane < 16;
-    constexpr int SC = D / 2;
-    const size_t state_at = ((size_t)seg.n * p.H + h) * D * D + (size_t)srow * D + half * SC;
-    const size_t carry_at = ((size_t)slot * p.H + h) * D * D + (size_t)srow * D + half * SC;
-    const int trow = tid & 127;  // this thread's token where V' is formed, and of P and O
-    const uint32_t sw = (uint32_t)(trow & 7);
-    const float gain = BACK ? p.scale : 1.f;
-    Tiles t;
-    if constexpr (MODE != OUTPUTS) t.v = 2;
-    Decays la;
-    float reach = 0.f;  // ENDS: log2 of the decay from the chunk to the segment's end (start)
-    if (nch > 0) la.load(p, row0 + chunk_of(0) * CHUNK, rows_of(chunk_of(0)), h);
-    int c = 0;
-    for (; c < nch && ok; ++c) {
-      const uint32_t par = c & 1;
-      const int ci = chunk_of(c), rows = rows_of(ci);
-      const long long row = row0 + (long long)ci * CHUNK;
-      const uint32_t v_at = sb + t.v * W::TILE, k_at = sb + t.k * W::TILE;
-      // every warp sums the decays for itself; all write the same numbers
-      float* g = s_g + par * 128;
-      const float4 g4 = la.sum();
-      *reinterpret_cast<float4*>(g + 4 * lane) = g4;
-      const float end = __shfl_sync(~0u, g4.w, 31);
-      if (c + 1 < nch) la.load(p, row0 + chunk_of(c + 1) * CHUNK, rows_of(chunk_of(c + 1)), h);
-      __syncwarp();
-      const float g_mine = g[trow];
-      if (MODE == OUTPUTS) {
-        if (tid < 128) s_first[(c + 1) % 3 * 128 + tid] = 0x7fffffff;
-        if (tid == 0) s_bad[(c + 1) % 3] = 0;
-      }
-
-      // ---- the state as an operand, and what is left of it after the chunk
-      if (c > 0) {
-        if (!(ok = mbar_wait(kv_done, par ^ 1))) break;
-        tc_fence_after_sync();
-      }
-      uint32_t s_rest[FINE ? SC / 2 : 1];
-      if constexpr (MODE != ENDS) {
-        const float keep = ex2(end);
-        const float* from = !first_seg ? w.carry + carry_at : p.s_in ? p.s_in + state_at : nullptr;
-#pragma unroll
-        for (int b = 0; b < SC; b += 32) {
-          float s[2][16];
-          if (c > 0) {
-            tmem_ld16(my + W::T_S + half * SC + b, s[0]);
-            tmem_ld16(my + W::T_S + half * SC + b + 16, s[1]);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 x = from && has_srow ? *reinterpret_cast<const float4*>(from + b + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-              s[i / 16][i % 16] = x.x;
-              s[i / 16][i % 16 + 1] = x.y;
-              s[i / 16][i % 16 + 2] = x.z;
-              s[i / 16][i % 16 + 3] = x.w;
-            }
-          }
-          uint32_t u[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float x = s[i / 8][2 * i % 16], y = s[i / 8][2 * i % 16 + 1];
-            if constexpr (FINE) u[i] = split_bf16x2(x, y, &s_rest[b / 2 + i]);
-            else u[i] = pack_bf16x2(x, y);
-          }
-          const int col = half * SC + b;
-          const uint32_t line = (uint32_t)(col / 64) * W::IMAGE_BLOCK + (uint32_t)srow * 128;
-          if (has_srow) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t at = line + ((((uint32_t)(col % 64) / 8 + i) ^ (uint32_t)(srow & 7)) << 4);
-              if constexpr (MODE == OUTPUTS) {
-                st_shared_v4(sb + W::Y + at, u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
-              } else {
-                uint8_t* to = w.images + ((first_chunk(p, seg) + (row - seg.row0) / CHUNK) * p.H + h) * W::IMAGE;
-                *reinterpret_cast<uint4*>(to + at) = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i / 16][i % 16] *= keep;
-          tmem_st16(my + W::T_S + half * SC + b, s[0]);
-          tmem_st16(my + W::T_S + half * SC + b + 16, s[1]);
-        }
-        tmem_st_wait();
-        tc_fence_before_sync();
-        if constexpr (MODE == OUTPUTS) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(s_ready);
-        }
-      }
-
-      // ---- the weighted values
-      if (!(ok = mbar_wait(full + t.v, t.phase >> t.v & 1))) break;
-      const bool tail = rows < CHUNK;
-      if (tail && !(ok = mbar_wait(full + t.k, t.phase >> t.k & 1))) break;
-      constexpr int PIECES = D == 128 ? 8 : 4;  // of 16 bytes, to a thread
-      uint32_t v_rest[4 * PIECES];
-      {
-        const bool real = trow < rows;
-        const float weight = gain * ex2(MODE == ENDS ? reach + (BACK ? g_mine : end - g_mine) : BACK ? g_mine : end - g_mine);
-        const uint32_t block = D == 128 ? half * W::BLOCK : 0;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-          const uint32_t at = block + trow * 128 + (((uint32_t)(D == 128 ? i : 4 * half + i) ^ sw) << 4);
-          uint32_t u[4], o[4];
-          lds_v4(v_at + at, u);
-          if (MODE == OUTPUTS && real) {
-            bool odd = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) odd |= (u[j] & 0x7f80u) == 0x7f80u || (u[j] & 0x7f800000u) == 0x7f800000u;
-            if (odd) {  // such a value is taken out of the product with the weights, where zeros would meet it
-              uint32_t z[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                z[j] = u[j];
-                const int ch = half * (D / 2) + 8 * i + 2 * j;
-                if ((u[j] & 0x7f80u) == 0x7f80u) {
-                  z[j] &= 0xffff0000u;
-                  atomicMin(s_first + c % 3 * 128 + ch, trow);
-                }
-                if ((u[j] & 0x7f800000u) == 0x7f800000u) {
-                  z[j] &= 0xffffu;
-                  atomicMin(s_first + c % 3 * 128 + ch + 1, trow);
-                }
-              }
-              st_shared_v4(v_at + at, z[0], z[1], z[2], z[3]);
-              s_bad[c % 3] = 1;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[j] = real ? split_bf16x2(lo_f32(u[j]) * weight, hi_f32(u[j]) * weight, &v_rest[4 * i + j]) : (v_rest[4 * i + j] = 0u);
-          st_shared_v4(sb + W::X + at, o[0], o[1], o[2], o[3]);
-          if constexpr (MODE != OUTPUTS)
-            st_shared_v4(sb + W::Y + at, v_rest[4 * i], v_rest[4 * i + 1], v_rest[4 * i + 2], v_rest[4 * i + 3]);
-          if (tail && !real) {  // rows of other sequences
-            st_shared_v4(v_at + at, 0u, 0u, 0u, 0u);
-            st_shared_v4(k_at + at, 0u, 0u, 0u, 0u);
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_ready);
-      if constexpr (MODE == ENDS) reach += end;
-
-      if constexpr (MODE == OUTPUTS) {
-        // ---- the weights, in place of the scores
-        if (!(ok = mbar_wait(a_done, par))) break;
-        tc_fence_after_sync();
-        uint32_t u[32], rest[32];
-#pragma unroll
-        for (int b = 0; b < 64; b += 16) {
-          const int j0 = 64 * half + b;
-          if (j0 <= 32 * quarter + 31) {
-            float a[16];
-            tmem_ld16(my + W::T_A + j0, a);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 gj = *reinterpret_cast<const float4*>(g + j0 + j);
-              a[j] = j0 + j <= trow ? a[j] * p.scale * ex2(g_mine - gj.x) : 0.f;
-              a[j + 1] = j0 + j + 1 <= trow ? a[j + 1] * p.scale * ex2(g_mine - gj.y) : 0.f;
-              a[j + 2] = j0 + j + 2 <= trow ? a[j + 2] * p.scale * ex2(g_mine - gj.z) : 0.f;
-              a[j + 3] = j0 + j + 3 <= trow ? a[j + 3] * p.scale * ex2(g_mine - gj.w) : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[b / 2 + j] = split_bf16x2(a[2 * j], a[2 * j + 1], &rest[b / 2 + j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[b / 2 + j] = rest[b / 2 + j] = 0u;
-          }
-        }
-        // (a half's pieces lie where its own scores were, all of which it has read)
-        tmem_st16u(my + W::T_A + 64 * half, u);
-        tmem_st16u(my + W::T_A + 64 * half + 16, u + 16);
-        if (FINE) {
-          tmem_st16u(my + W::T_A + 64 * half + 32, rest);
-          tmem_st16u(my + W::T_A + 64 * half + 48, rest + 16);
-        }
-        tmem_st_wait();
-        tc_fence_before_sync();
+    } else if (warp == 26) {
+      // -------------------------------------------------------------- decays
+      Decays la;
+      if (nch > 0) la.load(p, row0 + chunk_of(0) * CHUNK, rows_of(chunk_of(0)), h);
+      for (int c = 0; c < nch; ++c) {
+        const float4 g4 = la.sum(p);
+        if (c + 1 < nch) la.load(p, row0 + chunk_of(c + 1) * CHUNK, rows_of(chunk_of(c + 1)), h);
+        if (c > 1 && !(ok = wait_for(g_free + (c & 1), (c >> 1 & 1) ^ 1))) break;
+        *reinterpret_cast<float4*>(s_g + (c & 1) * 128 + 4 * lane) = make_float4(-g4.x, -g4.y, -g4.z, -g4.w);
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready);
-
-        // ---- what the operands' first numbers left takes the state's place
-        if (!(ok = mbar_wait(qs_done, par))) break;
-        if constexpr (FINE) {
-#pragma unroll
-          for (int i = 0; i < SC / 8; ++i) {
-            const int col = half * SC + 8 * i;
-            if (has_srow)
-              st_shared_v4(sb + W::Y + (uint32_t)(col / 64) * W::IMAGE_BLOCK + (uint32_t)srow * 128 +
-                               ((((uint32_t)(col % 64) / 8) ^ (uint32_t)(srow & 7)) << 4),
-                           s_rest[4 * i], s_rest[4 * i + 1], s_rest[4 * i + 2], s_rest[4 * i + 3]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(f_ready);
-          if (!(ok = mbar_wait(f_done, par))) break;
-        }
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-          const uint32_t at = (D == 128 ? half * W::BLOCK : 0) + trow * 128 + (((uint32_t)(D == 128 ? i : 4 * half + i) ^ sw) << 4);
-          st_shared_v4(sb + W::Y + at, v_rest[4 * i], v_rest[4 * i + 1], v_rest[4 * i + 2], v_rest[4 * i + 3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(l_ready);
-
-        // ---- the outputs
-        if (!(ok = mbar_wait(pv_done, par))) break;
-        tc_fence_after_sync();
-        const float lead = p.scale * ex2(g_mine);
-        const bool bad = s_bad[c % 3] != 0;
-        const size_t out_at = ((size_t)(row + trow) * p.H + h) * D + half * SC;
-#pragma unroll
-        for (int b = 0; b < SC; b += 16) {
-          float x[16], y[16];
-          tmem_ld16(my + W::T_O1 + half * SC + b, x);
-          tmem_ld16(my + W::T_O2 + half * SC + b, y);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) y[i] += lead * x[i];
-          if (bad) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (s_first[c % 3 * 128 + half * SC + b + i] <= trow) y[i] = NAN;
-          }
-          if (trow < rows) {
-            if constexpr (FINE) {
-              float* to = static_cast<float*>(p.out) + out_at + b;
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-            } else {
-              __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + out_at + b;
-#pragma unroll
-              for (int i = 0; i < 16; i += 8)
-                *reinterpret_cast<uint4*>(to + i) = make_uint4(pack_bf16x2(y[i], y[i + 1]), pack_bf16x2(y[i + 2], y[i + 3]),
-                                                               pack_bf16x2(y[i + 4], y[i + 5]), pack_bf16x2(y[i + 6], y[i + 7]));
-            }
-          }
-        }
-        tc_fence_before_sync();
+        if (lane == 0) mbar_arrive(g_ready + (c & 1));
       }
-      t.next(c);
     }
-    // ---- the state behind the segment
-    if (ok && nch > 0) ok = mbar_wait(kv_done, (nch - 1) & 1);
-    if (!ok) {
-      if (lane == 0) atomicExch(p.status, (int)KDA_ERR_TIMEOUT);
-    } else if (MODE == ENDS || (last_seg && p.s_out)) {
-      tc_fence_after_sync();
-      float* to = MODE == ENDS ? w.carry + carry_at : p.s_out + state_at;
-      if (nch > 0) {
-#pragma unroll
-        for (int b = 0; b < SC; b += 16) {
-          float s[16];
-          tmem_ld16(my + W::T_S + half * SC + b, s);
-          tmem_ld_wait();
-          if (has_srow) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(to + b + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-          }
-        }
-      } else if (has_srow) {  // an empty sequence
-        for (int i = 0; i < SC; i += 4)
-          *reinterpret_cast<float4*>(to + i) = p.s_in ? *reinterpret_cast<const float4*>(p.s_in + state_at + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      if (MODE == ENDS && tid == 0) w.decay[(size_t)slot * p.H + h] = reach;
-    }
-    tc_fence_before_sync();
   }
+  if (!ok && lane == 0) atomicExch(p.status, (int)KDA_ERR_TIMEOUT);
+  tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 0) tmem_dealloc(tb, 512);
@@ -680,16 +845,27 @@ template <bool BACK> __global__ void __launch_bounds__(256) linear_scan_kernel(W
   const long long first = p.cu_seqlens ? row0 / w.seg_len + n : (long long)n * w.segs;
   const size_t at = (size_t)part * 1024 + threadIdx.x * 4, size = (size_t)p.d * p.d;
   float4 e = p.s_in ? *reinterpret_cast<const float4*>(p.s_in + (size_t)nh * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < count; ++i) {
-    const size_t slot = (size_t)(first + (BACK ? count - 1 - i : i)) * p.H + h;
-    float4* here = reinterpret_cast<float4*>(w.carry + slot * size + at);
-    if (i + 1 < count) {
-      const float4 z = *here;
-      const float keep = ex2(w.decay[slot]);
-      *here = e;
-      e = make_float4(keep * e.x + z.x, keep * e.y + z.y, keep * e.z + z.z, keep * e.w + z.w);
-    } else {
-      *here = e;
+  // the contributions of AHEAD segments are on their way together
+  constexpr int AHEAD = 8;
+  for (int i0 = 0; i0 < count; i0 += AHEAD) {
+    float4 z[AHEAD];
+    float keep[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const size_t slot = (size_t)(first + (BACK ? count - 1 - i0 - i : i0 + i)) * p.H + h;
+      if (i0 + i + 1 < count) {
+        z[i] = *reinterpret_cast<const float4*>(w.carry + slot * size + at);
+        keep[i] = w.decay[slot];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const size_t slot = (size_t)(first + (BACK ? count - 1 - i0 - i : i0 + i)) * p.H + h;
+      if (i0 + i < count) *reinterpret_cast<float4*>(w.carry + slot * size + at) = e;
+      if (i0 + i + 1 < count) {
+        const float k = ex2(keep[i]);
+        e = make_float4(k * e.x + z[i].x, k * e.y + z[i].y, k * e.z + z[i].z, k * e.w + z[i].w);
+      }
     }
   }
 }
@@ -730,7 +906,7 @@ inline int segment_tokens(int n_seq, int T, int H, bool packed, int sms) {
   for (long long segs = 1; segs <= 256 && segs * 4 <= std::max(chunks, 4LL); ++segs) {
     const long long of = (chunks + segs - 1) / segs;
     const long long items = (packed ? chunks / of + n_seq : n_seq * ((chunks + of - 1) / of)) * H;
-    const long long cost = (items + sms - 1) / sms * of * (segs > 1 ? 3 : 2);
+    const long long cost = (items + sms - 1) / sms * (of + 3) * (segs > 1 ? 3 : 2);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       best = of;
