@@ -30,9 +30,8 @@
 // IMAGES leaves each chunk's entering state in memory, as the bf16 operand
 // image that the gradient kernel copies into its shared memory.
 //
-// Warps: 0-3 keep the state, 4-11 turn scores into weights, 12-15 form V' (in
-// the other modes 4-11 do), 16-23 write the outputs, 24 loads, 25 issues, 26
-// sums up the decays (a token's lie a row apart: 32 sectors to a load, too many
+// Warps: 0-3 keep the state, 4-11 form V' and turn scores into weights, 12-19
+// write the outputs, 20 loads, 21 issues, 22 sums up the decays (a token's lie a row apart: 32 sectors to a load, too many
 // for every warp to read them by itself, which held up all others).  They meet
 // at mbarriers only, with bounded waits.  Shared memory holds seven tiles: V',
 // the operand S, and five for the inputs, which follow one another into
@@ -144,6 +143,10 @@ __device__ __forceinline__ void tmem_ld8(uint32_t at, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_st8u(uint32_t at, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
 __device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -185,16 +188,14 @@ __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) {
   return u;
 }
 
-// Waits for a phase, 2 s at most; looks at the clock now and then only.
+// Waits for a phase; a try waits a while by itself (a microsecond or so), so this ends after a second or a few.
+// Short, as everything in the walk's loops: their instructions come around once a chunk, and what does not stay
+// in the instruction cache takes longer to fetch than to run.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity) {
-  uint64_t t0 = 0;
-  for (int i = 0;; ++i) {
+#pragma unroll 1
+  for (int i = 0; i < 1 << 20; ++i)
     if (mbar_try_wait(bar, parity)) return true;
-    if (i % 64 == 63) {
-      if (!t0) t0 = globaltimer_ns();
-      else if (globaltimer_ns() - t0 > WAIT_NS) return false;
-    }
-  }
+  return false;
 }
 
 // Descriptors of 128-byte-swizzled operands: rows along K (a tile's channels), or rows along the other
@@ -239,13 +240,12 @@ template <int D, Mode MODE, bool BACK, bool FINE> struct WalkShape : Shape<D> {
   static constexpr uint32_t SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   // scores and weights; what the state gives; what the weights give; the chunk's part of the state
   static constexpr uint32_t T_A = 0, T_O1 = 128, T_O2 = 128 + D, T_Z = 128 + 2 * D;
-  static constexpr int VALUE_WARPS = MODE == OUTPUTS ? 4 : 8;
 };
 
-constexpr int WALK_THREADS = 896;
+constexpr int WALK_THREADS = 768;
 // The launch's registers, split anew by warpgroup (in every mode: one group waits for what others give back).
-constexpr int LAUNCH_REGS = 72, STATE_REGS = 160, WEIGHT_REGS = 56, VALUE_REGS = 48, OUTPUT_REGS = 64, OTHER_REGS = 56;
-static_assert(4 * STATE_REGS + 8 * WEIGHT_REGS + 4 * VALUE_REGS + 8 * OUTPUT_REGS + 4 * OTHER_REGS <= 28 * LAUNCH_REGS, "registers");
+constexpr int LAUNCH_REGS = 80, STATE_REGS = 152, WEIGHT_REGS = 72, OUTPUT_REGS = 72, OTHER_REGS = 40;
+static_assert(4 * STATE_REGS + 8 * WEIGHT_REGS + 8 * OUTPUT_REGS + 4 * OTHER_REGS <= 24 * LAUNCH_REGS, "registers");
 
 // The tiles of a chunk's inputs.  Where there are queries: the next chunk's keys and queries are already on
 // their way; its values take the place of this one's keys, and the keys and queries of the chunk after it
@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < 5; ++i) mbar_init(full + i, 1);
     mbar_init(s_ready, 4);
-    mbar_init(v_ready, W::VALUE_WARPS);
-    mbar_init(l_ready, W::VALUE_WARPS);
+    mbar_init(v_ready, 8);
+    mbar_init(l_ready, 8);
     mbar_init(p_ready, 8);
     mbar_init(f_ready, 4);
     mbar_init(z_free, 4);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
       mbar_init(f_done + i, 1);
       mbar_init(o_done + i, 8);
       mbar_init(g_ready + i, 1);
-      mbar_init(g_free + i, MODE == ENDS ? 8 : MODE == IMAGES ? 12 : 24);
+      mbar_init(g_free + i, MODE == ENDS ? 8 : MODE == IMAGES ? 12 : 20);
     }
     mbar_fence_init();
     for (int i = 0; i < 3; ++i) s_bad[i] = 0;
@@ -343,135 +343,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
   const int quarter = warp & 3;
   const uint32_t my = tb + ((uint32_t)(32 * quarter) << 16);
   bool ok = true;
-
-  // ---- V' of chunk c from the values' tile, by W::VALUE_WARPS warps: a thread has a token and, where there
-  // are eight warps, half of its channels.  The weight is two bf16 numbers, w1 + w2: the first number of v w is
-  // v w1 rounded, what that leaves of v w1 is exact, and v w2 is added to it (16 bits together).
-  auto form_values = [&]() {
-    constexpr int PIECES = D / 8 / (W::VALUE_WARPS / 4);  // of 16 bytes, to a thread
-    const int part = W::VALUE_WARPS == 8 ? warp >> 2 & 1 : 0, trow = 32 * quarter + lane;
-    const uint32_t sw = (uint32_t)(trow & 7);
-    auto piece = [&](int i) {
-      const int x = part * PIECES + i;
-      return (uint32_t)(x / 8) * W::BLOCK + trow * 128 + (((uint32_t)(x % 8) ^ sw) << 4);
-    };
-    const float gain = BACK ? p.scale : 1.f;
-    const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-    float reach = 0.f;  // ENDS: log2 of the decay from the chunk to the segment's end (start)
-    Tiles<MODE> t;
-    for (int c = 0; c < nch && ok; ++c) {
-      const uint32_t par = c & 1;
-      const int rows = rows_of(chunk_of(c));
-      const uint32_t v_at = sb + t.v * W::TILE, k_at = sb + t.k * W::TILE;
-      if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
-      const float g_mine = -s_g[par * 128 + trow], end = -s_g[par * 128 + 127];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(g_free + par);
-      if (MODE == OUTPUTS) {
-        if (c > 1 && !(ok = wait_for(o_done + par, (c >> 1 & 1) ^ 1))) break;
-        s_first[(c + 1) % 3 * 128 + trow] = 0x7fffffff;
-        if (trow == 0) s_bad[(c + 1) % 3] = 0;
-      }
-      const bool real = trow < rows;
-      const float weight = gain * ex2(MODE == ENDS ? reach + (BACK ? g_mine : end - g_mine) : BACK ? g_mine : end - g_mine);
-      const __nv_bfloat162 w1 = __float2bfloat162_rn(weight), w2 = __float2bfloat162_rn(weight - __low2float(w1));
-      if constexpr (MODE == ENDS) reach += end;
-      if (!(ok = wait_for(full + t.v, t.phase >> t.v & 1))) break;
-      const bool tail = rows < CHUNK;
-      if (tail && !(ok = wait_for(full + t.k, t.phase >> t.k & 1))) break;
-      if (c > 0 && !(ok = wait_for(z_done + (par ^ 1), c - 1 >> 1 & 1))) break;
-      __nv_bfloat162 odd = zero;
-#pragma unroll
-      for (int i = 0; i < PIECES; i += 4) {
-        uint32_t u[4][4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) lds_v4(v_at + piece(i + z), u[z]);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          uint32_t y[4], rest[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 x = as_bf16x2(u[z][j]), first = __hmul2_rn(x, w1);
-            if (MODE == OUTPUTS) odd = __hfma2(x, zero, odd);  // NaN if one of them is not finite
-            y[j] = real ? as_u32(first) : 0u;
-            if constexpr (MODE != OUTPUTS) rest[j] = real ? as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(first)))) : 0u;
-          }
-          st_shared_v4(sb + W::X + piece(i + z), y[0], y[1], y[2], y[3]);
-          if constexpr (MODE != OUTPUTS) st_shared_v4(sb + W::Y + piece(i + z), rest[0], rest[1], rest[2], rest[3]);
-        }
-      }
-      if (!real) {  // rows of other sequences
-        for (int i = 0; i < PIECES; ++i) {
-          st_shared_v4(v_at + piece(i), 0u, 0u, 0u, 0u);
-          st_shared_v4(k_at + piece(i), 0u, 0u, 0u, 0u);
-        }
-      } else if (MODE == OUTPUTS && !__hbeq2(odd, zero)) {
-        // such a value is taken out of the product with the weights, where zeros would meet it
-        for (int i = 0; i < PIECES; ++i) {
-          uint32_t u[4];
-          lds_v4(v_at + piece(i), u);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int ch = 8 * (part * PIECES + i) + 2 * j;
-            if ((u[j] & 0x7f80u) == 0x7f80u) {
-              u[j] &= 0xffff0000u;
-              atomicMin(s_first + c % 3 * 128 + ch, trow);
-            }
-            if ((u[j] & 0x7f800000u) == 0x7f800000u) {
-              u[j] &= 0xffffu;
-              atomicMin(s_first + c % 3 * 128 + ch + 1, trow);
-            }
-          }
-          st_shared_v4(v_at + piece(i), u[0], u[1], u[2], u[3]);
-        }
-        s_bad[c % 3] = 1;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(v_ready);
-      if (MODE == OUTPUTS && exact) {  // the second numbers take the place of the first ones
-        if (!(ok = wait_for(zh_done, par))) break;
-#pragma unroll
-        for (int i = 0; i < PIECES; i += 4) {
-          uint32_t u[4][4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) lds_v4(v_at + piece(i + z), u[z]);
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 x = as_bf16x2(u[z][j]);
-              u[z][j] = real ? as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(__hmul2_rn(x, w1))))) : 0u;
-            }
-            st_shared_v4(sb + W::X + piece(i + z), u[z][0], u[z][1], u[z][2], u[z][3]);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(l_ready);
-      }
-      t.next(c);
-    }
-    if constexpr (MODE == ENDS) {  // the segment's contribution
-      if (ok && nch > 0) ok = wait_for(z_done + ((nch - 1) & 1), nch - 1 >> 1 & 1);
-      if (ok) {
-        tc_fence_after_sync();
-        const int srow = D == 128 ? 32 * quarter + lane : 16 * quarter + (lane & 15);
-        float* to = w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)srow * D + part * (D / 2);
-#pragma unroll
-        for (int b = 0; b < D / 2; b += 16) {
-          float s[16];
-          tmem_ld16(my + W::T_Z + part * (D / 2) + b, s);
-          tmem_ld_wait();
-          if (D == 128 || lane < 16) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(to + b + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
-          }
-        }
-        if (part == 0 && trow == 0) w.decay[(size_t)slot * p.H + h] = reach;
-      }
-    }
-  };
 
   if (warp < 4) {
     // ---------------------------------------------------------------- the state: a lane has one of its rows
@@ -559,57 +430,189 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
       }
     }
   } else if (warp < 12) {
-    // ---------------------------------------------------------------- the weights, in place of the scores
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(WEIGHT_REGS));
+    // a thread has a token and half of the channels of V', half of the tokens before it of P
+    const int half = warp >> 2 & 1, trow = 32 * quarter + lane;
+    constexpr int PIECES = D / 16;  // of 16 bytes, of V'
+    auto piece = [&](int i) {
+      const int x = half * PIECES + i;
+      return (uint32_t)(x / 8) * W::BLOCK + trow * 128 + (((uint32_t)(x % 8) ^ (uint32_t)(trow & 7)) << 4);
+    };
+    float reach = 0.f;  // ENDS: log2 of the decay from the chunk to the segment's end (start)
+    Tiles<MODE> t;
+
+    // ---------------------------------------------------------------- the weighted values
+    // The weight is two bf16 numbers, w1 + w2: the first number of v w is v w1 rounded, what that leaves of
+    // v w1 is exact, and v w2 is added to it (16 bits together).
+    auto values = [&](int c) {
+      const uint32_t par = c & 1;
+      const int rows = rows_of(chunk_of(c));
+      const uint32_t v_at = sb + t.v * W::TILE, k_at = sb + t.k * W::TILE;
+      if (!wait_for(g_ready + par, c >> 1 & 1)) return false;
+      const float g_mine = -s_g[par * 128 + trow], end = -s_g[par * 128 + 127];
+      if (MODE == OUTPUTS) {
+        if (c > 1 && !wait_for(o_done + par, (c >> 1 & 1) ^ 1)) return false;
+        if (half == 0) s_first[(c + 1) % 3 * 128 + trow] = 0x7fffffff;
+        if (half == 0 && trow == 0) s_bad[(c + 1) % 3] = 0;
+      } else {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(g_free + par);
+      }
+      const bool real = trow < rows;
+      const float gain = BACK ? p.scale : 1.f;
+      const float weight = gain * ex2(MODE == ENDS ? reach + (BACK ? g_mine : end - g_mine) : BACK ? g_mine : end - g_mine);
+      const __nv_bfloat162 w1 = __float2bfloat162_rn(weight), w2 = __float2bfloat162_rn(weight - __low2float(w1));
+      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+      if constexpr (MODE == ENDS) reach += end;
+      if (!wait_for(full + t.v, t.phase >> t.v & 1)) return false;
+      if (rows < CHUNK && !wait_for(full + t.k, t.phase >> t.k & 1)) return false;
+      if (c > 0 && !wait_for(z_done + (par ^ 1), c - 1 >> 1 & 1)) return false;
+      __nv_bfloat162 odd = zero;
+#pragma unroll 1
+      for (int i = 0; i < PIECES; i += 4) {
+        uint32_t u[4][4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) lds_v4(v_at + piece(i + z), u[z]);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          uint32_t y[4], rest[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 x = as_bf16x2(u[z][j]), first = __hmul2_rn(x, w1);
+            if (MODE == OUTPUTS) odd = __hfma2(x, zero, odd);  // NaN if one of them is not finite
+            y[j] = real ? as_u32(first) : 0u;
+            if constexpr (MODE != OUTPUTS) rest[j] = real ? as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(first)))) : 0u;
+          }
+          st_shared_v4(sb + W::X + piece(i + z), y[0], y[1], y[2], y[3]);
+          if constexpr (MODE != OUTPUTS) st_shared_v4(sb + W::Y + piece(i + z), rest[0], rest[1], rest[2], rest[3]);
+        }
+      }
+      if (!real) {  // rows of other sequences
+#pragma unroll 1
+        for (int i = 0; i < PIECES; ++i) {
+          st_shared_v4(v_at + piece(i), 0u, 0u, 0u, 0u);
+          st_shared_v4(k_at + piece(i), 0u, 0u, 0u, 0u);
+        }
+      } else if (MODE == OUTPUTS && !__hbeq2(odd, zero)) {
+        // such a value is taken out of the product with the weights, where zeros would meet it
+#pragma unroll 1
+        for (int i = 0; i < PIECES; ++i) {
+          uint32_t u[4];
+          lds_v4(v_at + piece(i), u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int ch = 8 * (half * PIECES + i) + 2 * j;
+            if ((u[j] & 0x7f80u) == 0x7f80u) {
+              u[j] &= 0xffff0000u;
+              atomicMin(s_first + c % 3 * 128 + ch, trow);
+            }
+            if ((u[j] & 0x7f800000u) == 0x7f800000u) {
+              u[j] &= 0xffffu;
+              atomicMin(s_first + c % 3 * 128 + ch + 1, trow);
+            }
+          }
+          st_shared_v4(v_at + piece(i), u[0], u[1], u[2], u[3]);
+        }
+        s_bad[c % 3] = 1;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_ready);
+      if (MODE == OUTPUTS && exact) {  // the second numbers take the place of the first ones
+        if (!wait_for(zh_done, par)) return false;
+#pragma unroll 1
+        for (int i = 0; i < PIECES; i += 4) {
+          uint32_t u[4][4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) lds_v4(v_at + piece(i + z), u[z]);
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 x = as_bf16x2(u[z][j]);
+              u[z][j] = real ? as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(__hmul2_rn(x, w1))))) : 0u;
+            }
+            st_shared_v4(sb + W::X + piece(i + z), u[z][0], u[z][1], u[z][2], u[z][3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(l_ready);
+      }
+      t.next(c);
+      return true;
+    };
+
     if constexpr (MODE != OUTPUTS) {
-      form_values();
+      for (int c = 0; c < nch && ok; ++c) ok = values(c);
+      if constexpr (MODE == ENDS) {  // the segment's contribution
+        if (ok && nch > 0) ok = wait_for(z_done + ((nch - 1) & 1), nch - 1 >> 1 & 1);
+        if (ok) {
+          tc_fence_after_sync();
+          const int srow = D == 128 ? trow : 16 * quarter + (lane & 15);
+          float* to = w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)srow * D + half * (D / 2);
+#pragma unroll
+          for (int b = 0; b < D / 2; b += 16) {
+            float s[16];
+            tmem_ld16(my + W::T_Z + half * (D / 2) + b, s);
+            tmem_ld_wait();
+            if (D == 128 || lane < 16) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(to + b + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+            }
+          }
+          if (half == 0 && trow == 0) w.decay[(size_t)slot * p.H + h] = reach;
+        }
+      }
     } else {
-      const int half = warp >> 2 & 1, trow = 32 * quarter + lane;
+      if (nch > 0) ok = values(0);
       for (int c = 0; c < nch && ok; ++c) {
+        // -------------------------------------------------------------- the weights, in place of the scores
         const uint32_t par = c & 1;
         const float* minus_g = s_g + par * 128;
-        if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
         const float g_mine = -minus_g[trow];
         if (!(ok = wait_for(a_done, par))) break;
         tc_fence_after_sync();
-        uint32_t u[32], rest[FINE ? 32 : 1];
+        // 16 columns at a time; a piece's place is that of scores already read (FINE: its second numbers', 32
+        // columns on, is not, so they wait)
+        const uint32_t at = my + W::T_A + 64 * half;
+        uint32_t held[FINE ? 32 : 1];
+#pragma unroll(FINE ? 4 : 1)
+        for (int b = 0; b < 4; ++b) {
+          const int j0 = 64 * half + 16 * b;
+          uint32_t u[8], rest[8];
 #pragma unroll
-        for (int b = 0; b < 64; b += 16) {
-          const int j0 = 64 * half + b;
+          for (int j = 0; j < 8; ++j) u[j] = rest[j] = 0u;
           if (j0 <= 32 * quarter + 31) {
-            float a[16];
-            tmem_ld16(my + W::T_A + j0, a);
+            float x[16];
+            tmem_ld16(at + 16 * b, x);
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
               const uint64_t to = add2(pair(g_mine, g_mine), *reinterpret_cast<const uint64_t*>(minus_g + j0 + j));
-              float x, y;
-              unpair(to, &x, &y);
-              unpair(mul2(pair(a[j], a[j + 1]), pair(ex2(x), ex2(y))), &a[j], &a[j + 1]);
+              float y, z;
+              unpair(to, &y, &z);
+              unpair(mul2(pair(x[j], x[j + 1]), pair(ex2(y), ex2(z))), &x[j], &x[j + 1]);
             }
             if (j0 + 15 > 32 * quarter) {  // what comes after some of the warp's tokens
 #pragma unroll
-              for (int j = 0; j < 16; ++j) a[j] = j0 + j <= trow ? a[j] : 0.f;
+              for (int j = 0; j < 16; ++j) x[j] = j0 + j <= trow ? x[j] : 0.f;
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              if constexpr (FINE) u[b / 2 + j] = split_bf16x2(a[2 * j], a[2 * j + 1], &rest[b / 2 + j]);
-              else u[b / 2 + j] = pack_bf16x2(a[2 * j], a[2 * j + 1]);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              u[b / 2 + j] = 0u;
-              if constexpr (FINE) rest[b / 2 + j] = 0u;
+              if constexpr (FINE) u[j] = split_bf16x2(x[2 * j], x[2 * j + 1], &rest[j]);
+              else u[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
             }
           }
+          tmem_st8u(at + 8 * b, u);
+          if constexpr (FINE) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) held[8 * b + j] = rest[j];
+          }
         }
-        // (a half's pieces lie where its own scores were, all of which it has read)
-        tmem_st16u(my + W::T_A + 64 * half, u);
-        tmem_st16u(my + W::T_A + 64 * half + 16, u + 16);
         if constexpr (FINE) {
-          tmem_st16u(my + W::T_A + 64 * half + 32, rest);
-          tmem_st16u(my + W::T_A + 64 * half + 48, rest + 16);
+          tmem_st16u(at + 32, held);
+          tmem_st16u(at + 48, held + 16);
         }
         tmem_st_wait();
         tc_fence_before_sync();
@@ -618,12 +621,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
           mbar_arrive(p_ready);
           mbar_arrive(g_free + par);
         }
+        if (c + 1 < nch) ok = values(c + 1);
       }
     }
-  } else if (warp < 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(VALUE_REGS));
-    if constexpr (MODE == OUTPUTS) form_values();
-  } else if (warp < 24) {
+  } else if (warp < 20) {
     // ---------------------------------------------------------------- the outputs: 32 rows and 128 bytes
     // (d = 64: 64) of each at a time, turned in this warp's part of the values' tile so that 8 lanes write a
     // row's piece
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
       for (int c = 0; c < nch && ok; ++c) {
         const uint32_t par = c & 1;
         const int rows = rows_of(chunk_of(c));
-        const uint32_t turn = sb + t.v * W::TILE + (warp - 16) * (W::TILE / 8);
+        const uint32_t turn = sb + t.v * W::TILE + (warp - 12) * (W::TILE / 8);
         if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
         const float lead = p.scale * ex2(-s_g[par * 128 + trow]);
         __syncwarp();
@@ -645,61 +646,80 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
         tc_fence_after_sync();
         const bool bad = s_bad[c % 3] != 0;
         uint8_t* to = static_cast<uint8_t*>(p.out) + (size_t)(row0 + chunk_of(c) * CHUNK + 32 * quarter) * row_bytes + (h * D + half * SC) * ES;
-#pragma unroll
+        const uint32_t my_row = turn + lane * (LANES * 16), my_turn = (lane * LANES / 8 % LANES) << 4;
+#pragma unroll 1
         for (int b = 0; b < SC; b += TURN) {
-          uint32_t o[TURN * ES / 4];
-#pragma unroll
-          for (int z = 0; z < TURN; z += 8) {
-            float x[8], y[8];
-            tmem_ld8(my + W::T_O1 + half * SC + b + z, x);
-            tmem_ld8(my + W::T_O2 + half * SC + b + z, y);
+          constexpr int COLS = 16 / ES;  // to a piece of 16 bytes
+#pragma unroll 1
+          for (int z = 0; z < LANES; z += 2) {
+            float x[2][8], y[2][8];
+            uint32_t u[2][4];
+            const uint32_t at = my + half * SC + b + z * COLS;
+            tmem_ld8(at + W::T_O1, x[0]);
+            tmem_ld8(at + W::T_O2, y[0]);
+            if constexpr (!FINE) {
+              tmem_ld8(at + W::T_O1 + 8, x[1]);
+              tmem_ld8(at + W::T_O2 + 8, y[1]);
+            }
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; i += 2)
-              unpair(fma2(pair(lead, lead), pair(x[i], x[i + 1]), mul2(pair(p.scale, p.scale), pair(y[i], y[i + 1]))), &y[i], &y[i + 1]);
-            if (bad) {
+            for (int i = 0; i < (FINE ? 1 : 2); ++i)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (s_first[c % 3 * 128 + half * SC + b + z + i] <= trow) y[i] = NAN;
-            }
+              for (int j = 0; j < 8; j += 2) {
+                float m, n;
+                unpair(fma2(pair(lead, lead), pair(x[i][j], x[i][j + 1]), mul2(pair(p.scale, p.scale), pair(y[i][j], y[i][j + 1]))), &m, &n);
+                if constexpr (FINE) {
+                  u[j / 4][j % 4] = __float_as_uint(m);
+                  u[j / 4][j % 4 + 1] = __float_as_uint(n);
+                } else {
+                  u[i][j / 2] = pack_bf16x2(m, n);
+                }
+              }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if constexpr (FINE) o[z + i] = __float_as_uint(y[i]);
-              else if (i % 2) o[(z + i) / 2] = pack_bf16x2(y[i - 1], y[i]);
-            }
+            for (int i = 0; i < 2; ++i) st_shared_v4(my_row + (((z + i) << 4) ^ my_turn), u[i][0], u[i][1], u[i][2], u[i][3]);
+          }
+          if (bad) {  // in place, column by column
+#pragma unroll 1
+            for (int i = 0; i < TURN; ++i)
+              if (s_first[c % 3 * 128 + half * SC + b + i] <= trow) {
+                const uint32_t at = my_row + (((i * ES >> 4) << 4) ^ my_turn) + (i * ES & 15);
+                if (FINE) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(0x7fffffffu) : "memory");
+                else st_shared_u16(at, 0x7fff);
+              }
           }
           if (b + TURN == SC) {
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(o_read);
-          } else if (b) {
+          } else {
             __syncwarp();
           }
-#pragma unroll
-          for (int i = 0; i < LANES; ++i)
-            st_shared_v4(turn + lane * (LANES * 16) + ((i ^ (lane * LANES / 8 % LANES)) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          __syncwarp();
+          uint32_t o[LANES][4];
 #pragma unroll
           for (int i = 0; i < LANES; ++i) {
             const int r = i * (32 / LANES) + lane / LANES, at = lane % LANES;
-            lds_v4(turn + r * (LANES * 16) + ((at ^ (r * LANES / 8 % LANES)) << 4), *reinterpret_cast<uint32_t(*)[4]>(o + 4 * i));
+            lds_v4(turn + r * (LANES * 16) + ((at ^ (r * LANES / 8 % LANES)) << 4), o[i]);
+          }
+          if (b + TURN == SC) {
+            fence_proxy_async_smem();  // the tile's next content comes by TMA
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_done + par);
+          } else {
+            __syncwarp();
           }
 #pragma unroll
           for (int i = 0; i < LANES; ++i) {
             const int r = i * (32 / LANES) + lane / LANES, at = lane % LANES;
             if (32 * quarter + r < rows)
-              *reinterpret_cast<uint4*>(to + r * row_bytes + b * ES + at * 16) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              *reinterpret_cast<uint4*>(to + r * row_bytes + b * ES + at * 16) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
           }
         }
-        fence_proxy_async_smem();  // the tile's next content comes by TMA
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_done + par);
         t.next(c);
       }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-    if (warp == 24 && lane == 0) {
+    if (warp == 20 && lane == 0) {
       // -------------------------------------------------------------- loads
       auto load = [&](const CUtensorMap* map, int tile, int c) {
         mbar_arrive_expect_tx(full + tile, W::TILE);
@@ -740,32 +760,37 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
         const bool any = MODE == OUTPUTS ? nch > (i < 3 ? 0 : 1) : nch > (i & 1);
         if (any) ok = wait_for(full + i, (loads >> i & 1) ^ 1) && ok;
       }
-    } else if (warp == 25 && lane == 0) {
+    } else if (warp == 21 && lane == 0) {
       // -------------------------------------------------------------- products
       constexpr uint32_t ID_A = make_idesc_bf16(128, 128, false, false), ID_O = make_idesc_bf16(128, D, false, true),
                          ID_Z = make_idesc_bf16(D, D, true, true);
       Tiles<MODE> t;
-      auto state_part = [&](uint32_t k_at, uint32_t v_at, bool add) {
-        const uint64_t a = desc_mn(k_at, W::BLOCK), b = desc_mn(v_at, W::BLOCK);
+      // D = (D +) A B over K = 64 n; descriptors advance by `in` for each 16 of K and `out` for each 64
+      constexpr uint32_t K_IN = 2, K_OUT = W::BLOCK >> 4, MN_IN = 128, MN_OUT = 512;
+      auto product = [&](uint32_t to, uint64_t a, uint32_t a_in, uint32_t a_out, uint64_t b, uint32_t b_in, uint32_t b_out, uint32_t id,
+                         int n, uint32_t add) {
+#pragma unroll 1
+        for (int o = 0; o < n; ++o)
 #pragma unroll
-        for (int i = 0; i < 128; i += 16) umma_bf16(tb + W::T_Z, desc_adv(a, i, true), desc_adv(b, i, true), ID_Z, add || i ? 1u : 0u);
+          for (int i = 0; i < 4; ++i) {
+            umma_bf16(to, a + o * a_out + i * a_in, b + o * b_out + i * b_in, id, add);
+            add = 1;
+          }
+      };
+      auto state_part = [&](uint32_t k_at, uint32_t v_at, bool add) {
+        product(tb + W::T_Z, desc_mn(k_at, W::BLOCK), MN_IN, MN_OUT, desc_mn(v_at, W::BLOCK), MN_IN, MN_OUT, ID_Z, 2, add);
       };
       auto from_state = [&](uint32_t q_at, bool add) {
-        const uint64_t a = desc_k(q_at), b = desc_mn(sb + W::Y, W::IMAGE_BLOCK);
-#pragma unroll
-        for (int i = 0; i < D; i += 16)
-          umma_bf16(tb + W::T_O1, desc_adv(a, i, false, W::BLOCK), desc_adv(b, i, true), ID_O, add || i ? 1u : 0u);
+        product(tb + W::T_O1, desc_k(q_at), K_IN, K_OUT, desc_mn(sb + W::Y, W::IMAGE_BLOCK), MN_IN, MN_OUT, ID_O, D / 64, add);
       };
+#pragma unroll 1
       for (int c = 0; c < nch && ok; ++c) {
         const uint32_t par = c & 1;
         const uint32_t k_at = sb + t.k * W::TILE, v_at = sb + t.v * W::TILE, q_at = sb + t.q * W::TILE;
         if (!(ok = wait_for(full + t.k, t.phase >> t.k & 1))) break;
         if constexpr (MODE == OUTPUTS) {
           if (!(ok = wait_for(full + t.q, t.phase >> t.q & 1))) break;
-          const uint64_t a = desc_k(q_at), b = desc_k(k_at);
-#pragma unroll
-          for (int i = 0; i < D; i += 16)
-            umma_bf16(tb + W::T_A, desc_adv(a, i, false, W::BLOCK), desc_adv(b, i, false, W::BLOCK), ID_A, i ? 1u : 0u);
+          product(tb + W::T_A, desc_k(q_at), K_IN, K_OUT, desc_k(k_at), K_IN, K_OUT, ID_A, D / 64, 0);
           umma_commit(a_done);
         }
         if (!(ok = wait_for(v_ready, par))) break;
@@ -792,12 +817,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
           if (!(ok = wait_for(p_ready, par))) break;
           tc_fence_after_sync();
           const uint64_t b = desc_mn(v_at, W::BLOCK);
+#pragma unroll 1
+          for (int o = 0; o < (FINE ? 4 : 2); ++o)
 #pragma unroll
-          for (int x = 0; x <= (FINE ? 1 : 0); ++x)
-#pragma unroll
-            for (int i = 0; i < 128; i += 16)
-              umma_f16_ta(tb + W::T_O2, tb + W::T_A + (i >= 64 ? 64 : 0) + (i % 64) / 2 + 32 * x, desc_adv(b, i, true), ID_O,
-                          x || i ? 1u : 0u);
+            for (int i = 0; i < 4; ++i)
+              umma_f16_ta(tb + W::T_O2, tb + W::T_A + 64 * (o & 1) + 16 * (o & 2) + 8 * i, b + (o & 1) * MN_OUT + i * MN_IN, ID_O, o || i ? 1u : 0u);
           umma_commit(pv_done);
         } else {
           state_part(k_at, sb + W::Y, true);
@@ -811,7 +835,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
         (void)wait_for(pv_done, 0);
         (void)wait_for(pv_done, 1);
       }
-    } else if (warp == 26) {
+    } else if (warp == 22) {
       // -------------------------------------------------------------- decays
       Decays la;
       if (nch > 0) la.load(p, row0 + chunk_of(0) * CHUNK, rows_of(chunk_of(0)), h);
