@@ -30,8 +30,8 @@
 // IMAGES leaves each chunk's entering state in memory, as the bf16 operand
 // image that the gradient kernel copies into its shared memory.
 //
-// Warps: 0-3 keep the state, 4-11 form V' and turn scores into weights, 12-19
-// write the outputs, 20 loads, 21 issues, 22 sums up the decays (a token's lie a row apart: 32 sectors to a load, too many
+// Warps: 0-3 keep the state, 4-11 turn scores into weights, 12-19 form V',
+// 20-27 write the outputs, 28 loads, 29 issues, 30 sums up the decays (a token's lie a row apart: 32 sectors to a load, too many
 // for every warp to read them by itself, which held up all others).  They meet
 // at mbarriers only, with bounded waits.  Shared memory holds seven tiles: V',
 // the operand S, and five for the inputs, which follow one another into
@@ -242,10 +242,10 @@ template <int D, Mode MODE, bool BACK, bool FINE> struct WalkShape : Shape<D> {
   static constexpr uint32_t T_A = 0, T_O1 = 128, T_O2 = 128 + D, T_Z = 128 + 2 * D;
 };
 
-constexpr int WALK_THREADS = 768;
+constexpr int WALK_THREADS = 1024;
 // The launch's registers, split anew by warpgroup (in every mode: one group waits for what others give back).
-constexpr int LAUNCH_REGS = 80, STATE_REGS = 152, WEIGHT_REGS = 72, OUTPUT_REGS = 72, OTHER_REGS = 40;
-static_assert(4 * STATE_REGS + 8 * WEIGHT_REGS + 8 * OUTPUT_REGS + 4 * OTHER_REGS <= 24 * LAUNCH_REGS, "registers");
+constexpr int LAUNCH_REGS = 64, STATE_REGS = 152, WEIGHT_REGS = 56, VALUE_REGS = 48, OUTPUT_REGS = 56, OTHER_REGS = 40;
+static_assert(4 * STATE_REGS + 8 * (WEIGHT_REGS + VALUE_REGS + OUTPUT_REGS) + 4 * OTHER_REGS <= 32 * LAUNCH_REGS, "registers");
 
 // The tiles of a chunk's inputs.  Where there are queries: the next chunk's keys and queries are already on
 // their way; its values take the place of this one's keys, and the keys and queries of the chunk after it
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
       mbar_init(f_done + i, 1);
       mbar_init(o_done + i, 8);
       mbar_init(g_ready + i, 1);
-      mbar_init(g_free + i, MODE == ENDS ? 8 : MODE == IMAGES ? 12 : 20);
+      mbar_init(g_free + i, MODE == ENDS ? 8 : MODE == IMAGES ? 12 : 28);
     }
     mbar_fence_init();
     for (int i = 0; i < 3; ++i) s_bad[i] = 0;
@@ -431,9 +431,71 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
     }
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(WEIGHT_REGS));
-    // a thread has a token and half of the channels of V', half of the tokens before it of P
+    if constexpr (MODE == OUTPUTS) {
+      const int half = warp >> 2 & 1, trow = 32 * quarter + lane;
+      for (int c = 0; c < nch && ok; ++c) {
+        // -------------------------------------------------------------- the weights, in place of the scores
+        const uint32_t par = c & 1;
+        const float* minus_g = s_g + par * 128;
+        if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
+        const float g_mine = -minus_g[trow];
+        if (!(ok = wait_for(a_done, par))) break;
+        tc_fence_after_sync();
+        // 16 columns at a time; a piece's place is that of scores already read (FINE: its second numbers', 32
+        // columns on, is not, so they wait)
+        const uint32_t at = my + W::T_A + 64 * half;
+        uint32_t held[FINE ? 32 : 1];
+#pragma unroll(FINE ? 4 : 1)
+        for (int b = 0; b < 4; ++b) {
+          const int j0 = 64 * half + 16 * b;
+          uint32_t u[8], rest[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) u[j] = rest[j] = 0u;
+          if (j0 <= 32 * quarter + 31) {
+            float x[16];
+            tmem_ld16(at + 16 * b, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              const uint64_t to = add2(pair(g_mine, g_mine), *reinterpret_cast<const uint64_t*>(minus_g + j0 + j));
+              float y, z;
+              unpair(to, &y, &z);
+              unpair(mul2(pair(x[j], x[j + 1]), pair(ex2(y), ex2(z))), &x[j], &x[j + 1]);
+            }
+            if (j0 + 15 > 32 * quarter) {  // what comes after some of the warp's tokens
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = j0 + j <= trow ? x[j] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (FINE) u[j] = split_bf16x2(x[2 * j], x[2 * j + 1], &rest[j]);
+              else u[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+            }
+          }
+          tmem_st8u(at + 8 * b, u);
+          if constexpr (FINE) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) held[8 * b + j] = rest[j];
+          }
+        }
+        if constexpr (FINE) {
+          tmem_st16u(at + 32, held);
+          tmem_st16u(at + 48, held + 16);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(p_ready);
+          mbar_arrive(g_free + par);
+        }
+      }
+    }
+  } else if (warp < 20) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(VALUE_REGS));
+    // a thread has a token and half of its channels
     const int half = warp >> 2 & 1, trow = 32 * quarter + lane;
-    constexpr int PIECES = D / 16;  // of 16 bytes, of V'
+    constexpr int PIECES = D / 16;  // of 16 bytes, to a thread
     auto piece = [&](int i) {
       const int x = half * PIECES + i;
       return (uint32_t)(x / 8) * W::BLOCK + trow * 128 + (((uint32_t)(x % 8) ^ (uint32_t)(trow & 7)) << 4);
@@ -454,10 +516,9 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
         if (c > 1 && !wait_for(o_done + par, (c >> 1 & 1) ^ 1)) return false;
         if (half == 0) s_first[(c + 1) % 3 * 128 + trow] = 0x7fffffff;
         if (half == 0 && trow == 0) s_bad[(c + 1) % 3] = 0;
-      } else {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(g_free + par);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(g_free + par);
       const bool real = trow < rows;
       const float gain = BACK ? p.scale : 1.f;
       const float weight = gain * ex2(MODE == ENDS ? reach + (BACK ? g_mine : end - g_mine) : BACK ? g_mine : end - g_mine);
@@ -543,7 +604,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
       return true;
     };
 
-    if constexpr (MODE != OUTPUTS) {
+    {
+#pragma unroll 1
       for (int c = 0; c < nch && ok; ++c) ok = values(c);
       if constexpr (MODE == ENDS) {  // the segment's contribution
         if (ok && nch > 0) ok = wait_for(z_done + ((nch - 1) & 1), nch - 1 >> 1 & 1);
@@ -564,67 +626,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
           if (half == 0 && trow == 0) w.decay[(size_t)slot * p.H + h] = reach;
         }
       }
-    } else {
-      if (nch > 0) ok = values(0);
-      for (int c = 0; c < nch && ok; ++c) {
-        // -------------------------------------------------------------- the weights, in place of the scores
-        const uint32_t par = c & 1;
-        const float* minus_g = s_g + par * 128;
-        const float g_mine = -minus_g[trow];
-        if (!(ok = wait_for(a_done, par))) break;
-        tc_fence_after_sync();
-        // 16 columns at a time; a piece's place is that of scores already read (FINE: its second numbers', 32
-        // columns on, is not, so they wait)
-        const uint32_t at = my + W::T_A + 64 * half;
-        uint32_t held[FINE ? 32 : 1];
-#pragma unroll(FINE ? 4 : 1)
-        for (int b = 0; b < 4; ++b) {
-          const int j0 = 64 * half + 16 * b;
-          uint32_t u[8], rest[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) u[j] = rest[j] = 0u;
-          if (j0 <= 32 * quarter + 31) {
-            float x[16];
-            tmem_ld16(at + 16 * b, x);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const uint64_t to = add2(pair(g_mine, g_mine), *reinterpret_cast<const uint64_t*>(minus_g + j0 + j));
-              float y, z;
-              unpair(to, &y, &z);
-              unpair(mul2(pair(x[j], x[j + 1]), pair(ex2(y), ex2(z))), &x[j], &x[j + 1]);
-            }
-            if (j0 + 15 > 32 * quarter) {  // what comes after some of the warp's tokens
-#pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = j0 + j <= trow ? x[j] : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if constexpr (FINE) u[j] = split_bf16x2(x[2 * j], x[2 * j + 1], &rest[j]);
-              else u[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
-            }
-          }
-          tmem_st8u(at + 8 * b, u);
-          if constexpr (FINE) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) held[8 * b + j] = rest[j];
-          }
-        }
-        if constexpr (FINE) {
-          tmem_st16u(at + 32, held);
-          tmem_st16u(at + 48, held + 16);
-        }
-        tmem_st_wait();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(p_ready);
-          mbar_arrive(g_free + par);
-        }
-        if (c + 1 < nch) ok = values(c + 1);
-      }
     }
-  } else if (warp < 20) {
+  } else if (warp < 28) {
     // ---------------------------------------------------------------- the outputs: 32 rows and 128 bytes
     // (d = 64: 64) of each at a time, turned in this warp's part of the values' tile so that 8 lanes write a
     // row's piece
@@ -637,7 +640,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
       for (int c = 0; c < nch && ok; ++c) {
         const uint32_t par = c & 1;
         const int rows = rows_of(chunk_of(c));
-        const uint32_t turn = sb + t.v * W::TILE + (warp - 12) * (W::TILE / 8);
+        const uint32_t turn = sb + t.v * W::TILE + (warp - 20) * (W::TILE / 8);
         if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
         const float lead = p.scale * ex2(-s_g[par * 128 + trow]);
         __syncwarp();
@@ -719,7 +722,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
-    if (warp == 20 && lane == 0) {
+    if (warp == 28 && lane == 0) {
       // -------------------------------------------------------------- loads
       auto load = [&](const CUtensorMap* map, int tile, int c) {
         mbar_arrive_expect_tx(full + tile, W::TILE);
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
         const bool any = MODE == OUTPUTS ? nch > (i < 3 ? 0 : 1) : nch > (i & 1);
         if (any) ok = wait_for(full + i, (loads >> i & 1) ^ 1) && ok;
       }
-    } else if (warp == 21 && lane == 0) {
+    } else if (warp == 29 && lane == 0) {
       // -------------------------------------------------------------- products
       constexpr uint32_t ID_A = make_idesc_bf16(128, 128, false, false), ID_O = make_idesc_bf16(128, D, false, true),
                          ID_Z = make_idesc_bf16(D, D, true, true);
@@ -835,7 +838,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
         (void)wait_for(pv_done, 0);
         (void)wait_for(pv_done, 1);
       }
-    } else if (warp == 22) {
+    } else if (warp == 30) {
       // -------------------------------------------------------------- decays
       Decays la;
       if (nch > 0) la.load(p, row0 + chunk_of(0) * CHUNK, rows_of(chunk_of(0)), h);
