@@ -7,15 +7,17 @@
 // One pass: a row's entries are read once, wait in registers for the row's
 // maximum and sum, and are written once as probabilities, so HBM bounds it
 // (2 x 4 bytes an entry in fp32).  A cluster of up to 8 CTAs takes the rows of
-// a request; CTA c holds entries [c slice, (c + 1) slice) of each.  Each CTA
+// a request; CTA c holds entries [c slice, (c + 1) slice) of each.  Each warp
 // takes its exponentials against its own maximum and leaves (maximum, sum) in
-// every other CTA's shared memory: one cluster barrier a row.
+// every CTA's shared memory: one cluster barrier a row, and no other.
 //
 // What has been said is counted once for a request, in shared memory, one
 // 32-bit word an entry of the slice: 2 * (how often in the reply) + (whether
 // in the prompt).  The counts are whole numbers, so the order of the adding
 // does not matter; a request's biases are kept in their order.  A row's
 // drafts are added as the rows go by.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +32,7 @@ constexpr int PER = 32;      // entries a thread holds
 constexpr int LIST = 1024;   // biases held at a time
 constexpr float LOG2E = 1.4426950408889634f;
 
-struct Part { float top, sum; int at; };  // of a slice: the largest entry, the sum against it, its lowest index
+struct __align__(16) Part { float top, sum; int at, unused; };  // of some entries: the largest, the sum against it, its lowest index
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
   namespace cg = cooperative_groups;
   constexpr int E = VEC ? Vec<T>::E : 1, TILE = THREADS * PER, WARPS = THREADS / 32;
   extern __shared__ __align__(16) uint32_t s_said[];  // [slice], only where something is counted
-  __shared__ Part s_warp[WARPS], s_parts[2][MOST];
+  __shared__ Part s_parts[2][MOST * WARPS];
   __shared__ int s_id[LIST];
   __shared__ float s_bias[LIST];
   __shared__ int s_listed, s_more;
@@ -116,7 +118,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
   const float repetition = u.repetition ? u.repetition[n] : 1.f, presence = u.presence ? u.presence[n] : 0.f;
   const float frequency = u.frequency ? u.frequency[n] : 0.f, temperature = u.temperature ? u.temperature[n] : 1.f;
   const bool greedy = !(temperature > 0.f);
-  const float factor = greedy ? 0.f : LOG2E / temperature;
+  // (finite and not 0: the largest entry's 0 times it is 0, a masked one's -infinity stays)
+  const float factor = greedy ? 1.f : fmaxf(fminf(LOG2E / temperature, 1e37f), 1e-37f), one_over_repetition = 1.f / repetition;
   // the biases of this slice in their order, as many as the list holds; the rest is looked up in memory
   if (warp == 0) {
     int have = 0, j0 = 0;
@@ -148,28 +151,53 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
       if (i == mine) x[i] += b;
   };
   // the entries of the tile that starts at `from`, with everything but the temperature; those that are
-  // masked or past the end are -infinity
+  // masked or past the end are -infinity.  (Addresses past the end are those of the last entries instead, so
+  // that no load waits for another.)
   auto load = [&](float (&x)[PER], int r, int from) {
     const T* row = static_cast<const T*>(p.logits) + n * p.stride_n + r * p.stride_r;
+    const int last = max(hi, E) - E;
+    // the 32 words that cover the warp's entries, one to a lane: E of them for each of its PER / E vectors
+    uint32_t bits = 0;
+    if (u.mask) {
+      const int word = ((from + (lane / E * THREADS + warp * 32) * E) >> 5) + lane % E;
+      bits = (u.mask + n * u.mask_stride_n + r * u.mask_stride_r)[min(word, (p.V - 1) >> 5)];
+    }
+    if constexpr (VEC) {
+      uint4 raw[PER / E];
 #pragma unroll
-    for (int i = 0; i < PER; i += E) {
-      const int at = from + (i / E * THREADS + tid) * E;
-      if (at < hi) {
-        if constexpr (VEC) unpack<T>(*reinterpret_cast<const uint4*>(row + at), x + i);
-        else x[i] = to_f32(row[at]);
-      } else {
+      for (int i = 0; i < PER / E; ++i) raw[i] = *reinterpret_cast<const uint4*>(row + min(from + (i * THREADS + tid) * E, last));
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[i + e] = -INFINITY;
-      }
+      for (int i = 0; i < PER / E; ++i) unpack<T>(raw[i], x + i * E);
+    } else {
+      T raw[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) raw[i] = row[min(from + i * THREADS + tid, last)];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) x[i] = to_f32(raw[i]);
     }
     if (counted) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int at = from + (i / E * THREADS + tid) * E + i % E;
-        const uint32_t c = at < hi ? s_said[at - lo] : 0;
-        if (c) {
-          x[i] = x[i] > 0.f ? x[i] / repetition : x[i] * repetition;
-          if (c > 1) x[i] -= frequency * (float)(c >> 1) + presence;
+      for (int i = 0; i < PER; i += E) {
+        const int at = from + (i / E * THREADS + tid) * E;
+        uint32_t c[E];
+        if constexpr (VEC) {
+#pragma unroll
+          for (int e = 0; e < E; e += 4) {
+            const uint4 w = at < hi ? *reinterpret_cast<const uint4*>(s_said + at - lo + e) : make_uint4(0, 0, 0, 0);
+            c[e] = w.x; c[e + 1] = w.y; c[e + 2] = w.z; c[e + 3] = w.w;
+          }
+        } else {
+          c[0] = at < hi ? s_said[at - lo] : 0u;
+        }
+        uint32_t any = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) any |= c[e];
+        if (any) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float y = x[i + e] * (x[i + e] > 0.f ? one_over_repetition : repetition);
+            x[i + e] = c[e] > 1 ? y - fmaf(frequency, (float)(c[e] >> 1), presence) : c[e] ? y : x[i + e];
+          }
         }
       }
     }
@@ -177,62 +205,52 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
       for (int j = 0; j < s_listed; ++j) add_bias(x, from, s_id[j], s_bias[j]);
       for (int j = s_more; j < u.J; ++j) add_bias(x, from, u.bias_ids[(size_t)n * u.J + j], u.bias[(size_t)n * u.J + j]);
     }
-    if (u.mask) {
-      const int* bits = u.mask + n * u.mask_stride_n + r * u.mask_stride_r;
 #pragma unroll
-      for (int i = 0; i < PER; i += E) {
-        const int at = from + (i / E * THREADS + tid) * E;
-        const uint32_t word = at < hi ? (uint32_t)bits[at >> 5] >> (at & 31) : 0;  // E entries never straddle a word
+    for (int i = 0; i < PER; i += E) {
+      const int at = from + (i / E * THREADS + tid) * E;
+      uint32_t word = ~0u;
+      if (u.mask) word = __shfl_sync(~0u, bits, i + lane * E / 32) >> (at & 31);
+      if (at >= hi) word = 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (!(word >> e & 1)) x[i + e] = -INFINITY;
-      }
+      for (int e = 0; e < E; ++e)
+        if (!(word >> e & 1)) x[i + e] = -INFINITY;
     }
   };
-  // 2^((x - top) factor), 1 at the top whatever the factor is
-  auto weight = [&](float x, float top) {
-    const float d = x - top;
-    return x == -INFINITY || d == 0.f ? (x == -INFINITY ? 0.f : 1.f) : exp2_fast(d * factor);
+  // 2^((x - top) factor), 0 where x is -infinity
+  auto weight = [&](float x, float top) { return exp2_fast((x - (top == -INFINITY ? 0.f : top)) * factor); };
+
+  auto join = [&](const Part& a, const Part& b) {
+    const float both = fmaxf(a.top, b.top);
+    return Part{both, a.sum * weight(a.top, both) + b.sum * weight(b.top, both), b.top > a.top ? b.at : b.top == a.top ? min(a.at, b.at) : a.at, 0};
   };
 
   cg::cluster_group all = cg::this_cluster();
   all.sync();  // no CTA stores to one that has not started
   for (int r = r0; r < r1; ++r) {
     float x[PER];
-    Part mine{-INFINITY, 0.f, 0x7fffffff};
+    Part mine{-INFINITY, 0.f, 0x7fffffff, 0};
     for (int from = lo; from < hi || from == lo; from += TILE) {
       load(x, r, from);
-      // ---- the tile's largest entry, over the CTA
-      float top = -INFINITY;
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        top = fmaxf(top, x[i]);
-        nan |= x[i] != x[i];
-      }
+      float top = -INFINITY, sum = 0.f;
       int at = 0x7fffffff;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) top = fmaxf(top, x[i]);
       if (greedy) {
 #pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
+        for (int i = PER - 1; i >= 0; --i) {
           if (x[i] == top && top > -INFINITY) at = min(at, from + (i / E * THREADS + tid) * E + i % E);
+          if (!(x[i] < INFINITY)) sum = NAN;
+        }
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) {
         const float t = __shfl_xor_sync(~0u, top, o);
-        const int a = __shfl_xor_sync(~0u, at, o);
-        at = t > top ? a : t == top ? min(a, at) : at;
+        if (greedy) {
+          const int a = __shfl_xor_sync(~0u, at, o);
+          at = t > top ? a : t == top ? min(a, at) : at;
+        }
         top = fmaxf(top, t);
       }
-      if (lane == 0) s_warp[warp] = {top, 0.f, at};
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const Part q = s_warp[w];
-        at = q.top > top ? q.at : q.top == top ? min(q.at, at) : at;
-        top = fmaxf(top, q.top);
-      }
-      // ---- the sum against it
-      float sum = nan ? NAN : 0.f;
       if (!greedy) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
@@ -242,31 +260,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      __syncthreads();
-      if (lane == 0) s_warp[warp].sum = sum;
-      __syncthreads();
-      sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) sum += s_warp[w].sum;
-      // ---- joined with the tiles before
-      const float both = fmaxf(mine.top, top);
-      mine.sum = mine.sum * weight(mine.top, both) + sum * weight(top, both);
-      mine.at = top > mine.top ? at : mine.at;
-      mine.top = both;
-      __syncthreads();  // s_warp is written again
+      mine = join(mine, {top, sum, at, 0});
     }
-    // ---- and with the other CTAs' slices
-    const int turn = r & 1;
-    if (tid < cluster) *all.map_shared_rank(&s_parts[turn][rank], tid) = mine;
+    // ---- with the other warps' entries, in every CTA
+    const int turn = r & 1, parts = cluster * WARPS;
+    if (lane < cluster) *all.map_shared_rank(&s_parts[turn][rank * WARPS + warp], lane) = mine;
     all.sync();
-    Part whole = s_parts[turn][0];
-    for (int c = 1; c < cluster; ++c) {
-      const Part q = s_parts[turn][c];
-      const float both = fmaxf(whole.top, q.top);
-      whole.sum = whole.sum * weight(whole.top, both) + q.sum * weight(q.top, both);
-      whole.at = q.top > whole.top ? q.at : whole.at;
-      whole.top = both;
-    }
+    Part whole{-INFINITY, 0.f, 0x7fffffff, 0};
+    for (int i = lane; i < parts; i += 32) whole = join(whole, s_parts[turn][i]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      whole = join(whole, {__shfl_xor_sync(~0u, whole.top, o), __shfl_xor_sync(~0u, whole.sum, o), __shfl_xor_sync(~0u, whole.at, o), 0});
     O* to = static_cast<O*>(p.out) + ((size_t)n * p.R + r) * p.V;
     const float mul = greedy ? whole.sum : whole.sum > 0.f ? weight(mine.top, whole.top) / whole.sum : whole.sum;
     for (int from = lo; from < hi; from += TILE) {
@@ -335,8 +339,10 @@ template <typename T, typename O> cudaError_t launch_typed(const LogitsProblem& 
                             ((long long)p.N * p.R * cluster < sms && p.V >= cluster * 4096)))
     cluster *= 2;
   const int slice = ((p.V + cluster - 1) / cluster + 31) / 32 * 32;
-  // a request's rows one after the other, its history counted once, unless that leaves SMs without work
-  const int rows = (long long)p.N * p.R * cluster <= 2 * sms ? 1 : p.R;
+  // a request's rows one after the other, its history counted once, but no fewer CTAs than two rounds of the
+  // resident ones (2 on an SM)
+  const long long per_row = (long long)p.N * cluster;
+  const int groups = (int)std::min((long long)p.R, (4LL * sms + per_row - 1) / per_row), rows = (p.R + groups - 1) / groups;
   if (slice <= 512 * PER) {
     if (vec) return launch_kernel<T, O, 512, true>(p, cluster, slice, rows, stream);
     return launch_kernel<T, O, 512, false>(p, cluster, slice, rows, stream);
