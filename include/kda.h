@@ -679,7 +679,7 @@ KDA_API kda_status_t kda_linear_commit(const void* k, const void* v, long long k
  *            logits where that is contiguous and of out_dtype
  * A row all of whose entries are masked or -infinity becomes all 0; one with a
  * NaN or +infinity that is not masked becomes all NaN.  All sums are fp32.
- * With a penalty V is at most 425984 (a row's counts are held on chip).
+ * With a penalty V is at most 409600 (a row's counts are held on chip).
  * Results do not depend on anything but the arguments.
  */
 typedef struct {

@@ -11,11 +11,16 @@
 // takes its exponentials against its own maximum and leaves (maximum, sum) in
 // every CTA's shared memory: one cluster barrier a row, and no other.
 //
+// Vectors of 16 bytes are read where memory has them, also where a row starts
+// between two of them (an odd vocabulary): entry numbers are shifted by up to
+// seven then, and what a vector holds of neighbours is left out.
+//
 // What has been said is counted once for a request, in shared memory, one
 // 32-bit word an entry of the slice: 2 * (how often in the reply) + (whether
-// in the prompt).  The counts are whole numbers, so the order of the adding
-// does not matter; a request's biases are kept in their order.  A row's
-// drafts are added as the rows go by.
+// in the prompt); where rows start between vectors, a word is left out after
+// every 32 so that lanes 4 or 8 entries apart meet no bank twice.  The counts are whole numbers, so the order
+// of the adding does not matter; a request's biases are kept in their order.  A
+// row's drafts are added as the rows go by.
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -79,11 +84,12 @@ template <typename O, int E> __device__ __forceinline__ void store_vec(O* to, co
   }
 }
 
-template <typename T, typename O, int THREADS, bool VEC>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsProblem p, int cluster, int slice, int rows) {
+// EVEN: every row starts with a vector.
+template <typename T, typename O, int THREADS, bool EVEN>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsProblem p, int cluster, int slice, int rows, int step) {
   namespace cg = cooperative_groups;
-  constexpr int E = VEC ? Vec<T>::E : 1, TILE = THREADS * PER, WARPS = THREADS / 32;
-  extern __shared__ __align__(16) uint32_t s_said[];  // [slice], only where something is counted
+  constexpr int E = Vec<T>::E, TILE = THREADS * PER, WARPS = THREADS / 32;
+  extern __shared__ __align__(16) uint32_t s_said[];  // [slice], see said_at; only where something is counted
   __shared__ Part s_parts[2][MOST * WARPS];
   __shared__ int s_id[LIST];
   __shared__ float s_bias[LIST];
@@ -98,8 +104,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
 
   // ---- what this request has said, and its biases
   const bool counted = u.repetition || u.presence || u.frequency;
+  auto said_at = [&](int t) { return EVEN ? t - lo : t - lo + ((t - lo) >> 5); };
   if (counted) {
-    for (int i = tid; i < hi - lo; i += THREADS) s_said[i] = 0;
+    for (int i = tid; i < (EVEN ? slice : slice + slice / 32); i += THREADS) s_said[i] = 0;
     __syncthreads();
     const int L = u.tokens ? (u.lens ? min(max(u.lens[n], 0), u.L) : u.L) : 0;
     const int prompt = u.prompt_lens ? u.prompt_lens[n] : 0;
@@ -107,12 +114,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
     for (int i = tid; i < L; i += THREADS) {
       const int t = said[i];
       if (t < lo || t >= hi) continue;
-      if (i < prompt) atomicOr(&s_said[t - lo], 1u);
-      else atomicAdd(&s_said[t - lo], 2u);
+      if (i < prompt) atomicOr(&s_said[said_at(t)], 1u);
+      else atomicAdd(&s_said[said_at(t)], 2u);
     }
     for (int i = tid; u.drafts && i < r0; i += THREADS) {
       const int t = u.drafts[(size_t)n * (p.R - 1) + i];
-      if (t >= lo && t < hi) atomicAdd(&s_said[t - lo], 2u);
+      if (t >= lo && t < hi) atomicAdd(&s_said[said_at(t)], 2u);
     }
   }
   const float repetition = u.repetition ? u.repetition[n] : 1.f, presence = u.presence ? u.presence[n] : 0.f;
@@ -141,55 +148,69 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
   }
   __syncthreads();
 
-  // adds b to the entry t where this thread holds it in x (tile at `from`)
-  auto add_bias = [&](float (&x)[PER], int from, int t, float b) {
-    const int at = t - from;
+  const T* logits = static_cast<const T*>(p.logits) + n * p.stride_n;
+  // the first entry that a tile's vectors hold: that of the vector in which entry `from` of row r lies
+  auto first_of = [&](int r, int from) {
+    return EVEN ? from : from - (int)((reinterpret_cast<uintptr_t>(logits + r * p.stride_r + from) & 15) / sizeof(T));
+  };
+  // adds b to the entry t where this thread holds it in x (vectors from `base` on)
+  auto add_bias = [&](float (&x)[PER], int base, int t, float b) {
+    const int at = t - base;
     if (at < 0 || at >= TILE || at / E % THREADS != tid) return;
     const int mine = at / (E * THREADS) * E + at % E;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (i == mine) x[i] += b;
   };
-  // the entries of the tile that starts at `from`, with everything but the temperature; those that are
-  // masked or past the end are -infinity.  (Addresses past the end are those of the last entries instead, so
-  // that no load waits for another.)
-  auto load = [&](float (&x)[PER], int r, int from) {
-    const T* row = static_cast<const T*>(p.logits) + n * p.stride_n + r * p.stride_r;
-    const int last = max(hi, E) - E;
-    // the 32 words that cover the warp's entries, one to a lane: E of them for each of its PER / E vectors
+  // the entries [from, end) of the tile of vectors that starts at entry `base`, with everything but the
+  // temperature; all others are -infinity, as masked ones are.  (Vectors past the row's end are its last ones
+  // instead, so that no load waits for another.)
+  auto load = [&](float (&x)[PER], int r, int base, int from, int end) {
+    const T* row = logits + r * p.stride_r;
+    const int* mask = u.mask ? u.mask + n * u.mask_stride_n + r * u.mask_stride_r : nullptr;
+    const int last_word = (p.V - 1) >> 5;
+    const bool whole = EVEN || base % 32 == 0;
+    // where the vectors start with a word of the mask, the 32 words that cover the warp's entries, one to a
+    // lane: E of them for each of its PER / E vectors
     uint32_t bits = 0;
-    if (u.mask) {
-      const int word = ((from + (lane / E * THREADS + warp * 32) * E) >> 5) + lane % E;
-      bits = (u.mask + n * u.mask_stride_n + r * u.mask_stride_r)[min(word, (p.V - 1) >> 5)];
-    }
-    if constexpr (VEC) {
-      uint4 raw[PER / E];
+    if (mask && whole) bits = mask[min(((base + (lane / E * THREADS + warp * 32) * E) >> 5) + lane % E, last_word)];
+    uint4 raw[PER / E];
 #pragma unroll
-      for (int i = 0; i < PER / E; ++i) raw[i] = *reinterpret_cast<const uint4*>(row + min(from + (i * THREADS + tid) * E, last));
+    for (int i = 0; i < PER / E; ++i) {
+      const int at = base + (i * THREADS + tid) * E;
+      if constexpr (EVEN) {
+        raw[i] = *reinterpret_cast<const uint4*>(row + min(at, p.V - E));
+        continue;
+      }
+      const int most = p.V - E - ((p.V - base) % E + E) % E;  // the last vector that lies within the row
+      if (at >= 0 && most >= 0) {
+        raw[i] = *reinterpret_cast<const uint4*>(row + min(at, most));
+        unpack<T>(raw[i], x + i * E);
+      }
+      if (at < 0 || (at > most && at < p.V)) {  // a vector that holds something else, too
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i * E + e] = at + e >= 0 && at + e < p.V ? to_f32(row[at + e]) : 0.f;
+      }
+    }
+    if constexpr (EVEN) {
 #pragma unroll
       for (int i = 0; i < PER / E; ++i) unpack<T>(raw[i], x + i * E);
-    } else {
-      T raw[PER];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) raw[i] = row[min(from + i * THREADS + tid, last)];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) x[i] = to_f32(raw[i]);
     }
     if (counted) {
 #pragma unroll
       for (int i = 0; i < PER; i += E) {
-        const int at = from + (i / E * THREADS + tid) * E;
-        uint32_t c[E];
-        if constexpr (VEC) {
+        const int at = base + (i / E * THREADS + tid) * E;
+        uint32_t c[E], any = 0;
+        if constexpr (EVEN) {
 #pragma unroll
           for (int e = 0; e < E; e += 4) {
-            const uint4 w = at < hi ? *reinterpret_cast<const uint4*>(s_said + at - lo + e) : make_uint4(0, 0, 0, 0);
+            const uint4 w = at < end ? *reinterpret_cast<const uint4*>(s_said + at - lo + e) : make_uint4(0, 0, 0, 0);
             c[e] = w.x; c[e + 1] = w.y; c[e + 2] = w.z; c[e + 3] = w.w;
           }
         } else {
-          c[0] = at < hi ? s_said[at - lo] : 0u;
+#pragma unroll
+          for (int e = 0; e < E; ++e) c[e] = at + e >= from && at + e < end ? s_said[said_at(at + e)] : 0u;
         }
-        uint32_t any = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) any |= c[e];
         if (any) {
@@ -202,18 +223,31 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
       }
     }
     if (u.bias_ids) {
-      for (int j = 0; j < s_listed; ++j) add_bias(x, from, s_id[j], s_bias[j]);
-      for (int j = s_more; j < u.J; ++j) add_bias(x, from, u.bias_ids[(size_t)n * u.J + j], u.bias[(size_t)n * u.J + j]);
+      for (int j = 0; j < s_listed; ++j) add_bias(x, base, s_id[j], s_bias[j]);
+      for (int j = s_more; j < u.J; ++j) add_bias(x, base, u.bias_ids[(size_t)n * u.J + j], u.bias[(size_t)n * u.J + j]);
     }
 #pragma unroll
     for (int i = 0; i < PER; i += E) {
-      const int at = from + (i / E * THREADS + tid) * E;
+      const int at = base + (i / E * THREADS + tid) * E;
       uint32_t word = ~0u;
-      if (u.mask) word = __shfl_sync(~0u, bits, i + lane * E / 32) >> (at & 31);
-      if (at >= hi) word = 0;
+      if (mask) {
+        if (whole) {
+          word = __shfl_sync(~0u, bits, i + lane * E / 32) >> (at & 31);
+        } else {
+          const int w = at >> 5;  // (rounded down, also below 0)
+          word = __funnelshift_r((uint32_t)mask[min(max(w, 0), last_word)], (uint32_t)mask[min(w + 1, last_word)], at & 31);
+        }
+      }
+      if (EVEN || (at >= from && at + E <= end)) {
+        if (EVEN && at >= end) word = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (!(word >> e & 1)) x[i + e] = -INFINITY;
+        for (int e = 0; e < E; ++e)
+          if (!(word >> e & 1)) x[i + e] = -INFINITY;
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (!(word >> e & 1) || at + e < from || at + e >= end) x[i + e] = -INFINITY;
+      }
     }
   };
   // 2^((x - top) factor), 0 where x is -infinity
@@ -229,8 +263,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
   for (int r = r0; r < r1; ++r) {
     float x[PER];
     Part mine{-INFINITY, 0.f, 0x7fffffff, 0};
-    for (int from = lo; from < hi || from == lo; from += TILE) {
-      load(x, r, from);
+    for (int from = lo; from < hi || from == lo; from += step) {
+      const int base = first_of(r, from);
+      load(x, r, base, from, min(from + step, hi));
       float top = -INFINITY, sum = 0.f;
       int at = 0x7fffffff;
 #pragma unroll
@@ -238,7 +273,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
       if (greedy) {
 #pragma unroll
         for (int i = PER - 1; i >= 0; --i) {
-          if (x[i] == top && top > -INFINITY) at = min(at, from + (i / E * THREADS + tid) * E + i % E);
+          if (x[i] == top && top > -INFINITY) at = min(at, base + (i / E * THREADS + tid) * E + i % E);
           if (!(x[i] < INFINITY)) sum = NAN;
         }
       }
@@ -273,39 +308,46 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
       whole = join(whole, {__shfl_xor_sync(~0u, whole.top, o), __shfl_xor_sync(~0u, whole.sum, o), __shfl_xor_sync(~0u, whole.at, o), 0});
     O* to = static_cast<O*>(p.out) + ((size_t)n * p.R + r) * p.V;
     const float mul = greedy ? whole.sum : whole.sum > 0.f ? weight(mine.top, whole.top) / whole.sum : whole.sum;
-    for (int from = lo; from < hi; from += TILE) {
-      if (slice > TILE) {
-        load(x, r, from);
+    for (int from = lo; from < hi; from += step) {
+      const int base = first_of(r, from), end = min(from + step, hi);
+      if (slice > step) {
+        load(x, r, base, from, end);
         if (!greedy) {
 #pragma unroll
           for (int i = 0; i < PER; ++i) x[i] = weight(x[i], mine.top);
         }
       }
+      const bool vec = EVEN || ((reinterpret_cast<uintptr_t>(to) + base * (long long)sizeof(O)) & 15) == 0;
 #pragma unroll
       for (int i = 0; i < PER; i += E) {
-        const int at = from + (i / E * THREADS + tid) * E;
-        if (at >= hi) continue;
+        const int at = base + (i / E * THREADS + tid) * E;
+        if (at + E <= from || at >= end) continue;
         float y[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = greedy ? (at + e == whole.at ? 1.f + mul : mul) : x[i + e] * mul;
-        if constexpr (VEC) store_vec<O, E>(to + at, y);
-        else to[at] = from_f32<O>(y[0]);
+        if (EVEN || (vec && at >= from && at + E <= end)) {
+          store_vec<O, E>(to + at, y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (at + e >= from && at + e < end) to[at + e] = from_f32<O>(y[e]);
+        }
       }
     }
     if (counted && u.drafts && r + 1 < r1) {  // this row's draft has been said before the next row
       __syncthreads();
       const int t = u.drafts[(size_t)n * (p.R - 1) + r];
-      if (tid == 0 && t >= lo && t < hi) s_said[t - lo] += 2;
+      if (tid == 0 && t >= lo && t < hi) s_said[said_at(t)] += 2;
       __syncthreads();
     }
   }
 }
 
-template <typename T, typename O, int THREADS, bool VEC>
-cudaError_t launch_kernel(const LogitsProblem& p, int cluster, int slice, int rows, cudaStream_t stream) {
+template <typename T, typename O, int THREADS, bool EVEN>
+cudaError_t launch_kernel(const LogitsProblem& p, int cluster, int slice, int rows, int step, cudaStream_t stream) {
   const bool counted = p.rules.repetition || p.rules.presence || p.rules.frequency;
-  const size_t smem = counted ? (size_t)slice * 4 : 0;
-  auto kernel = logits_kernel<T, O, THREADS, VEC>;
+  const size_t smem = counted ? (size_t)(EVEN ? slice : slice + slice / 32) * 4 : 0;
+  auto kernel = logits_kernel<T, O, THREADS, EVEN>;
   if (smem > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -320,22 +362,23 @@ cudaError_t launch_kernel(const LogitsProblem& p, int cluster, int slice, int ro
   attr[0].val.clusterDim = {(unsigned)cluster, 1u, 1u};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, slice, rows);
+  return cudaLaunchKernelEx(&cfg, kernel, p, cluster, slice, rows, step);
 }
 
 template <typename T, typename O> cudaError_t launch_typed(const LogitsProblem& p, cudaStream_t stream) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  constexpr int E = Vec<T>::E;
+  // a tile of vectors holds up to 32 entries less than its size of a row that does not start with one
   auto in16 = [](const void* x, long long stride) {
     return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (stride * (long long)sizeof(T)) % 16 == 0;
   };
-  const bool vec = in16(p.logits, p.stride_n) && in16(nullptr, p.stride_r) && p.V % E == 0 &&
-                   (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  const bool even = in16(p.logits, p.N > 1 ? p.stride_n : 0) && in16(nullptr, p.R > 1 ? p.stride_r : 0) && p.V % Vec<T>::E == 0 &&
+                    (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  const int less = even ? 0 : 32;
   // the fewest CTAs that hold a row in registers, more while some SMs have none
   int cluster = 1;
-  while (cluster < MOST && (p.V > cluster * 512 * PER ||
+  while (cluster < MOST && (p.V > cluster * (512 * PER - less) ||
                             ((long long)p.N * p.R * cluster < sms && p.V >= cluster * 4096)))
     cluster *= 2;
   const int slice = ((p.V + cluster - 1) / cluster + 31) / 32 * 32;
@@ -343,18 +386,18 @@ template <typename T, typename O> cudaError_t launch_typed(const LogitsProblem& 
   // resident ones (2 on an SM)
   const long long per_row = (long long)p.N * cluster;
   const int groups = (int)std::min((long long)p.R, (4LL * sms + per_row - 1) / per_row), rows = (p.R + groups - 1) / groups;
-  if (slice <= 512 * PER) {
-    if (vec) return launch_kernel<T, O, 512, true>(p, cluster, slice, rows, stream);
-    return launch_kernel<T, O, 512, false>(p, cluster, slice, rows, stream);
-  }
-  if (vec) return launch_kernel<T, O, 1024, true>(p, cluster, slice, rows, stream);
-  return launch_kernel<T, O, 1024, false>(p, cluster, slice, rows, stream);
+  const bool narrow = slice <= 512 * PER - less;
+  const int step = (narrow ? 512 : 1024) * PER - less;
+  if (narrow && even) return launch_kernel<T, O, 512, true>(p, cluster, slice, rows, step, stream);
+  if (narrow) return launch_kernel<T, O, 512, false>(p, cluster, slice, rows, step, stream);
+  if (even) return launch_kernel<T, O, 1024, true>(p, cluster, slice, rows, step, stream);
+  return launch_kernel<T, O, 1024, false>(p, cluster, slice, rows, step, stream);
 }
 
 }  // namespace
 
 // The counts of a row fit the shared memory of a cluster up to here.
-int logits_most_counted() { return MOST * 53248; }
+int logits_most_counted() { return MOST * 51200; }
 
 cudaError_t launch_logits_probs(const LogitsProblem& p, cudaStream_t stream) {
   if (p.N == 0 || p.R == 0) return cudaSuccess;

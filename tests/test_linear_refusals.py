@@ -74,6 +74,6 @@ def test_logits(lib):
     assert call(x=None) == call(out=None) == call(N=-1) == call(R=-1) == call(V=0) == call(sn=-1) == 1
     assert call(L=-1) == call(J=-1) == call(tokens_stride=-1) == call(mask_stride_n=-1) == call(J=2, bias=16) == 1
     assert call(dt=3) == call(odt=0) == call(dt=0, odt=2) == call(V=(1 << 30) + 1) == 2
-    assert call(V=425985, presence=16) == call(N=1 << 20, R=1 << 10) == 2
+    assert call(V=409601, presence=16) == call(N=1 << 20, R=1 << 10) == 2
     assert call(x=ctypes.c_void_p(18)) == call(dt=0, x=ODD) == call(tokens=18) == call(temperature=17) == call(out=ODD) == 3
     assert call(N=0) == call(R=0) == 0

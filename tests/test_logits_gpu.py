@@ -121,7 +121,7 @@ def test_rules(N, R, V, L, J, mask, dtype, out_dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("V", [131072, 131080, 200000, 262145, 300000, 425984])
+@pytest.mark.parametrize("V", [131072, 131080, 200000, 262145, 300000, 409600])
 def test_large_vocabularies(V, dtype):
     check(logits_of(1, 2, V, dtype, V), rules(1, 2, V, 300, 9, True, V), torch.float32)
 
