@@ -698,22 +698,25 @@ def kda_draft_accept(draft_tokens, draft_probs, target_probs, uniform, draft_len
     return counts, tokens
 
 
-def _linear_tokens(k, lead, **others):
-    """Heads, head dim, GPU and token strides of k and of the others, all [*lead, H, d] in bf16."""
+def _linear_tokens(k, lead, others, names):
+    """Heads, head dim, GPU and the token strides of k and of the others, all [*lead, H, d] in bf16."""
     shape = k.shape
     if len(shape) != lead + 2:
         raise ValueError(f"k must have {lead + 2} dimensions here")
-    H, d = shape[-2:]
-    dev = k.get_device()
-    if dev < 0:
-        raise ValueError("q, k and v must be CUDA tensors")
+    H, d, dev, st = shape[-2], shape[-1], k.get_device(), k.stride()
+    if dev < 0 or k.dtype != torch.bfloat16:
+        raise ValueError("q, k and v must be CUDA tensors of bfloat16")
     one = shape[:-2].numel() <= 1  # no stride between tokens
-    strides = []
-    for name, x in (("k", k), *others.items()):
+    first = H * d if one else _token_stride(k, H, d, "k", dev)
+    strides = [first]
+    for x, name in zip(others, names):
         if x.shape != shape or x.dtype != torch.bfloat16:
             raise ValueError(f"{name} must be bfloat16 of k's shape {tuple(shape)}")
-        s = _token_stride(x, H, d, name, dev)
-        strides.append(H * d if one else s)
+        if x.stride() == st and x.get_device() == dev:
+            strides.append(first)
+        else:
+            s = _token_stride(x, H, d, name, dev)
+            strides.append(H * d if one else s)
     return H, d, dev, strides
 
 
@@ -785,7 +788,7 @@ def kda_linear_fwd(q, k, v, log_alpha, initial_state=None, scale=1.0, out_dtype=
     lib = _lib or load()
     shape = k.shape
     N, T, lead = _linear_sequences(shape, cu_seqlens)
-    H, d, dev, (ks, qs, vs) = _linear_tokens(k, len(lead), q=q, v=v)
+    H, d, dev, (ks, qs, vs) = _linear_tokens(k, len(lead), (q, v), ("q", "v"))
     decay = _linear_decay(log_alpha, lead, H, dev)
     states = (N, H, d, d)
     s0 = _linear_state(initial_state, states, "initial_state", dev)
@@ -815,7 +818,7 @@ def kda_linear_bwd(q, k, v, log_alpha, d_out, initial_state=None, d_final_state=
     lib = _lib or load()
     shape = k.shape
     N, T, lead = _linear_sequences(shape, cu_seqlens)
-    H, d, dev, (ks, qs, vs, os_) = _linear_tokens(k, len(lead), q=q, v=v, d_out=d_out)
+    H, d, dev, (ks, qs, vs, os_) = _linear_tokens(k, len(lead), (q, v, d_out), ("q", "v", "d_out"))
     decay = _linear_decay(log_alpha, lead, H, dev)
     states = (N, H, d, d)
     s0 = _linear_state(initial_state, states, "initial_state", dev)
@@ -841,7 +844,7 @@ def kda_linear_step(q, k, v, log_alpha, state, scale=1.0, out=None, out_dtype=to
     """One token per sequence of the linear attention; `state` [N,H,d,d] fp32 is
     updated in place.  q, k, v [N,H,d] bf16; log_alpha [N,H] or [H].  Returns out [N,H,d]."""
     lib = _lib or load()
-    H, d, dev, (ks, qs, vs) = _linear_tokens(k, 1, q=q, v=v)
+    H, d, dev, (ks, qs, vs) = _linear_tokens(k, 1, (q, v), ("q", "v"))
     N = k.shape[0]
     decay = _linear_decay(log_alpha, (N,), H, dev)
     s = _linear_state(state, (N, H, d, d), "state", dev)
@@ -859,7 +862,7 @@ def kda_linear_verify(q, k, v, log_alpha, state, scale=1.0, out_dtype=torch.floa
     `state` (only read).  q, k, v [N,K,H,d] bf16; log_alpha [N,K,H] or [H].
     Returns out [N,K,H,d]."""
     lib = _lib or load()
-    H, d, dev, (ks, qs, vs) = _linear_tokens(k, 2, q=q, v=v)
+    H, d, dev, (ks, qs, vs) = _linear_tokens(k, 2, (q, v), ("q", "v"))
     N, K = k.shape[:2]
     decay = _linear_decay(log_alpha, (N, K), H, dev)
     s = _linear_state(state, (N, H, d, d), "state", dev)
@@ -876,7 +879,7 @@ def kda_linear_commit(k, v, log_alpha, state, accepted, stream=None):
     """Advance `state` in place by the first accepted[n] of each sequence's K
     drafted tokens (accepted: int32 [N] on the device)."""
     lib = _lib or load()
-    H, d, dev, (ks, vs) = _linear_tokens(k, 2, v=v)
+    H, d, dev, (ks, vs) = _linear_tokens(k, 2, (v,), ("v",))
     N, K = k.shape[:2]
     decay = _linear_decay(log_alpha, (N, K), H, dev)
     if accepted is None:

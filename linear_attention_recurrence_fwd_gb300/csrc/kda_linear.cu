@@ -8,11 +8,6 @@ namespace {
 
 using namespace linear;
 
-__global__ void check_offsets_kernel(LinearProblem p) {
-  for (int n = blockIdx.x * blockDim.x + threadIdx.x; n < p.n_seq; n += gridDim.x * blockDim.x)
-    if (!offsets_good(p, n)) atomicExch(p.status, (int)KDA_ERR_INVALID_ARG);
-}
-
 struct Plan {
   int seg_len, slots;
   bool cut;
@@ -36,14 +31,21 @@ Plan plan_for(int n_seq, int T, int H, int d, bool packed) {
 template <int D> cudaError_t run(const LinearProblem& p, void* workspace, cudaStream_t stream) {
   const Plan a = plan_for(p.n_seq, p.T, p.H, D, p.cu_seqlens != nullptr);
   Walk w{p, a.seg_len, std::max((p.len + a.seg_len - 1) / a.seg_len, 1), a.slots, static_cast<float*>(workspace), nullptr, nullptr};
+  CUtensorMap mq, mk, mv;
+  if (p.T > 0 && (!make_rows_map(&mq, p.q, p.q_stride, p) || !make_rows_map(&mk, p.k, p.k_stride, p) ||
+                  !make_rows_map(&mv, p.v, p.v_stride, p)))
+    return cudaErrorInvalidValue;
   if (a.cut) {
     w.decay = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + a.decay_at);
-    cudaError_t e = launch_walk<D, ENDS, false, false>(w, p.k, p.k_stride, p.v, p.v_stride, stream);
-    if (e == cudaSuccess) e = launch_scan<false>(w, stream);
+    cudaError_t e = launch(linear_walk_kernel<D, ENDS, false>, walk_ctas(w), WALK_THREADS, WalkShape<D, ENDS, false, false>::SMEM, false,
+                           stream, mk, mk, mv, w);
+    if (e == cudaSuccess) e = launch_scan(w, w, 1, stream);
     if (e != cudaSuccess) return e;
   }
-  return p.out_f32 ? launch_walk<D, OUTPUTS, false, true>(w, p.k, p.k_stride, p.v, p.v_stride, stream)
-                   : launch_walk<D, OUTPUTS, false, false>(w, p.k, p.k_stride, p.v, p.v_stride, stream);
+  return p.out_f32 ? launch(linear_walk_kernel<D, OUTPUTS, true>, walk_ctas(w), WALK_THREADS, WalkShape<D, OUTPUTS, false, true>::SMEM, a.cut,
+                            stream, mq, mk, mv, w)
+                   : launch(linear_walk_kernel<D, OUTPUTS, false>, walk_ctas(w), WALK_THREADS, WalkShape<D, OUTPUTS, false, false>::SMEM,
+                            a.cut, stream, mq, mk, mv, w);
 }
 
 }  // namespace

@@ -1,4 +1,4 @@
-// What the linear attention's kernels share: a sequence's rows and a token's decay.
+// What the linear attention's kernels share: a sequence's rows, a token's decay, packed arithmetic.
 #pragma once
 
 #include <cstdint>
@@ -32,10 +32,39 @@ __device__ __forceinline__ uint32_t load_decay_bits(const LinearProblem& p, long
 __device__ __forceinline__ float decay_of_bits(const LinearProblem& p, uint32_t bits) {
   return __uint_as_float(p.la_f32 ? bits : bits << 16);
 }
+// Whether a call's offsets are.
+static __global__ void __launch_bounds__(256) check_offsets_kernel(LinearProblem p) {
+  for (int n = threadIdx.x; n < p.n_seq; n += 256)
+    if (!offsets_good(p, n)) atomicExch(p.status, (int)KDA_ERR_INVALID_ARG);
+}
+
 __device__ __forceinline__ float load_decay(const LinearProblem& p, long long row, int h) {
   const long long at = row * p.la_token_stride + h * p.la_head_stride;
   return p.la_f32 ? static_cast<const float*>(p.log_alpha)[at]
                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.log_alpha)[at]);
+}
+
+// Two fp32 numbers in a register pair, and what sm_100 does with both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float* a, float* b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
 }
 
 }  // namespace kda

@@ -73,7 +73,8 @@ constexpr int GRAD_THREADS = 288;
 template <int D>
 __global__ void __launch_bounds__(GRAD_THREADS, 1)
     linear_grad_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do, Grad a) {
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                       const __grid_constant__ Grad a) {
   using W = GradShape<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const LinearProblem& p = a.p;
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
         tma_load_3d(smem + W::Q + b * W::BLOCK, &map_q, landed, 64 * b, h, row0);
         tma_load_3d(smem + W::K + b * W::BLOCK, &map_k, landed, 64 * b, h, row0);
       }
+      dependency_wait();
       const size_t image = ((size_t)slot * p.H + h) * W::IMAGE;
       bulk_g2s(smem + W::S, a.s_images + image, W::IMAGE, landed);
       bulk_g2s(smem + W::DS, a.ds_images + image, W::IMAGE, landed);
@@ -475,11 +477,6 @@ __global__ void __launch_bounds__(256) decay_sum_kernel(LinearProblem p, const f
   else static_cast<__nv_bfloat16*>(dla)[h] = __float2bfloat16_rn(s[0]);
 }
 
-__global__ void __launch_bounds__(256) check_offsets_kernel(LinearProblem p) {
-  for (int n = threadIdx.x; n < p.n_seq; n += 256)
-    if (!offsets_good(p, n)) atomicExch(p.status, (int)KDA_ERR_INVALID_ARG);
-}
-
 struct Plan {
   int seg_len, slots;
   long long chunks;
@@ -492,7 +489,7 @@ Plan plan_for(int n_seq, int T, int H, int d, bool packed) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) sms = 152;
   auto whole = [](size_t x) { return (x + 255) / 256 * 256; };
-  a.seg_len = segment_tokens(n_seq, T, H, packed, sms);
+  a.seg_len = segment_tokens(n_seq, T, 2 * H, packed, sms);  // both directions in one launch
   a.slots = segment_slots(n_seq, T, a.seg_len, packed);
   a.chunks = most_chunks(n_seq, T, packed);
   a.cut = a.slots > n_seq;
@@ -510,35 +507,35 @@ template <int D> cudaError_t run(const LinearProblem& p, const LinearGrads& g, v
   const Plan a = plan_for(p.n_seq, p.T, p.H, D, p.cu_seqlens != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int segs = std::max((p.len + a.seg_len - 1) / a.seg_len, 1);
-  Walk ahead{p, a.seg_len, segs, a.slots, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + a.carry), ws + a.at_images};
+  Walk ahead{p, a.seg_len, segs, a.slots, reinterpret_cast<float*>(ws),
+             a.cut ? reinterpret_cast<float*>(ws + a.carry) : nullptr, ws + a.at_images};
   ahead.p.s_out = nullptr;
   Walk back = ahead;
   back.p.s_in = g.d_final;
   back.p.s_out = g.ds0;
   back.carry = reinterpret_cast<float*>(ws + a.at_back);
-  back.decay = reinterpret_cast<float*>(ws + a.at_back + a.carry);
+  if (a.cut) back.decay = reinterpret_cast<float*>(ws + a.at_back + a.carry);
   back.images = ahead.images + a.images;
+  CUtensorMap mq, mk, mv, mo;
+  if (p.T > 0 && (!make_rows_map(&mq, p.q, p.q_stride, p) || !make_rows_map(&mk, p.k, p.k_stride, p) ||
+                  !make_rows_map(&mv, p.v, p.v_stride, p) || !make_rows_map(&mo, g.d_out, g.d_out_stride, p)))
+    return cudaErrorInvalidValue;
+  const dim3 both(walk_ctas(ahead), 2);
   cudaError_t e = cudaSuccess;
   if (a.cut) {
-    e = launch_walk<D, ENDS, false, false>(ahead, p.k, p.k_stride, p.v, p.v_stride, stream);
-    if (e == cudaSuccess) e = launch_scan<false>(ahead, stream);
-    if (e == cudaSuccess) e = launch_walk<D, ENDS, true, false>(back, p.q, p.q_stride, g.d_out, g.d_out_stride, stream);
-    if (e == cudaSuccess) e = launch_scan<true>(back, stream);
+    e = launch(linear_walks_kernel<D, ENDS>, both, WALK_THREADS, WalkShape<D, ENDS, false, false>::SMEM, false, stream, mk, mv, mq, mo, ahead,
+               back);
+    if (e == cudaSuccess) e = launch_scan(ahead, back, 2, stream);
   }
-  if (e == cudaSuccess) e = launch_walk<D, IMAGES, false, false>(ahead, p.k, p.k_stride, p.v, p.v_stride, stream);
-  if (e == cudaSuccess) e = launch_walk<D, IMAGES, true, false>(back, p.q, p.q_stride, g.d_out, g.d_out_stride, stream);
+  if (e == cudaSuccess)
+    e = launch(linear_walks_kernel<D, IMAGES>, both, WALK_THREADS, WalkShape<D, IMAGES, false, false>::SMEM, a.cut, stream, mk, mv, mq, mo,
+               ahead, back);
   if (e != cudaSuccess) return e;
-  Grad x{p, ahead.images, back.images, g.dq, g.dk, g.dv, g.dla,
-         g.dla && g.sum_la ? reinterpret_cast<float*>(ws + a.at_sums) : nullptr};
+  const Grad x{p, ahead.images, back.images, g.dq, g.dk, g.dv, g.dla,
+               g.dla && g.sum_la ? reinterpret_cast<float*>(ws + a.at_sums) : nullptr};
   if (p.T > 0) {
-    CUtensorMap mq, mk, mv, mo;
-    if (!make_rows_map(&mq, p.q, p.q_stride, p) || !make_rows_map(&mk, p.k, p.k_stride, p) || !make_rows_map(&mv, p.v, p.v_stride, p) ||
-        !make_rows_map(&mo, g.d_out, g.d_out_stride, p))
-      return cudaErrorInvalidValue;
-    auto kernel = linear_grad_kernel<D>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradShape<D>::SMEM);
+    e = launch(linear_grad_kernel<D>, dim3((unsigned)(a.chunks * p.H)), GRAD_THREADS, GradShape<D>::SMEM, true, stream, mq, mk, mv, mo, x);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)(a.chunks * p.H), GRAD_THREADS, GradShape<D>::SMEM, stream>>>(mq, mk, mv, mo, x);
   }
   if (g.dla && g.sum_la) decay_sum_kernel<<<p.H, 256, 0, stream>>>(p, reinterpret_cast<float*>(ws + a.at_sums), p.T > 0 ? a.chunks : 0, g.dla);
   return cudaGetLastError();

@@ -41,11 +41,10 @@ __global__ void __launch_bounds__(128) linear_tokens_kernel(LinearProblem p) {
 
   const int j = tid % 16, g = tid / 16;
   const size_t off = (size_t)nh * D * D + part * COLS + 4 * j;
-  float4 s[R];
+  ulonglong2 s[R];  // four columns of a row, as pairs
 #pragma unroll
   for (int i = 0; i < R; ++i)
-    s[i] = p.s_in ? *reinterpret_cast<const float4*>(p.s_in + off + (size_t)(g * R + i) * D)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    s[i] = p.s_in ? *reinterpret_cast<const ulonglong2*>(p.s_in + off + (size_t)(g * R + i) * D) : make_ulonglong2(0, 0);
 
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + h * D;
   const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(p.k) + h * D;
@@ -55,35 +54,53 @@ __global__ void __launch_bounds__(128) linear_tokens_kernel(LinearProblem p) {
   for (int t0 = 0; t0 < steps; t0 += KT) {
     const int nt = min(KT, steps - t0);
     if (t0) __syncthreads();  // the previous tokens' readers are done
+    // all loads of the KT tokens together (past the last one that one again)
+    __nv_bfloat16 rk[KT], rq[KT], rv[KT];
+    uint32_t ra[KT];
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-      if (t >= nt) break;
-      const long long row = row0 + t0 + t;
-      if (tid < D) {
-        s_k[t][tid] = __bfloat162float(k[row * p.k_stride + tid]);
-        if (out) s_q[t][tid] = __bfloat162float(q[row * p.q_stride + tid]);
-      }
-      if (tid < COLS) s_v[t][tid] = __bfloat162float(v[row * p.v_stride + tid]);
-      if (tid == 127) s_a[t] = expf(load_decay(p, row, h));
+      const long long row = row0 + t0 + min(t, nt - 1);
+      if (tid < D) rk[t] = k[row * p.k_stride + tid];
+      if (tid < D && out) rq[t] = q[row * p.q_stride + tid];
+      if (tid < COLS) rv[t] = v[row * p.v_stride + tid];
+      if (tid == 127) ra[t] = load_decay_bits(p, row, h);
+    }
+#pragma unroll
+    for (int t = 0; t < KT; ++t) {
+      if (tid < D) s_k[t][tid] = __bfloat162float(rk[t]);
+      if (tid < D && out) s_q[t][tid] = __bfloat162float(rq[t]);
+      if (tid < COLS) s_v[t][tid] = __bfloat162float(rv[t]);
+      if (tid == 127) s_a[t] = expf(decay_of_bits(p, ra[t]));
     }
     __syncthreads();
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+      const uint64_t a = pair(s_a[t], s_a[t]);
+      const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(&s_v[t][4 * j]);
+      ulonglong2 b = make_ulonglong2(0, 0);
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      if (t >= nt) break;
-      const float a = s_a[t];
-      const float4 x = *reinterpret_cast<const float4*>(&s_v[t][4 * j]);
-      float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < R; i0 += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(&s_k[t][g * R + i0]);
+        const float kc[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const float kc = s_k[t][g * R + i];
-        s[i].x = a * s[i].x + kc * x.x; s[i].y = a * s[i].y + kc * x.y;
-        s[i].z = a * s[i].z + kc * x.z; s[i].w = a * s[i].w + kc * x.w;
+        for (int i = 0; i < 4; ++i) {
+          ulonglong2& y = s[i0 + i];
+          const uint64_t k2 = pair(kc[i], kc[i]);
+          y.x = fma2(a, y.x, mul2(k2, x.x));
+          y.y = fma2(a, y.y, mul2(k2, x.y));
+        }
         if (out) {
-          const float qc = s_q[t][g * R + i];
-          b.x += s[i].x * qc; b.y += s[i].y * qc; b.z += s[i].z * qc; b.w += s[i].w * qc;
+          const float4 q4 = *reinterpret_cast<const float4*>(&s_q[t][g * R + i0]);
+          const float qc[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t q2 = pair(qc[i], qc[i]);
+            b.x = fma2(s[i0 + i].x, q2, b.x);
+            b.y = fma2(s[i0 + i].y, q2, b.y);
+          }
         }
       }
-      if (out) *reinterpret_cast<float4*>(&s_part[t][g][4 * j]) = b;
+      if (out) *reinterpret_cast<ulonglong2*>(&s_part[t][g][4 * j]) = b;
     }
     if (out) {
       __syncthreads();
@@ -98,7 +115,7 @@ __global__ void __launch_bounds__(128) linear_tokens_kernel(LinearProblem p) {
   }
   if (p.s_out) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(p.s_out + off + (size_t)(g * R + i) * D) = s[i];
+    for (int i = 0; i < R; ++i) *reinterpret_cast<ulonglong2*>(p.s_out + off + (size_t)(g * R + i) * D) = s[i];
   }
 }
 
@@ -114,8 +131,8 @@ cudaError_t launch_typed(const LinearProblem& p, cudaStream_t stream) {
 
 cudaError_t launch_linear_tokens(const LinearProblem& p, cudaStream_t stream) {
   if (p.n_seq == 0 || p.H == 0) return cudaSuccess;
-  if (p.d == 128) return p.len == 1 ? launch_typed<128, 1>(p, stream) : launch_typed<128, 4>(p, stream);
-  return p.len == 1 ? launch_typed<64, 1>(p, stream) : launch_typed<64, 4>(p, stream);
+  if (p.d == 128) return p.len == 1 ? launch_typed<128, 1>(p, stream) : launch_typed<128, 5>(p, stream);
+  return p.len == 1 ? launch_typed<64, 1>(p, stream) : launch_typed<64, 5>(p, stream);
 }
 
 }  // namespace kda

@@ -56,7 +56,7 @@ struct Walk {
   LinearProblem p;
   int seg_len, segs, slots;  // tokens to a segment; segments to a sequence (fixed lengths), and of all sequences
   float* carry;              // [slots][H][d][d]: ENDS writes contributions, the other modes read states
-  float* decay;              // [slots][H]: log2 of each segment's decay
+  float* decay;              // [slots][H]: log2 of each segment's decay; null where no sequence is cut
   uint8_t* images;           // IMAGES: [chunks][H][d x d bf16]
 };
 
@@ -155,28 +155,6 @@ __device__ __forceinline__ void tmem_st16u(uint32_t at, const uint32_t* v) {
       "r"(v[14]), "r"(v[15]) : "memory");
 }
 
-// Two fp32 numbers in a register pair, and what sm_100 does with both at once.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-  return v;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float* a, float* b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v)); }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t v;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t v;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t v;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
-  return v;
-}
 __device__ __forceinline__ __nv_bfloat162 as_bf16x2(uint32_t u) {
   __nv_bfloat162 v;
   memcpy(&v, &u, 4);
@@ -232,6 +210,11 @@ struct Decays {
   }
 };
 
+// A launch may start while the one before it in its stream runs, up to the point where it needs what that one
+// leaves: every launch lets the next one start at once, and none ends without having waited.
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int D, Mode MODE, bool BACK, bool FINE> struct WalkShape : Shape<D> {
   using Shape<D>::TILE;
   static constexpr int IN = MODE == OUTPUTS ? 5 : 4;  // input tiles
@@ -272,9 +255,7 @@ template <Mode MODE> struct Tiles {
 
 // FINE: fp32 outputs, P and S as two bf16 numbers each.
 template <int D, Mode MODE, bool BACK, bool FINE>
-__global__ void __launch_bounds__(WALK_THREADS, 1)
-    linear_walk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                       const __grid_constant__ CUtensorMap map_v, Walk w) {
+__device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v, const Walk& w) {
   using W = WalkShape<D, MODE, BACK, FINE>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const LinearProblem& p = w.p;
@@ -288,7 +269,6 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
     return;
   }
   const bool last_seg = BACK ? seg.index == 0 : seg.index == seg.count - 1;  // in the order of the walk
-  const bool first_seg = BACK ? seg.index == seg.count - 1 : seg.index == 0;
   if (MODE == ENDS && last_seg) return;  // what it would find nobody asks for
   const bool exact = MODE != OUTPUTS || FINE || (last_seg && p.s_out);  // V' as two numbers
   const int nch = max((seg.tokens + CHUNK - 1) / CHUNK, 0);
@@ -352,8 +332,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
       const bool has_row = D == 128 || lane < 16;
       const size_t state_at = ((size_t)seg.n * p.H + h) * D * D + (size_t)srow * D;
       uint64_t s[D / 2];  // two columns each
+      dependency_wait();  // the joined states
       {
-        const float* from = !first_seg ? w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)srow * D : p.s_in ? p.s_in + state_at : nullptr;
+        // (a call that is cut takes all of them from there: where the caller's states are one buffer, a CTA may
+        // have written its own before another has started)
+        const float* from = w.decay ? w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)srow * D : p.s_in ? p.s_in + state_at : nullptr;
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) {
           const float4 x = from ? *reinterpret_cast<const float4*>(from + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -859,9 +842,28 @@ __global__ void __launch_bounds__(WALK_THREADS, 1)
   if (warp == 0) tmem_dealloc(tb, 512);
 }
 
+template <int D, Mode MODE, bool FINE>
+__global__ void __launch_bounds__(WALK_THREADS, 1)
+    linear_walk_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                       const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Walk w) {
+  dependents_may_start();
+  walk<D, MODE, false, FINE>(map_q, map_k, map_v, w);
+}
+
+// Both directions: keys and values ahead, queries and the outputs' gradients back.
+template <int D, Mode MODE>
+__global__ void __launch_bounds__(WALK_THREADS, 1)
+    linear_walks_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+                        const __grid_constant__ Walk ahead, const __grid_constant__ Walk back) {
+  dependents_may_start();
+  if (blockIdx.y == 0) walk<D, MODE, false, false>(map_k, map_k, map_v, ahead);
+  else walk<D, MODE, true, false>(map_q, map_q, map_do, back);
+}
+
 // The states at the segments' starts (BACK: the gradients at their ends) from the segments' contributions,
 // which they replace: E = 2^decay E + Z, one after the other, 1024 entries of a state to a CTA.
-template <bool BACK> __global__ void __launch_bounds__(256) linear_scan_kernel(Walk w) {
+template <bool BACK> __device__ __forceinline__ void scan(const Walk& w) {
   const LinearProblem& p = w.p;
   const int parts = p.d * p.d / 1024;
   const int part = blockIdx.x % parts, nh = blockIdx.x / parts, n = nh / p.H, h = nh % p.H;
@@ -871,6 +873,7 @@ template <bool BACK> __global__ void __launch_bounds__(256) linear_scan_kernel(W
   const int count = max((len + w.seg_len - 1) / w.seg_len, 1);
   const long long first = p.cu_seqlens ? row0 / w.seg_len + n : (long long)n * w.segs;
   const size_t at = (size_t)part * 1024 + threadIdx.x * 4, size = (size_t)p.d * p.d;
+  dependency_wait();
   float4 e = p.s_in ? *reinterpret_cast<const float4*>(p.s_in + (size_t)nh * size + at) : make_float4(0.f, 0.f, 0.f, 0.f);
   // the contributions of AHEAD segments are on their way together
   constexpr int AHEAD = 8;
@@ -897,6 +900,12 @@ template <bool BACK> __global__ void __launch_bounds__(256) linear_scan_kernel(W
   }
 }
 
+static __global__ void __launch_bounds__(256) linear_scan_kernel(const __grid_constant__ Walk ahead, const __grid_constant__ Walk back) {
+  dependents_may_start();
+  if (blockIdx.y == 0) scan<false>(ahead);
+  else scan<true>(back);
+}
+
 // ---------------------------------------------------------------- host
 
 inline bool make_rows_map(CUtensorMap* map, const void* base, long long stride, const LinearProblem& p) {
@@ -904,25 +913,31 @@ inline bool make_rows_map(CUtensorMap* map, const void* base, long long stride, 
                           CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int D, Mode MODE, bool BACK, bool FINE>
-cudaError_t launch_walk(const Walk& w, const void* k, long long k_stride, const void* v, long long v_stride, cudaStream_t stream) {
-  using W = WalkShape<D, MODE, BACK, FINE>;
-  CUtensorMap mq, mk, mv;
-  const LinearProblem& p = w.p;
-  if (p.T > 0 && (!make_rows_map(&mk, k, k_stride, p) || !make_rows_map(&mv, v, v_stride, p) ||
-                  !make_rows_map(&mq, MODE == OUTPUTS ? p.q : k, MODE == OUTPUTS ? p.q_stride : k_stride, p)))
-    return cudaErrorInvalidValue;
-  auto kernel = linear_walk_kernel<D, MODE, BACK, FINE>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W::SMEM);
-  if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)((long long)w.slots * p.H), WALK_THREADS, W::SMEM, stream>>>(mq, mk, mv, w);
-  return cudaGetLastError();
+// A launch; `after`: it may start while the one before it in the stream runs, which this call made.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool after, cudaStream_t stream, A... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <bool BACK> cudaError_t launch_scan(const Walk& w, cudaStream_t stream) {
-  const LinearProblem& p = w.p;
-  linear_scan_kernel<BACK><<<(unsigned)((long long)p.n_seq * p.H * (p.d * p.d / 1024)), 256, 0, stream>>>(w);
-  return cudaGetLastError();
+inline unsigned walk_ctas(const Walk& w) { return (unsigned)((long long)w.slots * w.p.H); }
+inline cudaError_t launch_scan(const Walk& ahead, const Walk& back, int directions, cudaStream_t stream) {
+  const LinearProblem& p = ahead.p;
+  return launch(linear_scan_kernel, dim3((unsigned)((long long)p.n_seq * p.H * (p.d * p.d / 1024)), directions), 256, 0, true, stream,
+                ahead, back);
 }
 
 // Tokens to a segment: whole chunks, such that the walk (and, where it is cut, the half as long one before

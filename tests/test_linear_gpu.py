@@ -198,6 +198,14 @@ def test_state_in_place_split_and_repeat():
     assert (held - last).norm() <= 2.0 ** -15 * last.norm()
 
 
+def test_long_prompt_with_its_state_in_place():
+    x = on_gpu(inputs((2, 6000), 3, 128, "slow", 26))
+    s = torch.randn((2, 3, 128, 128), device="cuda")
+    want, last = kda.kda_linear_fwd(x["q"], x["k"], x["v"], x["log_alpha"], initial_state=s)
+    out, state = kda.kda_linear_fwd(x["q"], x["k"], x["v"], x["log_alpha"], initial_state=s, final_state=s)
+    assert state is s and torch.equal(out, want) and torch.equal(s, last)
+
+
 def test_captured_and_replayed_on_another_stream():
     x = on_gpu(inputs((1, 700), 2, 128, "mixed", 19))
     want, last = kda.kda_linear_fwd(x["q"], x["k"], x["v"], x["log_alpha"])
