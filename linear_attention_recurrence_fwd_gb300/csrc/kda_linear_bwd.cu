@@ -26,8 +26,8 @@
 // summed from the sequence's end, cancels: after a few thousand tokens the
 // rounding of dq and dk is all that is left of it.)
 //
-// Warps: 0-7 compute (two to each quarter of the lanes, with half of the
-// columns each), 8 loads and issues.  One CTA on an SM; six tiles of shared
+// Warps: 0-15 compute (four to each quarter of the lanes, with a quarter of the
+// columns each), 16 loads and issues.  One CTA on an SM; six tiles of shared
 // memory (Q, K, V, dO, S, dS), through which the gradients leave once their
 // content has been used.
 #include <algorithm>
@@ -49,9 +49,15 @@ struct Grad {
 template <int D> struct GradShape : Shape<D> {
   using Shape<D>::TILE;
   static constexpr uint32_t Q = 0, K = TILE, V = 2 * TILE, DO = 3 * TILE, S = 4 * TILE, DS = 5 * TILE, MISC = 6 * TILE;
-  static constexpr uint32_t SMEM_USED = MISC + 6144, SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr uint32_t SMEM_USED = MISC + 8192, SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   static constexpr uint32_t T0 = 0, T1 = 128, T2 = 256, T3 = 384;  // tensor memory
 };
+
+__device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
+  float a, b;
+  unpair(v, &a, &b);
+  return pack_bf16x2(a, b);
+}
 
 // Sums over the warp's lanes of 16 numbers each; lane l gets that of number l >> 1.
 __device__ __forceinline__ float sum_lanes(float (&x)[16]) {
@@ -68,7 +74,7 @@ __device__ __forceinline__ float sum_lanes(float (&x)[16]) {
   return x[0] + __shfl_xor_sync(~0u, x[0], 1);
 }
 
-constexpr int GRAD_THREADS = 288;
+constexpr int GRAD_WARPS = 16, GRAD_THREADS = 32 * GRAD_WARPS + 32;
 
 template <int D>
 __global__ void __launch_bounds__(GRAD_THREADS, 1)
@@ -93,25 +99,36 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
   const int rows = seg.tokens, row0 = (int)(seg.row0 + (long long)seg.index * CHUNK);
 
   float* s_g = reinterpret_cast<float*>(smem + W::MISC);  // [128]: -g
-  float* s_out = s_g + 128;                               // [2][128]: sums over later tokens, and of k . y, by half
-  float* s_in = s_out + 256;                              // [4][128]: sums over earlier tokens, by quarter
-  float* s_x = s_in + 512;                                // [2][128]: q . x, by half
-  float* s_dot = s_x + 256;                               // [8]: <S, dS>, by warp
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W::MISC + 5120);
-  uint64_t *landed = bars, *clean = bars + 1, *b_done = bars + 2, *bt_done = bars + 3, *at_done = bars + 4, *x_done = bars + 5,
-           *r_ready = bars + 6, *w_ready = bars + 7, *x_ready = bars + 8, *dq_done = bars + 9, *y_done = bars + 10,
-           *dq_read = bars + 11, *y_ready = bars + 12, *z_done = bars + 13, *z_ready = bars + 14, *dk_done = bars + 15,
-           *dv_done = bars + 16, *sums_ready = bars + 17;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 18);
+  float* s_out = s_g + 128;                               // [4][128]: sums over later tokens, and of k . y, by part of the columns
+  float* s_in = s_out + 512;                              // [4][128]: sums over earlier tokens, by quarter of the lanes
+  float* s_x = s_in + 512;                                // [4][128]: q . x, by part of the columns
+  float* s_dot = s_x + 512;                               // [16]: <S, dS>, by warp
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W::MISC + 7168);
+  uint64_t* done = bars;  // [9] the products, in their order
+  uint64_t *bt_done = done, *at_done = done + 1, *b_done = done + 2, *x_done = done + 3, *dq_done = done + 4, *y_done = done + 5,
+           *z_done = done + 6, *dk_done = done + 7, *dv_done = done + 8;
+  uint64_t *landed = bars + 9, *images = bars + 10;
+  uint64_t *clean = bars + 11, *r_ready = bars + 12, *w_ready = bars + 13, *x_ready = bars + 14, *dq_read = bars + 15,
+           *y_ready = bars + 16, *z_ready = bars + 17, *sums_ready = bars + 18;  // by all warps
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 19);
 
   if (warp == 1) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
   }
-  if (tid == 0) {
-    for (int i = 0; i < 18; ++i) mbar_init(bars + i, 1);
-    for (uint64_t* b : {clean, r_ready, w_ready, x_ready, dq_read, y_ready, z_ready, sums_ready}) mbar_init(b, 8);
+  if (warp == GRAD_WARPS && lane == 0) {
+#pragma unroll 1
+    for (int i = 0; i < 19; ++i) mbar_init(bars + i, i < 11 ? 1 : GRAD_WARPS);
     mbar_fence_init();
+    fence_proxy_async_smem();
+    // on their way while the rest of the CTA is made ready
+    mbar_arrive_expect_tx(landed, 4 * W::TILE);
+    for (int b = 0; b < D / 64; ++b) {
+      tma_load_3d(smem + W::V + b * W::BLOCK, &map_v, landed, 64 * b, h, row0);
+      tma_load_3d(smem + W::DO + b * W::BLOCK, &map_do, landed, 64 * b, h, row0);
+      tma_load_3d(smem + W::K + b * W::BLOCK, &map_k, landed, 64 * b, h, row0);
+      tma_load_3d(smem + W::Q + b * W::BLOCK, &map_q, landed, 64 * b, h, row0);
+    }
   }
   if (warp == 0) {
     Decays la;
@@ -125,159 +142,82 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
   const uint32_t tb = *s_tmem;
   bool ok = true;
 
-  if (warp == 8) {
+  if (warp == GRAD_WARPS) {
     if (lane == 0) {
-      // -------------------------------------------------------------- loads, then products in the order of their needs
-      mbar_arrive_expect_tx(landed, 4 * W::TILE + 2 * W::IMAGE);
-      for (int b = 0; b < D / 64; ++b) {
-        tma_load_3d(smem + W::DO + b * W::BLOCK, &map_do, landed, 64 * b, h, row0);
-        tma_load_3d(smem + W::V + b * W::BLOCK, &map_v, landed, 64 * b, h, row0);
-        tma_load_3d(smem + W::Q + b * W::BLOCK, &map_q, landed, 64 * b, h, row0);
-        tma_load_3d(smem + W::K + b * W::BLOCK, &map_k, landed, 64 * b, h, row0);
-      }
+      // -------------------------------------------------------------- the states, then products in the order of their needs
       dependency_wait();
       const size_t image = ((size_t)slot * p.H + h) * W::IMAGE;
-      bulk_g2s(smem + W::S, a.s_images + image, W::IMAGE, landed);
-      bulk_g2s(smem + W::DS, a.ds_images + image, W::IMAGE, landed);
+      mbar_arrive_expect_tx(images, 2 * W::IMAGE);
+      bulk_g2s(smem + W::S, a.s_images + image, W::IMAGE, images);
+      bulk_g2s(smem + W::DS, a.ds_images + image, W::IMAGE, images);
+      // As steps of one loop, so that the issuing of a product comes once in the code.  A step's tiles, tensor
+      // memory and so on are hexadecimal digits, the first step's the last one: tiles Q 0, K 1, V 2, dO 3, S 4,
+      // dS 5; scores over channels (0), sums from the states over channels as they lie (1) or read transposed
+      // (2), sums over tokens with weights from tensor memory, added to what is there (3).
+      constexpr uint64_t TO = 0x303033021, A = 0x211203312, B = 0x305514203, KIND = 0x332131000;
+      static_assert(W::T1 == 128 && W::T2 == 256 && W::T3 == 384, "their digits");
       constexpr uint32_t ID_SCORE = make_idesc_bf16(128, 128, false, false), ID_ROWS = make_idesc_bf16(128, D, false, false),
                          ID_COLS = make_idesc_bf16(128, D, false, true);
-      constexpr uint32_t K_IN = 2, K_OUT = W::BLOCK >> 4, I_OUT = W::IMAGE_BLOCK >> 4, MN_IN = 128, MN_OUT = 512;
-      // over channels: both operands' rows along K
-      auto over_channels = [&](uint32_t to, uint32_t x, uint64_t b, uint32_t b_in, uint32_t b_out, uint32_t id) {
-        const uint64_t d = desc_k(sb + x);
 #pragma unroll 1
-        for (int o = 0; o < D / 64; ++o)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) umma_bf16(tb + to, d + o * K_OUT + i * K_IN, b + o * b_out + i * b_in, id, o || i ? 1u : 0u);
-      };
-      // over tokens: weights from tensor memory, added to what is there
-      auto over_tokens = [&](uint32_t to, uint32_t weights, uint32_t x) {
-        const uint64_t b = desc_mn(sb + x, W::BLOCK);
+      for (int step = 0; step < 9 && ok; ++step) {
+        auto digit = [&](uint64_t digits) { return (uint32_t)(digits >> (4 * step)) & 15u; };
+        if (step == 0) ok = wait_for(landed, 0) && wait_for(clean, 0);
+        if (step == 3) ok = wait_for(images, 0);
+        if (step == 4) ok = wait_for(r_ready, 0) && wait_for(x_ready, 0);
+        if (step == 6) ok = wait_for(dq_read, 0);
+        if (step == 7) ok = wait_for(w_ready, 0) && wait_for(y_ready, 0);
+        if (step == 8) ok = wait_for(z_ready, 0);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint32_t kind = digit(KIND), to = tb + 128 * digit(TO), b_at = sb + digit(B) * W::TILE;
+        const bool rows_k = kind < 2;  // B's rows lie along K
+        const uint32_t id = kind == 0 ? ID_SCORE : kind == 1 ? ID_ROWS : ID_COLS, block = kind == 0 || kind == 3 ? W::BLOCK : W::IMAGE_BLOCK;
+        const uint64_t b = rows_k ? desc_k(b_at) : desc_mn(b_at, block), a = desc_k(sb + digit(A) * W::TILE);
+        const uint32_t b_in = rows_k ? 2 : 128, b_out = rows_k ? block >> 4 : 512, weights = tb + 128 * digit(A);
+        if (kind == 3) {
 #pragma unroll 1
-        for (int o = 0; o < 2; ++o)
+          for (int o = 0; o < 2; ++o)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) umma_f16_ta(tb + to, tb + weights + 64 * o + 8 * i, b + o * MN_OUT + i * MN_IN, ID_COLS, 1u);
-      };
-      ok = mbar_wait(landed, 0) && mbar_wait(clean, 0);
-      if (ok) {
-        over_channels(W::T1, W::V, desc_k(sb + W::DO), K_IN, K_OUT, ID_SCORE);
-        umma_commit(bt_done);
-        over_channels(W::T2, W::K, desc_k(sb + W::Q), K_IN, K_OUT, ID_SCORE);
-        umma_commit(at_done);
-        over_channels(W::T0, W::DO, desc_k(sb + W::V), K_IN, K_OUT, ID_SCORE);
-        umma_commit(b_done);
-        over_channels(W::T3, W::DO, desc_k(sb + W::S), K_IN, I_OUT, ID_ROWS);
-        umma_commit(x_done);
-        ok = mbar_wait(r_ready, 0) && mbar_wait(x_ready, 0);
+            for (int i = 0; i < 4; ++i)
+              umma_f16_ta(to, weights + 64 * o + 32 * (i >> 1) + 8 * (i & 1), b + o * 512 + i * 128, ID_COLS, 1u);
+        } else {
+#pragma unroll 1
+          for (int o = 0; o < D / 64; ++o)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) umma_bf16(to, a + o * (W::BLOCK >> 4) + i * 2, b + o * b_out + i * b_in, id, o || i ? 1u : 0u);
+        }
+        umma_commit(done + step);
       }
-      if (ok) {
-        tc_fence_after_sync();
-        over_tokens(W::T3, W::T0, W::K);
-        umma_commit(dq_done);
-        over_channels(W::T0, W::V, desc_k(sb + W::DS), K_IN, I_OUT, ID_ROWS);  // (after the product that reads T0)
-        umma_commit(y_done);
-        ok = mbar_wait(dq_read, 0);
-      }
-      if (ok) {
-        tc_fence_after_sync();
-        over_channels(W::T3, W::K, desc_mn(sb + W::DS, W::IMAGE_BLOCK), MN_IN, MN_OUT, ID_COLS);
-        umma_commit(z_done);
-        ok = mbar_wait(w_ready, 0) && mbar_wait(y_ready, 0);
-      }
-      if (ok) {
-        tc_fence_after_sync();
-        over_tokens(W::T0, W::T1, W::Q);
-        umma_commit(dk_done);
-        ok = mbar_wait(z_ready, 0);
-      }
-      if (ok) {
-        tc_fence_after_sync();
-        over_tokens(W::T3, W::T2, W::DO);
+      if (!ok) {  // what has been issued ends before the CTA does
         umma_commit(dv_done);
-      } else {  // what has been issued ends before the CTA does
-        umma_commit(dv_done);
+        (void)wait_for(dv_done, 0);
       }
-      ok = mbar_wait(dv_done, 0) && ok;
     }
   } else {
-    const int quarter = warp & 3, half = warp >> 2, trow = 32 * quarter + lane;
+    const int quarter = warp & 3, part = warp >> 2, trow = 32 * quarter + lane;
     const uint32_t my = tb + ((uint32_t)(32 * quarter) << 16);
     const float g_mine = -s_g[trow], lead = p.scale * ex2(g_mine), trail = ex2(-s_g[127] - g_mine), keep = ex2(-s_g[127]);
-    constexpr int SC = D / 2;
+    constexpr int SC = D / 4;
     const uint32_t row_at = (uint32_t)trow * 128;
     auto piece = [&](int x) { return (uint32_t)(x / 8) * W::BLOCK + row_at + (((uint32_t)(x % 8) ^ (uint32_t)(trow & 7)) << 4); };
 
-    // half a row of an accumulator times `by`, written back; returns its product with the same half of a tile's row
-    auto scale_and_dot = [&](uint32_t t, float by, uint32_t tile) {
-      uint64_t sum = pair(0.f, 0.f);
-#pragma unroll 1
-      for (int b = 0; b < SC; b += 16) {
-        float x[16];
-        uint32_t u[2][4];
-        tmem_ld16(my + t + half * SC + b, x);
-        lds_v4(sb + tile + piece((half * SC + b) / 8), u[0]);
-        lds_v4(sb + tile + piece((half * SC + b) / 8 + 1), u[1]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const uint32_t w = u[i / 8][i % 8 / 2];
-          const uint64_t y = mul2(pair(x[i], x[i + 1]), pair(by, by));
-          sum = fma2(y, pair(lo_f32(w), hi_f32(w)), sum);
-          unpair(y, &x[i], &x[i + 1]);
-        }
-        tmem_st16(my + t + half * SC + b, x);
-      }
-      tmem_st_wait();
-      tc_fence_before_sync();
-      float s, z;
-      unpair(sum, &s, &z);
-      return s + z;
-    };
-    // an accumulator to memory, through this warp's part of a tile so that whole lines are written
-    auto write_out = [&](uint32_t t, uint32_t tile, void* out, uint64_t* read) {
-      constexpr int LANES = W::TILE / 256 / 16;  // to a row's piece of SC channels
-      const uint32_t turn = sb + tile + warp * (W::TILE / 8), mine = turn + lane * (LANES * 16);
-#pragma unroll 1
-      for (int z = 0; z < LANES; z += 2) {
-        float x[16];
-        tmem_ld16(my + t + half * SC + 8 * z, x);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          st_shared_v4(mine + (((z + i) ^ (lane * LANES / 8 % LANES)) << 4), pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
-                       pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
-      }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (read && lane == 0) mbar_arrive(read);
-      uint32_t o[LANES][4];
-#pragma unroll
-      for (int i = 0; i < LANES; ++i) {
-        const int r = i * (32 / LANES) + lane / LANES, at = lane % LANES;
-        lds_v4(turn + r * (LANES * 16) + ((at ^ (r * LANES / 8 % LANES)) << 4), o[i]);
-      }
-      uint8_t* to = static_cast<uint8_t*>(out) + ((size_t)(row0 + 32 * quarter) * p.H + h) * D * 2 + half * D;
-#pragma unroll
-      for (int i = 0; i < LANES; ++i) {
-        const int r = i * (32 / LANES) + lane / LANES, at = lane % LANES;
-        if (32 * quarter + r < rows) *reinterpret_cast<uint4*>(to + (size_t)r * p.H * D * 2 + at * 16) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
-      }
-    };
-
-    ok = mbar_wait(landed, 0);
+    ok = wait_for(landed, 0);
     if (ok) {
       if (rows < CHUNK && trow >= rows) {  // rows of other sequences
 #pragma unroll 1
-        for (int i = 0; i < D / 16; ++i)
-          for (uint32_t tile : {W::Q, W::K, W::V, W::DO}) st_shared_v4(sb + tile + piece(half * (D / 16) + i), 0u, 0u, 0u, 0u);
+        for (int i = 0; i < D / 32; ++i)
+          for (uint32_t tile : {W::Q, W::K, W::V, W::DO}) st_shared_v4(sb + tile + piece(part * (D / 32) + i), 0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(clean);
+      ok = wait_for(images, 0);
+    }
+    if (ok) {
       // <S, dS>: 16 bytes of either at a time, wherever they belong
       float dot = 0.f;
 #pragma unroll 1
-      for (uint32_t i = tid * 16; i < W::IMAGE; i += 256 * 16) {
+      for (uint32_t i = tid * 16; i < W::IMAGE; i += 32 * GRAD_WARPS * 16) {
         uint32_t u[4], v[4];
         lds_v4(sb + W::S + i, u);
         lds_v4(sb + W::DS + i, v);
@@ -287,58 +227,66 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
 #pragma unroll
       for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(~0u, dot, o);
       if (lane == 0) s_dot[warp] = dot;
-      ok = mbar_wait(bt_done, 0) && mbar_wait(at_done, 0);
+      ok = wait_for(bt_done, 0) && wait_for(at_done, 0);
     }
     if (ok) {
       // ---- R^T and P^T, earlier tokens on the lanes, 16 later ones at a time, and what a pair gives to the decays
       tc_fence_after_sync();
-      float later = 0.f;
+      uint64_t later = pair(0.f, 0.f);
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
-        const int i0 = 64 * half + 16 * b;
+      for (int b = 0; b < 2; ++b) {
+        const int i0 = 32 * part + 16 * b;
         uint32_t u[8], v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[i] = v[i] = 0u;
-        float w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = 0.f;
+        float earlier = 0.f;
         if (i0 + 15 >= 32 * quarter) {
-          float x[16], y[16];
+          float x[16], y[16], w[16];
           tmem_ld16(my + W::T1 + i0, x);
           tmem_ld16(my + W::T2 + i0, y);
           tmem_ld_wait();
+          float e[16];  // log2 of the decays between
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float d = i0 + i >= trow ? p.scale * ex2(-s_g[i0 + i] - g_mine) : 0.f;
-            w[i] = i0 + i > trow ? d * x[i] * y[i] : 0.f;
-            later += w[i];
-            x[i] = i0 + i >= trow ? d * x[i] : 0.f;
-            y[i] = i0 + i >= trow ? d * y[i] : 0.f;
+          for (int i = 0; i < 16; i += 2)
+            unpair(add2(*reinterpret_cast<const uint64_t*>(s_g + i0 + i), pair(g_mine, g_mine)), &e[i], &e[i + 1]);
+          if (i0 < 32 * quarter + 31) {  // some of the warp's tokens are not before all of these
+#pragma unroll
+            for (int i = 0; i < 16; ++i) e[i] = i0 + i >= trow ? e[i] : INFINITY;
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            u[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-            v[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+          for (int i = 0; i < 16; i += 2) {
+            const uint64_t decay = mul2(pair(ex2(-e[i]), ex2(-e[i + 1])), pair(p.scale, p.scale)), z = mul2(decay, pair(x[i], x[i + 1]));
+            u[i / 2] = to_bf16x2(z);
+            v[i / 2] = to_bf16x2(mul2(decay, pair(y[i], y[i + 1])));
+            unpair(mul2(z, pair(y[i], y[i + 1])), &w[i], &w[i + 1]);
           }
+          if (i0 <= 32 * quarter + 31) {  // a token's pair with itself straddles no decay
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = i0 + i == trow ? 0.f : w[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) later = add2(later, pair(w[i], w[i + 1]));
+          earlier = sum_lanes(w);
         }
-        tmem_st8u(my + W::T1 + 64 * half + 8 * b, u);
-        tmem_st8u(my + W::T2 + 64 * half + 8 * b, v);
-        const float earlier = sum_lanes(w);
+        tmem_st8u(my + W::T1 + 32 * part + 8 * b, u);
+        tmem_st8u(my + W::T2 + 32 * part + 8 * b, v);
         if (lane % 2 == 0) s_in[quarter * 128 + i0 + lane / 2] = earlier;
       }
-      s_out[half * 128 + trow] = later;
+      float later_0, later_1;
+      unpair(later, &later_0, &later_1);
+      s_out[part * 128 + trow] = later_0 + later_1;
       tmem_st_wait();
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(w_ready);
-      ok = mbar_wait(b_done, 0);
+      ok = wait_for(b_done, 0);
     }
     if (ok) {
       // ---- R, later tokens on the lanes
       tc_fence_after_sync();
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
-        const int j0 = 64 * half + 16 * b;
+      for (int b = 0; b < 2; ++b) {
+        const int j0 = 32 * part + 16 * b;
         uint32_t u[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) u[j] = 0u;
@@ -346,111 +294,142 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
           float x[16];
           tmem_ld16(my + W::T0 + j0, x);
           tmem_ld_wait();
+          float e[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) x[j] = j0 + j <= trow ? p.scale * ex2(g_mine + s_g[j0 + j]) * x[j] : 0.f;
+          for (int j = 0; j < 16; j += 2)
+            unpair(add2(*reinterpret_cast<const uint64_t*>(s_g + j0 + j), pair(g_mine, g_mine)), &e[j], &e[j + 1]);
+          if (j0 + 15 > 32 * quarter) {  // some come after some of the warp's tokens
 #pragma unroll
-          for (int j = 0; j < 8; ++j) u[j] = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+            for (int j = 0; j < 16; ++j) e[j] = j0 + j <= trow ? e[j] : -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const uint64_t decay = mul2(pair(ex2(e[j]), ex2(e[j + 1])), pair(p.scale, p.scale));
+            u[j / 2] = to_bf16x2(mul2(decay, pair(x[j], x[j + 1])));
+          }
         }
-        tmem_st8u(my + W::T0 + 64 * half + 8 * b, u);
+        tmem_st8u(my + W::T0 + 32 * part + 8 * b, u);
       }
       tmem_st_wait();
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(r_ready);
-      ok = mbar_wait(x_done, 0);
     }
-    if (ok) {
-      tc_fence_after_sync();
-      s_x[half * 128 + trow] = scale_and_dot(W::T3, lead, W::Q);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(x_ready);
-      ok = mbar_wait(dq_done, 0);
-    }
-    if (ok) {
-      tc_fence_after_sync();
-      write_out(W::T3, W::S, a.dq, dq_read);
-      ok = mbar_wait(y_done, 0);
-    }
-    if (ok) {
-      tc_fence_after_sync();
-      s_out[half * 128 + trow] += scale_and_dot(W::T0, trail, W::K);
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(y_ready);
-        mbar_arrive(sums_ready);
-      }
-      ok = mbar_wait(z_done, 0);
-    }
-    if (ok) {
-      tc_fence_after_sync();
+    // ---- accumulators scaled and written back (0, 2 and 3, of dQ, dK and dV), then, the other products added,
+    // written out (1, 4 and 5): as steps of one loop, so that either comes once in the code
 #pragma unroll 1
-      for (int b = 0; b < SC; b += 16) {
-        float x[16];
-        tmem_ld16(my + W::T3 + half * SC + b, x);
-        tmem_ld_wait();
+    for (int step = 0; step < 6 && ok; ++step) {
+      const uint32_t t = step == 2 || step == 4 ? W::T0 : W::T3;
+      ok = wait_for(step == 0 ? x_done : step == 1 ? dq_done : step == 2 ? y_done : step == 3 ? z_done : step == 4 ? dk_done : dv_done, 0);
+      if (!ok) break;
+      tc_fence_after_sync();
+      if (step == 0 || step == 2 || step == 3) {
+        const float by = step == 0 ? lead : trail;
+        const uint32_t tile = step == 0 ? W::Q : W::K;  // its rows' products with the accumulator's are the decays' part
+        uint64_t sum = pair(0.f, 0.f);
+#pragma unroll 1
+        for (int b = 0; b < SC; b += 16) {
+          float x[16];
+          uint32_t u[2][4];
+          tmem_ld16(my + t + part * SC + b, x);
+          lds_v4(sb + tile + piece((part * SC + b) / 8), u[0]);
+          lds_v4(sb + tile + piece((part * SC + b) / 8 + 1), u[1]);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= trail;
-        tmem_st16(my + W::T3 + half * SC + b, x);
+          for (int i = 0; i < 16; i += 2) {
+            const uint32_t w = u[i / 8][i % 8 / 2];
+            const uint64_t y = mul2(pair(x[i], x[i + 1]), pair(by, by));
+            sum = fma2(y, pair(lo_f32(w), hi_f32(w)), sum);
+            unpair(y, &x[i], &x[i + 1]);
+          }
+          tmem_st16(my + t + part * SC + b, x);
+        }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        float s, z;
+        unpair(sum, &s, &z);
+        if (step == 0) s_x[part * 128 + trow] = s + z;
+        if (step == 2) s_out[part * 128 + trow] += s + z;
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(step == 0 ? x_ready : step == 2 ? y_ready : z_ready);
+          if (step == 2) mbar_arrive(sums_ready);
+        }
+      } else {
+        // through this warp's part of a tile whose content has been used, so that whole lines are written
+        constexpr int LANES = W::TILE / 512 / 16;  // to a row's piece of SC channels
+        const uint32_t turn = sb + (step == 1 ? W::S : step == 4 ? W::V : W::K) + warp * (W::TILE / 16), mine = turn + lane * (LANES * 16);
+#pragma unroll 1
+        for (int z = 0; z < LANES; z += 2) {
+          float x[16];
+          tmem_ld16(my + t + part * SC + 8 * z, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            st_shared_v4(mine + (((z + i) ^ (lane * LANES / 8 & (LANES - 1))) << 4), pack_bf16x2(x[8 * i], x[8 * i + 1]),
+                         pack_bf16x2(x[8 * i + 2], x[8 * i + 3]), pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (step == 1 && lane == 0) mbar_arrive(dq_read);
+        uint32_t o[LANES][4];
+#pragma unroll
+        for (int i = 0; i < LANES; ++i) {
+          const int r = i * (32 / LANES) + lane / LANES, at = lane % LANES;
+          lds_v4(turn + r * (LANES * 16) + ((at ^ (r * LANES / 8 & (LANES - 1))) << 4), o[i]);
+        }
+        uint8_t* to = static_cast<uint8_t*>(step == 1 ? a.dq : step == 4 ? a.dk : a.dv) + ((size_t)(row0 + 32 * quarter) * p.H + h) * D * 2 + part * SC * 2;
+#pragma unroll
+        for (int i = 0; i < LANES; ++i) {
+          const int r = i * (32 / LANES) + lane / LANES, at = lane % LANES;
+          if (32 * quarter + r < rows) *reinterpret_cast<uint4*>(to + (size_t)r * p.H * D * 2 + at * 16) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        }
       }
-      tmem_st_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(z_ready);
-      // ---- the decays' gradients
-      if (warp == 0 && (a.dla || a.sums) && (ok = mbar_wait(sums_ready, 0))) {
-        float total = 0.f, e[4], run = 0.f, x4[4];
+    }
+    // ---- the decays' gradients
+    if (ok && warp == 0 && (a.dla || a.sums) && (ok = wait_for(sums_ready, 0))) {
+      float total = 0.f, e[4], run = 0.f, x4[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) total += s_dot[i];
-        total *= keep;
+      for (int i = 0; i < GRAD_WARPS; ++i) total += s_dot[i];
+      total *= keep;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 4 * lane + i;
-          const float in = s_in[t] + s_in[128 + t] + s_in[256 + t] + s_in[384 + t];
-          x4[i] = t < rows ? s_x[t] + s_x[128 + t] : 0.f;
-          e[i] = run;
-          run += t < rows ? s_out[t] + s_out[128 + t] - in - x4[i] : 0.f;
-        }
-        float all = x4[0] + x4[1] + x4[2] + x4[3], before = run;
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * lane + i;
+        const float in = s_in[t] + s_in[128 + t] + s_in[256 + t] + s_in[384 + t];
+        x4[i] = t < rows ? s_x[t] + s_x[128 + t] + s_x[256 + t] + s_x[384 + t] : 0.f;
+        e[i] = run;
+        run += t < rows ? s_out[t] + s_out[128 + t] + s_out[256 + t] + s_out[384 + t] - in - x4[i] : 0.f;
+      }
+      float all = x4[0] + x4[1] + x4[2] + x4[3], before = run;
 #pragma unroll
-        for (int o = 16; o; o /= 2) all += __shfl_xor_sync(~0u, all, o);
+      for (int o = 16; o; o /= 2) all += __shfl_xor_sync(~0u, all, o);
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-          const float x = __shfl_up_sync(~0u, before, o);
-          if (lane >= o) before += x;
-        }
-        before = __shfl_up_sync(~0u, before, 1);
-        if (lane == 0) before = 0.f;
-        total += all;
-        float sum = 0.f;
+      for (int o = 1; o < 32; o *= 2) {
+        const float x = __shfl_up_sync(~0u, before, o);
+        if (lane >= o) before += x;
+      }
+      before = __shfl_up_sync(~0u, before, 1);
+      if (lane == 0) before = 0.f;
+      total += all;
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 4 * lane + i;
-          const float x = total + (before + e[i]);
-          if (t < rows) {
-            sum += x;
-            const size_t at = (size_t)(row0 + t) * p.H + h;
-            if (!a.sums) {
-              if (p.la_f32) static_cast<float*>(a.dla)[at] = x;
-              else static_cast<__nv_bfloat16*>(a.dla)[at] = __float2bfloat16_rn(x);
-            }
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * lane + i;
+        const float x = total + (before + e[i]);
+        if (t < rows) {
+          sum += x;
+          const size_t at = (size_t)(row0 + t) * p.H + h;
+          if (!a.sums) {
+            if (p.la_f32) static_cast<float*>(a.dla)[at] = x;
+            else static_cast<__nv_bfloat16*>(a.dla)[at] = __float2bfloat16_rn(x);
           }
         }
-        if (a.sums) {
-#pragma unroll
-          for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
-          if (lane == 0) a.sums[(size_t)slot * p.H + h] = sum;
-        }
       }
-      ok = ok && mbar_wait(dk_done, 0);
-    }
-    if (ok) {
-      tc_fence_after_sync();
-      write_out(W::T0, W::V, a.dk, nullptr);
-      ok = mbar_wait(dv_done, 0);
-    }
-    if (ok) {
-      tc_fence_after_sync();
-      write_out(W::T3, W::K, a.dv, nullptr);
+      if (a.sums) {
+#pragma unroll
+        for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) a.sums[(size_t)slot * p.H + h] = sum;
+      }
     }
   }
   if (!ok && lane == 0) atomicExch(p.status, (int)KDA_ERR_TIMEOUT);
