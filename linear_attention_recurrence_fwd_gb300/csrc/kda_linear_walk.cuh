@@ -218,7 +218,7 @@ __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol
 template <int D, Mode MODE, bool BACK, bool FINE> struct WalkShape : Shape<D> {
   using Shape<D>::TILE;
   static constexpr int IN = MODE == OUTPUTS ? 5 : 4;  // input tiles
-  static constexpr uint32_t X = IN * TILE, Y = X + TILE, MISC = Y + TILE, SMEM_USED = MISC + 3072;
+  static constexpr uint32_t X = IN * TILE, Y = X + TILE, LEAVING = Y + TILE, MISC = LEAVING + (MODE == IMAGES ? TILE : 0), SMEM_USED = MISC + 3072;
   // one CTA on an SM: each takes all of tensor memory
   static constexpr uint32_t SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   // scores and weights; what the state gives; what the weights give; the chunk's part of the state
@@ -381,12 +381,22 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
             if (lane == 0) mbar_arrive(f_ready);
           }
         } else {
-          uint8_t* image = w.images + ((first_chunk(p, seg) + seg.index * (w.seg_len / CHUNK) + chunk_of(c)) * p.H + h) * W::IMAGE;
+          // the image leaves by way of shared memory, each warp's rows by themselves
+          if (lane == 0) bulk_wait_reads();
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < D / 8; ++i)
             place(i, false, [&](uint32_t at, const uint32_t (&u)[4]) {
-              if (has_row) *reinterpret_cast<uint4*>(image + at) = make_uint4(u[0], u[1], u[2], u[3]);
+              if (has_row) st_shared_v4(sb + W::LEAVING + at, u[0], u[1], u[2], u[3]);
             });
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            constexpr uint32_t ROWS = D / 4 * 128;  // bytes of a warp's rows in a block
+            uint8_t* image = w.images + ((first_chunk(p, seg) + seg.index * (w.seg_len / CHUNK) + chunk_of(c)) * p.H + h) * W::IMAGE;
+            for (uint32_t at = quarter * ROWS; at < W::IMAGE; at += W::IMAGE_BLOCK) bulk_s2g(image + at, sb + W::LEAVING + at, ROWS);
+            bulk_commit();
+          }
         }
         if (!(ok = wait_for(z_done + par, c >> 1 & 1))) break;
         tc_fence_after_sync();
@@ -402,6 +412,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
         __syncwarp();
         if (lane == 0) mbar_arrive(z_free);
       }
+      if (MODE == IMAGES && lane == 0) bulk_wait_all();
       if (ok && last_seg && p.s_out && has_row) {
 #pragma unroll
         for (int i = 0; i < D / 4; ++i) {
