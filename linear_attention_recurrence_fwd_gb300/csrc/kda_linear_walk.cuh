@@ -215,6 +215,12 @@ struct Decays {
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Where a warp turns its rows of a state, 32 columns at a time, between memory, where 8 lanes take a row's 128
+// bytes, and registers, where a lane has its own row.
+__device__ __forceinline__ uint32_t turned(uint32_t region, int row, int piece) {
+  return region + row * 128 + ((uint32_t)(piece ^ (row & 7)) << 4);
+}
+
 template <int D, Mode MODE, bool BACK, bool FINE> struct WalkShape : Shape<D> {
   using Shape<D>::TILE;
   static constexpr int IN = MODE == OUTPUTS ? 5 : 4;  // input tiles
@@ -330,18 +336,38 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
     if constexpr (MODE != ENDS) {
       const int srow = D == 128 ? 32 * quarter + lane : 16 * quarter + (lane & 15);
       const bool has_row = D == 128 || lane < 16;
-      const size_t state_at = ((size_t)seg.n * p.H + h) * D * D + (size_t)srow * D;
+      constexpr int ROWS = D / 4;  // of a warp
+      const size_t warp_rows = (size_t)quarter * ROWS * D, state_at = ((size_t)seg.n * p.H + h) * D * D + warp_rows;
       uint64_t s[D / 2];  // two columns each
+      // turned where this warp's part of the operand (of the leaving image) lies
+      const uint32_t region = sb + (MODE == IMAGES ? W::LEAVING : W::Y) + quarter * ROWS * 128;
       dependency_wait();  // the joined states
       {
         // (a call that is cut takes all of them from there: where the caller's states are one buffer, a CTA may
         // have written its own before another has started)
-        const float* from = w.decay ? w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)srow * D : p.s_in ? p.s_in + state_at : nullptr;
+        const float* from = w.decay ? w.carry + ((size_t)slot * p.H + h) * D * D + warp_rows : p.s_in ? p.s_in + state_at : nullptr;
+        // all of its loads are on their way together
+        float4 raw[D / 32][ROWS / 4];
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i) {
-          const float4 x = from ? *reinterpret_cast<const float4*>(from + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-          s[2 * i] = pair(x.x, x.y);
-          s[2 * i + 1] = pair(x.z, x.w);
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+          for (int i = 0; i < ROWS / 4; ++i)
+            raw[b][i] = from ? *reinterpret_cast<const float4*>(from + (4 * i + lane / 8) * D + 32 * b + 4 * (lane % 8)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < ROWS / 4; ++i)
+            st_shared_v4(turned(region, 4 * i + lane / 8, lane % 8), __float_as_uint(raw[b][i].x), __float_as_uint(raw[b][i].y),
+                         __float_as_uint(raw[b][i].z), __float_as_uint(raw[b][i].w));
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t u[4];
+            lds_v4(turned(region, lane & (ROWS - 1), i), u);
+            s[16 * b + 2 * i] = pair(__uint_as_float(u[0]), __uint_as_float(u[1]));
+            s[16 * b + 2 * i + 1] = pair(__uint_as_float(u[2]), __uint_as_float(u[3]));
+          }
         }
       }
       // eight columns to their place in the operand, as the first (second) of their two numbers
@@ -413,13 +439,28 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
         if (lane == 0) mbar_arrive(z_free);
       }
       if (MODE == IMAGES && lane == 0) bulk_wait_all();
-      if (ok && last_seg && p.s_out && has_row) {
+      if (ok && last_seg && p.s_out) {
+        // (the operand's tile: its last product is done, or waited for here)
+        if (MODE == OUTPUTS && nch > 0) ok = wait_for((FINE ? f_done : qs_done) + ((nch - 1) & 1), nch - 1 >> 1 & 1);
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i) {
-          float4 x;
-          unpair(s[2 * i], &x.x, &x.y);
-          unpair(s[2 * i + 1], &x.z, &x.w);
-          *reinterpret_cast<float4*>(p.s_out + state_at + 4 * i) = x;
+        for (int b = 0; b < D / 32; ++b) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 x;
+            unpair(s[16 * b + 2 * i], &x.x, &x.y);
+            unpair(s[16 * b + 2 * i + 1], &x.z, &x.w);
+            if (has_row)
+              st_shared_v4(turned(region, lane, i), __float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < ROWS / 4; ++i) {
+            const int r = 4 * i + lane / 8;
+            uint32_t u[4];
+            lds_v4(turned(region, r, lane % 8), u);
+            if (ok) *reinterpret_cast<uint4*>(p.s_out + state_at + r * D + 32 * b + 4 * (lane % 8)) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
         }
       }
     }
@@ -605,17 +646,30 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
         if (ok && nch > 0) ok = wait_for(z_done + ((nch - 1) & 1), nch - 1 >> 1 & 1);
         if (ok) {
           tc_fence_after_sync();
-          const int srow = D == 128 ? trow : 16 * quarter + (lane & 15);
-          float* to = w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)srow * D + half * (D / 2);
-#pragma unroll
+          // (through the tiles of V', whose products are done)
+          const uint32_t region = sb + W::X + (half * 4 + quarter) * (64 * D);
+          float* to = w.carry + ((size_t)slot * p.H + h) * D * D + (size_t)quarter * (D / 4) * D + half * (D / 2);
+          constexpr int ROW = D * 2;  // bytes of half a row
+#pragma unroll 1
           for (int b = 0; b < D / 2; b += 16) {
             float s[16];
             tmem_ld16(my + W::T_Z + half * (D / 2) + b, s);
             tmem_ld_wait();
             if (D == 128 || lane < 16) {
 #pragma unroll
-              for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(to + b + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+              for (int i = 0; i < 4; ++i)
+                st_shared_v4(region + lane * ROW + ((uint32_t)((b / 4 + i) ^ (lane & (ROW / 16 - 1))) << 4), __float_as_uint(s[4 * i]),
+                             __float_as_uint(s[4 * i + 1]), __float_as_uint(s[4 * i + 2]), __float_as_uint(s[4 * i + 3]));
             }
+          }
+          __syncwarp();
+          constexpr int LANES = ROW / 16;  // to a row
+#pragma unroll 4
+          for (int i = 0; i < D / 4 * LANES / 32; ++i) {
+            const int r = i * (32 / LANES) + lane / LANES, x = lane % LANES;
+            uint32_t u[4];
+            lds_v4(region + r * ROW + ((uint32_t)(x ^ (r & (LANES - 1))) << 4), u);
+            *reinterpret_cast<uint4*>(to + (size_t)r * D + 4 * x) = make_uint4(u[0], u[1], u[2], u[3]);
           }
           if (half == 0 && trow == 0) w.decay[(size_t)slot * p.H + h] = reach;
         }
