@@ -59,18 +59,19 @@ __device__ __forceinline__ uint32_t to_bf16x2(uint64_t v) {
   return pack_bf16x2(a, b);
 }
 
-// Sums over the warp's lanes of 16 numbers each; lane l gets that of number l >> 1.
-__device__ __forceinline__ float sum_lanes(float (&x)[16]) {
+// Sums over the warp's lanes of 8 numbers each; lane l gets that of number l >> 2.
+__device__ __forceinline__ float sum_lanes(float (&x)[8]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 8; k; k /= 2) {
-    const bool up = lane & (2 * k);
+  for (int k = 4; k; k /= 2) {
+    const bool up = lane & (4 * k);
 #pragma unroll
     for (int i = 0; i < k; ++i) {
       const float keep = up ? x[i + k] : x[i], give = up ? x[i] : x[i + k];
-      x[i] = keep + __shfl_xor_sync(~0u, give, 2 * k);
+      x[i] = keep + __shfl_xor_sync(~0u, give, 4 * k);
     }
   }
+  x[0] += __shfl_xor_sync(~0u, x[0], 2);
   return x[0] + __shfl_xor_sync(~0u, x[0], 1);
 }
 
@@ -230,31 +231,27 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
       ok = wait_for(bt_done, 0) && wait_for(at_done, 0);
     }
     if (ok) {
-      // ---- R^T and P^T, earlier tokens on the lanes, 16 later ones at a time, and what a pair gives to the decays
+      // ---- R^T and P^T, earlier tokens on the lanes, 8 later ones at a time, and what a pair gives to the decays
       tc_fence_after_sync();
       uint64_t later = pair(0.f, 0.f);
 #pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        const int i0 = 32 * part + 16 * b;
-        uint32_t u[8], v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = v[i] = 0u;
+      for (int i0 = 32 * part; i0 < 32 * part + 32; i0 += 8) {
+        uint32_t u[4] = {0u, 0u, 0u, 0u}, v[4] = {0u, 0u, 0u, 0u};
         float earlier = 0.f;
-        if (i0 + 15 >= 32 * quarter) {
-          float x[16], y[16], w[16];
-          tmem_ld16(my + W::T1 + i0, x);
-          tmem_ld16(my + W::T2 + i0, y);
+        if (i0 + 7 >= 32 * quarter) {
+          float x[8], y[8], w[8], e[8];  // e: log2 of the decays between, with the other sign
+          tmem_ld8(my + W::T1 + i0, x);
+          tmem_ld8(my + W::T2 + i0, y);
           tmem_ld_wait();
-          float e[16];  // log2 of the decays between
 #pragma unroll
-          for (int i = 0; i < 16; i += 2)
+          for (int i = 0; i < 8; i += 2)
             unpair(add2(*reinterpret_cast<const uint64_t*>(s_g + i0 + i), pair(g_mine, g_mine)), &e[i], &e[i + 1]);
           if (i0 < 32 * quarter + 31) {  // some of the warp's tokens are not before all of these
 #pragma unroll
-            for (int i = 0; i < 16; ++i) e[i] = i0 + i >= trow ? e[i] : INFINITY;
+            for (int i = 0; i < 8; ++i) e[i] = i0 + i >= trow ? e[i] : INFINITY;
           }
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < 8; i += 2) {
             const uint64_t decay = mul2(pair(ex2(-e[i]), ex2(-e[i + 1])), pair(p.scale, p.scale)), z = mul2(decay, pair(x[i], x[i + 1]));
             u[i / 2] = to_bf16x2(z);
             v[i / 2] = to_bf16x2(mul2(decay, pair(y[i], y[i + 1])));
@@ -262,15 +259,16 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
           }
           if (i0 <= 32 * quarter + 31) {  // a token's pair with itself straddles no decay
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = i0 + i == trow ? 0.f : w[i];
+            for (int i = 0; i < 8; ++i) w[i] = i0 + i == trow ? 0.f : w[i];
           }
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) later = add2(later, pair(w[i], w[i + 1]));
+          for (int i = 0; i < 8; i += 2) later = add2(later, pair(w[i], w[i + 1]));
           earlier = sum_lanes(w);
         }
-        tmem_st8u(my + W::T1 + 32 * part + 8 * b, u);
-        tmem_st8u(my + W::T2 + 32 * part + 8 * b, v);
-        if (lane % 2 == 0) s_in[quarter * 128 + i0 + lane / 2] = earlier;
+        const int at = 32 * part + (i0 - 32 * part) / 2;
+        tmem_st4u(my + W::T1 + at, u);
+        tmem_st4u(my + W::T2 + at, v);
+        if (lane % 4 == 0) s_in[quarter * 128 + i0 + lane / 4] = earlier;
       }
       float later_0, later_1;
       unpair(later, &later_0, &later_1);
@@ -285,30 +283,26 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
       // ---- R, later tokens on the lanes
       tc_fence_after_sync();
 #pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        const int j0 = 32 * part + 16 * b;
-        uint32_t u[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] = 0u;
+      for (int j0 = 32 * part; j0 < 32 * part + 32; j0 += 8) {
+        uint32_t u[4] = {0u, 0u, 0u, 0u};
         if (j0 <= 32 * quarter + 31) {
-          float x[16];
-          tmem_ld16(my + W::T0 + j0, x);
+          float x[8], e[8];
+          tmem_ld8(my + W::T0 + j0, x);
           tmem_ld_wait();
-          float e[16];
 #pragma unroll
-          for (int j = 0; j < 16; j += 2)
+          for (int j = 0; j < 8; j += 2)
             unpair(add2(*reinterpret_cast<const uint64_t*>(s_g + j0 + j), pair(g_mine, g_mine)), &e[j], &e[j + 1]);
-          if (j0 + 15 > 32 * quarter) {  // some come after some of the warp's tokens
+          if (j0 + 7 > 32 * quarter) {  // some come after some of the warp's tokens
 #pragma unroll
-            for (int j = 0; j < 16; ++j) e[j] = j0 + j <= trow ? e[j] : -INFINITY;
+            for (int j = 0; j < 8; ++j) e[j] = j0 + j <= trow ? e[j] : -INFINITY;
           }
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
+          for (int j = 0; j < 8; j += 2) {
             const uint64_t decay = mul2(pair(ex2(e[j]), ex2(e[j + 1])), pair(p.scale, p.scale));
             u[j / 2] = to_bf16x2(mul2(decay, pair(x[j], x[j + 1])));
           }
         }
-        tmem_st8u(my + W::T0 + 32 * part + 8 * b, u);
+        tmem_st4u(my + W::T0 + 32 * part + (j0 - 32 * part) / 2, u);
       }
       tmem_st_wait();
       tc_fence_before_sync();
@@ -388,21 +382,25 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
     }
     // ---- the decays' gradients
     if (ok && warp == 0 && (a.dla || a.sums) && (ok = wait_for(sums_ready, 0))) {
-      float total = 0.f, e[4], run = 0.f, x4[4];
+      float total = lane < GRAD_WARPS ? keep * s_dot[lane] : 0.f;
+#pragma unroll 1
+      for (int t = lane; t < 128; t += 32) {  // (what has been added up takes the place of its first part)
+        float in = 0.f, out = 0.f, x = 0.f;
 #pragma unroll
-      for (int i = 0; i < GRAD_WARPS; ++i) total += s_dot[i];
-      total *= keep;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 4 * lane + i;
-        const float in = s_in[t] + s_in[128 + t] + s_in[256 + t] + s_in[384 + t];
-        x4[i] = t < rows ? s_x[t] + s_x[128 + t] + s_x[256 + t] + s_x[384 + t] : 0.f;
-        e[i] = run;
-        run += t < rows ? s_out[t] + s_out[128 + t] + s_out[256 + t] + s_out[384 + t] - in - x4[i] : 0.f;
+        for (int i = 0; i < 512; i += 128) {
+          in += s_in[i + t];
+          out += s_out[i + t];
+          x += s_x[i + t];
+        }
+        total += t < rows ? x : 0.f;
+        s_out[t] = t < rows ? out - in - x : 0.f;
       }
-      float all = x4[0] + x4[1] + x4[2] + x4[3], before = run;
 #pragma unroll
-      for (int o = 16; o; o /= 2) all += __shfl_xor_sync(~0u, all, o);
+      for (int o = 16; o; o /= 2) total += __shfl_xor_sync(~0u, total, o);
+      __syncwarp();
+      const float4 e = *reinterpret_cast<const float4*>(s_out + 4 * lane);
+      const float run = (e.x + e.y) + (e.z + e.w);
+      float before = run;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
         const float x = __shfl_up_sync(~0u, before, o);
@@ -410,19 +408,17 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
       }
       before = __shfl_up_sync(~0u, before, 1);
       if (lane == 0) before = 0.f;
-      total += all;
+      *reinterpret_cast<float4*>(s_x + 4 * lane) = make_float4(before, before + e.x, before + (e.x + e.y), before + (e.x + e.y + e.z));
+      __syncwarp();
       float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 4 * lane + i;
-        const float x = total + (before + e[i]);
-        if (t < rows) {
-          sum += x;
-          const size_t at = (size_t)(row0 + t) * p.H + h;
-          if (!a.sums) {
-            if (p.la_f32) static_cast<float*>(a.dla)[at] = x;
-            else static_cast<__nv_bfloat16*>(a.dla)[at] = __float2bfloat16_rn(x);
-          }
+#pragma unroll 1
+      for (int t = lane; t < rows; t += 32) {
+        const float x = total + s_x[t];
+        sum += x;
+        const size_t at = (size_t)(row0 + t) * p.H + h;
+        if (!a.sums) {
+          if (p.la_f32) static_cast<float*>(a.dla)[at] = x;
+          else static_cast<__nv_bfloat16*>(a.dla)[at] = __float2bfloat16_rn(x);
         }
       }
       if (a.sums) {
