@@ -239,25 +239,20 @@ constexpr int WALK_THREADS = 1024;
 constexpr int LAUNCH_REGS = 64, STATE_REGS = 152, WEIGHT_REGS = 56, VALUE_REGS = 48, OUTPUT_REGS = 56, OTHER_REGS = 40;
 static_assert(4 * STATE_REGS + 8 * (WEIGHT_REGS + VALUE_REGS + OUTPUT_REGS) + 4 * OTHER_REGS <= 32 * LAUNCH_REGS, "registers");
 
-// The tiles of a chunk's inputs.  Where there are queries: the next chunk's keys and queries are already on
-// their way; its values take the place of this one's keys, and the keys and queries of the chunk after it
-// those of the queries and values.  `phase` has a bit for each tile.
-template <Mode MODE> struct Tiles {
-  int k = 0, q = 1, v = 2, k2 = 3, q2 = 4;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int c) {
-    if constexpr (MODE == OUTPUTS) {
-      phase ^= 1u << k | 1u << q | 1u << v;
-      const int k0 = k, q0 = q, v0 = v;
-      k = k2;
-      q = q2;
-      v = k0;
-      k2 = q0;
-      q2 = v0;
-    } else {
-      phase ^= 1u << k | 1u << v;
-      k = (c + 1) & 1;
-      v = 2 + ((c + 1) & 1);
+// The input tiles are a ring that keys, queries and values (keys and values) go through in this order, chunk
+// after chunk: so a chunk's values take the place of the keys of the one before, which are free first, and the
+// next keys and queries that of its queries and values.
+template <Mode MODE> struct Ring {
+  static constexpr int KINDS = MODE == OUTPUTS ? 3 : 2, TILES = MODE == OUTPUTS ? 5 : 4;
+  int tile = 0;        // of a chunk's keys
+  uint32_t turn = 0;   // how often the ring has been gone through, odd or even
+  __device__ __forceinline__ int at(int kind) const { return tile + kind < TILES ? tile + kind : tile + kind - TILES; }
+  __device__ __forceinline__ uint32_t phase(int kind) const { return turn ^ (tile + kind >= TILES ? 1u : 0u); }
+  __device__ __forceinline__ void move(int kinds) {
+    tile += kinds;
+    if (tile >= TILES) {
+      tile -= TILES;
+      turn ^= 1;
     }
   }
 };
@@ -293,9 +288,10 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
   uint64_t *z_free = full + 10, *o_read = full + 11, *a_done = full + 12, *pv_done = full + 13, *zh_done = full + 14;
   // for odd and even chunks: a wait tells a phase from the next one, not from the one after that, and
   // those who wait for these may be a chunk behind
-  uint64_t *qs_done = full + 15, *z_done = full + 17, *f_done = full + 19, *o_done = full + 21, *g_ready = full + 23, *g_free = full + 25;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 27);
-  int* s_bad = reinterpret_cast<int*>(full + 28);                     // [3] some value of the chunk is not finite
+  uint64_t *qs_done = full + 15, *z_done = full + 17, *f_done = full + 19, *o_done = full + 21, *g_ready = full + 23, *g_free = full + 25,
+           *n_ready = full + 27;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(full + 29);
+  int* s_bad = reinterpret_cast<int*>(full + 30);                     // [3] some value of the chunk is not finite
 
   if (tid == 0) {
     for (int i = 0; i < 5; ++i) mbar_init(full + i, 1);
@@ -315,6 +311,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
       mbar_init(f_done + i, 1);
       mbar_init(o_done + i, 8);
       mbar_init(g_ready + i, 1);
+      mbar_init(n_ready + i, 8);
       mbar_init(g_free + i, MODE == ENDS ? 8 : MODE == IMAGES ? 12 : 28);
     }
     mbar_fence_init();
@@ -539,7 +536,8 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
       return (uint32_t)(x / 8) * W::BLOCK + trow * 128 + (((uint32_t)(x % 8) ^ (uint32_t)(trow & 7)) << 4);
     };
     float reach = 0.f;  // ENDS: log2 of the decay from the chunk to the segment's end (start)
-    Tiles<MODE> t;
+    Ring<MODE> t;
+    constexpr int VALUES = MODE == OUTPUTS ? 2 : 1;
 
     // ---------------------------------------------------------------- the weighted values
     // The weight is two bf16 numbers, w1 + w2: the first number of v w is v w1 rounded, what that leaves of
@@ -547,7 +545,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
     auto values = [&](int c) {
       const uint32_t par = c & 1;
       const int rows = rows_of(chunk_of(c));
-      const uint32_t v_at = sb + t.v * W::TILE, k_at = sb + t.k * W::TILE;
+      const uint32_t v_at = sb + t.at(VALUES) * W::TILE, k_at = sb + t.tile * W::TILE;
       if (!wait_for(g_ready + par, c >> 1 & 1)) return false;
       const float g_mine = -s_g[par * 128 + trow], end = -s_g[par * 128 + 127];
       if (MODE == OUTPUTS) {
@@ -563,10 +561,10 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
       const __nv_bfloat162 w1 = __float2bfloat162_rn(weight), w2 = __float2bfloat162_rn(weight - __low2float(w1));
       const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
       if constexpr (MODE == ENDS) reach += end;
-      if (!wait_for(full + t.v, t.phase >> t.v & 1)) return false;
-      if (rows < CHUNK && !wait_for(full + t.k, t.phase >> t.k & 1)) return false;
+      if (!wait_for(full + t.at(VALUES), t.phase(VALUES))) return false;
+      if (rows < CHUNK && !wait_for(full + t.tile, t.turn)) return false;
       if (c > 0 && !wait_for(z_done + (par ^ 1), c - 1 >> 1 & 1)) return false;
-      __nv_bfloat162 odd = zero;
+      // (what comes before the first products goes without anything that they do not wait for)
 #pragma unroll 1
       for (int i = 0; i < PIECES; i += 4) {
         uint32_t u[4][4];
@@ -578,9 +576,8 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const __nv_bfloat162 x = as_bf16x2(u[z][j]), first = __hmul2_rn(x, w1);
-            if (MODE == OUTPUTS) odd = __hfma2(x, zero, odd);  // NaN if one of them is not finite
-            y[j] = real ? as_u32(first) : 0u;
-            if constexpr (MODE != OUTPUTS) rest[j] = real ? as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(first)))) : 0u;
+            y[j] = as_u32(first);
+            if constexpr (MODE != OUTPUTS) rest[j] = as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(first))));
           }
           st_shared_v4(sb + W::X + piece(i + z), y[0], y[1], y[2], y[3]);
           if constexpr (MODE != OUTPUTS) st_shared_v4(sb + W::Y + piece(i + z), rest[0], rest[1], rest[2], rest[3]);
@@ -589,56 +586,73 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
       if (!real) {  // rows of other sequences
 #pragma unroll 1
         for (int i = 0; i < PIECES; ++i) {
+          st_shared_v4(sb + W::X + piece(i), 0u, 0u, 0u, 0u);
+          if (MODE != OUTPUTS) st_shared_v4(sb + W::Y + piece(i), 0u, 0u, 0u, 0u);
           st_shared_v4(v_at + piece(i), 0u, 0u, 0u, 0u);
           st_shared_v4(k_at + piece(i), 0u, 0u, 0u, 0u);
         }
-      } else if (MODE == OUTPUTS && !__hbeq2(odd, zero)) {
-        // such a value is taken out of the product with the weights, where zeros would meet it
-#pragma unroll 1
-        for (int i = 0; i < PIECES; ++i) {
-          uint32_t u[4];
-          lds_v4(v_at + piece(i), u);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int ch = 8 * (half * PIECES + i) + 2 * j;
-            if ((u[j] & 0x7f80u) == 0x7f80u) {
-              u[j] &= 0xffff0000u;
-              atomicMin(s_first + c % 3 * 128 + ch, trow);
-            }
-            if ((u[j] & 0x7f800000u) == 0x7f800000u) {
-              u[j] &= 0xffffu;
-              atomicMin(s_first + c % 3 * 128 + ch + 1, trow);
-            }
-          }
-          st_shared_v4(v_at + piece(i), u[0], u[1], u[2], u[3]);
-        }
-        s_bad[c % 3] = 1;
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(v_ready);
-      if (MODE == OUTPUTS && exact) {  // the second numbers take the place of the first ones
-        if (!wait_for(zh_done, par)) return false;
+      if constexpr (MODE == OUTPUTS) {
+        // a value that is not finite is taken out of the product with the weights, where zeros would meet it
+        __nv_bfloat162 odd = zero;
 #pragma unroll 1
         for (int i = 0; i < PIECES; i += 4) {
           uint32_t u[4][4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) lds_v4(v_at + piece(i + z), u[z]);
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
+          for (int j = 0; j < 16; ++j) odd = __hfma2(as_bf16x2(u[j / 4][j % 4]), zero, odd);  // NaN if one of them is not finite
+        }
+        if (!__hbeq2(odd, zero)) {
+#pragma unroll 1
+          for (int i = 0; i < PIECES; ++i) {
+            uint32_t u[4];
+            lds_v4(v_at + piece(i), u);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 x = as_bf16x2(u[z][j]);
-              u[z][j] = real ? as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(__hmul2_rn(x, w1))))) : 0u;
+              const int ch = 8 * (half * PIECES + i) + 2 * j;
+              if ((u[j] & 0x7f80u) == 0x7f80u) {
+                u[j] &= 0xffff0000u;
+                atomicMin(s_first + c % 3 * 128 + ch, trow);
+              }
+              if ((u[j] & 0x7f800000u) == 0x7f800000u) {
+                u[j] &= 0xffffu;
+                atomicMin(s_first + c % 3 * 128 + ch + 1, trow);
+              }
             }
-            st_shared_v4(sb + W::X + piece(i + z), u[z][0], u[z][1], u[z][2], u[z][3]);
+            st_shared_v4(v_at + piece(i), u[0], u[1], u[2], u[3]);
           }
+          s_bad[c % 3] = 1;
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(l_ready);
+        if (lane == 0) mbar_arrive(n_ready + par);
+        if (exact) {  // the second numbers take the place of the first ones
+          if (!wait_for(zh_done, par)) return false;
+#pragma unroll 1
+          for (int i = 0; i < PIECES; i += 4) {
+            uint32_t u[4][4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) lds_v4(v_at + piece(i + z), u[z]);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 x = as_bf16x2(u[z][j]);
+                u[z][j] = as_u32(__hfma2(x, w2, __hfma2(x, w1, __hneg2(__hmul2_rn(x, w1)))));
+              }
+              st_shared_v4(sb + W::X + piece(i + z), u[z][0], u[z][1], u[z][2], u[z][3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(l_ready);
+        }
       }
-      t.next(c);
+      t.move(Ring<MODE>::KINDS);
       return true;
     };
 
@@ -687,11 +701,11 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
       constexpr int SC = D / 2, ES = FINE ? 4 : 2, TURN = W::TILE / 256 / ES, LANES = W::TILE / 256 / 16;  // columns; lanes to a row's piece
       const int half = warp >> 2 & 1, trow = 32 * quarter + lane;
       const size_t row_bytes = (size_t)p.H * D * ES;
-      Tiles<MODE> t;
+      Ring<MODE> t;
       for (int c = 0; c < nch && ok; ++c) {
         const uint32_t par = c & 1;
         const int rows = rows_of(chunk_of(c));
-        const uint32_t turn = sb + t.v * W::TILE + (warp - 20) * (W::TILE / 8);
+        const uint32_t turn = sb + t.at(2) * W::TILE + (warp - 20) * (W::TILE / 8);
         if (!(ok = wait_for(g_ready + par, c >> 1 & 1))) break;
         const float lead = p.scale * ex2(-s_g[par * 128 + trow]);
         __syncwarp();
@@ -768,57 +782,51 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
               *reinterpret_cast<uint4*>(to + r * row_bytes + b * ES + at * 16) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
           }
         }
-        t.next(c);
+        t.move(3);
       }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(OTHER_REGS));
     if (warp == 28 && lane == 0) {
       // -------------------------------------------------------------- loads
-      auto load = [&](const CUtensorMap* map, int tile, int c) {
-        mbar_arrive_expect_tx(full + tile, W::TILE);
-        for (int b = 0; b < D / 64; ++b)
-          tma_load_3d(smem + tile * W::TILE + b * W::BLOCK, map, full + tile, 64 * b, h, row0 + chunk_of(c) * CHUNK);
-      };
-      uint32_t loads = 0;  // parity of each tile's number of loads
-      if constexpr (MODE == OUTPUTS) {
-        Tiles<MODE> t;
-        if (nch > 0) { load(&map_k, 0, 0); load(&map_q, 1, 0); load(&map_v, 2, 0); loads = 7; }
-        if (nch > 1) { load(&map_k, 3, 1); load(&map_q, 4, 1); loads = 31; }
-        for (int c = 0; c + 1 < nch && ok; ++c) {
-          const int odd = c & 1;
-          const uint32_t par = c >> 1 & 1;
-          if (!(ok = wait_for(z_done + odd, par))) break;
-          load(&map_v, t.k, c + 1);
-          loads ^= 1u << t.k;
-          if (c + 2 < nch) {
-            if (!(ok = wait_for((FINE ? f_done : qs_done) + odd, par))) break;
-            load(&map_k, t.q, c + 2);
-            loads ^= 1u << t.q;
-            if (!(ok = wait_for(o_done + odd, par))) break;
-            load(&map_q, t.v, c + 2);
-            loads ^= 1u << t.v;
+      constexpr int KINDS = Ring<MODE>::KINDS, TILES = Ring<MODE>::TILES;
+      const int items = KINDS * nch;
+      Ring<MODE> t;
+      int kind = 0, c = 0, used = 0, used_c = 0;  // of the item, and of the one whose place it takes
+#pragma unroll 1
+      for (int i = 0; i < items && ok; ++i) {
+        if (i >= TILES) {
+          uint64_t* free = used == 0 ? z_done : MODE != OUTPUTS ? z_done : used == 1 ? (FINE ? f_done : qs_done) : o_done;
+          if (!(ok = wait_for(free + (used_c & 1), used_c >> 1 & 1))) break;
+          if (++used == KINDS) {
+            used = 0;
+            ++used_c;
           }
-          t.next(c);
         }
-      } else {
-        for (int c = 0; c < nch && ok; ++c) {
-          if (c > 1 && !(ok = wait_for(z_done + (c & 1), (c >> 1 & 1) ^ 1))) break;
-          load(&map_k, c & 1, c);
-          load(&map_v, 2 + (c & 1), c);
-          loads ^= 5u << (c & 1);
+        const CUtensorMap* map = kind == 0 ? &map_k : MODE == OUTPUTS && kind == 1 ? &map_q : &map_v;
+        mbar_arrive_expect_tx(full + t.tile, W::TILE);
+#pragma unroll 1
+        for (int b = 0; b < D / 64; ++b)
+          tma_load_3d(smem + t.tile * W::TILE + b * W::BLOCK, map, full + t.tile, 64 * b, h, row0 + chunk_of(c) * CHUNK);
+        t.move(1);
+        if (++kind == KINDS) {
+          kind = 0;
+          ++c;
         }
       }
-      // no copy is in flight when the CTA ends: the last one into each tile has landed
-      for (int i = 0; i < W::IN; ++i) {
-        const bool any = MODE == OUTPUTS ? nch > (i < 3 ? 0 : 1) : nch > (i & 1);
-        if (any) ok = wait_for(full + i, (loads >> i & 1) ^ 1) && ok;
+      // no copy is in flight when the CTA ends: the last one into each tile has landed (after a wait that ran
+      // out, fewer may be on their way than are waited for)
+      Ring<MODE> last;
+      for (int i = 0; i < items; ++i) {
+        if (i + TILES >= items) ok = wait_for(full + last.tile, last.turn) && ok;
+        last.move(1);
       }
     } else if (warp == 29 && lane == 0) {
       // -------------------------------------------------------------- products
       constexpr uint32_t ID_A = make_idesc_bf16(128, 128, false, false), ID_O = make_idesc_bf16(128, D, false, true),
                          ID_Z = make_idesc_bf16(D, D, true, true);
-      Tiles<MODE> t;
+      Ring<MODE> t;
+      constexpr int VALUES = MODE == OUTPUTS ? 2 : 1;
       // D = (D +) A B over K = 64 n; descriptors advance by `in` for each 16 of K and `out` for each 64
       constexpr uint32_t K_IN = 2, K_OUT = W::BLOCK >> 4, MN_IN = 128, MN_OUT = 512;
       auto product = [&](uint32_t to, uint64_t a, uint32_t a_in, uint32_t a_out, uint64_t b, uint32_t b_in, uint32_t b_out, uint32_t id,
@@ -840,10 +848,10 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
 #pragma unroll 1
       for (int c = 0; c < nch && ok; ++c) {
         const uint32_t par = c & 1;
-        const uint32_t k_at = sb + t.k * W::TILE, v_at = sb + t.v * W::TILE, q_at = sb + t.q * W::TILE;
-        if (!(ok = wait_for(full + t.k, t.phase >> t.k & 1))) break;
+        const uint32_t k_at = sb + t.tile * W::TILE, v_at = sb + t.at(VALUES) * W::TILE, q_at = sb + t.at(1) * W::TILE;
+        if (!(ok = wait_for(full + t.tile, t.turn))) break;
         if constexpr (MODE == OUTPUTS) {
-          if (!(ok = wait_for(full + t.q, t.phase >> t.q & 1))) break;
+          if (!(ok = wait_for(full + t.at(1), t.phase(1)))) break;
           product(tb + W::T_A, desc_k(q_at), K_IN, K_OUT, desc_k(k_at), K_IN, K_OUT, ID_A, D / 64, 0);
           umma_commit(a_done);
         }
@@ -868,7 +876,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
             from_state(q_at, true);
             umma_commit(f_done + par);
           }
-          if (!(ok = wait_for(p_ready, par))) break;
+          if (!(ok = wait_for(p_ready, par) && wait_for(n_ready + par, c >> 1 & 1))) break;
           tc_fence_after_sync();
           const uint64_t b = desc_mn(v_at, W::BLOCK);
 #pragma unroll 1
@@ -881,7 +889,7 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
           state_part(k_at, sb + W::Y, true);
           umma_commit(z_done + par);
         }
-        t.next(c);
+        t.move(Ring<MODE>::KINDS);
       }
       if (!ok) {  // what has been issued ends before the CTA does
         umma_commit(pv_done);
@@ -891,11 +899,12 @@ __device__ __forceinline__ void walk(const CUtensorMap& map_q, const CUtensorMap
       }
     } else if (warp == 30) {
       // -------------------------------------------------------------- decays
-      Decays la;
-      if (nch > 0) la.load(p, row0 + chunk_of(0) * CHUNK, rows_of(chunk_of(0)), h);
-      for (int c = 0; c < nch; ++c) {
+      Decays la = {};
+#pragma unroll 1
+      for (int c = -1; c < nch; ++c) {
         const float4 g4 = la.sum(p);
         if (c + 1 < nch) la.load(p, row0 + chunk_of(c + 1) * CHUNK, rows_of(chunk_of(c + 1)), h);
+        if (c < 0) continue;
         if (c > 1 && !(ok = wait_for(g_free + (c & 1), (c >> 1 & 1) ^ 1))) break;
         *reinterpret_cast<float4*>(s_g + (c & 1) * 128 + 4 * lane) = make_float4(-g4.x, -g4.y, -g4.z, -g4.w);
         __syncwarp();
