@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include "kda_internal.h"
+#include "kda_linear.cuh"
 #include "kda_types.cuh"
 
 namespace kda {
@@ -167,8 +168,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
   };
   // adds b to the entry t where this thread holds it in x (vectors from `base` on)
   auto add_bias = [&](float (&x)[PER], int base, int t, float b) {
-    const int at = t - base;
-    if (at < 0 || at >= TILE || at / E % THREADS != tid) return;
+    const unsigned at = t - base;
+    if ((at / E & (THREADS - 1)) != tid || at >= (unsigned)TILE) return;
     const int mine = at / (E * THREADS) * E + at % E;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
@@ -187,26 +188,27 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
     uint32_t bits = 0;
     if (mask && whole) bits = mask[min(((base + (lane / E * THREADS + warp * 32) * E) >> 5) + lane % E, last_word)];
     uint4 raw[PER / E];
+    // the first and the last vector that lie within the row
+    const int least = base < 0 ? base + E : base, most = EVEN ? p.V - E : p.V - E - ((p.V - base) % E + E) % E;
+    if (EVEN || most >= least) {
 #pragma unroll
-    for (int i = 0; i < PER / E; ++i) {
-      const int at = base + (i * THREADS + tid) * E;
-      if constexpr (EVEN) {
-        raw[i] = *reinterpret_cast<const uint4*>(row + min(at, p.V - E));
-        continue;
-      }
-      const int most = p.V - E - ((p.V - base) % E + E) % E;  // the last vector that lies within the row
-      if (at >= 0 && most >= 0) {
-        raw[i] = *reinterpret_cast<const uint4*>(row + min(at, most));
-        unpack<T>(raw[i], x + i * E);
-      }
-      if (at < 0 || (at > most && at < p.V)) {  // a vector that holds something else, too
+      for (int i = 0; i < PER / E; ++i)
+        raw[i] = *reinterpret_cast<const uint4*>(row + min(EVEN ? base + (i * THREADS + tid) * E : max(base + (i * THREADS + tid) * E, least), most));
+    } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[i * E + e] = at + e >= 0 && at + e < p.V ? to_f32(row[at + e]) : 0.f;
-      }
+      for (int i = 0; i < PER / E; ++i) raw[i] = make_uint4(0, 0, 0, 0);
     }
-    if constexpr (EVEN) {
 #pragma unroll
-      for (int i = 0; i < PER / E; ++i) unpack<T>(raw[i], x + i * E);
+    for (int i = 0; i < PER / E; ++i) unpack<T>(raw[i], x + i * E);
+    if constexpr (!EVEN) {
+#pragma unroll
+      for (int i = 0; i < PER / E; ++i) {
+        const int at = base + (i * THREADS + tid) * E;
+        if (at < least || (at > most && at < p.V)) {  // a vector that holds something else, too
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[i * E + e] = at + e >= 0 && at + e < p.V ? to_f32(row[at + e]) : 0.f;
+        }
+      }
     }
     if (counted) {
 #pragma unroll
@@ -235,7 +237,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
       }
     }
     if (u.bias_ids) {
-      for (int j = 0; j < s_listed; ++j) add_bias(x, base, s_id[j], s_bias[j]);
+      // (of 32 listed ones, those that some lane of this warp holds, in their order)
+      for (int j = 0; j < s_listed; j += 32) {
+        const int id = j + lane < s_listed ? s_id[j + lane] : -1;
+        const unsigned at = id - base;
+        unsigned who = __ballot_sync(~0u, at < (unsigned)TILE && (int)(at / E & (THREADS - 1)) >> 5 == warp);
+        for (; who; who &= who - 1) {
+          const int i = __ffs(who) - 1;
+          add_bias(x, base, s_id[j + i], s_bias[j + i]);
+        }
+      }
       for (int j = s_more; j < u.J; ++j) add_bias(x, base, u.bias_ids[(size_t)n * u.J + j], u.bias[(size_t)n * u.J + j]);
     }
 #pragma unroll
@@ -265,6 +276,22 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
   // 2^((x - top) factor), 0 where x is -infinity
   auto weight = [&](float x, float top) { return exp2_fast((x - (top == -INFINITY ? 0.f : top)) * factor); };
 
+  // all of a tile's, two at a time, and their sum
+  auto weights = [&](float (&x)[PER], float top) {
+    const uint64_t less = pair(top == -INFINITY ? -0.f : -top, top == -INFINITY ? -0.f : -top), by = pair(factor, factor);
+    uint64_t sum = pair(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < PER; i += 2) {
+      float a, b;
+      unpair(mul2(add2(pair(x[i], x[i + 1]), less), by), &a, &b);
+      x[i] = exp2_fast(a);
+      x[i + 1] = exp2_fast(b);
+      sum = add2(sum, pair(x[i], x[i + 1]));
+    }
+    float a, b;
+    unpair(sum, &a, &b);
+    return a + b;
+  };
   auto join = [&](const Part& a, const Part& b) {
     const float both = fmaxf(a.top, b.top);
     return Part{both, a.sum * weight(a.top, both) + b.sum * weight(b.top, both), b.top > a.top ? b.at : b.top == a.top ? min(a.at, b.at) : a.at, 0};
@@ -298,51 +325,65 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
         }
         top = fmaxf(top, t);
       }
-      if (!greedy) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          x[i] = weight(x[i], top);
-          sum += x[i];
-        }
-      }
+      if (!greedy) sum = weights(x, top);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      mine = join(mine, {top, sum, at, 0});
+      if (from == lo) mine = {top, sum, at, 0};
+      else mine = join(mine, {top, sum, at, 0});
     }
     // ---- with the other warps' entries, in every CTA
     const int turn = r & 1, parts = cluster * WARPS;
     if (lane < cluster) *all.map_shared_rank(&s_parts[turn][rank * WARPS + warp], lane) = mine;
     all.sync();
-    Part whole{-INFINITY, 0.f, 0x7fffffff, 0};
-    for (int i = lane; i < parts; i += 32) whole = join(whole, s_parts[turn][i]);
+    // the largest of all, then the sums against it; a lane has every 32nd part
+    constexpr int MINE = MOST * WARPS / 32;
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-      whole = join(whole, {__shfl_xor_sync(~0u, whole.top, o), __shfl_xor_sync(~0u, whole.sum, o), __shfl_xor_sync(~0u, whole.at, o), 0});
+    for (int i = 0; i < MINE; ++i)
+      if (lane + 32 * i < parts) top = fmaxf(top, s_parts[turn][lane + 32 * i].top);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+      if (lane + 32 * i >= parts) break;
+      const Part q = s_parts[turn][lane + 32 * i];
+      sum += q.sum * weight(q.top, top);
+      if (q.top == top) at = min(at, q.at);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (greedy) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) at = min(at, __shfl_xor_sync(~0u, at, o));
+    }
     O* to = static_cast<O*>(p.out) + ((size_t)n * p.R + r) * p.V;
-    const float mul = greedy ? whole.sum : whole.sum > 0.f ? weight(mine.top, whole.top) / whole.sum : whole.sum;
+    const float mul = greedy ? sum : sum > 0.f ? weight(mine.top, top) / sum : sum;
     for (int from = lo; from < hi; from += step) {
       const int base = first_of(r, from), end = min(from + step, hi);
       if (slice > step) {
         load(x, r, base, from, end);
-        if (!greedy) {
-#pragma unroll
-          for (int i = 0; i < PER; ++i) x[i] = weight(x[i], mine.top);
-        }
+        if (!greedy) (void)weights(x, mine.top);
       }
       const bool vec = EVEN || ((reinterpret_cast<uintptr_t>(to) + base * (long long)sizeof(O)) & 15) == 0;
 #pragma unroll
       for (int i = 0; i < PER; i += E) {
-        const int at = base + (i / E * THREADS + tid) * E;
-        if (at + E <= from || at >= end) continue;
+        const int id = base + (i / E * THREADS + tid) * E;
+        if (id + E <= from || id >= end) continue;
         float y[E];
+        if (greedy) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = greedy ? (at + e == whole.at ? 1.f + mul : mul) : x[i + e] * mul;
-        if (EVEN || (vec && at >= from && at + E <= end)) {
-          store_vec<O, E>(to + at, y);
+          for (int e = 0; e < E; ++e) y[e] = id + e == at ? 1.f + mul : mul;
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; e += 2) unpair(mul2(pair(x[i + e], x[i + e + 1]), pair(mul, mul)), &y[e], &y[e + 1]);
+        }
+        if (EVEN || (vec && id >= from && id + E <= end)) {
+          store_vec<O, E>(to + id, y);
         } else {
 #pragma unroll
           for (int e = 0; e < E; ++e)
-            if (at + e >= from && at + e < end) to[at + e] = from_f32<O>(y[e]);
+            if (id + e >= from && id + e < end) to[id + e] = from_f32<O>(y[e]);
         }
       }
     }
