@@ -84,7 +84,8 @@ typedef enum {
 } kda_status_t;
 
 /* KDA_F16 and KDA_E4M3 (8 bits: 4 of exponent, 3 of fraction, no infinities)
- * are types of the paged cache and the draft calls only. */
+ * are types of the paged cache and the draft calls only, KDA_F16 also of
+ * kda_logits_probs. */
 typedef enum { KDA_BF16 = 0, KDA_F32 = 1, KDA_F16 = 2, KDA_E4M3 = 3 } kda_dtype_t;
 
 /*
@@ -553,7 +554,8 @@ KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft
  * For the calls below
  *   q, k, v     : bf16, token rows *_stride elements apart (multiples of 16
  *                 bytes), heads of a token d apart, so that slices of one
- *                 projection's output are taken as they are
+ *                 projection's output are taken as they are; kda_linear_fwd
+ *                 and kda_linear_bwd refuse rows that overlap
  *   log_alpha   : la_dtype (KDA_BF16 or KDA_F32), that of row t and head h at
  *                 t * la_token_stride + h * la_head_stride (0 and 1: a fixed
  *                 decay per head).  At most 0; -infinity (and in the chunked
@@ -581,8 +583,9 @@ KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft
  * running sum within a chunk.  Products are sums in fp32.  Operands that are
  * not given in bf16 (weighted values, weights, states) enter them as two bf16
  * numbers each (16 bits), but with KDA_BF16 outputs the weights and the states
- * that only outputs see enter as one.  A value that is not finite makes its
- * channel NaN from its token on; earlier tokens do not see it.
+ * that only outputs see enter as one.  A value that is not finite leaves its
+ * channel not finite from its token on; earlier tokens do not see it.  (Prompts
+ * of up to 24 tokens are taken token by token, without chunks.)
  */
 KDA_API kda_status_t kda_linear_fwd(const void* q, const void* k, const void* v, long long q_stride,
                                     long long k_stride, long long v_stride, const void* log_alpha,
@@ -607,6 +610,8 @@ KDA_API size_t kda_linear_fwd_workspace_size(int N, int T, int H, int d_k, int d
  *                     gradient of decays that are fixed per head)
  *   d_initial_state : fp32, or NULL (not written)
  *   workspace       : kda_linear_bwd_workspace_size() bytes, 16-byte aligned
+ * Gradients alias no input.  Products are of bf16 operands (states, their
+ * gradients and weights are rounded to it once), sums in fp32.
  * Results do not depend on anything but the arguments (no atomics).
  */
 KDA_API kda_status_t kda_linear_bwd(const void* q, const void* k, const void* v, const void* d_out,
@@ -627,6 +632,7 @@ KDA_API size_t kda_linear_bwd_workspace_size(int N, int T, int H, int d_k, int d
  * kda_decode_verify and kda_decode_commit: outputs of K drafted tokens
  * [N, K, H, d] from states that are only read, and the states advanced in
  * place by the first accepted[n] (clamped to [0, K]) of the same tokens.
+ * No output aliases another argument.
  */
 KDA_API kda_status_t kda_linear_step(const void* q, const void* k, const void* v, long long q_stride,
                                      long long k_stride, long long v_stride, const void* log_alpha,

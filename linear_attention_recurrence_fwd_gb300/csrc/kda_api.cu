@@ -514,6 +514,14 @@ kda_status_t validate_linear(const void* q, const void* k, const void* v, long l
   return KDA_OK;
 }
 
+// Row strides of the chunked calls: rows that overlap, or lie further apart than a tensor map reaches, are refused;
+// the stride of a single row says nothing.
+kda_status_t chunked_stride(long long& stride, long long T, int H, int d) {
+  if (T <= 1) stride = (long long)H * d;
+  if (stride < (long long)H * d) return KDA_ERR_INVALID_ARG;
+  return stride < 1LL << 38 ? KDA_OK : KDA_ERR_UNSUPPORTED;
+}
+
 kda_status_t run_linear_tokens(const void* q, const void* k, const void* v, long long q_stride,
                                long long k_stride, long long v_stride, const void* log_alpha,
                                kda_dtype_t la_dtype, long long la_token_stride, long long la_head_stride,
@@ -554,6 +562,10 @@ kda_status_t kda_linear_fwd(const void* q, const void* k, const void* v, long lo
   if (out_dtype != KDA_BF16 && out_dtype != KDA_F32) return KDA_ERR_UNSUPPORTED;
   if ((T > 0 && !out) || (N == 0 ? T > 0 : !cu_seqlens && T % N)) return KDA_ERR_INVALID_ARG;
   if (!aligned16(out) || !aligned16(final_state)) return KDA_ERR_ALIGNMENT;
+  for (long long* s : {&q_stride, &k_stride, &v_stride}) {
+    const kda_status_t apart = chunked_stride(*s, T, H, d_k);
+    if (apart != KDA_OK) return apart;
+  }
   if (N == 0) return KDA_OK;
   const size_t need = kda_linear_fwd_workspace_size(N, T, H, d_k, d_v, cu_seqlens != nullptr);
   if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
@@ -585,6 +597,10 @@ kda_status_t kda_linear_bwd(const void* q, const void* k, const void* v, const v
       !aligned16(dv) || !aligned16(d_initial_state) ||
       (reinterpret_cast<uintptr_t>(dlog_alpha) & (element_bytes(la_dtype) - 1)))
     return KDA_ERR_ALIGNMENT;
+  for (long long* s : {&q_stride, &k_stride, &v_stride, &d_out_stride}) {
+    const kda_status_t apart = chunked_stride(*s, T, H, d_k);
+    if (apart != KDA_OK) return apart;
+  }
   if (N == 0) return KDA_OK;
   const size_t need = kda_linear_bwd_workspace_size(N, T, H, d_k, d_v, cu_seqlens != nullptr);
   if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;

@@ -45,6 +45,18 @@ def test_backward(lib, args, code):
     assert bwd(lib, **args) == code
 
 
+@pytest.mark.parametrize("name", ["qs", "ks", "vs"])
+def test_rows_that_overlap_or_lie_too_far_apart(lib, name):
+    # one tensor map holds an operand's rows: 2^40 bytes between two at most
+    assert fwd(lib, **{name: 248}) == fwd(lib, **{name: 0}) == 1
+    assert fwd(lib, **{name: 1 << 38}) == 2
+
+
+def test_gradient_rows_that_overlap_or_lie_too_far_apart(lib):
+    assert bwd(lib, dos=248) == bwd(lib, dos=0) == 1
+    assert bwd(lib, dos=1 << 38) == 2
+
+
 def test_nothing_to_do_and_workspaces(lib):
     assert fwd(lib, N=0, T=0, q=None, k=None, v=None, la=None, out=None) == 0
     assert lib.kda_linear_fwd_workspace_size(0, 10, 2, 128, 128, 0) == 0
