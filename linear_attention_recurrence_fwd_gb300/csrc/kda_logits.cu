@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
     if (u.bias_ids) {
       // (of 32 listed ones, those that some lane of this warp holds, in their order)
       for (int j = 0; j < s_listed; j += 32) {
-        const int id = j + lane < s_listed ? s_id[j + lane] : -1;
+        const int id = j + lane < s_listed ? s_id[j + lane] : 0x7fffffff;  // (no tile's: tiles start from -7 on)
         const unsigned at = id - base;
         unsigned who = __ballot_sync(~0u, at < (unsigned)TILE && (int)(at / E & (THREADS - 1)) >> 5 == warp);
         for (; who; who &= who - 1) {

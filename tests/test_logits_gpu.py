@@ -120,6 +120,18 @@ def test_rules(N, R, V, L, J, mask, dtype, out_dtype):
     check(logits_of(N, R, V, dtype, V), rules(N, R, V, L, J, mask, V), out_dtype)
 
 
+@pytest.mark.parametrize("V", [101, 4099, 20001])
+def test_biases_of_an_earlier_call_stay_there(V):
+    # Rows that start between vectors: the first vector holds entries before the row.  The earlier call leaves a full
+    # list of biases, of entries that the later one has and gives none for, in every SM's shared memory.
+    before = {"bias_ids": torch.arange(992, dtype=torch.int32).remainder(96).repeat(600, 1), "bias": torch.full((600, 992), 3.0)}
+    x = logits_of(600, 1, 128, torch.float32, 3)
+    u = {"bias_ids": torch.tensor([[50]], dtype=torch.int32), "bias": torch.tensor([[0.5]])}
+    for dtype in (torch.float32, torch.bfloat16):
+        kda.kda_logits_probs(x.cuda(), **{k: v.cuda() for k, v in before.items()})
+        check(logits_of(1, 8, V, dtype, V), u)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("V", [131072, 131080, 200000, 262145, 300000, 409600])
 def test_large_vocabularies(V, dtype):
