@@ -21,6 +21,13 @@
 // every 32 so that lanes 4 or 8 entries apart meet no bank twice.  The counts are whole numbers, so the order
 // of the adding does not matter; a request's biases are kept in their order.  A
 // row's drafts are added as the rows go by.
+//
+// Measured: 256 requests of 5 rows of 131072 (fp32, everything given) 332 us, floor 201; without rules 247, the mask
+// adds 9, biases 18, penalties 55.  DRAM is at 51 %, issue slots at 46 %: 189 million warp instructions, 36 to each 32
+// entries.  37 requests of 8 rows of 50021 in bf16 49 us, floor 9: 73 instructions to each 32 entries (edges, counts
+// read one by one), two groups of a request's rows that each count its history.  One request 6.4 to 8.4 us, dependent
+// loads and two barriers.  Dropped: 16 entries to each of 1024 threads, with the next row's loads ahead (705 us without
+// rules); sums and stores in one loop over tiles, so that the loads come once in the code (383 us, spills).
 #include <algorithm>
 
 #include <cooperative_groups.h>
