@@ -16,8 +16,8 @@
 // one barrier for KT tokens.
 //
 // Measured (32 heads of 128): one token for 256 requests 158 us, 6.8 TB/s, the
-// copy bandwidth; five tokens of 61 requests 38 us to verify (134 MB) and 43 to
-// commit (268 MB, 6.2 TB/s); one request 4.3 us.  KT of 2, 4, 5, 6 and 8 gave
+// copy bandwidth; five tokens of 61 requests 38 us to verify (140 MB) and 43 to
+// commit (264 MB, 6.1 TB/s); one request 4.3 us.  KT of 2, 4, 5, 6 and 8 gave
 // 43, 41, 38, 39 and 43 us for the verification, a launch bound of four CTAs on
 // an SM 55 us for the commit (spills).
 #include <cuda_bf16.h>
