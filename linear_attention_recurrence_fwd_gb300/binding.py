@@ -698,43 +698,54 @@ def kda_draft_accept(draft_tokens, draft_probs, target_probs, uniform, draft_len
     return counts, tokens
 
 
+def _linear_stride(x, H, d, name, dev):
+    """The elements between the tokens of x, whose heads must be packed; H * d where there are none between."""
+    if x.is_contiguous() and x.get_device() == dev:
+        return H * d
+    s = _token_stride(x, H, d, name, dev)
+    return s if x.numel() > H * d else H * d
+
+
 def _linear_tokens(k, lead, others, names):
     """Heads, head dim, GPU and the token strides of k and of the others, all [*lead, H, d] in bf16."""
     shape = k.shape
     if len(shape) != lead + 2:
         raise ValueError(f"k must have {lead + 2} dimensions here")
-    H, d, dev, st = shape[-2], shape[-1], k.get_device(), k.stride()
-    if dev < 0 or k.dtype != torch.bfloat16:
+    H, d, dev = shape[-2], shape[-1], k.get_device()
+    if dev < 0 or k.dtype is not torch.bfloat16:
         raise ValueError("q, k and v must be CUDA tensors of bfloat16")
-    one = shape[:-2].numel() <= 1  # no stride between tokens
-    first = H * d if one else _token_stride(k, H, d, "k", dev)
-    strides = [first]
+    strides = [_linear_stride(k, H, d, "k", dev)]
     for x, name in zip(others, names):
-        if x.shape != shape or x.dtype != torch.bfloat16:
+        if x.shape != shape or x.dtype is not torch.bfloat16:
             raise ValueError(f"{name} must be bfloat16 of k's shape {tuple(shape)}")
-        if x.stride() == st and x.get_device() == dev:
-            strides.append(first)
-        else:
-            s = _token_stride(x, H, d, name, dev)
-            strides.append(H * d if one else s)
+        strides.append(_linear_stride(x, H, d, name, dev))
     return H, d, dev, strides
 
 
-def _linear_decay(log_alpha, lead, H, dev):
-    """What the C calls take of log_alpha [*lead, H], or [H] for fixed decays: address, type, strides."""
+def _linear_decay(log_alpha, rows, H, dev):
+    """What the C calls take of log_alpha of shape `rows` = [*lead, H], or [H] for fixed decays: address, type, strides."""
     code = _CODES.get(log_alpha.dtype)
     if code not in (KDA_BF16, KDA_F32) or log_alpha.get_device() != dev:
         raise ValueError(f"log_alpha must be bfloat16 or float32 on cuda:{dev}")
-    s = log_alpha.stride()
-    if log_alpha.shape == (H,):
-        return log_alpha.data_ptr(), code, 0, s[0]
-    if log_alpha.shape != tuple(lead) + (H,):
-        raise ValueError(f"log_alpha must be {tuple(lead) + (H,)} or ({H},)")
-    if len(lead) == 2:
-        if lead[0] > 1 and lead[1] > 1 and s[0] != lead[1] * s[1]:
+    if log_alpha.shape == rows:
+        if log_alpha.is_contiguous():
+            return log_alpha.data_ptr(), code, H, 1
+        s = log_alpha.stride()
+        if len(rows) == 2:
+            return log_alpha.data_ptr(), code, s[0], s[1]
+        if rows[0] > 1 and rows[1] > 1 and s[0] != rows[1] * s[1]:
             raise ValueError("the tokens of log_alpha must be evenly spaced")
-        return log_alpha.data_ptr(), code, s[1] if lead[1] > 1 else s[0], s[2]
-    return log_alpha.data_ptr(), code, s[0], s[1]
+        return log_alpha.data_ptr(), code, s[1] if rows[1] > 1 else s[0], s[2]
+    if log_alpha.shape != (H,):
+        raise ValueError(f"log_alpha must be {tuple(rows)} or ({H},)")
+    return log_alpha.data_ptr(), code, 0, log_alpha.stride(0)
+
+
+def _linear_like(k, dtype, stream):
+    """A new contiguous tensor of k's shape."""
+    if stream is None and dtype is torch.bfloat16 and k.is_contiguous():
+        return torch.empty_like(k)
+    return _empty(k.shape, dtype, k.device, stream)
 
 
 def _linear_state(state, shape, name, dev):
@@ -746,15 +757,15 @@ def _linear_state(state, shape, name, dev):
     return state.data_ptr()
 
 
-def _linear_out(out, shape, dtype, device, dev, stream):
-    """A contiguous output of this shape: `out`, checked, or a new one."""
+def _linear_out(out, k, dtype, dev, stream):
+    """A contiguous output of k's shape: `out`, checked, or a new one."""
     if out is None:
         if dtype not in (torch.bfloat16, torch.float32):
             raise ValueError(f"unsupported output dtype {dtype}")
-        return _empty(shape, dtype, device, stream)
-    if out.shape != shape or out.get_device() != dev or not out.is_contiguous() or out.dtype not in (
+        return _linear_like(k, dtype, stream)
+    if out.shape != k.shape or out.get_device() != dev or not out.is_contiguous() or out.dtype not in (
             torch.bfloat16, torch.float32):
-        raise ValueError(f"out must be a contiguous bfloat16 or float32 tensor {tuple(shape)} on cuda:{dev}")
+        raise ValueError(f"out must be a contiguous bfloat16 or float32 tensor {tuple(k.shape)} on cuda:{dev}")
     return out
 
 
@@ -767,14 +778,14 @@ def _linear_workspace(back, device, N, T, H, d, packed):
 
 
 def _linear_sequences(shape, cu_seqlens):
-    """(sequences, token rows, [*lead]) of k [B, T, H, d], or [T, H, d] with cu_seqlens."""
+    """(sequences, token rows) of k [B, T, H, d], or [T, H, d] with cu_seqlens."""
     if cu_seqlens is None:
         if len(shape) != 4:
             raise ValueError("q, k and v must be [B, T, H, d], or [T, H, d] with cu_seqlens")
-        return shape[0], shape[0] * shape[1], shape[:2]
+        return shape[0], shape[0] * shape[1]
     if len(shape) != 3:
         raise ValueError("with cu_seqlens q, k and v must be [T, H, d]")
-    return cu_seqlens.numel() - 1, shape[0], shape[:1]
+    return cu_seqlens.numel() - 1, shape[0]
 
 
 def kda_linear_fwd(q, k, v, log_alpha, initial_state=None, scale=1.0, out_dtype=torch.float32,
@@ -787,14 +798,14 @@ def kda_linear_fwd(q, k, v, log_alpha, initial_state=None, scale=1.0, out_dtype=
     initial_state [N,H,d,d] fp32 or None.  Returns (out, final_state fp32 or None)."""
     lib = _lib or load()
     shape = k.shape
-    N, T, lead = _linear_sequences(shape, cu_seqlens)
-    H, d, dev, (ks, qs, vs) = _linear_tokens(k, len(lead), (q, v), ("q", "v"))
-    decay = _linear_decay(log_alpha, lead, H, dev)
+    N, T = _linear_sequences(shape, cu_seqlens)
+    H, d, dev, (ks, qs, vs) = _linear_tokens(k, len(shape) - 2, (q, v), ("q", "v"))
+    decay = _linear_decay(log_alpha, shape[:-1], H, dev)
     states = (N, H, d, d)
     s0 = _linear_state(initial_state, states, "initial_state", dev)
     cu = _int32_ptr(cu_seqlens, N + 1, "cu_seqlens", dev)
     raw_stream = _stream_of(stream, dev)
-    out = _linear_out(out, shape, out_dtype, k.device, dev, stream)
+    out = _linear_out(out, k, out_dtype, dev, stream)
     if final_state is None and output_final_state:
         final_state = _empty(states, torch.float32, k.device, stream)
     s1 = _linear_state(final_state, states, "final_state", dev)
@@ -817,27 +828,27 @@ def kda_linear_bwd(q, k, v, log_alpha, d_out, initial_state=None, d_final_state=
     asked for)."""
     lib = _lib or load()
     shape = k.shape
-    N, T, lead = _linear_sequences(shape, cu_seqlens)
-    H, d, dev, (ks, qs, vs, os_) = _linear_tokens(k, len(lead), (q, v, d_out), ("q", "v", "d_out"))
-    decay = _linear_decay(log_alpha, lead, H, dev)
+    N, T = _linear_sequences(shape, cu_seqlens)
+    H, d, dev, (ks, qs, vs, os_) = _linear_tokens(k, len(shape) - 2, (q, v, d_out), ("q", "v", "d_out"))
+    decay = _linear_decay(log_alpha, shape[:-1], H, dev)
     states = (N, H, d, d)
     s0 = _linear_state(initial_state, states, "initial_state", dev)
     d1 = _linear_state(d_final_state, states, "d_final_state", dev)
     cu = _int32_ptr(cu_seqlens, N + 1, "cu_seqlens", dev)
     raw_stream = _stream_of(stream, dev)
-    g = {n: _empty(shape, torch.bfloat16, k.device, stream) for n in ("q", "k", "v")}
-    g["log_alpha"] = _empty(log_alpha.shape, log_alpha.dtype, k.device, stream) if want_log_alpha_grad else None
-    g["initial_state"] = _empty(states, torch.float32, k.device, stream) if want_initial_state_grad else None
+    dq, dk, dv = (_linear_like(k, torch.bfloat16, stream) for _ in range(3))
+    dla = _empty(log_alpha.shape, log_alpha.dtype, k.device, stream) if want_log_alpha_grad else None
+    ds0 = _empty(states, torch.float32, k.device, stream) if want_initial_state_grad else None
     need = _linear_workspace(True, dev, N, T, H, d, cu is not None)
     ws = _empty(need, torch.uint8, k.device, stream) if need else None
     code = lib.kda_linear_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), d_out.data_ptr(), qs, ks, vs, os_, *decay, cu, s0, d1,
-        *(g[n].data_ptr() for n in ("q", "k", "v")), g["log_alpha"].data_ptr() if want_log_alpha_grad else None,
-        log_alpha.dim() == 1, g["initial_state"].data_ptr() if want_initial_state_grad else None, N, T, H, d, d, scale,
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), None if dla is None else dla.data_ptr(), log_alpha.dim() == 1,
+        None if ds0 is None else ds0.data_ptr(), N, T, H, d, d, scale,
         None if ws is None else ws.data_ptr(), need, raw_stream)
     if code:
         raise KDAError(code, "kda_linear_bwd")
-    return g
+    return {"q": dq, "k": dk, "v": dv, "log_alpha": dla, "initial_state": ds0}
 
 
 def kda_linear_step(q, k, v, log_alpha, state, scale=1.0, out=None, out_dtype=torch.float32, stream=None):
@@ -846,10 +857,10 @@ def kda_linear_step(q, k, v, log_alpha, state, scale=1.0, out=None, out_dtype=to
     lib = _lib or load()
     H, d, dev, (ks, qs, vs) = _linear_tokens(k, 1, (q, v), ("q", "v"))
     N = k.shape[0]
-    decay = _linear_decay(log_alpha, (N,), H, dev)
+    decay = _linear_decay(log_alpha, k.shape[:-1], H, dev)
     s = _linear_state(state, (N, H, d, d), "state", dev)
     raw_stream = _stream_of(stream, dev)
-    out = _linear_out(out, k.shape, out_dtype, k.device, dev, stream)
+    out = _linear_out(out, k, out_dtype, dev, stream)
     code = lib.kda_linear_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, *decay, s, out.data_ptr(),
                                _CODES[out.dtype], N, H, d, d, scale, raw_stream)
     if code:
@@ -864,10 +875,10 @@ def kda_linear_verify(q, k, v, log_alpha, state, scale=1.0, out_dtype=torch.floa
     lib = _lib or load()
     H, d, dev, (ks, qs, vs) = _linear_tokens(k, 2, (q, v), ("q", "v"))
     N, K = k.shape[:2]
-    decay = _linear_decay(log_alpha, (N, K), H, dev)
+    decay = _linear_decay(log_alpha, k.shape[:-1], H, dev)
     s = _linear_state(state, (N, H, d, d), "state", dev)
     raw_stream = _stream_of(stream, dev)
-    out = _linear_out(out, k.shape, out_dtype, k.device, dev, stream)
+    out = _linear_out(out, k, out_dtype, dev, stream)
     code = lib.kda_linear_verify(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, *decay, s, out.data_ptr(),
                                  _CODES[out.dtype], N, K, H, d, d, scale, raw_stream)
     if code:
@@ -881,7 +892,7 @@ def kda_linear_commit(k, v, log_alpha, state, accepted, stream=None):
     lib = _lib or load()
     H, d, dev, (ks, vs) = _linear_tokens(k, 2, (v,), ("v",))
     N, K = k.shape[:2]
-    decay = _linear_decay(log_alpha, (N, K), H, dev)
+    decay = _linear_decay(log_alpha, k.shape[:-1], H, dev)
     if accepted is None:
         raise ValueError("accepted is needed")
     code = lib.kda_linear_commit(k.data_ptr(), v.data_ptr(), ks, vs, *decay,

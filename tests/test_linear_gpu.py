@@ -292,6 +292,25 @@ def test_step_slices_and_fixed_decays():
     assert torch.equal(out, same) and torch.equal(a, b)
 
 
+def test_heads_of_a_single_token_must_be_packed():
+    x = on_gpu(inputs((1,), 2, 64, "mixed", 26))
+    s = torch.zeros((1, 2, 64, 64), device="cuda")
+    apart = {n: torch.cat([x[n], x[n]], -1)[..., :64] for n in "qkv"}  # the same values, heads 128 apart
+    for n in "qkv":
+        y = {**x, n: apart[n]}
+        with pytest.raises(ValueError):
+            kda.kda_linear_step(y["q"], y["k"], y["v"], x["log_alpha"], s)
+        with pytest.raises(ValueError):
+            kda.kda_linear_fwd(y["q"][None], y["k"][None], y["v"][None], x["log_alpha"][None])
+    with pytest.raises(ValueError):
+        kda.kda_linear_step(*apart.values(), x["log_alpha"], s)
+    # a token's own place in a longer row is no matter
+    inside = {n: torch.cat([x[n], x[n]], 1)[:, :2] for n in "qkv"}
+    a, b = s.clone(), s.clone()
+    assert torch.equal(kda.kda_linear_step(x["q"], x["k"], x["v"], x["log_alpha"], a),
+                       kda.kda_linear_step(*inside.values(), x["log_alpha"], b)) and torch.equal(a, b)
+
+
 def test_arguments_are_checked():
     x = on_gpu(inputs((2, 5), 2, 64, "mixed", 25))
     q, k, v, la = x["q"], x["k"], x["v"], x["log_alpha"]
