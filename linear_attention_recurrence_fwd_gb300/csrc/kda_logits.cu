@@ -92,12 +92,17 @@ template <typename O, int E> __device__ __forceinline__ void store_vec(O* to, co
   }
 }
 
+// Words of shared memory for a slice's counts: where rows start between vectors, one is left out after every 32, and
+// some on either side stay 0, for the entries of a vector that lie outside.
+constexpr int BEFORE = 12;
+template <bool EVEN> constexpr __host__ __device__ int said_words(int slice) { return EVEN ? slice : slice + slice / 32 + 2 * BEFORE; }
+
 // EVEN: every row starts with a vector.
 template <typename T, typename O, int THREADS, bool EVEN>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsProblem p, int cluster, int slice, int rows, int step) {
   namespace cg = cooperative_groups;
   constexpr int E = Vec<T>::E, TILE = THREADS * PER, WARPS = THREADS / 32;
-  extern __shared__ __align__(16) uint32_t s_said[];  // [slice], see said_at; only where something is counted
+  extern __shared__ __align__(16) uint32_t s_said[];  // [said_words], see said_at; only where something is counted
   __shared__ Part s_parts[2][MOST * WARPS];
   __shared__ int s_id[LIST];
   __shared__ float s_bias[LIST];
@@ -112,7 +117,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
 
   // ---- what this request has said, and its biases
   const bool counted = u.repetition || u.presence || u.frequency;
-  auto said_at = [&](int t) { return EVEN ? t - lo : t - lo + ((t - lo) >> 5); };
+  auto said_at = [&](int t) { return EVEN ? t - lo : t - lo + ((t - lo) >> 5) + BEFORE; };
   if (counted) {
     const int L = u.tokens ? (u.lens ? min(max(u.lens[n], 0), u.L) : u.L) : 0;
     const int prompt = u.prompt_lens ? u.prompt_lens[n] : 0;
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
       for (int i = 0; i < AHEAD; ++i) t[i] = i0 + i * THREADS < L ? said[i0 + i * THREADS] : -1;
     };
     read(tid);
-    for (int i = 4 * tid; i < (EVEN ? slice : slice + slice / 32); i += 4 * THREADS)
+    for (int i = 4 * tid; i < said_words<EVEN>(slice); i += 4 * THREADS)
       *reinterpret_cast<uint4*>(s_said + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     for (int i0 = tid; i0 < L; i0 += AHEAD * THREADS) {
@@ -241,8 +246,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
             c[e] = w.x; c[e + 1] = w.y; c[e + 2] = w.z; c[e + 3] = w.w;
           }
         } else {
+          // (counts of entries outside the tile do no harm: those leave below)
+          const int o = min(at - lo, slice), turn = 32 - (o & 31);
+          const uint32_t* here = s_said + o + (o >> 5) + BEFORE;
 #pragma unroll
-          for (int e = 0; e < E; ++e) c[e] = at + e >= from && at + e < end ? s_said[said_at(at + e)] : 0u;
+          for (int e = 0; e < E; ++e) c[e] = (e >= turn ? here + 1 : here)[e];
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) any |= c[e];
@@ -419,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
 template <typename T, typename O, int THREADS, bool EVEN>
 cudaError_t launch_kernel(const LogitsProblem& p, int cluster, int slice, int rows, int step, cudaStream_t stream) {
   const bool counted = p.rules.repetition || p.rules.presence || p.rules.frequency;
-  const size_t smem = counted ? (size_t)(EVEN ? slice : (slice + slice / 32 + 3) / 4 * 4) * 4 : 0;
+  const size_t smem = counted ? (size_t)((said_words<EVEN>(slice) + 3) / 4 * 4) * 4 : 0;
   auto kernel = logits_kernel<T, O, THREADS, EVEN>;
   if (smem > 32 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
