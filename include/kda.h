@@ -580,7 +580,9 @@ KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft
  *   workspace     : kda_linear_fwd_workspace_size() bytes, 16-byte aligned.
  *                   Calls that share it must not overlap on the GPU.
  * Decays between tokens are exponentials of differences of log_alpha's fp32
- * running sum within a chunk.  Products are sums in fp32.  Operands that are
+ * running sum within a chunk, each at least -104: a weight is off by up to 2^-24
+ * of that sum for each addition (1e-6 of it where a chunk's decays multiply to
+ * e^-20, 1e-4 where strong ones among weak ones make that e^-1000).  Products are sums in fp32.  Operands that are
  * not given in bf16 (weighted values, weights, states) enter them as two bf16
  * numbers each (16 bits), but with KDA_BF16 outputs the weights and the states
  * that only outputs see enter as one.  A value that is not finite leaves its
@@ -611,7 +613,9 @@ KDA_API size_t kda_linear_fwd_workspace_size(int N, int T, int H, int d_k, int d
  *   d_initial_state : fp32, or NULL (not written)
  *   workspace       : kda_linear_bwd_workspace_size() bytes, 16-byte aligned
  * Gradients alias no input.  Products are of bf16 operands (states, their
- * gradients and weights are rounded to it once), sums in fp32.
+ * gradients and weights are rounded to it once), sums in fp32; so dlog_alpha is
+ * as good as bf16 operands make it in fp32, too (2^-8 of its terms, which may
+ * cancel).
  * Results do not depend on anything but the arguments (no atomics).
  */
 KDA_API kda_status_t kda_linear_bwd(const void* q, const void* k, const void* v, const void* d_out,
