@@ -582,8 +582,9 @@ KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft
  * Decays between tokens are exponentials of differences of log_alpha's fp32
  * running sum within a chunk, each at least -104: a weight is off by up to 2^-24
  * of that sum for each addition (1e-6 of it where a chunk's decays multiply to
- * e^-20, 1e-4 where strong ones among weak ones make that e^-1000).  Products are sums in fp32.  Operands that are
- * not given in bf16 (weighted values, weights, states) enter them as two bf16
+ * e^-20, 1e-4 where strong ones among weak ones make that e^-1000).  Products
+ * are sums in fp32.  Operands that are not given in bf16 (weighted values,
+ * weights, states) enter them as two bf16
  * numbers each (16 bits), but with KDA_BF16 outputs the weights and the states
  * that only outputs see enter as one.  A value that is not finite leaves its
  * channel not finite from its token on; earlier tokens do not see it.  (Prompts

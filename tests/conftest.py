@@ -1,3 +1,4 @@
+import ctypes
 import os
 import sys
 
@@ -20,3 +21,13 @@ def cuda_device():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     return torch.device("cuda:0")
+
+
+@pytest.fixture(autouse=True)
+def addressed_objects_live(request, monkeypatch):
+    """What a test on the CPU takes the address of lives until the test ends.  (The address of a temporary outlives it:
+    whether the freed structure's first field then reads as NULL depends on what else the heap holds.)"""
+    if request.node.get_closest_marker("gpu"):
+        return
+    address, kept = ctypes.addressof, []
+    monkeypatch.setattr(ctypes, "addressof", lambda x: (kept.append(x), address(x))[1])
