@@ -234,7 +234,7 @@ __device__ __forceinline__ uint32_t turned(uint32_t region, int row, int piece) 
 template <int D, Mode MODE, bool BACK, bool FINE> struct WalkShape : Shape<D> {
   using Shape<D>::TILE;
   static constexpr int IN = MODE == OUTPUTS ? 5 : 4;  // input tiles
-  static constexpr uint32_t X = IN * TILE, Y = X + TILE, LEAVING = Y + TILE, MISC = LEAVING + (MODE == IMAGES ? TILE : 0), SMEM_USED = MISC + 3072;
+  static constexpr uint32_t X = IN * TILE, Y = X + TILE, LEAVING = Y + TILE, MISC = LEAVING + (MODE == IMAGES ? TILE : 0), SMEM_USED = MISC + 3 * 1024;
   // one CTA on an SM: each takes all of tensor memory
   static constexpr uint32_t SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   // scores and weights; what the state gives; what the weights give; the chunk's part of the state
