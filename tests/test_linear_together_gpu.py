@@ -141,3 +141,36 @@ def test_a_repeated_token_is_penalised(example):
     others[[7, 9, 11]] = False
     ratio = (with_ / without)[0, 0, others]
     assert torch.allclose(ratio, ratio[:1].expand_as(ratio), rtol=1e-4)
+
+
+def test_offsets_past_32_bits():
+    T, cut, H, d = 600_000, 590_000, 32, 128  # 2.5 * 10^9 elements a tensor
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v, do = (torch.randn((1, T, H, d), generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    la = -0.1 * torch.rand((1, T, H), generator=g, device="cuda")
+    out, state = kda.kda_linear_fwd(q, k, v, la, scale=d ** -1.0, out_dtype=torch.bfloat16)
+    _, before = kda.kda_linear_fwd(q[:, :cut], k[:, :cut], v[:, :cut], la[:, :cut], scale=d ** -1.0, out_dtype=torch.bfloat16)
+    tail = [t[:, cut:] for t in (q, k, v, la)]
+    out_tail, state_tail = kda.kda_linear_fwd(*tail, before, scale=d ** -1.0, out_dtype=torch.bfloat16)
+
+    def off(a, b):
+        return float((a.double() - b.double()).norm() / b.double().norm())
+
+    # both are within 2.5 half-steps of bf16 (fp32 sums of 16-bit numbers for the state) of the same numbers, in the 2-norm
+    assert off(out[:, cut:], out_tail) < 2 * 2.5 * 2.0 ** -8 and off(state, state_tail) < 2 * 2.0 ** -15
+    a = kda.kda_linear_bwd(q, k, v, la, do, scale=d ** -1.0)
+    b = kda.kda_linear_bwd(*tail, do[:, cut:], before, scale=d ** -1.0)
+    for n in ("q", "k", "v", "log_alpha"):
+        assert off(a[n][:, cut:], b[n]) < 2 * 2.5 * 2.0 ** -8, n
+
+
+def test_probabilities_past_32_bits():
+    N, R, V = 1400, 4, 400_001
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.empty((N, R, V), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    u = {"tokens": torch.randint(0, V, (N, 300), generator=g, device="cuda", dtype=torch.int32),
+         "repetition": torch.full((N,), 1.2, device="cuda"),
+         "mask": torch.randint(-2 ** 31, 2 ** 31 - 1, (N, R, (V + 31) // 32), generator=g, device="cuda", dtype=torch.int32)}
+    p = kda.kda_logits_probs(x, out_dtype=torch.bfloat16, **u)
+    last = kda.kda_logits_probs(x[-2:].clone(), out_dtype=torch.bfloat16, **{n: t[-2:].clone() for n, t in u.items()})
+    assert torch.equal(p[-2:], last)
