@@ -588,7 +588,7 @@ KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft
  * numbers each (16 bits), but with KDA_BF16 outputs the weights and the states
  * that only outputs see enter as one.  A value that is not finite leaves its
  * channel not finite from its token on; earlier tokens do not see it.  (Prompts
- * of up to 24 tokens are taken token by token, without chunks.)
+ * of a few tokens are taken token by token, without chunks.)
  */
 KDA_API kda_status_t kda_linear_fwd(const void* q, const void* k, const void* v, long long q_stride,
                                     long long k_stride, long long v_stride, const void* log_alpha,

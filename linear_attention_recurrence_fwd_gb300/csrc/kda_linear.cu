@@ -54,11 +54,15 @@ size_t linear_fwd_workspace_bytes(int n_seq, int T, int H, int d, bool packed) {
 
 cudaError_t launch_linear_fwd(const LinearProblem& p, void* workspace, cudaStream_t stream) {
   if (p.cu_seqlens) check_offsets_kernel<<<1, 256, 0, stream>>>(p);
-  // Few tokens are sooner done one after the other, in one launch without tensor memory to set up: 32 heads of 128,
-  // 1 sequence, 4 / 24 / 32 tokens 6.2 / 12.3 / 16.4 us against 16.4 as a chunk; 16 sequences 12.3 / 43 / 55 against
-  // 53; 128 sequences 62 / 283 / 376 against 371 to 376 (heads of 64: 20 / 84 / 115 against 188; 1 sequence 6.2 / 12.4
-  // / 16.4 against 10.3).
-  if (p.len <= 24) return launch_linear_tokens(p, stream);
+  // Few tokens are sooner done one after the other, in one launch without tensor memory to set up.  32 heads of 128:
+  // 1 sequence of 8 / 16 / 24 tokens 8.4 / 10.4 / 14.4 us against 10.3 to 11 as a chunk, 16 sequences 21 / 33 / 45
+  // against 35, 128 sequences 127 / 221 / 303 against 213 to 217.  Heads of 64 have half the work in a token and more of
+  // a chunk's time in its chain: 1 sequence 8.3 / 12.3 / 14.4 against 10.3, 16 sequences 10.3 / 14.4 / 18.5 against 27,
+  // 128 sequences 37 / 67 / 90 (32 tokens: 120) against 168.
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  if (p.len <= (p.d == 64 && (long long)p.n_seq * p.H > 2 * sms ? 32 : 16)) return launch_linear_tokens(p, stream);
   return p.d == 128 ? run<128>(p, workspace, stream) : run<64>(p, workspace, stream);
 }
 
