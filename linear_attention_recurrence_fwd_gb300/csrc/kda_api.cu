@@ -601,7 +601,11 @@ kda_status_t kda_linear_bwd(const void* q, const void* k, const void* v, const v
     const kda_status_t apart = chunked_stride(*s, T, H, d_k);
     if (apart != KDA_OK) return apart;
   }
-  if (N == 0) return KDA_OK;
+  if (N == 0) {  // nothing to walk through; a sum over no rows is 0
+    return dlog_alpha && sum_log_alpha
+               ? from_cuda(cudaMemsetAsync(dlog_alpha, 0, (size_t)H * element_bytes(la_dtype), stream))
+               : KDA_OK;
+  }
   const size_t need = kda_linear_bwd_workspace_size(N, T, H, d_k, d_v, cu_seqlens != nullptr);
   if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   if (need && !aligned16(workspace)) return KDA_ERR_ALIGNMENT;
