@@ -44,6 +44,8 @@ namespace {
 constexpr int MOST = 8;      // CTAs to a cluster
 constexpr int PER = 32;      // entries a thread holds
 constexpr int LIST = 1024;   // biases held at a time
+constexpr int NARROW = 512 * PER;   // entries that 512 threads hold
+constexpr int MOST_SLICE = 51200;   // entries of a CTA's slice whose counts fit its shared memory
 constexpr float LOG2E = 1.4426950408889634f;
 
 struct __align__(16) Part { float top, sum; int at, unused; };  // of some entries: the largest, the sum against it, its lowest index
@@ -97,6 +99,7 @@ template <typename O, int E> __device__ __forceinline__ void store_vec(O* to, co
 // some on either side stay 0, for the entries of a vector that lie outside.
 constexpr int BEFORE = 12;
 template <bool EVEN> constexpr __host__ __device__ int said_words(int slice) { return EVEN ? slice : slice + slice / 32 + 2 * BEFORE; }
+template <bool EVEN> constexpr size_t said_bytes(int slice) { return (size_t)((said_words<EVEN>(slice) + 3) / 4 * 4) * 4; }
 
 // EVEN: every row starts with a vector.
 template <typename T, typename O, int THREADS, bool EVEN>
@@ -428,10 +431,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logits_kernel(LogitsP
 template <typename T, typename O, int THREADS, bool EVEN>
 cudaError_t launch_kernel(const LogitsProblem& p, int cluster, int slice, int rows, int step, cudaStream_t stream) {
   const bool counted = p.rules.repetition || p.rules.presence || p.rules.frequency;
-  const size_t smem = counted ? (size_t)((said_words<EVEN>(slice) + 3) / 4 * 4) * 4 : 0;
+  const size_t smem = counted ? said_bytes<EVEN>(slice) : 0;
   auto kernel = logits_kernel<T, O, THREADS, EVEN>;
   if (smem > 32 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // always to the most that a call may need: the limit is the function's, and another thread's call may be between
+    // its own setting and its launch
+    constexpr int MOST_BYTES = (int)said_bytes<EVEN>(THREADS == 1024 ? MOST_SLICE : NARROW);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST_BYTES);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
@@ -460,7 +466,7 @@ template <typename T, typename O> cudaError_t launch_typed(const LogitsProblem& 
   const int less = even ? 0 : 32;
   // the fewest CTAs that hold a row in registers, more while some SMs have none
   int cluster = 1;
-  while (cluster < MOST && (p.V > cluster * (512 * PER - less) ||
+  while (cluster < MOST && (p.V > cluster * (NARROW - less) ||
                             ((long long)p.N * p.R * cluster < sms && p.V >= cluster * 4096)))
     cluster *= 2;
   const int slice = ((p.V + cluster - 1) / cluster + 31) / 32 * 32;
@@ -469,8 +475,8 @@ template <typename T, typename O> cudaError_t launch_typed(const LogitsProblem& 
   // requests of 5 rows, 8 CTAs each, in 1 / 2 / 3 / 5 groups 384 / 408 / 435 / 480
   const long long groups = std::min((long long)p.R, std::max(2LL * sms / ((long long)p.N * cluster), 1LL));
   const int rows = (int)((p.R + groups - 1) / groups);
-  const bool narrow = slice <= 512 * PER - less;
-  const int step = (narrow ? 512 : 1024) * PER - less;
+  const bool narrow = slice <= NARROW - less;
+  const int step = (narrow ? NARROW : 1024 * PER) - less;
   if (narrow && even) return launch_kernel<T, O, 512, true>(p, cluster, slice, rows, step, stream);
   if (narrow) return launch_kernel<T, O, 512, false>(p, cluster, slice, rows, step, stream);
   if (even) return launch_kernel<T, O, 1024, true>(p, cluster, slice, rows, step, stream);
@@ -480,7 +486,7 @@ template <typename T, typename O> cudaError_t launch_typed(const LogitsProblem& 
 }  // namespace
 
 // The counts of a row fit the shared memory of a cluster up to here.
-int logits_most_counted() { return MOST * 51200; }
+int logits_most_counted() { return MOST * MOST_SLICE; }
 
 cudaError_t launch_logits_probs(const LogitsProblem& p, cudaStream_t stream) {
   if (p.N == 0 || p.R == 0) return cudaSuccess;
