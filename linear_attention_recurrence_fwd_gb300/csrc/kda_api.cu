@@ -333,6 +333,7 @@ kda_status_t kda_decode_commit(const void* q, const void* k, const void* v, cons
   kda_status_t st = validate_multi(q, k, v, log_alpha, beta, state, N, K, H, d_k, d_v);
   if (st != KDA_OK) return st;
   if (N > 0 && !accepted) return KDA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(accepted) & 3u) return KDA_ERR_ALIGNMENT;
   if ((long long)N * K == 0) return KDA_OK;
   return from_cuda(kda::launch_decode_tokens(q, k, v, log_alpha, beta, state, state, nullptr,
                                              true, accepted, N, K, H, 1.f, stream));
@@ -642,6 +643,7 @@ kda_status_t kda_linear_commit(const void* k, const void* v, long long k_stride,
                                long long la_head_stride, float* state, const int* accepted, int N, int K, int H,
                                int d_k, int d_v, cudaStream_t stream) {
   if (N > 0 && !accepted) return KDA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(accepted) & 3u) return KDA_ERR_ALIGNMENT;
   return run_linear_tokens(k, k, v, k_stride, k_stride, v_stride, log_alpha, la_dtype, la_token_stride, la_head_stride,
                            state, state, accepted, nullptr, KDA_F32, N, K, H, d_k, d_v, 1.f, stream);
 }
