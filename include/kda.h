@@ -683,7 +683,7 @@ KDA_API kda_status_t kda_linear_commit(const void* k, const void* v, long long k
  *                  requests mask_stride_n and rows mask_stride_r int32 apart
  *                  (0: shared); a bit that is not set masks its entry
  *   temperature  : fp32 [N]
- * Token ids outside [0, V) are left out everywhere.
+ * Token ids outside [0, V) are left out everywhere.  L and J are at most 2^30.
  *   logits : [N, R, V] in dtype (KDA_F32, KDA_BF16 or KDA_F16), vocabulary
  *            contiguous, rows stride_r and requests stride_n elements apart
  *   out    : [N, R, V] in out_dtype (KDA_F32 or dtype), contiguous; may be

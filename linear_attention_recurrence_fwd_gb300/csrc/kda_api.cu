@@ -662,6 +662,8 @@ kda_status_t kda_logits_probs(const void* logits, kda_dtype_t dtype, long long s
   if (u.L < 0 || u.J < 0 || u.tokens_stride < 0 || u.mask_stride_n < 0 || u.mask_stride_r < 0)
     return KDA_ERR_INVALID_ARG;
   if (!u.bias_ids != !u.bias && u.J > 0) return KDA_ERR_INVALID_ARG;
+  // the kernel counts past the last of them, in 32 bits
+  if (u.L > (1 << 30) || u.J > (1 << 30)) return KDA_ERR_UNSUPPORTED;
   if (u.J == 0) u.bias_ids = nullptr;
   if ((u.repetition || u.presence || u.frequency) && V > kda::logits_most_counted()) return KDA_ERR_UNSUPPORTED;
   for (const void* x : {(const void*)u.tokens, (const void*)u.lens, (const void*)u.prompt_lens, (const void*)u.drafts,
