@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
   const Segment seg = find_segment(p, CHUNK, (p.len + CHUNK - 1) / CHUNK, slot);
   if (seg.n < 0 || seg.tokens <= 0) {
     if (a.sums && tid == 0) a.sums[(size_t)slot * p.H + h] = 0.f;
+    // one CTA waits even if offsets leave no rows to any: what follows this launch relies on the ones before it
+    if (blockIdx.x == 0) dependency_wait();
     return;
   }
   if (sb & 1023u) {  // the tiles' swizzle goes by address

@@ -28,3 +28,16 @@ def test_the_gradient_of_an_empty_batch():
         assert g["q"].shape == x.shape and g["initial_state"].shape == (0, 5, 64, 64)
         assert g["log_alpha"].tolist() == [0.0] * 5
     assert kda.kda_last_device_status() == 0
+
+
+@pytest.mark.parametrize("rows", [40, 3000])
+def test_gradients_where_offsets_leave_no_rows(rows):
+    """Offsets that are not allowed (they end before the last row): flagged, and what does not depend on rows is there."""
+    H, d = 2, 128
+    x = [torch.randn((rows, H, d), device="cuda").to(torch.bfloat16) for _ in range(4)]
+    d_final = torch.randn((2, H, d, d), device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for _ in range(20):
+        g = kda.kda_linear_bwd(*x[:3], torch.full((H,), -0.1, device="cuda"), x[3], d_final_state=d_final, cu_seqlens=cu)
+        assert torch.equal(g["initial_state"], d_final) and g["log_alpha"].tolist() == [0.0] * H
+    assert kda.kda_last_device_status() == 1
