@@ -23,6 +23,11 @@ __device__ __forceinline__ bool offsets_good(const LinearProblem& p, int n) {
   const int a = p.cu_seqlens[n], b = p.cu_seqlens[n + 1];
   return a >= 0 && b >= a && b <= p.T && (n > 0 || a == 0) && (n < p.n_seq - 1 || b == p.T);
 }
+// Flags a call whose offsets are not, once for all of its launches.
+static __global__ void __launch_bounds__(256) check_offsets_kernel(LinearProblem p) {
+  for (int n = threadIdx.x; n < p.n_seq; n += 256)
+    if (!offsets_good(p, n)) atomicExch(p.status, (int)KDA_ERR_INVALID_ARG);
+}
 
 // A token's decay as it is stored, so that a load can be on its way for long, and what it stands for.
 __device__ __forceinline__ uint32_t load_decay_bits(const LinearProblem& p, long long row, int h) {
@@ -31,17 +36,6 @@ __device__ __forceinline__ uint32_t load_decay_bits(const LinearProblem& p, long
 }
 __device__ __forceinline__ float decay_of_bits(const LinearProblem& p, uint32_t bits) {
   return __uint_as_float(p.la_f32 ? bits : bits << 16);
-}
-// Whether a call's offsets are.
-static __global__ void __launch_bounds__(256) check_offsets_kernel(LinearProblem p) {
-  for (int n = threadIdx.x; n < p.n_seq; n += 256)
-    if (!offsets_good(p, n)) atomicExch(p.status, (int)KDA_ERR_INVALID_ARG);
-}
-
-__device__ __forceinline__ float load_decay(const LinearProblem& p, long long row, int h) {
-  const long long at = row * p.la_token_stride + h * p.la_head_stride;
-  return p.la_f32 ? static_cast<const float*>(p.log_alpha)[at]
-                  : __bfloat162float(static_cast<const __nv_bfloat16*>(p.log_alpha)[at]);
 }
 
 // Two fp32 numbers in a register pair, and what sm_100 does with both at once.

@@ -130,11 +130,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ void lds_v4(uint32_t at, uint32_t (&u)[4]) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(at) : "memory");
 }
-__device__ __forceinline__ float lds_f32(uint32_t at) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
-}
 __device__ __forceinline__ float lo_f32(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 // x as two bf16 numbers, two x to a word; what the first leaves is exact.
