@@ -617,7 +617,11 @@ KDA_API size_t kda_linear_fwd_workspace_size(int N, int T, int H, int d_k, int d
  * gradients and weights are rounded to it once), sums in fp32; so dlog_alpha is
  * as good as bf16 operands make it in fp32, too (2^-8 of its terms, which may
  * cancel).
- * Results do not depend on anything but the arguments (no atomics).
+ * A value that is not finite is in those gradients, and only in those, that the
+ * formulas have it in: one in q or d_out reaches back to its sequence's
+ * beginning, one in k or v on to its end (a log_alpha that is NaN may reach all
+ * of its sequence and head).
+ * Results do not depend on anything but the arguments (no atomics on sums).
  */
 KDA_API kda_status_t kda_linear_bwd(const void* q, const void* k, const void* v, const void* d_out,
                                     long long q_stride, long long k_stride, long long v_stride,

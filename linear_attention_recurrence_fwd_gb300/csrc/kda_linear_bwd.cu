@@ -38,9 +38,11 @@
 // a CTA that stays, with the next chunk's tiles on their way from the moment
 // theirs are free, took 177 instead of 188 us by itself and as long in the call
 // (302 to 307 us).  Two chunks at once would need twice the tensor memory (its
-// 512 columns are the four accumulators of one).  The code is kept within 32
-// KB, as the instruction cache holds it (313 -> 306 us).
+// 512 columns are the four accumulators of one).  The code that a chunk of
+// finite values runs is kept within 32 KB, as the instruction cache holds it
+// (313 -> 306 us).
 #include <algorithm>
+#include <cstddef>
 
 #include "kda_linear_walk.cuh"
 
@@ -59,7 +61,8 @@ struct Grad {
 template <int D> struct GradShape : Shape<D> {
   using Shape<D>::TILE;
   static constexpr uint32_t Q = 0, K = TILE, V = 2 * TILE, DO = 3 * TILE, S = 4 * TILE, DS = 5 * TILE, MISC = 6 * TILE;
-  static constexpr uint32_t SMEM_USED = MISC + 8192, SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr uint32_t ODD = MISC + 8192;
+  static constexpr uint32_t SMEM_USED = ODD + 2048, SMEM = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
   static constexpr uint32_t T0 = 0, T1 = 128, T2 = 256, T3 = 384;  // tensor memory
 };
 
@@ -86,6 +89,129 @@ __device__ __forceinline__ float sum_lanes(float (&x)[8]) {
 }
 
 constexpr int GRAD_WARPS = 16, GRAD_THREADS = 32 * GRAD_WARPS + 32;
+
+// Values that are not finite.  One reaches the gradients that the formulas put it into, and no others: in a query or an
+// output's gradient those of its own token and earlier ones, in a key or a value those of its own and later ones.  Weights
+// that are 0 would carry it further, into a whole chunk.  It shows in the sums over a chunk's pairs (0 times it is not
+// finite, either), so that other chunks pay nothing but a look at those: all that follows is in functions of their own, out
+// of the way of the code that every chunk runs (8192 tokens 307 -> 309 us; in the loops themselves 318 to 323).
+struct Odd {
+  static constexpr int NEVER = 0x7fffffff;
+  int edge[3][128];  // of channels of Q, K and dO: 127 less the last token (K: the first token) with such a value
+  int queries, keys; // 127 less the last token with one in Q or dO; the first token with one in K or V
+  int any;           // whether the chunk may have some
+};
+
+// In a chunk that may have some, before the weights' products: takes them out of Q, K and dO, of which the scores have been
+// formed (this thread's token's, in its part of the channels); makes the weights of pairs in the wrong order 0, which only
+// products with 0 have made so; and forms the decays' sums again of the pairs that some finite gradient of a decay needs:
+// a later token after the last odd one of the queries' side with an earlier one before the first odd one of the keys'.
+template <int D>
+__device__ __noinline__ bool without_odd(uint8_t* smem, uint32_t tb, uint64_t* cleared, const float* s_g, float* s_out, float* s_in, float scale) {
+  using W = GradShape<D>;
+  Odd* odd = reinterpret_cast<Odd*>(smem + W::ODD);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, part = warp >> 2, trow = 32 * quarter + lane;
+  auto at = [&](uint32_t tile, int row, int ch) {
+    return smem + tile + ch / 64 * W::BLOCK + row * 128 + (((uint32_t)(ch / 8 % 8) ^ (uint32_t)(row & 7)) << 4) + ch % 8 * 2;
+  };
+  if (threadIdx.x < offsetof(Odd, any) / 4) odd->edge[0][threadIdx.x] = Odd::NEVER;  // (and the two after the edges)
+  __syncwarp();
+  if (lane == 0) mbar_arrive(cleared);
+  if (!wait_for(cleared, 0)) return false;
+#pragma unroll 1
+  for (int tile = 0; tile < 4; ++tile) {
+    const bool keys = tile == 1 || tile == 2;
+    const int when = keys ? trow : 127 - trow;
+#pragma unroll 1
+    for (int ch = part * (D / 4); ch < (part + 1) * (D / 4); ++ch) {
+      uint16_t* x = reinterpret_cast<uint16_t*>(at(tile * W::TILE, trow, ch));
+      if ((*x & 0x7f80) != 0x7f80) continue;
+      atomicMin(keys ? &odd->keys : &odd->queries, when);
+      if (tile == 2) continue;  // (the values' side meets no weights)
+      atomicMin(&odd->edge[tile == 3 ? 2 : tile][ch], when);
+      *x = 0;
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(cleared);
+  if (!wait_for(cleared, 1)) return false;
+  const uint32_t weights = tb + ((uint32_t)(32 * quarter) << 16) + 32 * part;
+#pragma unroll 1
+  for (int c = 0; c < 12; ++c) {  // four pairs of later tokens (T0: earlier ones) at a time
+    uint32_t u[4];
+    const uint32_t from = weights + c / 4 * 128 + c % 4 * 4;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "r"(from));
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int other = 32 * part + c % 4 * 8 + 2 * i;
+      if (c < 4 ? other > trow : other < trow) u[i] &= 0xffff0000u;
+      if (c < 4 ? other + 1 > trow : other + 1 < trow) u[i] &= 0xffffu;
+    }
+    tmem_st4u(from, u);
+  }
+  tmem_st_wait();
+  const int after = 127 - min(odd->queries, 128), before = odd->keys;
+  float later = 0.f;
+#pragma unroll 1
+  for (int i = 32 * part; i < 32 * part + 32; ++i) {
+    float w = 0.f;
+    if (i > trow && i > after && trow < before) {
+      float a = 0.f, b = 0.f;
+#pragma unroll 1
+      for (int ch = 0; ch < D; ++ch) {
+        auto get = [&](uint32_t tile, int row) { return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at(tile, row, ch))); };
+        a = fmaf(get(W::Q, i), get(W::K, trow), a);
+        b = fmaf(get(W::DO, i), get(W::V, trow), b);
+      }
+      w = scale * ex2(-(s_g[i] - s_g[trow])) * a * b;
+    }
+    later += w;
+#pragma unroll
+    for (int o = 16; o; o /= 2) w += __shfl_xor_sync(~0u, w, o);
+    if (lane == 0) s_in[quarter * 128 + i] = w;
+  }
+  s_out[part * 128 + trow] = later;
+  return true;
+}
+
+// Afterwards: the channels that they reach, in gradients that have been written.
+template <int D> __device__ __noinline__ void mark_odd(const uint8_t* smem, const Grad& a, int row0, int rows, int h) {
+  const Odd* odd = reinterpret_cast<const Odd*>(smem + GradShape<D>::ODD);
+  const int warp = threadIdx.x >> 5, part = warp >> 2, trow = 32 * (warp & 3) + (threadIdx.x & 31);
+  __syncwarp();
+  if (trow >= rows) return;
+  const size_t at = ((size_t)(row0 + trow) * a.p.H + h) * D;
+#pragma unroll 1
+  for (int ch = part * (D / 4); ch < (part + 1) * (D / 4); ++ch) {
+    if (odd->edge[0][ch] <= 127 - trow) static_cast<uint16_t*>(a.dk)[at + ch] = 0x7fff;
+    if (odd->edge[1][ch] <= trow) static_cast<uint16_t*>(a.dq)[at + ch] = 0x7fff;
+    if (odd->edge[2][ch] <= 127 - trow) static_cast<uint16_t*>(a.dv)[at + ch] = 0x7fff;
+  }
+}
+
+// A warp, before the decays' gradients are formed: tokens' parts that only those take which are not finite.
+__device__ __noinline__ void drop_odd(const Odd* odd, float* s_out, float* s_x) {
+#pragma unroll 1
+  for (int i = threadIdx.x & 31; i < 512; i += 32) {
+    if (127 - i % 128 >= odd->queries) s_x[i] = 0.f;
+    if (i % 128 >= odd->keys) s_out[i] = 0.f;
+  }
+  __syncwarp();
+}
+// And afterwards those.
+__device__ __noinline__ void mark_odd_decays(const Odd* odd, const Grad& a, int row0, int rows, int slot, int h) {
+  __syncwarp();
+#pragma unroll 1
+  for (int t = threadIdx.x & 31; t < rows; t += 32) {
+    if (t <= odd->keys && 127 - t < odd->queries) continue;
+    const size_t at = (size_t)(row0 + t) * a.p.H + h;
+    if (a.sums) a.sums[(size_t)slot * a.p.H + h] = NAN;
+    else if (a.p.la_f32) static_cast<float*>(a.dla)[at] = NAN;
+    else static_cast<uint16_t*>(a.dla)[at] = 0x7fff;
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(GRAD_THREADS, 1)
@@ -123,7 +249,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
   uint64_t *landed = bars + 9, *images = bars + 10;
   uint64_t *clean = bars + 11, *r_ready = bars + 12, *w_ready = bars + 13, *x_ready = bars + 14, *dq_read = bars + 15,
            *y_ready = bars + 16, *z_ready = bars + 17, *sums_ready = bars + 18;  // by all warps
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 19);
+  uint64_t* cleared = bars + 19;  // by all warps, of a chunk with values that are not finite
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
+  Odd* s_odd = reinterpret_cast<Odd*>(smem + W::ODD);
 
   if (warp == 1) {
     tmem_alloc(s_tmem, 512);
@@ -131,7 +259,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
   }
   if (warp == GRAD_WARPS && lane == 0) {
 #pragma unroll 1
-    for (int i = 0; i < 19; ++i) mbar_init(bars + i, i < 11 ? 1 : GRAD_WARPS);
+    for (int i = 0; i < 20; ++i) mbar_init(bars + i, i < 11 ? 1 : GRAD_WARPS);
+    s_odd->any = 0;
     mbar_fence_init();
     fence_proxy_async_smem();
     // on their way while the rest of the CTA is made ready
@@ -212,6 +341,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
     const float g_mine = -s_g[trow], lead = p.scale * ex2(g_mine), trail = ex2(-s_g[127] - g_mine), keep = ex2(-s_g[127]);
     constexpr int SC = D / 4;
     const uint32_t row_at = (uint32_t)trow * 128;
+    bool odd = false;
     auto piece = [&](int x) { return (uint32_t)(x / 8) * W::BLOCK + row_at + (((uint32_t)(x % 8) ^ (uint32_t)(trow & 7)) << 4); };
 
     ok = wait_for(landed, 0);
@@ -285,6 +415,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
       float later_0, later_1;
       unpair(later, &later_0, &later_1);
       s_out[part * 128 + trow] = later_0 + later_1;
+      if (!(fabsf(later_0 + later_1) < INFINITY)) s_odd->any = 1;
       tmem_st_wait();
       tc_fence_before_sync();
       __syncwarp();
@@ -317,6 +448,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
         tmem_st4u(my + W::T0 + 32 * part + (j0 - 32 * part) / 2, u);
       }
       tmem_st_wait();
+      ok = wait_for(w_ready, 0);
+      odd = s_odd->any != 0;
+      if (ok && odd) ok = without_odd<D>(smem, tb, cleared, s_g, s_out, s_in, p.scale);
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(r_ready);
@@ -392,8 +526,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
         }
       }
     }
+    if (ok && odd) mark_odd<D>(smem, a, row0, rows, h);
     // ---- the decays' gradients
     if (ok && warp == 0 && (a.dla || a.sums) && (ok = wait_for(sums_ready, 0))) {
+      if (odd) drop_odd(s_odd, s_out, s_x);
       float total = lane < GRAD_WARPS ? keep * s_dot[lane] : 0.f;
 #pragma unroll 1
       for (int t = lane; t < 128; t += 32) {  // (what has been added up takes the place of its first part)
@@ -438,6 +574,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1)
         for (int o = 16; o; o /= 2) sum += __shfl_xor_sync(~0u, sum, o);
         if (lane == 0) a.sums[(size_t)slot * p.H + h] = sum;
       }
+      if (odd) mark_odd_decays(s_odd, a, row0, rows, slot, h);
     }
   }
   if (!ok && lane == 0) atomicExch(p.status, (int)KDA_ERR_TIMEOUT);
