@@ -586,7 +586,8 @@ KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft
  * are sums in fp32.  Operands that are not given in bf16 (weighted values,
  * weights, states) enter them as two bf16
  * numbers each (16 bits), but with KDA_BF16 outputs the weights and the states
- * that only outputs see enter as one.  A value that is not finite leaves its
+ * that only outputs see enter as one.  (So KDA_BF16 outputs of a sequence's last
+ * part may differ in their rounding from those of a call without final_state.)  A value that is not finite leaves its
  * channel not finite from its token on; earlier tokens do not see it.  (Prompts
  * of a few tokens are taken token by token, without chunks.)
  */
@@ -673,6 +674,8 @@ KDA_API kda_status_t kda_linear_commit(const void* k, const void* v, long long k
  *   x = x + each bias given for it; a masked entry gets probability 0;
  *   p = softmax(x / temperature); temperature <= 0 (or NaN): 1 at the largest
  *   entry, the first of equal ones, 0 elsewhere.
+ * (A repetition below 2^-126 counts as 0, a positive temperature below 2e-37 as
+ * about that.)
  * Of kda_logits_rules_t every pointer may be NULL (that rule is left out):
  *   tokens       : int32 [N, L], rows tokens_stride apart: each request's
  *                  history, of which the first lens[n] tokens are real

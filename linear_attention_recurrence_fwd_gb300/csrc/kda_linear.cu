@@ -58,7 +58,8 @@ cudaError_t launch_linear_fwd(const LinearProblem& p, void* workspace, cudaStrea
   // 1 sequence of 8 / 16 / 24 tokens 8.4 / 10.4 / 14.4 us against 10.3 to 11 as a chunk, 16 sequences 21 / 33 / 45
   // against 35, 128 sequences 127 / 221 / 303 against 213 to 217.  Heads of 64 have half the work in a token and more of
   // a chunk's time in its chain: 1 sequence 8.3 / 12.3 / 14.4 against 10.3, 16 sequences 10.3 / 14.4 / 18.5 against 27,
-  // 128 sequences 37 / 67 / 90 (32 tokens: 120) against 168.
+  // 128 sequences 37 / 67 / 90 (32 tokens: 120) against 168.  (Packed calls go by the rows of all sequences, as only the
+  // device knows each one's: 61 sequences of 5 tokens take 137 us as a chunk each, 37 token by token.)
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;

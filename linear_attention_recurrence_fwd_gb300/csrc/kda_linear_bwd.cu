@@ -31,14 +31,17 @@
 // memory (Q, K, V, dO, S, dS), through which the gradients leave once their
 // content has been used.
 //
-// Measured (8192 tokens, 32 heads of 128): 305 us, of which the segments' ends
-// take 50, their join 8, the images 70 and this kernel 177 to 188 (573 MB, 38 %
+// Measured (8192 tokens, 32 heads of 128): 308 us, of which the segments' ends
+// take 50, their join 8, the images 70 and this kernel 177 to 190 (573 MB, 38 %
 // of DRAM's throughput, tensor pipe 17 %, issue slots 31 %).  What bounds it is
 // the chain within a chunk, 13 us of products and the arithmetic between them:
 // a CTA that stays, with the next chunk's tiles on their way from the moment
 // theirs are free, took 177 instead of 188 us by itself and as long in the call
-// (302 to 307 us).  Two chunks at once would need twice the tensor memory (its
-// 512 columns are the four accumulators of one).  The code that a chunk of
+// (302 to 307 us).  Two chunks at once do not fit the tensor memory as it is
+// used: while scores are in it, one has three times 128 columns of them and 128
+// of sums.  Later on the weights leave half of the scores' columns free, but in
+// pieces of 16, one beside each 16 of weights, where no sum fits; weights laid
+// out together would make room.  The code that a chunk of
 // finite values runs is kept within 32 KB, as the instruction cache holds it
 // (313 -> 306 us).
 #include <algorithm>

@@ -19,7 +19,8 @@
 // copy bandwidth; five tokens of 61 requests 38 us to verify (140 MB) and 43 to
 // commit (264 MB, 6.1 TB/s); one request 4.3 us.  KT of 2, 4, 5, 6 and 8 gave
 // 43, 41, 38, 39 and 43 us for the verification, a launch bound of four CTAs on
-// an SM 55 us for the commit (spills).
+// an SM 55 us for the commit (spills).  (KT is chosen at these sizes alone; eight
+// tokens, as five and three, take 58 us to verify.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -18,9 +18,11 @@
 // caller gets, segments' ends, all of a call with fp32 outputs) and one where
 // only bf16 outputs see it; for fp32 outputs so are P and the operand S.
 //
-// A sequence is cut into segments of seg_len tokens where there are fewer
-// (sequence, head) pairs than SMs.  ENDS finds each segment's contribution to
-// the state at its end, linear_scan_kernel joins them into the states at the
+// A sequence is cut into segments of seg_len tokens where that takes the
+// machine fewer steps (segment_tokens).  How long packed sequences are only the
+// device knows, so such a call goes the cut way as soon as it has rows for a
+// segment: where no sequence is longer than one, ENDS does nothing and the scan
+// copies states.  ENDS finds each segment's contribution to the state at its end, linear_scan_kernel joins them into the states at the
 // segments' starts, and OUTPUTS walks every segment from there.  ENDS goes
 // through a segment backwards with weights that reach to the segment's end, so
 // the sum stays where it is in tensor memory.
@@ -38,8 +40,9 @@
 // whichever tile is free first; outputs pass through the values' tile, so that
 // they leave in whole lines.  One CTA on an SM.
 //
-// Measured (32 heads of 128): 8192 tokens 98 us (floor 40; ENDS 31, scan 5, OUTPUTS 66), 65536 packed ones 593 us
-// (floor 318; 196, 21, 378), of which the keys and values come twice: 3.2 GB in all, 5.4 TB/s.  OUTPUTS at 8192 tokens:
+// Measured (32 heads of 128): 8192 tokens 98 us (floor 40; ENDS 31, scan 5, OUTPUTS 66; with fp32 outputs 133, floor 50:
+// the weights' warps spill second numbers), 65536 packed ones 593 us (floor 318; 196, 21, 378), of which the keys and
+// values come twice: 3.2 GB in all, 5.4 TB/s.  OUTPUTS at 8192 tokens:
 // DRAM 48 %, tensor pipe 23 %, issue slots 30 %: what bounds it is the chain of a chunk, from the values to the state
 // and on to its operand, with 128 of 152 SMs at work.  A product of 128 x 128 x 128 takes 937 clocks with A's channels
 // along K, 561 with its tokens, 602 from tensor memory.  Code size matters most: loops that unrolled to 94 KB took 831
@@ -74,7 +77,9 @@ struct Segment {
 };
 
 // Sequence n of a packed call has slots row0 / seg_len + n and on, enough for its length; a warp looks for
-// the one that holds slot w.  (Offsets that overlap may give a slot twice; then the first sequence has it.)
+// the one that holds slot w, 32 sequences at a time from the first on, so that a CTA's start takes longer the more there
+// are (65536 rows of 32 heads: 4 sequences 0.62 ms, 512 of them, a chunk each, 3.45).  (Offsets that overlap may give a
+// slot twice; then the first sequence has it.)
 __device__ __forceinline__ Segment find_segment(const LinearProblem& p, int seg_len, int segs, int w) {
   Segment s{-1, 0, 0, 0, 0, 0};
   if (!p.cu_seqlens) {

@@ -24,8 +24,10 @@
 //
 // Measured: 256 requests of 5 rows of 131072 (fp32, everything given) 332 us, floor 201; without rules 247, the mask
 // adds 9, biases 18, penalties 55.  DRAM is at 51 %, issue slots at 46 %: 189 million warp instructions, 36 to each 32
-// entries.  37 requests of 8 rows of 50021 in bf16 43 us, floor 9: edges of rows, counts read one by one (48 us with
-// each one's place worked out by itself), two groups of a request's rows that each count its history.  One request 6.4
+// entries.  37 requests of 8 rows of 50021 in bf16 43 us, floor 9: 61 warp instructions to each 32 entries, for edges of
+// rows, counts read one by one (48 us with each one's place worked out by itself), two groups of a request's rows that each
+// count its history.  Where rows of logits and of probabilities start differently within 16 bytes (those 50021 entries in
+// rows 50048 apart) every store is one of an entry: 71 us, without biases, where rows packed alike take 39.  One request 6.4
 // to 8.4 us, dependent loads and two barriers.  Dropped: 16 entries to each of 1024 threads, with the next row's loads
 // ahead (705 us without rules); sums and stores in one loop over tiles, so that the loads come once in the code (383
 // us, spills).
