@@ -587,8 +587,9 @@ KDA_API kda_status_t kda_draft_accept(const int* draft_tokens, const void* draft
  * weights, states) enter them as two bf16
  * numbers each (16 bits), but with KDA_BF16 outputs the weights and the states
  * that only outputs see enter as one.  (So KDA_BF16 outputs of a sequence's last
- * part may differ in their rounding from those of a call without final_state.)  A value that is not finite leaves its
- * channel not finite from its token on; earlier tokens do not see it.  (Prompts
+ * part may differ in their rounding from those of a call without final_state.)
+ * A value that is not finite leaves its channel not finite from its token on;
+ * earlier tokens do not see it.  (Prompts
  * of a few tokens are taken token by token, without chunks.)
  */
 KDA_API kda_status_t kda_linear_fwd(const void* q, const void* k, const void* v, long long q_stride,
